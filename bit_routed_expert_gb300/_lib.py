@@ -12,7 +12,7 @@ from . import build as _build
 _lib = None
 
 BRE_OK, BRE_ERR_ARG, BRE_ERR_UNSUPPORTED, BRE_ERR_CUDA, BRE_ERR_WORKSPACE = range(5)
-BRE_DEVERR_EXPERT_ID, BRE_DEVERR_ROW_ID, BRE_DEVERR_TIMEOUT = 1, 2, 4
+BRE_DEVERR_EXPERT_ID, BRE_DEVERR_ROW_ID, BRE_DEVERR_TIMEOUT, BRE_DEVERR_PAGE = 1, 2, 4, 8
 BRE_FMT_Q2_K, BRE_FMT_Q8_0, BRE_FMT_Q2_K_R16 = 1, 2, 3
 
 # exported symbol -> (restype, argtypes)
@@ -32,6 +32,12 @@ SIGNATURES = {
     "moe_combine": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _P, _P, _P]),
     "moe_residual_norm": (_I, [_P, _P, _I, _I, _F, _F, _P, _P, _P]),
     "engram_gather_decode": (_I, [_P, _P, _I, _P, _I, _I, _P, _P, _P]),
+    "kv_append": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _I, _P, _I, _I, _P, _P]),
+    "kv_read": (_I, [_P, _P, _P, _I, _P, _I, _I, _P, _P, _P, _P]),
+    "kv_select_workspace": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "kv_select": (_I, [_P, _P, _I64, _I, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P, _P]),
+    "kv_attend_workspace": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "kv_attend": (_I, [_P, _P, _I64, _I, _P, _P, _I, _P, _I, _I, _P, _I, _F, _P, _P, _P, _SZ, _P, _P]),
     "bre_dequant": (_I, [_I, _P, _I64, _P, _P]),
     "bre_repack_q2k_r16": (_I, [_P, _P, _I, _I, _I, _I64, _I64, _P]),
     "bre_set_ffn_wait_limit": (_I, [_I64]),
@@ -43,6 +49,11 @@ class BreWeights(C.Structure):
                 ("n_experts", C.c_int32), ("d", C.c_int32), ("d_ff", C.c_int32),
                 ("expert_stride_gate", C.c_int64), ("expert_stride_up", C.c_int64),
                 ("expert_stride_down", C.c_int64)]
+
+
+class BreKvCache(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("bounds", C.c_void_p), ("bound_exp", C.c_void_p), ("n_pages", C.c_int32),
+                ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32)]
 
 
 class BreError(RuntimeError):

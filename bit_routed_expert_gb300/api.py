@@ -12,7 +12,8 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import BRE_FMT_Q2_K, BRE_FMT_Q2_K_R16, BRE_FMT_Q8_0, BreWeights, check, ptr, stream_handle
+from ._lib import (BRE_FMT_Q2_K, BRE_FMT_Q2_K_R16, BRE_FMT_Q8_0, BreKvCache, BreWeights, check, ptr,
+                   stream_handle)
 
 
 def _dev(t: torch.Tensor, name: str):
@@ -239,6 +240,150 @@ def bre_dequant(fmt: int, blocks, stream=None):
     out = torch.empty(n * (256 if fmt == BRE_FMT_Q2_K else 32), dtype=torch.float32, device=blocks.device)
     check(L.bre_dequant(fmt, ptr(_dev(blocks, "blocks")), n, ptr(out), stream_handle(stream)), "bre_dequant")
     return out
+
+
+KV_BLOCK = 64   # tokens of a cache page, and of a block of the selection
+
+
+@dataclass
+class KvCache:
+    """A paged key/value cache on the device (layout: bre_kv_cache in include/bre.h): pages uint8
+    [n_pages, n_kv_heads, 128 D + 128], bounds int8 [n_pages, n_kv_heads, 2, D], bound_exp int8
+    [n_pages, n_kv_heads].  Which page holds which block of a sequence is the caller's table."""
+    pages: torch.Tensor
+    bounds: torch.Tensor
+    bound_exp: torch.Tensor
+
+    def __post_init__(self):
+        n, H, _, D = self.bounds.shape
+        if self.pages.shape != (n, H, 2 * KV_BLOCK * (D + 1)) or self.bound_exp.shape != (n, H):
+            raise ValueError("pages, bounds and bound_exp do not belong together")
+        if self.pages.dtype != torch.uint8 or self.bounds.dtype != torch.int8 or self.bound_exp.dtype != torch.int8:
+            raise ValueError("pages must be uint8, bounds and bound_exp int8")
+        _dev(self.pages, "pages"), _dev(self.bounds, "bounds"), _dev(self.bound_exp, "bound_exp")
+        self.n_pages, self.n_kv_heads, self.head_dim = n, H, D
+        self._struct = BreKvCache(self.pages.data_ptr(), self.bounds.data_ptr(), self.bound_exp.data_ptr(), n, H, D)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, device) -> "KvCache":
+        """Pages as allocated: kv_append writes whatever is read later."""
+        return cls(torch.empty((n_pages, n_kv_heads, 2 * KV_BLOCK * (head_dim + 1)), dtype=torch.uint8, device=device),
+                   torch.empty((n_pages, n_kv_heads, 2, head_dim), dtype=torch.int8, device=device),
+                   torch.empty((n_pages, n_kv_heads), dtype=torch.int8, device=device))
+
+
+def _rows(t: torch.Tensor, name: str, T: int, heads: int | None, D: int) -> int:
+    """Row stride (elements) of [T, heads, D] BF16 rows, which may be a slice of wider rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.element_size() != 2 or t.dtype == torch.float16:
+        raise ValueError(f"{name} must be bfloat16 (or its 16-bit patterns)")
+    n, h, d = t.shape
+    if n != T or d != D or (heads is not None and h != heads):
+        raise ValueError(f"{name} must be [{T}, {'heads' if heads is None else heads}, {D}], got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (h > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: a token's heads must follow one another without gaps")
+    return t.stride(0) if T > 1 else (h * D + 7) // 8 * 8
+
+
+def _i32(t: torch.Tensor, name: str, shape) -> torch.Tensor:
+    if t.dtype != torch.int32 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+    return _dev(t, name)
+
+
+def _kv_tokens(seq, pos, table):
+    T = seq.shape[0]
+    _i32(seq, "seq", (T,)), _i32(pos, "pos", (T,))
+    B, N = table.shape
+    _i32(table, "table", (B, N))
+    return T, B, N
+
+
+def kv_append(cache: KvCache, k, v, seq, pos, table, dev_err=None, stream=None):
+    """Quantise and store the keys and values ([T, n_kv_heads, D] BF16, possibly slices of a fused
+    projection's rows) of tokens seq[t], pos[t] (int32 [T]) and refresh the bounds of their blocks;
+    table int32 [B, N] holds the page of each block of 64 positions of each sequence."""
+    L = _lib.load()
+    T, B, N = _kv_tokens(seq, pos, table)
+    ks = _rows(k, "k", T, cache.n_kv_heads, cache.head_dim)
+    vs = _rows(v, "v", T, cache.n_kv_heads, cache.head_dim)
+    check(L.kv_append(C.byref(cache._struct), ptr(k), ptr(v), ks, vs, ptr(seq), ptr(pos), T, ptr(table), B, N,
+                      ptr(dev_err), stream_handle(stream)), "kv_append")
+
+
+def kv_read(cache: KvCache, seq, pos, table, k_out=None, v_out=None, dev_err=None, stream=None):
+    """The stored keys and values of tokens seq[t], pos[t]: two BF16 tensors [T, n_kv_heads, D]."""
+    L = _lib.load()
+    T, B, N = _kv_tokens(seq, pos, table)
+    shape = (T, cache.n_kv_heads, cache.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=seq.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=seq.device)
+    if k_out.shape != shape or v_out.shape != shape or k_out.element_size() != 2 or v_out.element_size() != 2:
+        raise ValueError(f"k_out and v_out must be bfloat16 {list(shape)}")
+    check(L.kv_read(C.byref(cache._struct), ptr(seq), ptr(pos), T, ptr(table), B, N, ptr(_dev(k_out, "k_out")),
+                    ptr(_dev(v_out, "v_out")), ptr(dev_err), stream_handle(stream)), "kv_read")
+    return k_out, v_out
+
+
+def kv_select_workspace(T: int, n_heads: int, n_kv_heads: int, head_dim: int, B: int, N: int, k: int) -> int:
+    return _lib.load().kv_select_workspace(T, n_heads, n_kv_heads, head_dim, B, N, k)
+
+
+def kv_select(q, cache: KvCache, seq, pos, table, k: int, n_sink: int = 1, n_local: int = 2, ws=None, ids=None,
+              scores=None, dev_err=None, stream=None):
+    """For each token and kv head the k blocks to attend to: the first n_sink, the last n_local, and
+    the best-scored others.  q [T, n_heads, D] BF16.  Returns (ids int32 [T, n_kv_heads, k], ascending,
+    then -1; scores float32, then 0)."""
+    L = _lib.load()
+    T, B, N = _kv_tokens(seq, pos, table)
+    Hq, H, D = q.shape[1], cache.n_kv_heads, cache.head_dim
+    qs = _rows(q, "q", T, None, D)
+    if ws is None:
+        ws = torch.zeros(L.kv_select_workspace(T, Hq, H, D, B, N, k), dtype=torch.uint8, device=q.device)
+    ids = (torch.empty((T, H, k), dtype=torch.int32, device=q.device) if ids is None
+           else _i32(ids, "ids", (T, H, k)))
+    if scores is None:
+        scores = torch.empty((T, H, k), dtype=torch.float32, device=q.device)
+    elif scores.dtype != torch.float32 or scores.shape != (T, H, k):
+        raise ValueError(f"scores must be float32 {[T, H, k]}")
+    check(L.kv_select(C.byref(cache._struct), ptr(q), qs, Hq, ptr(seq), ptr(pos), T, ptr(table), B, N, k, n_sink,
+                      n_local, ptr(ids), ptr(_dev(scores, "scores")), ptr(ws), ws.numel(), ptr(dev_err),
+                      stream_handle(stream)), "kv_select")
+    return ids, scores
+
+
+def kv_attend_workspace(T: int, n_heads: int, n_kv_heads: int, head_dim: int, B: int, k: int) -> int:
+    return _lib.load().kv_attend_workspace(T, n_heads, n_kv_heads, head_dim, B, k)
+
+
+def kv_attend(q, cache: KvCache, seq, pos, table, ids, scale: float | None = None, ws=None, out=None, lse=None,
+              dev_err=None, stream=None):
+    """Attention of q [T, n_heads, D] (BF16) over the blocks ids [T, n_kv_heads, k] lists, up to each
+    token's own position; scale defaults to 1/sqrt(D).  Returns (out BF16 [T, n_heads, D], lse float32
+    [T, n_heads]); rows that see nothing are 0 and -inf."""
+    L = _lib.load()
+    T, B, N = _kv_tokens(seq, pos, table)
+    Hq, H, D = q.shape[1], cache.n_kv_heads, cache.head_dim
+    qs = _rows(q, "q", T, None, D)
+    k = ids.shape[2]
+    _i32(ids, "ids", (T, H, k))
+    if ws is None:
+        ws = torch.zeros(L.kv_attend_workspace(T, Hq, H, D, B, k), dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    elif out.shape != (T, Hq, D) or out.element_size() != 2:
+        raise ValueError(f"out must be bfloat16 {[T, Hq, D]}")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or lse.shape != (T, Hq):
+        raise ValueError(f"lse must be float32 {[T, Hq]}")
+    check(L.kv_attend(C.byref(cache._struct), ptr(q), qs, Hq, ptr(seq), ptr(pos), T, ptr(table), B, N, ptr(ids), k,
+                      D ** -0.5 if scale is None else scale, ptr(_dev(out, "out")), ptr(_dev(lse, "lse")), ptr(ws),
+                      ws.numel(), ptr(dev_err), stream_handle(stream)), "kv_attend")
+    return out, lse
 
 
 class MoeLayer:

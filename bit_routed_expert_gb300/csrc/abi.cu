@@ -199,6 +199,93 @@ bre_status engram_inject(const uint8_t* table, int64_t n_rows, const int64_t* ro
                                           gate_out, dev_err, ws, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// What every kv_* call checks: the cache's shape and buffers, and the token arrays.
+static bre_status kv_check(const bre_kv_cache* c, const int32_t* seq, const int32_t* pos, int T, const int32_t* table,
+                           int B, int N) {
+  if (!c || !c->pages || !c->bounds || !c->bound_exp || c->n_pages <= 0 || c->n_kv_heads <= 0 || T < 0 || B <= 0 ||
+      N <= 0 || !table || (T > 0 && (!seq || !pos)))
+    return BRE_ERR_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return BRE_ERR_UNSUPPORTED;
+  if ((int64_t)T * c->n_kv_heads > INT32_MAX / 2 || N > INT32_MAX / 64) return BRE_ERR_UNSUPPORTED;
+  if (!aligned(c->pages, 16) || !aligned(c->bounds, 16) || !aligned(seq, 4) || !aligned(pos, 4) || !aligned(table, 4))
+    return BRE_ERR_ARG;
+  return BRE_OK;
+}
+
+// Rows of `heads` heads, `stride` elements from one token to the next.
+static bool kv_rows_ok(const void* p, int64_t stride, int heads, int D) {
+  return p && aligned(p, 16) && stride % 8 == 0 && stride >= (int64_t)heads * D;
+}
+
+static bre_status kv_check_q(const bre_kv_cache* c, const void* q, int64_t q_stride, int n_heads, int k) {
+  if (n_heads <= 0 || k <= 0 || n_heads % c->n_kv_heads != 0) return BRE_ERR_ARG;
+  if (n_heads / c->n_kv_heads > 16 || k > 256) return BRE_ERR_UNSUPPORTED;
+  if (!kv_rows_ok(q, q_stride, n_heads, c->head_dim)) return BRE_ERR_ARG;
+  return BRE_OK;
+}
+
+bre_status kv_append(const bre_kv_cache* cache, const void* k_bf16, const void* v_bf16, int64_t k_stride,
+                     int64_t v_stride, const int32_t* seq, const int32_t* pos, int T, const int32_t* table, int B,
+                     int N, int32_t* dev_err, bre_stream_t stream) {
+  const bre_status st = kv_check(cache, seq, pos, T, table, B, N);
+  if (st != BRE_OK || T == 0) return st;
+  if (!kv_rows_ok(k_bf16, k_stride, cache->n_kv_heads, cache->head_dim) ||
+      !kv_rows_ok(v_bf16, v_stride, cache->n_kv_heads, cache->head_dim))
+    return BRE_ERR_ARG;
+  return cuda_status(launch_kv_append(cache, KvTokens{seq, pos, T, table, B, N}, static_cast<const uint16_t*>(k_bf16),
+                                      static_cast<const uint16_t*>(v_bf16), k_stride, v_stride, dev_err,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bre_status kv_read(const bre_kv_cache* cache, const int32_t* seq, const int32_t* pos, int T, const int32_t* table,
+                   int B, int N, void* k_out_bf16, void* v_out_bf16, int32_t* dev_err, bre_stream_t stream) {
+  const bre_status st = kv_check(cache, seq, pos, T, table, B, N);
+  if (st != BRE_OK || T == 0) return st;
+  if ((!k_out_bf16 && !v_out_bf16) || !aligned(k_out_bf16, 16) || !aligned(v_out_bf16, 16)) return BRE_ERR_ARG;
+  return cuda_status(launch_kv_read(cache, KvTokens{seq, pos, T, table, B, N}, static_cast<uint16_t*>(k_out_bf16),
+                                    static_cast<uint16_t*>(v_out_bf16), dev_err,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kv_select_workspace(int T, int n_heads, int n_kv_heads, int head_dim, int B, int N, int k) {
+  if (T <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || B <= 0 || N <= 0 || k <= 0) return 0;
+  return kv_select_ws_bytes(T, n_heads, n_kv_heads, head_dim, B, N, k);
+}
+
+bre_status kv_select(const bre_kv_cache* cache, const void* q_bf16, int64_t q_stride, int n_heads, const int32_t* seq,
+                     const int32_t* pos, int T, const int32_t* table, int B, int N, int k, int n_sink, int n_local,
+                     int32_t* ids, float* scores, void* ws, size_t ws_bytes, int32_t* dev_err, bre_stream_t stream) {
+  bre_status st = kv_check(cache, seq, pos, T, table, B, N);
+  if (st != BRE_OK || T == 0) return st;
+  if ((st = kv_check_q(cache, q_bf16, q_stride, n_heads, k)) != BRE_OK) return st;
+  if (!ids || n_sink < 0 || n_local < 0 || n_sink > k || n_local > k - n_sink) return BRE_ERR_ARG;
+  const size_t need = kv_select_ws_bytes(T, n_heads, cache->n_kv_heads, cache->head_dim, B, N, k);
+  if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return BRE_ERR_WORKSPACE;
+  return cuda_status(launch_kv_select(cache, KvTokens{seq, pos, T, table, B, N}, static_cast<const uint16_t*>(q_bf16),
+                                      q_stride, n_heads, k, n_sink, n_local, ids, scores, ws, dev_err,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kv_attend_workspace(int T, int n_heads, int n_kv_heads, int head_dim, int B, int k) {
+  if (T <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || B <= 0 || k <= 0) return 0;
+  return kv_attend_ws_bytes(T, n_heads, n_kv_heads, head_dim, B, k);
+}
+
+bre_status kv_attend(const bre_kv_cache* cache, const void* q_bf16, int64_t q_stride, int n_heads, const int32_t* seq,
+                     const int32_t* pos, int T, const int32_t* table, int B, int N, const int32_t* ids, int k,
+                     float scale, void* out_bf16, float* lse, void* ws, size_t ws_bytes, int32_t* dev_err,
+                     bre_stream_t stream) {
+  bre_status st = kv_check(cache, seq, pos, T, table, B, N);
+  if (st != BRE_OK || T == 0) return st;
+  if ((st = kv_check_q(cache, q_bf16, q_stride, n_heads, k)) != BRE_OK) return st;
+  if (!ids || !out_bf16 || !aligned(out_bf16, 16) || !(scale - scale == 0.0f)) return BRE_ERR_ARG;
+  const size_t need = kv_attend_ws_bytes(T, n_heads, cache->n_kv_heads, cache->head_dim, B, k);
+  if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return BRE_ERR_WORKSPACE;
+  return cuda_status(launch_kv_attend(cache, KvTokens{seq, pos, T, table, B, N}, static_cast<const uint16_t*>(q_bf16),
+                                      q_stride, n_heads, ids, k, scale, static_cast<uint16_t*>(out_bf16), lse, ws,
+                                      dev_err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 bre_status bre_set_ffn_wait_limit(int64_t cycles) {
   if (cycles < 0) return BRE_ERR_ARG;
   g_ffn_wait.store((long long)cycles, std::memory_order_relaxed);

@@ -58,6 +58,7 @@ typedef enum {
 #define BRE_DEVERR_EXPERT_ID 1 /* an expert id outside [0, E): pair excluded, its output zero */
 #define BRE_DEVERR_ROW_ID 2    /* an Engram row id outside [0, n_rows): row decoded as +0 */
 #define BRE_DEVERR_TIMEOUT 4   /* a bounded device wait gave up; outputs of that CTA are invalid */
+#define BRE_DEVERR_PAGE 8      /* a sequence, block or page outside the cache or the page table */
 
 typedef enum { BRE_FMT_Q2_K = 1, BRE_FMT_Q8_0 = 2, BRE_FMT_Q2_K_R16 = 3 } bre_fmt;
 
@@ -277,6 +278,91 @@ bre_status engram_inject(const uint8_t *table, int64_t n_rows, const int64_t *ro
                          int W, void *resid_bf16, const float *q_norm, const float *k_norm, const uint8_t *mask, int T,
                          float eps, float *kv_out, float *gate_out, int32_t *dev_err, void *ws, size_t ws_bytes,
                          bre_stream_t stream);
+
+/* Key/value cache: paged, quantised as it is written, read by attention over selected blocks.
+ *
+ * The attention half of a layer whose FFN half the calls above run ([S] "Results": compressed
+ * sparse attention with an indexer over blocks of 64; quantised cache types).  The pages print
+ * no formulas for it: the definitions below are this library's own.
+ *
+ * Tokens are a flat list of T entries, each with its sequence seq[t] in [0, B) and position
+ * pos[t]; a negative position is a padding entry: it stores nothing, selects nothing and its
+ * outputs are zeros.  table [B][N]: the page of each block of 64 consecutive positions of a
+ * sequence; a negative entry means that the block has no page (not yet, or given back).
+ * seq, pos and table are int32 device arrays.
+ *
+ *   pages [n_pages][n_kv_heads][128 D + 128] bytes, D = head_dim: for each head of a page 64 key
+ *     rows of D E4M3 codes (OCP: bias 7, no infinities), 64 value rows, 64 key scales, 64 value
+ *     scales; value = code * 2^(scale byte - 127).  16-byte aligned.
+ *   bounds [n_pages][n_kv_heads][2][D] int8, bound_exp [n_pages][n_kv_heads] int8: for each
+ *     channel of a page's stored keys, whole numbers hi and lo in [-63, 63] with
+ *     lo * 2^bound_exp <= key <= hi * 2^bound_exp, as tight as whole numbers are.
+ *     bounds 16-byte aligned.
+ * Pages need no initialisation: nothing is read of a slot before kv_append wrote it, and a
+ * page's bounds start anew when its slot 0 is written.  A cache holds up to 2^31 pages; byte
+ * offsets are 64 bits wide.  Requires D = 64 or 128.
+ * A seq, block (position / 64) or page outside its range sets BRE_DEVERR_PAGE in dev_err (may
+ * be NULL); the token or block then counts as one without a page.  T = 0 does nothing. */
+typedef struct {
+  void *pages;
+  int8_t *bounds;
+  int8_t *bound_exp;
+  int32_t n_pages;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+} bre_kv_cache;
+
+/* Store the keys and values of T tokens.  For a row x of D BF16 values: e = the least integer
+ * >= -64 with max|x| <= 448 * 2^e, codes e4m3_rne(x * 2^-e), scale byte e + 127.  NaN is stored as
+ * NaN and left out of the maximum; magnitudes above 448 * 2^119 (infinities too) saturate.
+ * The bounds of every block written to are brought up to date (a NaN key counts as 0 there):
+ * from this call's keys alone where its first token of the block is at slot 0, else together
+ * with the bounds that were there.  A position written again widens them only: they stay bounds.
+ *   k, v: row t starts t * stride elements after the base and holds [n_kv_heads][D]; bases 16-byte
+ *   aligned, strides multiples of 8.
+ * The call's tokens of one block follow one another in the list, and no page is written for two
+ * sequences.  A token to be stored whose block has no page sets BRE_DEVERR_PAGE. */
+bre_status kv_append(const bre_kv_cache *cache, const void *k_bf16, const void *v_bf16, int64_t k_stride,
+                     int64_t v_stride, const int32_t *seq, const int32_t *pos, int T, const int32_t *table, int B,
+                     int N, int32_t *dev_err, bre_stream_t stream);
+
+/* Read tokens back: k_out, v_out [T][n_kv_heads][D] BF16 (either may be NULL), exactly the stored
+ * values; zeros for padding and for tokens without a page (which set BRE_DEVERR_PAGE). */
+bre_status kv_read(const bre_kv_cache *cache, const int32_t *seq, const int32_t *pos, int T, const int32_t *table,
+                   int B, int N, void *k_out_bf16, void *v_out_bf16, int32_t *dev_err, bre_stream_t stream);
+
+/* Select blocks: for token t and kv head h with its G = n_heads / n_kv_heads query heads,
+ *   e = the least integer >= -64 with max|q| <= 127 * 2^e over the G * D values;
+ *   c = rint(q * 2^-e) (NaN: 0);  P = sum_g max(c, 0), M = sum_g max(-c, 0) per channel;
+ *   score(b) = (P . hi_b - M . lo_b) * 2^bound_exp_b * 2^e for every block b <= pos / 64 that has
+ *     a page: an upper bound of sum_g q_g . key over the block's keys, up to the rounding of q.
+ * The sums are whole numbers below 2^24, so the score is the same in any order of summation; blocks
+ * are compared before the common factor 2^e, whose product may overflow to an infinity in scores.
+ * Taken: the first n_sink blocks and the last n_local ones (the token's own block counts), then
+ * the others by score, highest first, lowest block first among equals, k in all.
+ *   ids [T][n_kv_heads][k] int32: the blocks taken, ascending, then -1;
+ *   scores [T][n_kv_heads][k] FP32 or NULL: their scores, then 0.
+ *   q: as k in kv_append, [n_heads][D] a row.  ws: kv_select_workspace(...) bytes, zero-filled
+ *   once after allocation (each call leaves it ready for the next).
+ * Requires G <= 16, 1 <= k <= 256, n_sink + n_local <= k. */
+size_t kv_select_workspace(int T, int n_heads, int n_kv_heads, int head_dim, int B, int N, int k);
+bre_status kv_select(const bre_kv_cache *cache, const void *q_bf16, int64_t q_stride, int n_heads, const int32_t *seq,
+                     const int32_t *pos, int T, const int32_t *table, int B, int N, int k, int n_sink, int n_local,
+                     int32_t *ids, float *scores, void *ws, size_t ws_bytes, int32_t *dev_err, bre_stream_t stream);
+
+/* Attention over listed blocks: for each query head of token t, over the tokens x <= pos[t] of
+ * the blocks that ids lists for its kv head (-1: none; a block listed twice counts twice),
+ *   s_x = scale * q . key_x,  out = sum_x exp(s_x) value_x / sum_x exp(s_x),  lse = log sum_x exp(s_x)
+ * A row that sees no token gives zeros and lse = -inf.  Logits, maxima and sums are FP32; the
+ * probabilities enter the second product as FP16 (relative error 2^-11), the codes exactly.
+ *   ids [T][n_kv_heads][k] int32, any order; out [T][n_heads][D] BF16; lse [T][n_heads] FP32 or
+ *   NULL (natural logarithm).  ws: kv_attend_workspace(...) bytes, zero-filled once after
+ *   allocation (each call leaves it ready for the next).  Requires G <= 16, k <= 256. */
+size_t kv_attend_workspace(int T, int n_heads, int n_kv_heads, int head_dim, int B, int k);
+bre_status kv_attend(const bre_kv_cache *cache, const void *q_bf16, int64_t q_stride, int n_heads, const int32_t *seq,
+                     const int32_t *pos, int T, const int32_t *table, int B, int N, const int32_t *ids, int k,
+                     float scale, void *out_bf16, float *lse, void *ws, size_t ws_bytes, int32_t *dev_err,
+                     bre_stream_t stream);
 
 /* Budget, in SM clock cycles, of the bounded waits inside the expert FFN kernels
  * (moe_expert_ffn, both paths) for calls made after this one, from any thread of the process;
