@@ -255,14 +255,16 @@ class KvCache:
     bound_exp: torch.Tensor
 
     def __post_init__(self):
-        n, H, _, D = self.bounds.shape
-        if self.pages.shape != (n, H, 2 * KV_BLOCK * (D + 1)) or self.bound_exp.shape != (n, H):
+        p, b, e = self.pages, self.bounds, self.bound_exp
+        n, H, _, D = b.shape
+        if p.shape != (n, H, 2 * KV_BLOCK * (D + 1)) or e.shape != (n, H):
             raise ValueError("pages, bounds and bound_exp do not belong together")
-        if self.pages.dtype != torch.uint8 or self.bounds.dtype != torch.int8 or self.bound_exp.dtype != torch.int8:
+        if p.dtype is not torch.uint8 or b.dtype is not torch.int8 or e.dtype is not torch.int8:
             raise ValueError("pages must be uint8, bounds and bound_exp int8")
-        _dev(self.pages, "pages"), _dev(self.bounds, "bounds"), _dev(self.bound_exp, "bound_exp")
+        _dev(p, "pages"), _dev(b, "bounds"), _dev(e, "bound_exp")
         self.n_pages, self.n_kv_heads, self.head_dim = n, H, D
-        self._struct = BreKvCache(self.pages.data_ptr(), self.bounds.data_ptr(), self.bound_exp.data_ptr(), n, H, D)
+        self._struct = BreKvCache(p.data_ptr(), b.data_ptr(), e.data_ptr(), n, H, D)
+        self._ref = C.byref(self._struct)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, device) -> "KvCache":
@@ -272,59 +274,71 @@ class KvCache:
                    torch.empty((n_pages, n_kv_heads), dtype=torch.int8, device=device))
 
 
+# The kv_* calls are made once or more a layer for every decoded token, so their marshalling is kept
+# to a few microseconds: plain integers for pointers, one condition for what is usually right (and
+# the reason looked for only where it is not), the raw current stream.
 def _rows(t: torch.Tensor, name: str, T: int, heads: int | None, D: int) -> int:
     """Row stride (elements) of [T, heads, D] BF16 rows, which may be a slice of wider rows."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.element_size() != 2 or t.dtype == torch.float16:
-        raise ValueError(f"{name} must be bfloat16 (or its 16-bit patterns)")
     n, h, d = t.shape
     if n != T or d != D or (heads is not None and h != heads):
         raise ValueError(f"{name} must be [{T}, {'heads' if heads is None else heads}, {D}], got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (h > 1 and t.stride(1) != D):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and h > 1):
         raise ValueError(f"{name}: a token's heads must follow one another without gaps")
-    return t.stride(0) if T > 1 else (h * D + 7) // 8 * 8
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not torch.bfloat16 and (t.element_size() != 2 or t.dtype is torch.float16):
+        raise ValueError(f"{name} must be bfloat16 (or its 16-bit patterns)")
+    return s0 if T > 1 else (h * D + 7) // 8 * 8
 
 
-def _i32(t: torch.Tensor, name: str, shape) -> torch.Tensor:
-    if t.dtype != torch.int32 or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
-    return _dev(t, name)
+def _like(t: torch.Tensor, name: str, dtype, shape) -> torch.Tensor:
+    if t.shape != shape or t.dtype is not dtype or not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    return t
 
 
 def _kv_tokens(seq, pos, table):
-    T = seq.shape[0]
-    _i32(seq, "seq", (T,)), _i32(pos, "pos", (T,))
+    T, = seq.shape
     B, N = table.shape
-    _i32(table, "table", (B, N))
+    i32 = torch.int32
+    _like(seq, "seq", i32, (T,)), _like(pos, "pos", i32, (T,)), _like(table, "table", i32, (B, N))
     return T, B, N
+
+
+def _stream(stream, t: torch.Tensor) -> int:
+    """Raw handle of `stream`, or of the current stream of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def kv_append(cache: KvCache, k, v, seq, pos, table, dev_err=None, stream=None):
     """Quantise and store the keys and values ([T, n_kv_heads, D] BF16, possibly slices of a fused
     projection's rows) of tokens seq[t], pos[t] (int32 [T]) and refresh the bounds of their blocks;
     table int32 [B, N] holds the page of each block of 64 positions of each sequence."""
-    L = _lib.load()
     T, B, N = _kv_tokens(seq, pos, table)
-    ks = _rows(k, "k", T, cache.n_kv_heads, cache.head_dim)
-    vs = _rows(v, "v", T, cache.n_kv_heads, cache.head_dim)
-    check(L.kv_append(C.byref(cache._struct), ptr(k), ptr(v), ks, vs, ptr(seq), ptr(pos), T, ptr(table), B, N,
-                      ptr(dev_err), stream_handle(stream)), "kv_append")
+    H, D = cache.n_kv_heads, cache.head_dim
+    ks, vs = _rows(k, "k", T, H, D), _rows(v, "v", T, H, D)
+    rc = _lib.load().kv_append(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, seq.data_ptr(), pos.data_ptr(), T,
+                               table.data_ptr(), B, N, _addr(dev_err), _stream(stream, seq))
+    if rc:
+        check(rc, "kv_append")
 
 
 def kv_read(cache: KvCache, seq, pos, table, k_out=None, v_out=None, dev_err=None, stream=None):
     """The stored keys and values of tokens seq[t], pos[t]: two BF16 tensors [T, n_kv_heads, D]."""
-    L = _lib.load()
     T, B, N = _kv_tokens(seq, pos, table)
-    shape = (T, cache.n_kv_heads, cache.head_dim)
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=seq.device)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=seq.device)
-    if k_out.shape != shape or v_out.shape != shape or k_out.element_size() != 2 or v_out.element_size() != 2:
-        raise ValueError(f"k_out and v_out must be bfloat16 {list(shape)}")
-    check(L.kv_read(C.byref(cache._struct), ptr(seq), ptr(pos), T, ptr(table), B, N, ptr(_dev(k_out, "k_out")),
-                    ptr(_dev(v_out, "v_out")), ptr(dev_err), stream_handle(stream)), "kv_read")
+    shape, bf16 = (T, cache.n_kv_heads, cache.head_dim), torch.bfloat16
+    k_out = seq.new_empty(shape, dtype=bf16) if k_out is None else _like(k_out, "k_out", bf16, shape)
+    v_out = seq.new_empty(shape, dtype=bf16) if v_out is None else _like(v_out, "v_out", bf16, shape)
+    rc = _lib.load().kv_read(cache._ref, seq.data_ptr(), pos.data_ptr(), T, table.data_ptr(), B, N, k_out.data_ptr(),
+                             v_out.data_ptr(), _addr(dev_err), _stream(stream, seq))
+    if rc:
+        check(rc, "kv_read")
     return k_out, v_out
 
 
@@ -342,16 +356,16 @@ def kv_select(q, cache: KvCache, seq, pos, table, k: int, n_sink: int = 1, n_loc
     Hq, H, D = q.shape[1], cache.n_kv_heads, cache.head_dim
     qs = _rows(q, "q", T, None, D)
     if ws is None:
-        ws = torch.zeros(L.kv_select_workspace(T, Hq, H, D, B, N, k), dtype=torch.uint8, device=q.device)
-    ids = (torch.empty((T, H, k), dtype=torch.int32, device=q.device) if ids is None
-           else _i32(ids, "ids", (T, H, k)))
-    if scores is None:
-        scores = torch.empty((T, H, k), dtype=torch.float32, device=q.device)
-    elif scores.dtype != torch.float32 or scores.shape != (T, H, k):
-        raise ValueError(f"scores must be float32 {[T, H, k]}")
-    check(L.kv_select(C.byref(cache._struct), ptr(q), qs, Hq, ptr(seq), ptr(pos), T, ptr(table), B, N, k, n_sink,
-                      n_local, ptr(ids), ptr(_dev(scores, "scores")), ptr(ws), ws.numel(), ptr(dev_err),
-                      stream_handle(stream)), "kv_select")
+        ws = seq.new_zeros(L.kv_select_workspace(T, Hq, H, D, B, N, k), dtype=torch.uint8)
+    shape = (T, H, k)
+    ids = seq.new_empty(shape) if ids is None else _like(ids, "ids", torch.int32, shape)
+    scores = (seq.new_empty(shape, dtype=torch.float32) if scores is None
+              else _like(scores, "scores", torch.float32, shape))
+    rc = L.kv_select(cache._ref, q.data_ptr(), qs, Hq, seq.data_ptr(), pos.data_ptr(), T, table.data_ptr(), B, N, k,
+                     n_sink, n_local, ids.data_ptr(), scores.data_ptr(), ws.data_ptr(), ws.numel(), _addr(dev_err),
+                     _stream(stream, seq))
+    if rc:
+        check(rc, "kv_select")
     return ids, scores
 
 
@@ -369,20 +383,18 @@ def kv_attend(q, cache: KvCache, seq, pos, table, ids, scale: float | None = Non
     Hq, H, D = q.shape[1], cache.n_kv_heads, cache.head_dim
     qs = _rows(q, "q", T, None, D)
     k = ids.shape[2]
-    _i32(ids, "ids", (T, H, k))
+    _like(ids, "ids", torch.int32, (T, H, k))
     if ws is None:
-        ws = torch.zeros(L.kv_attend_workspace(T, Hq, H, D, B, k), dtype=torch.uint8, device=q.device)
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    elif out.shape != (T, Hq, D) or out.element_size() != 2:
-        raise ValueError(f"out must be bfloat16 {[T, Hq, D]}")
-    if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or lse.shape != (T, Hq):
-        raise ValueError(f"lse must be float32 {[T, Hq]}")
-    check(L.kv_attend(C.byref(cache._struct), ptr(q), qs, Hq, ptr(seq), ptr(pos), T, ptr(table), B, N, ptr(ids), k,
-                      D ** -0.5 if scale is None else scale, ptr(_dev(out, "out")), ptr(_dev(lse, "lse")), ptr(ws),
-                      ws.numel(), ptr(dev_err), stream_handle(stream)), "kv_attend")
+        ws = seq.new_zeros(L.kv_attend_workspace(T, Hq, H, D, B, k), dtype=torch.uint8)
+    out = (seq.new_empty((T, Hq, D), dtype=torch.bfloat16) if out is None
+           else _like(out, "out", torch.bfloat16, (T, Hq, D)))
+    lse = (seq.new_empty((T, Hq), dtype=torch.float32) if lse is None
+           else _like(lse, "lse", torch.float32, (T, Hq)))
+    rc = L.kv_attend(cache._ref, q.data_ptr(), qs, Hq, seq.data_ptr(), pos.data_ptr(), T, table.data_ptr(), B, N,
+                     ids.data_ptr(), k, D ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(),
+                     ws.data_ptr(), ws.numel(), _addr(dev_err), _stream(stream, seq))
+    if rc:
+        check(rc, "kv_attend")
     return out, lse
 
 
