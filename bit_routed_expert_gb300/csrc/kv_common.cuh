@@ -77,6 +77,13 @@ __device__ __forceinline__ float ld_cluster_f32(const float* local, uint32_t ran
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra) : "memory");
   return v;
 }
+__device__ __forceinline__ int ld_cluster_s32(const int* local, uint32_t rank) {
+  uint32_t ra;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(ra) : "memory");
+  return v;
+}
 
 // Page of block b of sequence s; -1 where there is none (a negative table entry), with the
 // error bit where the sequence, the block or the page lies outside what the call was given.
