@@ -29,9 +29,11 @@ __device__ __forceinline__ uint32_t select_key(float sc, bool must) {
 // among equals) are passed to put(place, get(index)) in ascending order; returns how many there
 // are.  place <= index, and 32 entries at a time are got by all lanes before any is put: put may
 // write where get reads.
-// Entries live in registers, entry i in lane i % 32; the threshold comes by bisection of the key
-// range between the smallest and the largest key, which ends as soon as a value splits off
-// exactly `want` entries (about log2(n) + 3 steps), not after 32.
+// Entries live in registers, entry i in lane i % 32.  The threshold comes by bisection of the keys,
+// which ends as soon as a value splits off exactly `want` entries.  It starts between the largest
+// key and a lower bound that costs one register a lane: the `want`-th largest of the 32 lanes' own
+// largest keys (as many lanes, so as many entries, reach it); of 512 random keys about 24 lie
+// above the bound for want = 16, so three or four steps over all registers are left of twelve.
 struct Entry {
   float sc;
   int id;
@@ -39,7 +41,7 @@ struct Entry {
 template <int R, typename Key, typename Get, typename Put>
 __device__ __forceinline__ int warp_select(int n, int want, Key key_of, Get get, Put put) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[R], lo = 0xFFFFFFFFu, hi = 0;
+  uint32_t key[R], lo = 0xFFFFFFFFu, top = 0;   // of the entries that neither must nor cannot be taken
   int valid = 0, must = 0;
 #pragma unroll
   for (int j = 0; j < R; ++j) {
@@ -47,27 +49,39 @@ __device__ __forceinline__ int warp_select(int n, int want, Key key_of, Get get,
     key[j] = i < n ? key_of(i) : 0u;
     valid += key[j] != 0u;
     must += key[j] == 0xFFFFFFFFu;
-    if (key[j] != 0u && key[j] != 0xFFFFFFFFu) {
-      lo = min(lo, key[j]);
-      hi = max(hi, key[j]);
-    }
+    if (key[j] != 0xFFFFFFFFu) top = max(top, key[j]);
+    lo = min(lo, key[j] - 1u);   // a key of 0 becomes the largest
   }
   valid = __reduce_add_sync(0xffffffffu, valid);
   must = __reduce_add_sync(0xffffffffu, must);
   uint32_t thr = 1;        // entries with key >= thr are taken, of those equal to thr only the first `ties`
   int ties = 0x7fffffff;
   if (valid > want) {
-    lo = __reduce_min_sync(0xffffffffu, lo);        // count(>= lo) > want >= count(>= hi)
-    hi = __reduce_max_sync(0xffffffffu, hi) + 1;
-    int above = must;                               // count(>= hi)
+    // count(>= lo) >= want > count(>= hi) = above, or above == want
+    lo = __reduce_min_sync(0xffffffffu, lo) + 1u;
+    uint32_t hi = __reduce_max_sync(0xffffffffu, top) + 1u;
+    int above = must;
+    if (want - must <= 32 && want > must) {
+      uint32_t h = hi;
+      while (h - lo > 1) {
+        const uint32_t mid = lo + (h - lo) / 2;
+        const int c = __popc(__ballot_sync(0xffffffffu, top >= mid));
+        if (c >= want - must) {
+          lo = mid;
+          if (c == want - must) break;
+        } else {
+          h = mid;
+        }
+      }
+    }
     thr = hi;
-    while (above < want) {
+    for (bool first = true; above < want; first = false) {
       if (hi - lo == 1) {
         thr = lo;
         ties = want - above;
         break;
       }
-      const uint32_t mid = lo + (hi - lo) / 2;
+      const uint32_t mid = first ? lo : lo + (hi - lo) / 2;   // the bound may be the value itself
       int c = 0;
 #pragma unroll
       for (int j = 0; j < R; ++j) c += key[j] >= mid;
@@ -96,6 +110,66 @@ __device__ __forceinline__ int warp_select(int n, int want, Key key_of, Get get,
     }
   }
   return at;
+}
+
+// ---------------------------------------------------------------------------
+// the query's vector
+// ---------------------------------------------------------------------------
+// A lane's 2 W channels (W words, word j of head g at qr[g * stride + j]) of one token and kv head:
+// P into pl and M into mi; returns the exponent of the codes.  All 32 lanes together hold the G
+// heads' D channels.  rint(x 2^-e) is read off the low bits of fma(x, 2^-e, 1.5 * 2^23).  With S the
+// sum of the codes, M = P - S.
+template <int W>
+__device__ __forceinline__ int query_vector(const uint32_t* qr, int stride, int G, int (&pl)[2 * W], int (&mi)[2 * W]) {
+  constexpr float MAGIC = 12582912.0f;
+  constexpr int MAGIC_BITS = 0x4B400000;
+  uint32_t mx = 0;   // magnitudes of BF16 values compare like whole numbers
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int j = 0; j < W; ++j) mx = __vmaxu2(mx, __ldg(qr + g * stride + j) & 0x7FFF7FFFu);
+  mx = max(mx & 0xFFFFu, mx >> 16);
+  mx = __reduce_max_sync(0xffffffffu, mx);
+#pragma unroll
+  for (int i = 0; i < 2 * W; ++i) pl[i] = mi[i] = 0;
+  if (mx <= 0x7F60u) {   // KV_MAX
+    const int e = query_exp(bf16_bits_to_f32(mx));
+    const float down = pow2f(-e);
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const uint32_t w = __ldg(qr + g * stride + j);
+        const float x[2] = {__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int b = __float_as_int(fmaf(x[i], down, MAGIC)) - MAGIC_BITS;
+          pl[2 * j + i] += max(b, 0);
+          mi[2 * j + i] -= b;
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < 2 * W; ++i) mi[i] += pl[i];
+    return e;
+  }
+  // infinities count as the largest value, NaN as 0
+  float amax = 0.0f;
+  for (int pass = 0; pass < 2; ++pass) {
+    const float down = pow2f(-query_exp(amax));
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int j = 0; j < 2 * W; ++j) {
+        const uint32_t w = __ldg(qr + g * stride + j / 2);
+        const float x = kv_clamp(bf16_bits_to_f32(j & 1 ? w >> 16 : w & 0xFFFFu));
+        if (pass == 0) {
+          amax = fmaxf(amax, fabsf(x));
+        } else {
+          const int c = x == x ? __float2int_rn(x * down) : 0;
+          pl[j] += max(c, 0);
+          mi[j] += max(-c, 0);
+        }
+      }
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+  }
+  return query_exp(amax);
 }
 
 // ---------------------------------------------------------------------------
@@ -173,14 +247,15 @@ __device__ __forceinline__ int dot16(const int (&u)[8], const uint4& b) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(SR_WARPS * 32) kv_select_rows_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(SR_WARPS * 32, 2) kv_select_rows_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) unsigned char sm_raw[];
   __shared__ __align__(16) short u[2 * D];
-  __shared__ float red[SR_WARPS], best_sc[SEL_KMAX];
-  __shared__ int best_id[SEL_KMAX], warp_n[SR_WARPS], n_best;
+  __shared__ float best_sc[SEL_KMAX];
+  __shared__ int best_id[SEL_KMAX], n_best, eq_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
   const int row = blockIdx.x / ranks, t = row / a.H, h = row - t * a.H;
+  if (ranks > 1) cluster_arrive();
   pdl_wait();
   pdl_launch_dependents();
   const int p = __ldg(a.pos + t), s = __ldg(a.seq + t);
@@ -188,55 +263,40 @@ __global__ void __launch_bounds__(SR_WARPS * 32) kv_select_rows_kernel(const Sel
   if (p >= 0 && (!ok || p / KV_BLOCK >= a.tab.N) && tid == 0) set_err(a.err, BRE_DEVERR_PAGE);
   const int nb = ok ? min(p / KV_BLOCK + 1, a.tab.N) : 0;
   const int span = (nb + ranks - 1) / ranks, b0 = min(rank * span, nb), n = min(span, nb - b0);
-  // shared: pages, then scores, of this CTA's blocks; then the warps' lists
-  int* page = reinterpret_cast<int*>(sm_raw);
-  float* sc = reinterpret_cast<float*>(page + span);
-  float* list_sc = sc + span;
+  // shared: the lists (at the same place in every CTA), then pages and scores of this CTA's blocks
+  float* list_sc = reinterpret_cast<float*>(sm_raw);
   int* list_id = reinterpret_cast<int*>(list_sc + SR_WARPS * a.k);
-  for (int i = tid; i < n; i += SR_WARPS * 32) page[i] = kv_page(a.tab, s, b0 + i, a.err);
+  float* all_sc = reinterpret_cast<float*>(list_id + SR_WARPS * a.k);   // every CTA's list, in the first CTA
+  int* all_id = reinterpret_cast<int*>(all_sc + 8 * a.k);
+  int* page = all_id + 8 * a.k;
+  float* sc = reinterpret_cast<float*>(page + span);
+  if (warp < SR_WARPS - 1)
+    for (int i = tid; i < n; i += (SR_WARPS - 1) * 32) page[i] = kv_page(a.tab, s, b0 + i, a.err);
 
-  // the query's vector: a thread takes two channels of every head
-  const uint32_t* qr = reinterpret_cast<const uint32_t*>(a.q + t * a.q_stride + (size_t)h * a.G * D);
-  float amax = 0.0f;
-  for (int i = tid; i < a.G * D / 2; i += SR_WARPS * 32) {
-    const uint32_t w = __ldg(qr + i);
-    amax = fmaxf(amax, fmaxf(fabsf(kv_clamp(bf16_bits_to_f32(w & 0xFFFFu))), fabsf(kv_clamp(bf16_bits_to_f32(w >> 16)))));
-  }
+  // the query's vector, by the last warp (the others look up pages)
+  if (warp == SR_WARPS - 1) {
+    constexpr int W = D / 64;
+    int pl[2 * W], mi[2 * W];
+    const uint32_t* qr = reinterpret_cast<const uint32_t*>(a.q + t * a.q_stride + (size_t)h * a.G * D) + lane * W;
+    const int e = query_vector<W>(qr, D / 2, a.G, pl, mi);
+    if (lane == 0) eq_s = e;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (lane == 0) red[warp] = amax;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < SR_WARPS; ++w) amax = fmaxf(amax, red[w]);
-  const int eq = query_exp(amax);
-  if (tid < D / 2) {
-    int pl[2] = {0, 0}, mi[2] = {0, 0};
-    for (int g = 0; g < a.G; ++g) {
-      const uint32_t w = __ldg(qr + g * (D / 2) + tid);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float x = kv_clamp(bf16_bits_to_f32(j ? w >> 16 : w & 0xFFFFu));
-        const int c = x == x ? __float2int_rn(x * pow2f(-eq)) : 0;
-        pl[j] += max(c, 0);
-        mi[j] += max(-c, 0);
-      }
-    }
-    *reinterpret_cast<short2*>(&u[2 * tid]) = make_short2((short)pl[0], (short)pl[1]);
-    *reinterpret_cast<short2*>(&u[D + 2 * tid]) = make_short2((short)-mi[0], (short)-mi[1]);
+    for (int i = 0; i < 2 * W; ++i) u[2 * W * lane + i] = (short)pl[i], u[D + 2 * W * lane + i] = (short)-mi[i];
   }
   __syncthreads();
+  const int eq = eq_s;
 
-  // scores: 2 D / 16 lanes a block, four loads in flight
+  // scores: 2 D / 16 lanes a block, eight loads in flight
   constexpr int LB = 2 * D / 16, PW = 32 / LB;   // lanes a block, blocks a load
   int uu[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) uu[j] = reinterpret_cast<const int*>(u)[(lane % LB) * 8 + j];
   const int seg = (n + SR_WARPS - 1) / SR_WARPS, w0 = min(warp * seg, n), wn = min(seg, n - w0);
-  for (int i0 = 0; i0 < wn; i0 += 4 * PW) {
-    uint4 bd[4];
-    int e[4];
+  for (int i0 = 0; i0 < wn; i0 += 8 * PW) {
+    uint4 bd[8];
+    int e[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const int i = i0 + j * PW + lane / LB;
       const int pg = i < wn ? page[w0 + i] : -1;
       const size_t ph = (size_t)max(pg, 0) * a.H + h;
@@ -244,7 +304,7 @@ __global__ void __launch_bounds__(SR_WARPS * 32) kv_select_rows_kernel(const Sel
       e[j] = pg >= 0 ? (int)__ldg(a.bexp + ph) : -128;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       int d = dot16(uu, bd[j]);
 #pragma unroll
       for (int o = 1; o < LB; o *= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
@@ -252,53 +312,40 @@ __global__ void __launch_bounds__(SR_WARPS * 32) kv_select_rows_kernel(const Sel
       if (i < wn && lane % LB == 0) sc[w0 + i] = e[j] == -128 ? -INFINITY : (float)d * pow2f(e[j]);
     }
   }
-  __syncwarp();
-  const int first_local = p / KV_BLOCK - a.n_local + 1;
-  {
-    const int got = select_list(sc + w0, wn, a.k, a.n_sink, first_local, [&](int i) { return b0 + w0 + i; },
-                                list_sc + warp * a.k, list_id + warp * a.k);
-    if (lane == 0) warp_n[warp] = got;
-  }
   __syncthreads();
+  const int first_local = p / KV_BLOCK - a.n_local + 1;
+  // the lists' unused places are entries that cannot be taken
+  auto pad = [&](int got, float* lsc) {
+    for (int i = got + lane; i < a.k; i += 32) lsc[i] = -INFINITY;
+  };
+  if (n > SEL_CHUNK) {
+    float* lsc = list_sc + warp * a.k;
+    pad(select_list(sc + w0, wn, a.k, a.n_sink, first_local, [&](int i) { return b0 + w0 + i; }, lsc,
+                    list_id + warp * a.k), lsc);
+    __syncthreads();
+  }
   if (warp == 0) {
-    // the warps' lists one after the other (packed to the front: they are in ascending order already)
-    int total = 0;
-    for (int w = 0; w < SR_WARPS; ++w) {
-      const int m = warp_n[w];
-      for (int i0 = 0; i0 < m; i0 += 32) {
-        const int i = i0 + lane;
-        const float f = i < m ? list_sc[w * a.k + i] : 0.0f;
-        const int d = i < m ? list_id[w * a.k + i] : 0;
-        __syncwarp();
-        if (i < m) list_sc[total + i] = f, list_id[total + i] = d;
-        __syncwarp();
-      }
-      total += m;
-    }
-    const int got = select_list(list_sc, total, a.k, a.n_sink, first_local, [&](int i) { return list_id[i]; }, best_sc,
-                                best_id);
+    const int got = n > SEL_CHUNK
+                        ? select_list(list_sc, SR_WARPS * a.k, a.k, a.n_sink, first_local,
+                                      [&](int i) { return list_id[i]; }, best_sc, best_id)
+                        : select_list(sc, n, a.k, a.n_sink, first_local, [&](int i) { return b0 + i; }, best_sc, best_id);
     if (lane == 0) n_best = got;
   }
   if (ranks > 1) {
+    cluster_wait();   // the first CTA runs: its shared memory may be written
     __syncthreads();
-    cluster_sync_all();
-    if (rank == 0 && warp == 0) {
-      int total = n_best;
-      for (int i = lane; i < total; i += 32) list_sc[i] = best_sc[i], list_id[i] = best_id[i];
-      for (int r = 1; r < ranks; ++r) {
-        const int m = ld_cluster_s32(&n_best, r);
-        for (int i = lane; i < m; i += 32) {
-          list_sc[total + i] = ld_cluster_f32(&best_sc[i], r);
-          list_id[total + i] = ld_cluster_s32(&best_id[i], r);
-        }
-        total += m;
-      }
-      __syncwarp();
-      const int got = select_list(list_sc, total, a.k, a.n_sink, first_local, [&](int i) { return list_id[i]; },
+    for (int i = tid; i < a.k; i += SR_WARPS * 32) {
+      st_cluster_f32(&all_sc[rank * a.k + i], 0, i < n_best ? best_sc[i] : -INFINITY);
+      st_cluster_s32(&all_id[rank * a.k + i], 0, i < n_best ? best_id[i] : 0);
+    }
+    cluster_arrive();
+    if (rank != 0) return;
+    cluster_wait();
+    if (warp == 0) {
+      const int got = select_list(all_sc, ranks * a.k, a.k, a.n_sink, first_local, [&](int i) { return all_id[i]; },
                                   best_sc, best_id);
       if (lane == 0) n_best = got;
     }
-    cluster_sync_all();   // no CTA leaves while another reads its list
   }
   __syncthreads();
   if (rank == 0)
@@ -355,27 +402,8 @@ __global__ void __launch_bounds__(ST_WARPS * 32, 2) kv_select_tiles_kernel(const
   for (int r = warp; r < ST_ROWS; r += ST_WARPS) {
     const uint32_t* qr = reinterpret_cast<const uint32_t*>(a.q + (long long)(t0 + min(r, rows - 1)) * a.q_stride +
                                                            (size_t)h * a.G * D) + lane * (PL / 2);
-    float amax = 0.0f;
-    for (int i = 0; i < a.G; ++i)
-#pragma unroll
-      for (int j = 0; j < PL / 2; ++j) {
-        const uint32_t w = __ldg(qr + i * (D / 2) + j);
-        amax = fmaxf(amax, fmaxf(fabsf(kv_clamp(bf16_bits_to_f32(w & 0xFFFFu))), fabsf(kv_clamp(bf16_bits_to_f32(w >> 16)))));
-      }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const int eq = query_exp(amax);
-    const float down = pow2f(-eq);
-    int pl[PL] = {}, mi[PL] = {};
-    for (int i = 0; i < a.G; ++i)
-#pragma unroll
-      for (int j = 0; j < PL; ++j) {
-        const uint32_t w = __ldg(qr + i * (D / 2) + j / 2);
-        const float x = kv_clamp(bf16_bits_to_f32(j & 1 ? w >> 16 : w & 0xFFFFu));
-        const int c = x == x ? __float2int_rn(x * down) : 0;
-        pl[j] += max(c, 0);
-        mi[j] += max(-c, 0);
-      }
+    int pl[PL], mi[PL];
+    const int eq = query_vector<PL / 2>(qr, D / 2, a.G, pl, mi);
     if (lane == 0) row_eq[r] = eq;
 #pragma unroll
     for (int j = 0; j < PL; j += 2)
@@ -487,7 +515,7 @@ __global__ void __launch_bounds__(ST_WARPS * 32, 2) kv_select_tiles_kernel(const
 size_t kv_select_ws_bytes(int T, int Hq, int H, int D, int B, int N, int k) { return 0; }
 
 // Shared memory of the one-token kernel for stretches of `span` blocks.
-static size_t select_rows_smem(int span, int k) { return (size_t)span * 8 + (size_t)SR_WARPS * k * 8; }
+static size_t select_rows_smem(int span, int k) { return (size_t)span * 8 + (size_t)(SR_WARPS + 8) * k * 8; }
 
 cudaError_t launch_kv_select(const bre_kv_cache* c, const KvTokens& tk, const uint16_t* q, long long q_stride, int Hq,
                              int k, int n_sink, int n_local, int32_t* ids, float* scores, void* ws, int32_t* err,
