@@ -17,99 +17,152 @@ namespace {
 // ---------------------------------------------------------------------------
 // the best of a list, by one warp
 // ---------------------------------------------------------------------------
-// Order-preserving key of a score; 0 for a block that cannot be taken (score -inf), all ones for
-// one that must be.
-__device__ __forceinline__ uint32_t select_key(float sc, bool must) {
+// Scores are compared as keys: whole numbers in the scores' order, 0 for what cannot be taken.
+__device__ __forceinline__ uint32_t key_of_score(float sc) {
   const uint32_t u = __float_as_uint(sc);
-  const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-  return sc == -INFINITY ? 0u : must ? 0xFFFFFFFFu : key;
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float score_of_key(uint32_t key) {
+  return __uint_as_float(key ^ (~(uint32_t)((int32_t)key >> 31) | 0x80000000u));
 }
 
-// Of n <= 32 R entries in ascending order of block, the `want` with the largest keys (the first ones
-// among equals) are passed to put(place, get(index)) in ascending order; returns how many there
-// are.  place <= index, and 32 entries at a time are got by all lanes before any is put: put may
-// write where get reads.
-// Entries live in registers, entry i in lane i % 32.  The threshold comes by bisection of the keys,
-// which ends as soon as a value splits off exactly `want` entries.  It starts between the largest
-// key and a lower bound that costs one register a lane: the `want`-th largest of the 32 lanes' own
-// largest keys (as many lanes, so as many entries, reach it); of 512 random keys about 24 lie
-// above the bound for want = 16, so three or four steps over all registers are left of twelve.
-struct Entry {
-  float sc;
-  int id;
-};
-template <int R, typename Key, typename Get, typename Put>
-__device__ __forceinline__ int warp_select(int n, int want, Key key_of, Get get, Put put) {
+// Keys lie in shared memory with four unused words after every 16: a lane reads 4, 8 or 16 of them
+// in a row by 16-byte loads that meet no bank twice.
+__host__ __device__ constexpr int key_at(int i) { return i + 4 * (i >> 4); }
+constexpr int SEL_CHUNK = 512;   // entries of one selection
+
+// Of the entries first .. n - 1 (n <= 32 R; lane l holds entries R l ..) the `want` with the largest
+// keys, the first ones among equals: put(place, index, key) in ascending order; how many there are.
+//
+// The threshold comes by bisection of the keys, which ends as soon as a value splits off exactly
+// `want` entries.  It starts between the largest key and a lower bound that costs one register a
+// lane: the `want`-th largest of the 32 lanes' own largest keys (as many lanes, so as many entries,
+// reach it).  Of 512 random keys about 24 lie above that bound for want = 16, so three or four
+// steps over all registers are left of about twelve.
+template <int R, typename Put>
+__device__ __forceinline__ int warp_top(const uint32_t* keys, int first, int n, int want, Put put) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[R], lo = 0xFFFFFFFFu, top = 0;   // of the entries that neither must nor cannot be taken
-  int valid = 0, must = 0;
+  uint32_t key[R], top = 0;
+#pragma unroll
+  for (int j = 0; j < R; j += 4) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (R * lane + j < n) v = *reinterpret_cast<const uint4*>(keys + key_at(R * lane + j));
+    key[j] = v.x, key[j + 1] = v.y, key[j + 2] = v.z, key[j + 3] = v.w;
+  }
+  const int from = first - R * lane, to = n - R * lane;
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    const int i = 32 * j + lane;
-    key[j] = i < n ? key_of(i) : 0u;
-    valid += key[j] != 0u;
-    must += key[j] == 0xFFFFFFFFu;
-    if (key[j] != 0xFFFFFFFFu) top = max(top, key[j]);
-    lo = min(lo, key[j] - 1u);   // a key of 0 becomes the largest
+    if (j >= to || j < from) key[j] = 0u;
+    top = max(top, key[j]);
   }
-  valid = __reduce_add_sync(0xffffffffu, valid);
-  must = __reduce_add_sync(0xffffffffu, must);
-  uint32_t thr = 1;        // entries with key >= thr are taken, of those equal to thr only the first `ties`
-  int ties = 0x7fffffff;
-  if (valid > want) {
-    // count(>= lo) >= want > count(>= hi) = above, or above == want
-    lo = __reduce_min_sync(0xffffffffu, lo) + 1u;
-    uint32_t hi = __reduce_max_sync(0xffffffffu, top) + 1u;
-    int above = must;
-    if (want - must <= 32 && want > must) {
-      uint32_t h = hi;
-      while (h - lo > 1) {
-        const uint32_t mid = lo + (h - lo) / 2;
-        const int c = __popc(__ballot_sync(0xffffffffu, top >= mid));
-        if (c >= want - must) {
-          lo = mid;
-          if (c == want - must) break;
-        } else {
-          h = mid;
-        }
-      }
-    }
-    thr = hi;
-    for (bool first = true; above < want; first = false) {
-      if (hi - lo == 1) {
-        thr = lo;
-        ties = want - above;
-        break;
-      }
-      const uint32_t mid = first ? lo : lo + (hi - lo) / 2;   // the bound may be the value itself
-      int c = 0;
-#pragma unroll
-      for (int j = 0; j < R; ++j) c += key[j] >= mid;
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (c > want) {
+  uint32_t lo = 1, hi = __reduce_max_sync(0xffffffffu, top) + 1u;
+  if (want <= 0 || hi == 1u) return 0;
+  if (__popc(__ballot_sync(0xffffffffu, top != 0u)) >= want) {
+    uint32_t h = hi;   // as many lanes reach lo, fewer reach h
+    while (h - lo > 1) {
+      const uint32_t mid = lo + (h - lo) / 2;
+      const int c = __popc(__ballot_sync(0xffffffffu, top >= mid));
+      if (c < want)
+        h = mid;
+      else
         lo = mid;
-      } else {
-        hi = thr = mid;
-        above = c;
-      }
+      if (c == want) break;
     }
   }
-  int at = 0;
+  // count(>= lo) >= want unless lo = 1; count(>= hi) = above < want
+  auto count = [&](uint32_t v) {
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < R; ++j) c += key[j] >= v;
+    return (int)__reduce_add_sync(0xffffffffu, c);
+  };
+  uint32_t thr = lo;
+  int above = 0, got = count(lo);
+  const int at_least = got;   // entries that reach lo
+  while (got > want && hi - lo > 1) {
+    thr = lo + (hi - lo) / 2;
+    got = count(thr);
+    if (got > want) {
+      lo = thr;
+    } else if (got < want) {
+      hi = thr;
+      above = got;
+      got = want + 1;
+    }
+  }
+  const bool cut = got > want;   // hi - lo = 1: some of the entries equal to lo are left out
+  if (cut) thr = lo;
+  got = min(want, at_least);
+
+  int mine = 0, eq = 0;
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    if (32 * j < n) {
-      const uint32_t eq = __ballot_sync(0xffffffffu, key[j] == thr);
-      const uint32_t before = (1u << lane) - 1u;
-      const bool take = key[j] > thr || (key[j] == thr && __popc(eq & before) < ties);
-      ties -= min(ties, __popc(eq));
-      const uint32_t all = __ballot_sync(0xffffffffu, take);
-      const Entry e = take ? get(32 * j + lane) : Entry{0.0f, 0};
-      __syncwarp();
-      if (take) put(at + __popc(all & before), e);
-      at += __popc(all);
+    mine += key[j] > thr || (key[j] == thr && !cut);
+    eq += key[j] == thr;
+  }
+  int room = eq;   // of this lane's entries equal to thr, the first `room` are taken
+  if (cut) {
+    int before = eq;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    room = max(0, min(eq, want - above - (before - eq)));
+    mine += room;
+  }
+  int at = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += v;
+  }
+  at -= mine;
+  if (mine) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const bool tie = key[j] == thr;
+      if (key[j] > thr || (tie && room > 0)) put(at++, R * lane + j, key[j]);
+      room -= tie;
     }
   }
-  return at;
+  __syncwarp();
+  return got;
+}
+
+template <typename Put>
+__device__ __forceinline__ int warp_top_any(const uint32_t* keys, int first, int n, int want, Put put) {
+  return n <= 128 ? warp_top<4>(keys, first, n, want, put) : warp_top<16>(keys, first, n, want, put);
+}
+
+// The best `want` of `have` entries held in (ok, ob) and the entries first .. n - 1 (n <= SEL_CHUNK) of a
+// further piece, which come after them, block_of(i) their blocks -> (ok, ob); how many are held then.
+// (lk, lb): scratch for 2 want entries.
+template <typename Block>
+__device__ __forceinline__ int warp_top_piece(int have, const uint32_t* keys, int first, int n, Block block_of, int want,
+                                              uint32_t* ok, int* ob, uint32_t* lk, int* lb) {
+  const bool join = have > 0;
+  if (join)
+    for (int i = threadIdx.x & 31; i < have; i += 32) lk[key_at(i)] = ok[key_at(i)], lb[i] = ob[i];
+  const int got = warp_top_any(keys, first, n, want, [&](int p, int i, uint32_t key) {
+    if (join)
+      lk[key_at(have + p)] = key, lb[have + p] = block_of(i);
+    else
+      ok[key_at(p)] = key, ob[p] = block_of(i);
+  });
+  if (!join) return got;
+  return warp_top_any(lk, 0, have + got, want, [&](int p, int i, uint32_t key) { ok[key_at(p)] = key, ob[p] = lb[i]; });
+}
+
+// The same for a list of any length.
+template <typename Block>
+__device__ __forceinline__ int warp_top_list(const uint32_t* keys, int first, int n, Block block_of, int want, uint32_t* ok,
+                                             int* ob, uint32_t* lk, int* lb) {
+  int have = 0;
+  for (int base = 0; base < n; base += SEL_CHUNK)
+    have = warp_top_piece(have, keys + key_at(base), first - base, min(SEL_CHUNK, n - base),
+                          [&](int i) { return block_of(base + i); }, want, ok, ob, lk, lb);
+  return have;
 }
 
 // ---------------------------------------------------------------------------
@@ -172,16 +225,6 @@ __device__ __forceinline__ int query_vector(const uint32_t* qr, int stride, int 
   return query_exp(amax);
 }
 
-// ---------------------------------------------------------------------------
-// a token at a time: decode
-// ---------------------------------------------------------------------------
-// A cluster per (token, kv head); each CTA scores one stretch of the visible blocks and keeps its
-// best k, the first CTA takes the best of those.  Within a CTA each warp selects from its own
-// stretch of the scores, the first warp then from the warps' lists; a list that does not fit the
-// registers goes through in pieces, the best so far being the head of the next piece.
-constexpr int SR_WARPS = 8;
-constexpr int SEL_CHUNK = 512, SEL_KMAX = 256;   // entries a piece adds; most blocks taken
-
 struct SelectArgs {
   const int8_t* bounds;
   const int8_t* bexp;
@@ -197,41 +240,86 @@ struct SelectArgs {
   int32_t* err;
 };
 
-// One warp: the best k of the `have` entries held in (osc, oid) and m <= SEL_CHUNK more, sc[i] and
-// id_of(i), which follow them in order -> (osc, oid); returns how many are held then.
-template <typename Id>
-__device__ __forceinline__ int select_piece(int have, const float* sc, int m, int k, int n_sink, int first_local, Id id_of,
-                                            float* osc, int* oid) {
-  auto get = [&](int i) { return i < have ? Entry{osc[i], oid[i]} : Entry{sc[i - have], id_of(i - have)}; };
-  auto key = [&](int i) {
-    const Entry e = get(i);
-    return select_key(e.sc, e.id < n_sink || e.id >= first_local);
-  };
-  auto put = [&](int p, const Entry& e) { osc[p] = e.sc, oid[p] = e.id; };
-  const int total = have + m;
-  int got;
-  if (total <= 128)
-    got = warp_select<4>(total, k, key, get, put);
-  else if (total <= 256)
-    got = warp_select<8>(total, k, key, get, put);
-  else if (total <= 512)
-    got = warp_select<16>(total, k, key, get, put);
-  else
-    got = warp_select<(SEL_CHUNK + SEL_KMAX) / 32>(total, k, key, get, put);
-  __syncwarp();
-  return got;
+// ---------------------------------------------------------------------------
+// what must be taken
+// ---------------------------------------------------------------------------
+// The blocks that must be taken are the first n_sink and the last n_local: with the selection
+// between them the list is in order, and no entry needs a test of its own.
+struct Forced {
+  int sinks, local0, nb;   // blocks [0, sinks) and [local0, nb) must be taken; nb visible blocks
+  int paged;               // those of them that have pages
+  __device__ __forceinline__ int slots() const { return sinks + nb - local0; }
+  __device__ __forceinline__ int block(int slot) const { return slot < sinks ? slot : local0 + slot - sinks; }
+};
+// By one warp.
+__device__ __forceinline__ Forced forced_blocks(const SelectArgs& a, int s, int p, int nb) {
+  Forced f;
+  f.nb = nb;
+  f.sinks = min(a.n_sink, nb);
+  f.local0 = min(nb, max(f.sinks, p / KV_BLOCK + 1 - a.n_local));
+  f.paged = 0;
+  for (int i = threadIdx.x & 31; i < f.slots(); i += 32)
+    f.paged += (unsigned)__ldg(a.tab.table + (size_t)s * a.tab.N + f.block(i)) < (unsigned)a.tab.n_pages;
+  f.paged = __reduce_add_sync(0xffffffffu, f.paged);
+  return f;
 }
 
-// The best k of n entries, any number of them.
-template <typename Id>
-__device__ __forceinline__ int select_list(const float* sc, int n, int k, int n_sink, int first_local, Id id_of,
-                                           float* osc, int* oid) {
-  int have = 0;
-  for (int base = 0; base < n; base += SEL_CHUNK)
-    have = select_piece(have, sc + base, min(SEL_CHUNK, n - base), k, n_sink, first_local,
-                        [&](int i) { return id_of(base + i); }, osc, oid);
-  return have;
+// By one warp: the lists of (token, head) `row` from the forced blocks' keys (by slot; 0: no page)
+// and the n_mid best others.
+__device__ __forceinline__ void write_lists(const SelectArgs& a, size_t row, const Forced& f, const uint32_t* forced_k,
+                                            const uint32_t* mid_k, const int* mid_b, int n_mid, int eq) {
+  const int lane = threadIdx.x & 31, slots = f.slots();
+  const float up = pow2f(eq);
+  int32_t* ids = a.ids + row * a.k;
+  float* scores = a.scores ? a.scores + row * a.k : nullptr;
+  auto put = [&](int p, int b, uint32_t key) {
+    ids[p] = b;
+    if (scores) scores[p] = score_of_key(key) * up;
+  };
+  int at = 0;
+  for (int i0 = 0; i0 < slots || i0 == 0; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t key = i < slots ? forced_k[i] : 0u;
+    const uint32_t all = __ballot_sync(0xffffffffu, key != 0u);
+    const uint32_t early = __ballot_sync(0xffffffffu, key != 0u && i < f.sinks);
+    const int p = at + __popc(all & ((1u << lane) - 1u));
+    if (key != 0u) put(i < f.sinks ? p : p + n_mid, f.block(i), key);
+    if (i0 < f.sinks || i0 == 0) {   // the last such step knows where the others start
+      if (f.sinks <= i0 + 32)
+        for (int j = lane; j < n_mid; j += 32) put(at + __popc(early) + j, mid_b[j], mid_k[key_at(j)]);
+    }
+    at += __popc(all);
+  }
+  for (int i = at + n_mid + lane; i < a.k; i += 32) {
+    ids[i] = -1;
+    if (scores) scores[i] = 0.0f;
+  }
 }
+
+// ---------------------------------------------------------------------------
+// a token at a time: decode
+// ---------------------------------------------------------------------------
+// A cluster per (token, kv head).  Each CTA scores one stretch of the visible blocks, keeps the best
+// of it (each warp of a part of it first, where it is long) and writes them into the first CTA's
+// shared memory, which selects among them.
+constexpr int SR_WARPS = 8, SR_RANKS = 8;
+
+// Shared memory, in words; lists have kk places, k rounded up to whole groups of 16.
+struct SelectRowsMem {
+  int kk;
+  __host__ __device__ explicit SelectRowsMem(int k) : kk((k + 15) / 16 * 16) {}
+  __host__ __device__ int all_k() const { return 0; }                                     // every CTA's list
+  __host__ __device__ int all_b() const { return all_k() + SR_RANKS * key_at(kk); }
+  __host__ __device__ int loc_k() const { return all_b() + SR_RANKS * kk; }               // every warp's list
+  __host__ __device__ int loc_b() const { return loc_k() + SR_WARPS * key_at(kk); }
+  __host__ __device__ int fin_k() const { return loc_b() + SR_WARPS * kk; }               // the CTA's list
+  __host__ __device__ int fin_b() const { return fin_k() + key_at(kk); }
+  __host__ __device__ int forced() const { return fin_b() + kk; }
+  __host__ __device__ int scratch(int w) const { return forced() + kk + w * (key_at(2 * kk) + 2 * kk); }
+  __host__ __device__ int keys() const { return scratch(SR_WARPS); }
+  __host__ __device__ int pages(int span) const { return keys() + key_at((span + 15) / 16 * 16); }
+  __host__ __device__ size_t bytes(int span) const { return 4 * ((size_t)pages(span) + span); }
+};
 
 // Sixteen whole numbers of the query's vector against sixteen bytes of bounds.
 __device__ __forceinline__ int dot16(const int (&u)[8], const uint4& b) {
@@ -248,14 +336,15 @@ __device__ __forceinline__ int dot16(const int (&u)[8], const uint4& b) {
 
 template <int D>
 __global__ void __launch_bounds__(SR_WARPS * 32, 2) kv_select_rows_kernel(const SelectArgs a) {
-  extern __shared__ __align__(16) unsigned char sm_raw[];
+  extern __shared__ __align__(16) uint32_t sm[];
   __shared__ __align__(16) short u[2 * D];
-  __shared__ float best_sc[SEL_KMAX];
-  __shared__ int best_id[SEL_KMAX], n_best, eq_s;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ Forced f_s;
+  __shared__ int eq_s;
+  const SelectRowsMem mem(a.k);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kk = mem.kk;
   const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
   const int row = blockIdx.x / ranks, t = row / a.H, h = row - t * a.H;
-  if (ranks > 1) cluster_arrive();
+  cluster_arrive();
   pdl_wait();
   pdl_launch_dependents();
   const int p = __ldg(a.pos + t), s = __ldg(a.seq + t);
@@ -263,17 +352,10 @@ __global__ void __launch_bounds__(SR_WARPS * 32, 2) kv_select_rows_kernel(const 
   if (p >= 0 && (!ok || p / KV_BLOCK >= a.tab.N) && tid == 0) set_err(a.err, BRE_DEVERR_PAGE);
   const int nb = ok ? min(p / KV_BLOCK + 1, a.tab.N) : 0;
   const int span = (nb + ranks - 1) / ranks, b0 = min(rank * span, nb), n = min(span, nb - b0);
-  // shared: the lists (at the same place in every CTA), then pages and scores of this CTA's blocks
-  float* list_sc = reinterpret_cast<float*>(sm_raw);
-  int* list_id = reinterpret_cast<int*>(list_sc + SR_WARPS * a.k);
-  float* all_sc = reinterpret_cast<float*>(list_id + SR_WARPS * a.k);   // every CTA's list, in the first CTA
-  int* all_id = reinterpret_cast<int*>(all_sc + 8 * a.k);
-  int* page = all_id + 8 * a.k;
-  float* sc = reinterpret_cast<float*>(page + span);
-  if (warp < SR_WARPS - 1)
-    for (int i = tid; i < n; i += (SR_WARPS - 1) * 32) page[i] = kv_page(a.tab, s, b0 + i, a.err);
+  uint32_t* keys = sm + mem.keys();
+  int* page = reinterpret_cast<int*>(sm + mem.pages(span));
 
-  // the query's vector, by the last warp (the others look up pages)
+  // the query's vector by the last warp, what must be taken by the one before, pages by the others
   if (warp == SR_WARPS - 1) {
     constexpr int W = D / 64;
     int pl[2 * W], mi[2 * W];
@@ -282,16 +364,22 @@ __global__ void __launch_bounds__(SR_WARPS * 32, 2) kv_select_rows_kernel(const 
     if (lane == 0) eq_s = e;
 #pragma unroll
     for (int i = 0; i < 2 * W; ++i) u[2 * W * lane + i] = (short)pl[i], u[D + 2 * W * lane + i] = (short)-mi[i];
+  } else if (warp == SR_WARPS - 2) {
+    const Forced f = forced_blocks(a, s, p, nb);
+    if (lane == 0) f_s = f;
+  } else {
+    for (int i = tid; i < n; i += (SR_WARPS - 2) * 32) page[i] = kv_page(a.tab, s, b0 + i, a.err);
   }
   __syncthreads();
-  const int eq = eq_s;
+  const Forced f = f_s;
 
   // scores: 2 D / 16 lanes a block, eight loads in flight
   constexpr int LB = 2 * D / 16, PW = 32 / LB;   // lanes a block, blocks a load
   int uu[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) uu[j] = reinterpret_cast<const int*>(u)[(lane % LB) * 8 + j];
-  const int seg = (n + SR_WARPS - 1) / SR_WARPS, w0 = min(warp * seg, n), wn = min(seg, n - w0);
+  // a warp's part: whole groups of 16, so that parts are lists of their own
+  const int part = (n + 16 * SR_WARPS - 1) / (16 * SR_WARPS) * 16, w0 = min(warp * part, n), wn = min(part, n - w0);
   for (int i0 = 0; i0 < wn; i0 += 8 * PW) {
     uint4 bd[8];
     int e[8];
@@ -309,50 +397,52 @@ __global__ void __launch_bounds__(SR_WARPS * 32, 2) kv_select_rows_kernel(const 
 #pragma unroll
       for (int o = 1; o < LB; o *= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
       const int i = i0 + j * PW + lane / LB;
-      if (i < wn && lane % LB == 0) sc[w0 + i] = e[j] == -128 ? -INFINITY : (float)d * pow2f(e[j]);
+      if (i < wn && lane % LB == 0) keys[key_at(w0 + i)] = e[j] == -128 ? 0u : key_of_score((float)d * pow2f(e[j]));
     }
   }
   __syncthreads();
-  const int first_local = p / KV_BLOCK - a.n_local + 1;
-  // the lists' unused places are entries that cannot be taken
-  auto pad = [&](int got, float* lsc) {
-    for (int i = got + lane; i < a.k; i += 32) lsc[i] = -INFINITY;
-  };
+
+  // the stretch's best of the blocks between the forced ones
+  const int want = a.k - f.paged, m0 = f.sinks - b0, m1 = min(n, f.local0 - b0);
+  uint32_t* fin_k = sm + mem.fin_k();
+  int* fin_b = reinterpret_cast<int*>(sm + mem.fin_b());
+  uint32_t* lk = sm + mem.scratch(warp);
+  int* lb = reinterpret_cast<int*>(lk + key_at(2 * kk));
+  int got = 0;
   if (n > SEL_CHUNK) {
-    float* lsc = list_sc + warp * a.k;
-    pad(select_list(sc + w0, wn, a.k, a.n_sink, first_local, [&](int i) { return b0 + w0 + i; }, lsc,
-                    list_id + warp * a.k), lsc);
+    uint32_t* loc_k = sm + mem.loc_k();
+    int* loc_b = reinterpret_cast<int*>(sm + mem.loc_b());
+    got = warp_top_list(keys + key_at(w0), m0 - w0, min(wn, m1 - w0), [&](int i) { return b0 + w0 + i; }, want,
+                        loc_k + warp * key_at(kk), loc_b + warp * kk, lk, lb);
+    for (int i = got + lane; i < kk; i += 32) loc_k[key_at(warp * kk + i)] = 0u;
     __syncthreads();
+    if (warp == 0)
+      got = warp_top_list(loc_k, 0, SR_WARPS * kk, [&](int i) { return loc_b[i]; }, want, fin_k, fin_b, lk, lb);
+  } else if (warp == 0) {
+    got = warp_top_list(keys, m0, m1, [&](int i) { return b0 + i; }, want, fin_k, fin_b, lk, lb);
   }
+  cluster_wait();   // the first CTA runs: its shared memory may be written
   if (warp == 0) {
-    const int got = n > SEL_CHUNK
-                        ? select_list(list_sc, SR_WARPS * a.k, a.k, a.n_sink, first_local,
-                                      [&](int i) { return list_id[i]; }, best_sc, best_id)
-                        : select_list(sc, n, a.k, a.n_sink, first_local, [&](int i) { return b0 + i; }, best_sc, best_id);
-    if (lane == 0) n_best = got;
+    __syncwarp();
+    for (int i = lane; i < kk; i += 32) {
+      st_cluster_u32(sm + mem.all_k() + key_at(rank * kk + i), 0, i < got ? fin_k[key_at(i)] : 0u);
+      st_cluster_u32(sm + mem.all_b() + rank * kk + i, 0, i < got ? (uint32_t)fin_b[i] : 0u);
+    }
+  } else if (warp == 1) {
+    for (int i = lane; i < f.slots(); i += 32) {
+      const int b = f.block(i) - b0;
+      if (b >= 0 && b < n) st_cluster_u32(sm + mem.forced() + i, 0, keys[key_at(b)]);
+    }
   }
+  cluster_arrive();
+  if (rank != 0) return;
+  cluster_wait();
+  if (warp != 0) return;
   if (ranks > 1) {
-    cluster_wait();   // the first CTA runs: its shared memory may be written
-    __syncthreads();
-    for (int i = tid; i < a.k; i += SR_WARPS * 32) {
-      st_cluster_f32(&all_sc[rank * a.k + i], 0, i < n_best ? best_sc[i] : -INFINITY);
-      st_cluster_s32(&all_id[rank * a.k + i], 0, i < n_best ? best_id[i] : 0);
-    }
-    cluster_arrive();
-    if (rank != 0) return;
-    cluster_wait();
-    if (warp == 0) {
-      const int got = select_list(all_sc, ranks * a.k, a.k, a.n_sink, first_local, [&](int i) { return all_id[i]; },
-                                  best_sc, best_id);
-      if (lane == 0) n_best = got;
-    }
+    const int* all_b = reinterpret_cast<const int*>(sm + mem.all_b());
+    got = warp_top_list(sm + mem.all_k(), 0, ranks * kk, [&](int i) { return all_b[i]; }, want, fin_k, fin_b, lk, lb);
   }
-  __syncthreads();
-  if (rank == 0)
-    for (int i = tid; i < a.k; i += SR_WARPS * 32) {
-      a.ids[(size_t)row * a.k + i] = i < n_best ? best_id[i] : -1;
-      if (a.scores) a.scores[(size_t)row * a.k + i] = i < n_best ? best_sc[i] * pow2f(eq) : 0.0f;
-    }
+  write_lists(a, row, f, sm + mem.forced(), fin_k, fin_b, got, eq_s);
 }
 
 // ---------------------------------------------------------------------------
@@ -360,10 +450,11 @@ __global__ void __launch_bounds__(SR_WARPS * 32, 2) kv_select_rows_kernel(const 
 // ---------------------------------------------------------------------------
 // A CTA per (32 tokens, kv head).  The tokens' vectors lie in shared memory as FP16 fragments, the
 // bounds' bytes become FP16 in registers (1024 + 128 + b in the mantissa, minus 1152: exact), and
-// mma.m16n8k16 multiplies them, 512 blocks at a time; each warp then selects for four of the
+// mma.m16n8k16 multiplies them, 512 blocks at a time; each warp then selects for two of the
 // tokens, from the scores in shared memory and the best of the blocks before.  Tokens of one
 // sequence share the work; a tile that spans sequences goes through each of them in turn.
-constexpr int ST_WARPS = 8, ST_ROWS = 32, ST_LD = SEL_CHUNK + 8;   // padded: the fragments' rows fall into different banks
+constexpr int ST_WARPS = 16, ST_ROWS = 32, ST_NT = 2;   // ST_NT: column tiles (of 8 blocks) of a warp at a time
+constexpr int ST_LD = key_at(SEL_CHUNK) + 8;   // padded: the fragments' rows fall into different banks
 
 __device__ __forceinline__ uint32_t s8x2_to_f16x2(uint32_t biased, uint32_t sel) {
   uint32_t r;
@@ -371,8 +462,11 @@ __device__ __forceinline__ uint32_t s8x2_to_f16x2(uint32_t biased, uint32_t sel)
   return r;
 }
 
-__host__ __device__ constexpr size_t select_tiles_smem(int D, int k) {
-  return (size_t)ST_ROWS * 2 * D * 2 + (size_t)ST_ROWS * ST_LD * 4 + SEL_CHUNK * 8 + (size_t)ST_ROWS * k * 8;
+// Shared memory: the fragments, the keys of a piece, its pages and units, the rows' lists (kk places, k
+// rounded up to whole groups of 16) and forced blocks' keys, the warps' scratch.
+__host__ __device__ constexpr size_t select_tiles_smem(int D, int kk) {
+  return (size_t)ST_ROWS * 2 * D * 2 + (size_t)ST_ROWS * ST_LD * 4 + SEL_CHUNK * 8 +
+         (size_t)ST_ROWS * (key_at(kk) + 2 * kk) * 4 + (size_t)ST_WARPS * (key_at(2 * kk) + 2 * kk) * 4;
 }
 
 template <int D>
@@ -380,12 +474,16 @@ __global__ void __launch_bounds__(ST_WARPS * 32, 2) kv_select_tiles_kernel(const
   constexpr int KS = 2 * D / 16;   // k steps; a group of four covers 64 channels
   extern __shared__ __align__(16) unsigned char sm_raw[];
   uint4* af = reinterpret_cast<uint4*>(sm_raw);                        // [2 row tiles][KS][32 lanes]
-  float* sc = reinterpret_cast<float*>(sm_raw + ST_ROWS * 2 * D * 2);   // [ST_ROWS][ST_LD]
-  int* page = reinterpret_cast<int*>(sc + ST_ROWS * ST_LD);            // [SEL_CHUNK]
+  uint32_t* keys = reinterpret_cast<uint32_t*>(sm_raw + ST_ROWS * 2 * D * 2);   // [ST_ROWS][ST_LD]
+  int* page = reinterpret_cast<int*>(keys + ST_ROWS * ST_LD);          // [SEL_CHUNK]
   float* unit = reinterpret_cast<float*>(page + SEL_CHUNK);            // [SEL_CHUNK] 2^bound_exp, 0: no page
-  float* best_sc = unit + SEL_CHUNK;                                   // [ST_ROWS][k]
-  int* best_id = reinterpret_cast<int*>(best_sc + ST_ROWS * a.k);
-  __shared__ int row_seq[ST_ROWS], row_pos[ST_ROWS], row_eq[ST_ROWS];
+  const int kk = (a.k + 15) / 16 * 16;
+  uint32_t* best_k = reinterpret_cast<uint32_t*>(unit + SEL_CHUNK);    // [ST_ROWS][key_at(kk)]
+  int* best_b = reinterpret_cast<int*>(best_k + ST_ROWS * key_at(kk)); // [ST_ROWS][kk]
+  uint32_t* forced_k = reinterpret_cast<uint32_t*>(best_b + ST_ROWS * kk);   // [ST_ROWS][kk]
+  uint32_t* scratch = forced_k + ST_ROWS * kk;
+  __shared__ int row_seq[ST_ROWS], row_pos[ST_ROWS], row_eq[ST_ROWS], row_have[ST_ROWS];
+  __shared__ Forced row_f[ST_ROWS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int t0 = blockIdx.x * ST_ROWS, h = blockIdx.y, rows = min(ST_ROWS, a.T - t0);
   pdl_wait();
@@ -428,7 +526,11 @@ __global__ void __launch_bounds__(ST_WARPS * 32, 2) kv_select_tiles_kernel(const
       ++r1;
     }
     nb_max = min(nb_max, a.tab.N);
-    int have[ST_ROWS / ST_WARPS] = {};
+    for (int r = r0 + warp; r < r1; r += ST_WARPS) {
+      const int p = row_pos[r];
+      const Forced f = forced_blocks(a, s, p, p >= 0 ? min(p / KV_BLOCK + 1, a.tab.N) : 0);
+      if (lane == 0) row_f[r] = f, row_have[r] = 0;
+    }
     for (int base = 0; base < nb_max; base += SEL_CHUNK) {
       const int nc = min(SEL_CHUNK, nb_max - base);
       __syncthreads();   // the scores and pages of the piece before are done with
@@ -438,32 +540,31 @@ __global__ void __launch_bounds__(ST_WARPS * 32, 2) kv_select_tiles_kernel(const
         unit[i] = pg >= 0 ? pow2f(__ldg(a.bexp + (size_t)pg * a.H + h)) : 0.0f;
       }
       __syncthreads();
-      // 32 blocks (four column tiles) of a warp at a time
-      for (int c0 = warp * 32; c0 < nc; c0 += ST_WARPS * 32) {
-        float acc[4][2][4];
+      for (int c0 = warp * 8 * ST_NT; c0 < nc; c0 += ST_WARPS * 8 * ST_NT) {
+        float acc[ST_NT][2][4];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int nt = 0; nt < ST_NT; ++nt)
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[nt][mt][j] = 0.0f;
-        const int8_t* bp[4];
+        const int8_t* bp[ST_NT];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
+        for (int nt = 0; nt < ST_NT; ++nt) {
           const int pg = page[c0 + 8 * nt + g];
           bp[nt] = pg >= 0 ? a.bounds + ((size_t)pg * a.H + h) * 2 * D + 16 * t4 : nullptr;
         }
 #pragma unroll
         for (int cg = 0; cg < KS / 4; ++cg) {
-          uint4 b[4];
+          uint4 b[ST_NT];
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
+          for (int nt = 0; nt < ST_NT; ++nt)
             b[nt] = bp[nt] ? __ldg(reinterpret_cast<const uint4*>(bp[nt] + cg * 64)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint4 a0 = af[(cg * 4 + i) * 32 + lane], a1 = af[(KS + cg * 4 + i) * 32 + lane];
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
+            for (int nt = 0; nt < ST_NT; ++nt) {
               const uint32_t w = (i == 0 ? b[nt].x : i == 1 ? b[nt].y : i == 2 ? b[nt].z : b[nt].w) ^ 0x80808080u;
               const uint32_t b0 = s8x2_to_f16x2(w, 0x4140u), b1 = s8x2_to_f16x2(w, 0x4342u);
               mma_f16_16816(acc[nt][0], a0.x, a0.y, a0.z, a0.w, b0, b1);
@@ -472,40 +573,39 @@ __global__ void __launch_bounds__(ST_WARPS * 32, 2) kv_select_tiles_kernel(const
           }
         }
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
+        for (int nt = 0; nt < ST_NT; ++nt) {
           const int col = c0 + 8 * nt + 2 * t4;
           const float u0 = unit[col], u1 = unit[col + 1];
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              *reinterpret_cast<float2*>(sc + (16 * mt + 8 * r + g) * ST_LD + col) =
-                  make_float2(u0 == 0.0f ? -INFINITY : acc[nt][mt][2 * r] * u0,
-                              u1 == 0.0f ? -INFINITY : acc[nt][mt][2 * r + 1] * u1);
+              *reinterpret_cast<uint2*>(keys + (16 * mt + 8 * r + g) * ST_LD + key_at(col)) =
+                  make_uint2(u0 == 0.0f ? 0u : key_of_score(acc[nt][mt][2 * r] * u0),
+                             u1 == 0.0f ? 0u : key_of_score(acc[nt][mt][2 * r + 1] * u1));
         }
       }
       __syncthreads();
-#pragma unroll
-      for (int j = 0; j < ST_ROWS / ST_WARPS; ++j) {
-        const int r = warp + j * ST_WARPS;
-        if (r < r0 || r >= r1 || row_pos[r] < 0) continue;
-        const int cur = row_pos[r] / KV_BLOCK, m = min(min(cur + 1, a.tab.N) - base, SEL_CHUNK);
-        if (m > 0)
-          have[j] = select_piece(have[j], sc + r * ST_LD, m, a.k, a.n_sink, cur - a.n_local + 1,
-                                 [&](int i) { return base + i; }, best_sc + r * a.k, best_id + r * a.k);
+      for (int r = r0 + warp; r < r1; r += ST_WARPS) {
+        const Forced f = row_f[r];
+        const int m = min(f.nb - base, SEL_CHUNK);
+        if (m <= 0) continue;
+        const uint32_t* kr = keys + r * ST_LD;
+        for (int i = lane; i < f.slots(); i += 32) {
+          const int b = f.block(i) - base;
+          if (b >= 0 && b < m) forced_k[r * kk + i] = kr[key_at(b)];
+        }
+        uint32_t* lk = scratch + warp * (key_at(2 * kk) + 2 * kk);
+        const int have = warp_top_piece(row_have[r], kr, f.sinks - base, min(m, f.local0 - base),
+                                        [&](int i) { return base + i; }, a.k - f.paged, best_k + r * key_at(kk),
+                                        best_b + r * kk, lk, reinterpret_cast<int*>(lk + key_at(2 * kk)));
+        if (lane == 0) row_have[r] = have;
       }
     }
-#pragma unroll
-    for (int j = 0; j < ST_ROWS / ST_WARPS; ++j) {
-      const int r = warp + j * ST_WARPS;
-      if (r < r0 || r >= r1) continue;
-      const size_t o = ((size_t)(t0 + r) * a.H + h) * a.k;
-      const float up = pow2f(row_eq[r]);
-      for (int i = lane; i < a.k; i += 32) {
-        a.ids[o + i] = i < have[j] ? best_id[r * a.k + i] : -1;
-        if (a.scores) a.scores[o + i] = i < have[j] ? best_sc[r * a.k + i] * up : 0.0f;
-      }
-    }
+    __syncwarp();
+    for (int r = r0 + warp; r < r1; r += ST_WARPS)
+      write_lists(a, (size_t)(t0 + r) * a.H + h, row_f[r], forced_k + r * kk, best_k + r * key_at(kk), best_b + r * kk,
+                  row_have[r], row_eq[r]);
     r0 = r1;
   }
 }
@@ -515,7 +615,7 @@ __global__ void __launch_bounds__(ST_WARPS * 32, 2) kv_select_tiles_kernel(const
 size_t kv_select_ws_bytes(int T, int Hq, int H, int D, int B, int N, int k) { return 0; }
 
 // Shared memory of the one-token kernel for stretches of `span` blocks.
-static size_t select_rows_smem(int span, int k) { return (size_t)span * 8 + (size_t)(SR_WARPS + 8) * k * 8; }
+static size_t select_rows_smem(int span, int k) { return SelectRowsMem(k).bytes(span); }
 
 cudaError_t launch_kv_select(const bre_kv_cache* c, const KvTokens& tk, const uint16_t* q, long long q_stride, int Hq,
                              int k, int n_sink, int n_local, int32_t* ids, float* scores, void* ws, int32_t* err,
@@ -525,7 +625,7 @@ cudaError_t launch_kv_select(const bre_kv_cache* c, const KvTokens& tk, const ui
                      q, q_stride, tk.seq, tk.pos, tk.T, k, n_sink, n_local, ids, scores, err};
   if (tk.T >= 16LL * tk.B) {
     auto kern = D == 128 ? kv_select_tiles_kernel<128> : kv_select_tiles_kernel<64>;
-    const size_t smem = select_tiles_smem(D, k);
+    const size_t smem = select_tiles_smem(D, (k + 15) / 16 * 16);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_k(kern, dim3((unsigned)((tk.T + ST_ROWS - 1) / ST_ROWS), (unsigned)H), dim3(ST_WARPS * 32), smem, s, a);
