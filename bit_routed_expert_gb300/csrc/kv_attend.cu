@@ -1,12 +1,9 @@
 // Attention over the listed blocks of the quantised cache.
-#include "kv_common.cuh"
+#include "kv_attend.cuh"
 
 namespace bre {
 
 namespace {
-
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-constexpr float P_SHIFT = 8.0f;   // weights are held times 2^8: FP16's normal range then reaches 2^-22 of the largest
 
 // ---------------------------------------------------------------------------
 // A token's heads at a time: decode and verify batches
@@ -28,34 +25,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-struct AttendArgs {
-  const uint8_t* pages;
-  int H, G;
-  KvTable tab;
-  const uint16_t* q;
-  long long q_stride;
-  const int32_t* seq;
-  const int32_t* pos;
-  int T;
-  const int32_t* ids;
-  int k;
-  float scale;
-  uint16_t* out;
-  float* lse;
-  int32_t* err;
-};
-
 // NT: groups of eight query heads.
 template <int D, int NT>
 __global__ void __launch_bounds__(AR_WARPS * 32) kv_attend_rows_kernel(const AttendArgs a) {
@@ -196,6 +165,14 @@ __global__ void __launch_bounds__(AR_WARPS * 32) kv_attend_rows_kernel(const Att
             for (int nt = 0; nt < NT; ++nt)
               mma_f16_16816(sc[nt][mt], a0, a1, a2, a3, qf[nt][hb][i][0], qf[nt][hb][i][1]);
           }
+      float kf2[2][2], evf[2][2];   // 2^ek; ev, or NaN where the token's key or value row is NaN
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          kf2[mt][r] = pow2f(ek[mt][r] - 127);
+          evf[mt][r] = ek[mt][r] == KV_NAN || ev[mt][r] == KV_NAN ? __int_as_float(0x7FC00000) : (float)(ev[mt][r] - 127);
+        }
       // weights; sc[mt][2 r + c] is token 16 mt + 8 r + g, head 2 t4 + c
       uint32_t pb[NT][2][2];
 #pragma unroll
@@ -208,8 +185,7 @@ __global__ void __launch_bounds__(AR_WARPS * 32) kv_attend_rows_kernel(const Att
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               float& v = sc[nt][mt][2 * r + c];
-              v = 16 * mt + 8 * r + g < n ? fmaf(v * qs[nt][c], pow2f(ek[mt][r] - 127), (float)(ev[mt][r] - 127))
-                                          : -INFINITY;
+              v = 16 * mt + 8 * r + g < n ? fmaf(v * qs[nt][c], kf2[mt][r], evf[mt][r]) : -INFINITY;
               mx[c] = fmaxf(mx[c], v);
             }
 #pragma unroll
@@ -330,6 +306,7 @@ cudaError_t launch_kv_attend(const bre_kv_cache* c, const KvTokens& tk, const ui
   const int H = c->n_kv_heads, D = c->head_dim, G = Hq / H;
   const AttendArgs a{static_cast<const uint8_t*>(c->pages), H,     G,     KvTable{tk.table, tk.B, tk.N, c->n_pages},
                      q, q_stride, tk.seq, tk.pos, tk.T, ids, k, scale, out, lse, err};
+  if (tk.T >= 16LL * tk.B) return launch_kv_attend_tiles(a, D, s);
   // CTAs of a (token, head): halves of blocks for every warp, as long as the GPU has room for them
   const long long rows = (long long)tk.T * H;
   int ranks = 1;

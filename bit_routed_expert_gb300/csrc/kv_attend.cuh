@@ -1,0 +1,41 @@
+// What the attention kernels over the quantised cache share.
+#pragma once
+#include "kv_common.cuh"
+
+namespace bre {
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float P_SHIFT = 8.0f;   // weights are held times 2^8: FP16's normal range then reaches 2^-22 of the largest
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+struct AttendArgs {
+  const uint8_t* pages;
+  int H, G;
+  KvTable tab;
+  const uint16_t* q;
+  long long q_stride;
+  const int32_t* seq;
+  const int32_t* pos;
+  int T;
+  const int32_t* ids;
+  int k;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  int32_t* err;
+};
+
+// 128 rows (tokens times query heads) at a time (kv_attend_tiles.cu)
+cudaError_t launch_kv_attend_tiles(const AttendArgs& a, int D, cudaStream_t s);
+
+}  // namespace bre

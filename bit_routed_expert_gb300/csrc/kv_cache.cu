@@ -38,11 +38,16 @@ __global__ void __launch_bounds__(128)
     for (int kv = 0; kv < 2; ++kv) {
       const uint16_t* row = kv ? v + t * v_stride : k + t * k_stride;
       float x[PL], a = 0.0f;
+      bool nan = false;
       for (int i = 0; i < PL; ++i) {
         x[i] = kv_clamp(bf16_bits_to_f32(row[h * D + lane * PL + i]));
+        nan |= x[i] != x[i];
         a = fmaxf(a, fabsf(x[i]));
       }
       for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+      nan = __any_sync(0xffffffffu, nan);
+      if (nan)
+        for (int i = 0; i < PL; ++i) x[i] = 0.0f;
       const int e = row_exp(a);
       uint8_t* dst = pg + kv * KV_BLOCK * D + slot * D + lane * PL;
       for (int i = 0; i < PL; i += 2) {
@@ -50,7 +55,7 @@ __global__ void __launch_bounds__(128)
         *reinterpret_cast<uint16_t*>(dst + i) = (uint16_t)c;
         if (kv == 0) {
           const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(c));
-          const float y[2] = {f.x == f.x ? f.x * pow2f(e) : 0.0f, f.y == f.y ? f.y * pow2f(e) : 0.0f};
+          const float y[2] = {f.x * pow2f(e), f.y * pow2f(e)};
           for (int j = 0; j < 2; ++j) {
             hi[i + j] = t == t0 ? y[j] : fmaxf(hi[i + j], y[j]);
             lo[i + j] = t == t0 ? y[j] : fminf(lo[i + j], y[j]);
@@ -58,7 +63,7 @@ __global__ void __launch_bounds__(128)
           }
         }
       }
-      if (lane == 0) pg[2 * KV_BLOCK * D + kv * KV_BLOCK + slot] = (uint8_t)(e + 127);
+      if (lane == 0) pg[2 * KV_BLOCK * D + kv * KV_BLOCK + slot] = (uint8_t)(nan ? KV_NAN : e + 127);
     }
   }
   for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));

@@ -18,6 +18,10 @@ namespace bre {
 
 constexpr int KV_BLOCK = 64;
 constexpr int KV_EXP_MIN = -64;   // rows below 2^-56 are stored in steps of 2^-73
+// Scale byte of a row that holds a NaN (E8M0's NaN); its codes are zeros and it reads as NaN throughout.
+// With one byte to look at, no kernel has to look for NaN among the codes, and a NaN value cannot
+// reach a row whose weight for it is zero through a matrix product.
+constexpr int KV_NAN = 255;
 
 __host__ __device__ constexpr int kv_page_bytes(int D) { return 2 * KV_BLOCK * D + 2 * KV_BLOCK; }
 

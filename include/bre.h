@@ -292,8 +292,9 @@ bre_status engram_inject(const uint8_t *table, int64_t n_rows, const int64_t *ro
  * seq, pos and table are int32 device arrays.
  *
  *   pages [n_pages][n_kv_heads][128 D + 128] bytes, D = head_dim: for each head of a page 64 key
- *     rows of D E4M3 codes (OCP: bias 7, no infinities), 64 value rows, 64 key scales, 64 value
- *     scales; value = code * 2^(scale byte - 127).  16-byte aligned.
+ *     rows of D E4M3 codes (OCP: bias 7, no infinities; the NaN codes do not occur), 64 value rows,
+ *     64 key scales, 64 value scales (E8M0); value = code * 2^(scale byte - 127), bytes 63 .. 246;
+ *     a row with the scale byte 255 is NaN throughout, its codes are zeros.  16-byte aligned.
  *   bounds [n_pages][n_kv_heads][2][D] int8, bound_exp [n_pages][n_kv_heads] int8: for each
  *     channel of a page's stored keys, whole numbers hi and lo in [-63, 63] with
  *     lo * 2^bound_exp <= key <= hi * 2^bound_exp, as tight as whole numbers are.
@@ -313,9 +314,9 @@ typedef struct {
 } bre_kv_cache;
 
 /* Store the keys and values of T tokens.  For a row x of D BF16 values: e = the least integer
- * >= -64 with max|x| <= 448 * 2^e, codes e4m3_rne(x * 2^-e), scale byte e + 127.  NaN is stored as
- * NaN and left out of the maximum; magnitudes above 448 * 2^119 (infinities too) saturate.
- * The bounds of every block written to are brought up to date (a NaN key counts as 0 there):
+ * >= -64 with max|x| <= 448 * 2^e, codes e4m3_rne(x * 2^-e), scale byte e + 127.  A row that holds a
+ * NaN is stored as a NaN row; magnitudes above 448 * 2^119 (infinities too) saturate.
+ * The bounds of every block written to are brought up to date (a NaN row counts as zeros there):
  * from this call's keys alone where its first token of the block is at slot 0, else together
  * with the bounds that were there.  A position written again widens them only: they stay bounds.
  *   k, v: row t starts t * stride elements after the base and holds [n_kv_heads][D]; bases 16-byte
@@ -353,7 +354,8 @@ bre_status kv_select(const bre_kv_cache *cache, const void *q_bf16, int64_t q_st
 /* Attention over listed blocks: for each query head of token t, over the tokens x <= pos[t] of
  * the blocks that ids lists for its kv head (-1: none; a block listed twice counts twice),
  *   s_x = scale * q . key_x,  out = sum_x exp(s_x) value_x / sum_x exp(s_x),  lse = log sum_x exp(s_x)
- * A row that sees no token gives zeros and lse = -inf.  Logits, maxima and sums are FP32; the
+ * A row that sees no token gives zeros and lse = -inf; one that sees a token whose key or value row
+ * is NaN gives NaN and lse = NaN.  Logits, maxima and sums are FP32; the
  * probabilities enter the second product as FP16 (relative error 2^-11), the codes exactly.
  *   ids [T][n_kv_heads][k] int32, any order; out [T][n_heads][D] BF16; lse [T][n_heads] FP32 or
  *   NULL (natural logarithm).  ws: kv_attend_workspace(...) bytes, zero-filled once after

@@ -45,8 +45,10 @@ VALUES = torch.tensor([e4m3_value(c) for c in range(256)], dtype=torch.float64)
 
 def store_row(row: torch.Tensor):
     """[D] -> (codes uint8 [D], scale byte)."""
+    if bool(row.isnan().any()):
+        return torch.zeros(len(row), dtype=torch.uint8), 255
     x = [v if v != v else max(-MAX, min(MAX, v)) for v in row.double().tolist()]
-    e = least_exp(max([abs(v) for v in x if v == v], default=0.0), 448.0)
+    e = least_exp(max(abs(v) for v in x), 448.0)
     return torch.tensor([e4m3_code(math.ldexp(v, -e)) for v in x], dtype=torch.uint8), e + 127
 
 
@@ -83,7 +85,7 @@ def append(pages, bounds, bexp, k, v, seq, pos, table):
                     slot = pos[i] % BLOCK
                     kc[pg, h, slot], ks[pg, h, slot] = store_row(k[i, h])
                     vc[pg, h, slot], vs[pg, h, slot] = store_row(v[i, h])
-                    new.append(VALUES[kc[pg, h, slot].long()].nan_to_num(0.0) * 2.0 ** (int(ks[pg, h, slot]) - 127))
+                    new.append(VALUES[kc[pg, h, slot].long()] * 2.0 ** (int(ks[pg, h, slot]) - 127))
                 new = torch.stack(new)
                 hi, lo, e = new.amax(0), new.amin(0), least_exp(float(new.abs().max()), 63.0)
                 if pos[t] % BLOCK:
@@ -101,8 +103,8 @@ def append(pages, bounds, bexp, k, v, seq, pos, table):
 def values(pages, D):
     """Stored keys and values [page, head, slot, D] in 64 bits."""
     kc, vc, ks, vs = views(pages, D)
-    return (VALUES[kc.long()] * 2.0 ** (ks.double() - 127)[..., None],
-            VALUES[vc.long()] * 2.0 ** (vs.double() - 127)[..., None])
+    scale = [torch.where(x == 255, math.nan, 2.0 ** (x.double() - 127))[..., None] for x in (ks, vs)]
+    return VALUES[kc.long()] * scale[0], VALUES[vc.long()] * scale[1]
 
 
 def select(q, bounds, bexp, seq, pos, table, k, n_sink, n_local):
@@ -181,7 +183,7 @@ def attend(q, pages, seq, pos, table, ids, scale):
             z = p.sum(1, keepdim=True)
             r = slice(h * G, (h + 1) * G)
             out[t, r], mass[t, r] = p @ vs / z, p @ vs.abs() / z
-            lse[t, r] = (m + torch.log(z))[:, 0]
+            lse[t, r] = (m + torch.log(z))[:, 0] if not bool(vs.isnan().any()) else math.nan   # a NaN value row too
             size[t, r] = (x.abs() @ ks.abs().T).amax(1) * abs(scale)
     return out, lse, mass, size, err
 

@@ -402,7 +402,7 @@ def test_attend_rows_of_very_different_size(cuda_dev, T):
 
 @pytest.mark.parametrize("T", [1, 40])
 def test_attend_nan_stays_in_its_rows(cuda_dev, T):
-    """A NaN key or value spoils the heads that see its token, and no others."""
+    """A NaN key or value row spoils the rows that see its token, and no others."""
     D, H, G = 64, 2, 2
     lens = [400]
     b = R.batch(lens, [T])
@@ -411,12 +411,12 @@ def test_attend_nan_stays_in_its_rows(cuda_dev, T):
     q[0, 1] = math.nan
     ids = some_ids(b, H, 7)
     clean, _, _, _, _ = R.attend(q, pages, b.seq, b.pos, b.table, ids, 0.125)
-    kc, vc, _, _ = R.views(pages, D)
-    kc[int(b.table[0, 1]), 0, 3, 9] = 0x7F
+    kc, vc, ks, vs = R.views(pages, D)
+    kc[int(b.table[0, 1]), 0, 3], ks[int(b.table[0, 1]), 0, 3] = 0, 255
     last = lens[0] - 1
-    kc[int(b.table[0, last // 64]), 0, last % 64 + 1:] = 0x7F     # never written, never seen
-    vc[int(b.table[0, last // 64]), :, last % 64 + 1:] = 0x7F
-    vc[int(b.table[0, 2]), 1, 4, 11] = 0xFF
+    for x in (kc, vc, ks, vs):     # never written, never seen
+        x[int(b.table[0, last // 64]), :, last % 64 + 1:] = 0xFF
+    vc[int(b.table[0, 2]), 1, 4], vs[int(b.table[0, 2]), 1, 4] = 0, 255
     c = on(cuda_dev, pages, torch.zeros((b.n_pages, H, 2, D), dtype=torch.int8), torch.zeros((b.n_pages, H), dtype=torch.int8))
     out, lse = kv_attend(q.to(cuda_dev), c, *b.on(cuda_dev), ids.to(cuda_dev), scale=0.125)
     want, wl, _, _, _ = R.attend(q, pages, b.seq, b.pos, b.table, ids, 0.125)
@@ -541,8 +541,9 @@ def test_binding_refuses(cuda_dev):
     for args in ((seq.long(), pos, table), (seq, pos[:1], table), (seq, pos, table.long())):
         with pytest.raises(ValueError):
             kv_read(c, *args)
-    with pytest.raises(BreError, match="workspace"):
-        kv_select(q, c, seq, pos, table, 4, ws=torch.zeros(0, dtype=torch.uint8, device=cuda_dev))
+    if kv_select_workspace(2, 4, 2, 64, 1, 2, 4):
+        with pytest.raises(BreError, match="workspace"):
+            kv_select(q, c, seq, pos, table, 4, ws=torch.zeros(0, dtype=torch.uint8, device=cuda_dev))
     with pytest.raises(BreError):
         kv_select(q, c, seq, pos, table, 2, n_sink=2, n_local=1)
     with pytest.raises(ValueError):
