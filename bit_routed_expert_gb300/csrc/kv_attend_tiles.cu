@@ -7,12 +7,12 @@
 // 4 * 128 * 64 * D operations whatever the number of rows that use it, against a row-by-row kernel's
 // 16 KB from L2 for every (token, block).
 //
-// Ten warps:
+// Fourteen warps:
 //   warps 0-3   softmax: a thread a row; S from tensor memory, weights back over it as FP16
-//   warps 4-7   turn the codes into FP16 (exact) in 128-byte-swizzled shared memory; the next block's
-//               codes are loaded into the registers that the current block's have left
-//   warp 8      merges the tokens' lists: the least next block over all tokens, and which tokens list it
-//   warp 9      issues the MMAs: S = Q K^T into tensor memory, O += P V with P read from tensor memory
+//   warps 4-7   turn the keys' codes into FP16 (exact) in 128-byte-swizzled shared memory
+//   warps 8-11  the values'; both have the next two blocks' codes under way into registers
+//   warp 12     merges the tokens' lists: the least next block over all tokens, and which tokens list it
+//   warp 13     issues the MMAs: S = Q K^T into tensor memory, O += P V with P read from tensor memory
 // K is K-major, V lies as it is in the cache (a token's channels in a row), which is the MN-major
 // form of the second product's operand.  S and P share two buffers, K and V have two stages each.
 //
@@ -26,7 +26,9 @@ namespace bre {
 
 namespace {
 
-constexpr int AT_THREADS = 320;
+constexpr int AT_CODES = 256;                       // threads that turn codes into FP16: keys, values
+constexpr int AT_THREADS = 128 + AT_CODES + 64;
+constexpr int W_MERGE = (128 + AT_CODES) / 32, W_MMA = W_MERGE + 1;
 constexpr int AT_RING = 4;                          // blocks that the merging warp may be ahead
 constexpr float AT_SLACK = 7.0f;                    // growth of a row's maximum (log2) that needs no rescaling
 constexpr long long AT_WAIT = 4000000000LL;         // cycles before a wait gives up (~2 s)
@@ -115,6 +117,36 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// The first try of a wait is inline, the bounded loop is not: with four roles in one kernel the
+// instruction caches are what runs short first.
+// A try suspends the warp for up to a millisecond: fourteen warps, half of them waiting, would otherwise take
+// the workers' issue slots.
+__device__ __forceinline__ bool try_wait_ms(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!try_wait_ms(bar, parity))
+    if (clock64() - t0 > AT_WAIT) return false;
+  return true;
+}
+
+// True in one lane.  The MMA warp stays together and lets one lane issue, so that the compiler keeps descriptors
+// and addresses in uniform registers, where the MMA instructions want them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Two FP32 values at a time.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
@@ -155,20 +187,20 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
   const int t0 = blockIdx.x * per, h = blockIdx.y, nt = min(per, a.T - t0), rows = nt * a.G;
 
   if (tid == 0) {
-    for (int i = 0; i < AT_RING; ++i) mbar_init(&blk_full[i], 1), mbar_init(&blk_empty[i], 9);
+    for (int i = 0; i < AT_RING; ++i) mbar_init(&blk_full[i], 1), mbar_init(&blk_empty[i], 4 + AT_CODES / 32 + 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 128);
+      mbar_init(&k_full[i], 4);
       mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 128);
+      mbar_init(&v_full[i], 4);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 4);
     }
     mbar_init(&o_done, 1);
     mbar_init(&drain, 1);
   }
   fence_mbar_init();
-  if (warp == 9) {
+  if (warp == W_MMA) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_s)), "n"(COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -177,32 +209,35 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
   pdl_launch_dependents();
 
   // queries: row r = (token r / G, head r % G) scaled by a power of two into FP16; K-major panels
-  {
-    constexpr int PL = D / 32;
-    for (int r = warp; r < 128; r += AT_THREADS / 32) {
-      const int tl = r / a.G;
-      uint32_t w[PL / 2] = {};
-      if (r < rows) {
-        const uint32_t* qr = reinterpret_cast<const uint32_t*>(a.q + (long long)(t0 + tl) * a.q_stride +
-                                                               (size_t)(h * a.G + r - tl * a.G) * D) + lane * (PL / 2);
+  constexpr int PL = D / 32, QW = AT_THREADS / 32;
+#pragma unroll 1
+  for (int r0 = warp; r0 < 128; r0 += 4 * QW) {
+    uint32_t w[4][PL / 2];
 #pragma unroll
-        for (int i = 0; i < PL / 2; ++i) w[i] = __ldg(qr + i);
-      }
-      float x[PL], amax = 0.0f;
+    for (int j = 0; j < 4; ++j) {
+      const int r = r0 + j * QW, tl = r / a.G;
+      const uint32_t* qr = reinterpret_cast<const uint32_t*>(a.q + (long long)(t0 + tl) * a.q_stride +
+                                                             (size_t)(h * a.G + r - tl * a.G) * D) + lane * (PL / 2);
 #pragma unroll
-      for (int i = 0; i < PL; ++i) {
-        x[i] = bf16_bits_to_f32(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
-        amax = fmaxf(amax, fabsf(kv_clamp(x[i])));
-      }
-      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-      const int e = query_exp(amax);
+      for (int i = 0; i < PL / 2; ++i) w[j][i] = r < rows ? __ldg(qr + i) : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = r0 + j * QW;
+      if (r >= 128) break;
+      uint32_t mx = 0;   // magnitudes of BF16 values compare like whole numbers; NaN and infinities count as 2^127
+#pragma unroll
+      for (int i = 0; i < PL / 2; ++i) mx = __vmaxu2(mx, w[j][i] & 0x7FFF7FFFu);
+      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
+      const int e = query_exp(bf16_bits_to_f32(min(mx, 0x7F00u)));
       const float down = pow2f(-e);
       if (lane == 0) q_factor[r] = a.scale * LOG2E * pow2f(e);
       const int c = lane * PL;
       unsigned char* dst = sm + M::q + (c / 64) * PANEL_Q + r * 128 + ((((c % 64) / 8) ^ (r & 7)) << 4) + (c % 8) * 2;
 #pragma unroll
       for (int i = 0; i < PL / 2; ++i)
-        reinterpret_cast<uint32_t*>(dst)[i] = pack_f16x2(x[2 * i] * down, x[2 * i + 1] * down);
+        reinterpret_cast<uint32_t*>(dst)[i] =
+            pack_f16x2(__uint_as_float(w[j][i] << 16) * down, __uint_as_float(w[j][i] & 0xFFFF0000u) * down);
     }
   }
   fence_proxy_async_smem();
@@ -213,7 +248,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
 
   bool ok = true;   // no wait of this thread has given up
   auto wait = [&](uint64_t* bar, int phase) {
-    if (ok && !mbar_wait_bounded(bar, phase & 1, AT_WAIT)) {
+    if (ok && !try_wait_ms(bar, phase & 1) && !wait_long(bar, phase & 1)) {
       ok = false;
       set_err(a.err, BRE_DEVERR_TIMEOUT);
     }
@@ -221,8 +256,8 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
   };
   auto warp_wait = [&](uint64_t* bar, int phase) { return ok = __all_sync(0xffffffffu, wait(bar, phase)); };
 
-  if (warp >= 8) {
-    if (warp == 8) {
+  if (warp >= W_MERGE) {
+    if (warp == W_MERGE) {
       // ---- merge: token 32 j + lane in slot j
       int pos[4], ptr[4] = {}, sq[4];
       uint32_t cur[4], run[4], starts[4];
@@ -268,6 +303,8 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
         if (key != 0xFFFFFFFFu) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
+            b.mask[j] = 0;
+            if (32 * j >= nt) continue;
             b.mask[j] = __ballot_sync(0xffffffffu, cur[j] == key);
             if (cur[j] == key) {
               top = max(top, pos[j]);
@@ -288,57 +325,68 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
         if (key == 0xFFFFFFFFu) break;
       }
     } else {
-      if (lane == 0) {
       // ---- MMA: kind::f16, FP32 sums, M = 128; second product with an MN-major B
       const uint32_t id_s = (1u << 4) | ((uint32_t)(KV_BLOCK >> 3) << 17) | ((128u >> 4) << 24);
       const uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
-      const uint32_t q0 = smem_u32(sm + M::q), k0 = smem_u32(sm + M::k), v0 = smem_u32(sm + M::v);
+      const uint64_t q0 = desc_k_major(smem_u32(sm + M::q)), k0 = desc_k_major(smem_u32(sm + M::k));
+      const uint64_t v0 = desc_mn_major(smem_u32(sm + M::v), PANEL);   // offsets count 16 bytes
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       auto pv = [&](int i) {
         const int st = i & 1;
-        if (!wait(&v_full[st], i >> 1) || !wait(&p_full[st], i >> 1)) return;
+        if (!warp_wait(&v_full[st], i >> 1) || !warp_wait(&p_full[st], i >> 1)) return;
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < KV_BLOCK / 16; ++kk)
-          mma_ts(tmem + 128, tmem + st * 64 + kk * 8, desc_mn_major(v0 + st * M::KV + kk * 2048, PANEL), id_o,
-                 i > 0 || kk > 0);
-        mma_commit(&v_empty[st]);
-        mma_commit(&o_done);
+          for (int kk = 0; kk < KV_BLOCK / 16; ++kk)
+            mma_ts(tm + 128, tm + st * 64 + kk * 8, v0 + ((st * M::KV + kk * 2048) >> 4), id_o, kk > 0 ? 1u : i > 0);
+          mma_commit(&v_empty[st]);
+          mma_commit(&o_done);
+        }
+        __syncwarp();
       };
-      int i = 0;
-      for (;; ++i) {
+#pragma unroll 1
+      for (int i = 0;; ++i) {
         const int st = i & 1;
-        if (!wait(&blk_full[i % AT_RING], i / AT_RING)) break;
+        if (!warp_wait(&blk_full[i % AT_RING], i / AT_RING)) break;
         const bool end = ring[i % AT_RING].page < 0;
-        mbar_arrive(&blk_empty[i % AT_RING]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&blk_empty[i % AT_RING]);
         if (!end) {
           // products into different accumulators may pass one another: the weights that lay in S's
           // columns must have been used
-          if (i > 1 && !wait(&o_done, i - 2)) break;
-          if (!wait(&k_full[st], i >> 1)) break;
+          if (i > 1 && !warp_wait(&o_done, i - 2)) break;
+          if (!warp_wait(&k_full[st], i >> 1)) break;
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + st * 64, desc_k_major(q0 + (kk / 4) * PANEL_Q + (kk % 4) * 32),
-                   desc_k_major(k0 + st * M::KV + (kk / 4) * PANEL + (kk % 4) * 32), id_s, kk > 0);
-          mma_commit(&s_full[st]);
-          mma_commit(&k_empty[st]);
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(tm + st * 64, q0 + (((kk / 4) * PANEL_Q + (kk % 4) * 32) >> 4),
+                     k0 + ((st * M::KV + (kk / 4) * PANEL + (kk % 4) * 32) >> 4), id_s, kk > 0);
+            mma_commit(&s_full[st]);
+            mma_commit(&k_empty[st]);
+          }
+          __syncwarp();
         }
         if (i > 0) pv(i - 1);
         if (end || !ok) break;
       }
       // every MMA has completed before tensor memory is given back
-      mma_commit(&drain);
-      mbar_wait_bounded(&drain, 0, AT_WAIT);
-      }
+      if (elect_one()) mma_commit(&drain);
       __syncwarp();
+      mbar_wait_bounded(&drain, 0, AT_WAIT);
     }
   } else if (warp >= 4) {
-    // ---- codes to FP16: 128 threads, 16 codes (one 16-byte load) at a time
+    // ---- codes to FP16: 128 threads for the keys, 128 for the values, 16 codes (a 16-byte load) at a time.
+    // A warp works on its own rows; one arrival a warp.
     constexpr int CH = D / 16, NL = KV_BLOCK * CH / 128;   // pieces a row, loads a thread
-    const int dt = tid - 128;
-    uint4 kr[NL], vr[NL];
-    int e2 = 0, ek = 0, ev = 0;   // key scales of tokens lane and lane + 32; scales of token dt
-    int page = 0, n = 0;  // of the block whose codes are loaded next
+    const bool values = warp >= 8;
+    const int dt = tid & 127;
+    uint64_t* const full = values ? v_full : k_full;
+    uint64_t* const empty = values ? v_empty : k_empty;
+    uint4 cur[NL], nxt[NL];
+    int e2 = 0, e2n = 0;     // key scales of tokens lane and lane + 32: this block's, the next one's
+    int ev = 0, evn = 0;     // value scale of token dt
+    int page = 0, n = 0;     // of the block that is loaded next
     const uint8_t* pg = nullptr;
     auto take = [&](int i) {
       if (!warp_wait(&blk_full[i % AT_RING], i / AT_RING)) {
@@ -351,70 +399,85 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       if (lane == 0) mbar_arrive(&blk_empty[i % AT_RING]);
       pg = a.pages + ((size_t)max(page, 0) * a.H + h) * kv_page_bytes(D);
     };
-    // of tokens that no row sees (they may never have been written) neither values nor scales are read
-    auto load_k = [&] {
+    // of tokens that no row sees (they may never have been written) neither codes nor scales are read
+    auto load = [&] {
+      const uint4* src = reinterpret_cast<const uint4*>(pg + (values ? KV_BLOCK * D : 0)) + dt;
+      const uint8_t* sc = pg + 2 * KV_BLOCK * D;
 #pragma unroll
-      for (int j = 0; j < NL; ++j) kr[j] = __ldg(reinterpret_cast<const uint4*>(pg) + dt + j * 128);
-      e2 = lane < n ? (int)__ldg(pg + 2 * KV_BLOCK * D + lane) : 0;
-      if (lane + 32 < n) e2 |= (int)__ldg(pg + 2 * KV_BLOCK * D + 32 + lane) << 8;
-      ek = dt < n ? (int)__ldg(pg + 2 * KV_BLOCK * D + dt % KV_BLOCK) : 0;
+      for (int j = 0; j < NL; ++j) nxt[j] = (dt + j * 128) / CH < n ? __ldg(src + j * 128) : make_uint4(0, 0, 0, 0);
+      e2n = lane < n ? (int)__ldg(sc + lane) : 0;
+      if (lane + 32 < n) e2n |= (int)__ldg(sc + 32 + lane) << 8;
+      if (values) evn = dt < n ? (int)__ldg(sc + KV_BLOCK + dt) : 127;
     };
-    auto load_v = [&] {
+    // where a thread puts its 16 values (token x0, channels 16 c ..; further loads are whole multiples of 8
+    // tokens on): two swizzled pieces of 16 bytes.  The lanes of odd panels start with the second piece, so that
+    // eight lanes meet all banks.
+    const int x0 = dt / CH, c = dt % CH;
+    const bool second = (c / 4) & 1;
+    const int p0 = (values ? M::v : M::k) + (c / 4) * PANEL + x0 * 128 + (((2 * (c % 4)) ^ (x0 & 7)) << 4);
+    unsigned char* const put0 = sm + (second ? p0 ^ 16 : p0);
+    unsigned char* const put1 = sm + (second ? p0 : p0 ^ 16);
+    auto shift = [&] {
 #pragma unroll
-      for (int j = 0; j < NL; ++j)
-        vr[j] = (dt + j * 128) / CH < n ? __ldg(reinterpret_cast<const uint4*>(pg + KV_BLOCK * D) + dt + j * 128)
-                                        : make_uint4(0, 0, 0, 0);
-      ev = dt < n ? (int)__ldg(pg + 2 * KV_BLOCK * D + KV_BLOCK + dt % KV_BLOCK) : 127;
+      for (int j = 0; j < NL; ++j) cur[j] = nxt[j];
+      e2 = e2n, ev = evn;
     };
-    // 16 values of token x, channels 16 c ..: two swizzled pieces of 16 bytes; the upper half of a quarter
-    // warp's lanes starts with its second piece, so that eight lanes meet all banks
-    auto put = [&](unsigned char* tile, int x, int c, const uint4& w, uint32_t f) {
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-      uint32_t o[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        o[2 * j] = mul_f16x2(e4m3x2_to_f16x2(u[j] & 0xFFFFu), f);
-        o[2 * j + 1] = mul_f16x2(e4m3x2_to_f16x2(u[j] >> 16), f);
-      }
-      unsigned char* row = tile + (c / 4) * PANEL + x * 128;
-      const int c0 = 2 * (c % 4), sw = x & 7;
-      const bool second = (c / 4) & 1;
-      const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-      *reinterpret_cast<uint4*>(row + (((c0 + (second ? 1 : 0)) ^ sw) << 4)) = second ? hi : lo;
-      *reinterpret_cast<uint4*>(row + (((c0 + (second ? 0 : 1)) ^ sw) << 4)) = second ? lo : hi;
-    };
+    int left = 0;   // blocks in registers
     take(0);
-    if (page >= 0) load_k(), load_v();
-    for (int i = 0; page >= 0; ++i) {
+    if (page >= 0) {
+      load();
+      shift();
+      left = 1;
+      take(1);
+      if (page >= 0) load(), left = 2;
+    }
+#pragma unroll 1
+    for (int i = 0; left > 0; ++i) {
       const int st = i & 1;
       // the block's largest key scale (a NaN row's does not count: its codes are zeros)
-      const int top = __reduce_max_sync(0xffffffffu, max((e2 & 255) == KV_NAN ? 0 : e2 & 255, (e2 >> 8) == KV_NAN ? 0 : e2 >> 8));
-      const bool nan_key = ek == KV_NAN;
-      if (!warp_wait(&k_empty[st], (i >> 1) + 1)) break;
-#pragma unroll
-      for (int j = 0; j < NL; ++j) {
-        const int x = (dt + j * 128) / CH, c = (dt + j * 128) % CH;
-        const int both = __shfl_sync(0xffffffffu, e2, x & 31);
-        const int d = max(top - (x < 32 ? both & 255 : both >> 8), 0);
-        const uint32_t f = d < 15 ? (uint32_t)(15 - d) << 10 : d < 25 ? 1u << (24 - d) : 0u;   // 2^-d in FP16
-        put(sm + M::k + st * M::KV, x, c, kr[j], f | f << 16);
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&k_full[st]);
-      take(i + 1);
-      if (page >= 0) load_k();
-      if (!warp_wait(&v_empty[st], (i >> 1) + 1)) break;   // and the softmax is done with the scales before
-      if (dt < KV_BLOCK) {
+      const int ea = e2 & 255, eb = e2 >> 8;
+      const int top = __reduce_max_sync(0xffffffffu, max(ea == KV_NAN ? 0 : ea, eb == KV_NAN ? 0 : eb));
+      // a free value stage also means that the softmax is done with the scales of two blocks before
+      if (!warp_wait(&empty[st], (i >> 1) + 1)) break;
+      if (values && dt < KV_BLOCK) {
         // a NaN row makes its token's logit NaN
-        ev_f[st][dt] = nan_key || ev == KV_NAN ? __int_as_float(0x7FC00000) : (float)(ev - 127);
+        const bool nan = (dt < 32 ? ea : eb) == KV_NAN || ev == KV_NAN;
+        ev_f[st][dt] = nan ? __int_as_float(0x7FC00000) : (float)(ev - 127);
         ev_inv[st][dt] = pow2f(127 - min(ev, 253));
         if (dt == 0) ek_top[st] = pow2f(max(top, 1) - 127);
       }
 #pragma unroll
-      for (int j = 0; j < NL; ++j) put(sm + M::v + st * M::KV, (dt + j * 128) / CH, (dt + j * 128) % CH, vr[j], 0x3C003C00u);
+      for (int j = 0; j < NL; ++j) {
+        const uint32_t u[4] = {second ? cur[j].z : cur[j].x, second ? cur[j].w : cur[j].y, second ? cur[j].x : cur[j].z,
+                               second ? cur[j].y : cur[j].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          o[2 * k] = e4m3x2_to_f16x2(u[k] & 0xFFFFu);
+          o[2 * k + 1] = e4m3x2_to_f16x2(u[k] >> 16);
+        }
+        if (!values) {
+          const int x = x0 + j * (128 / CH);
+          const int both = __shfl_sync(0xffffffffu, e2, x & 31);
+          const int d = max(top - (x < 32 ? both & 255 : both >> 8), 0);
+          const uint32_t f = d < 15 ? (uint32_t)(15 - d) << 10 : d < 25 ? 1u << (24 - d) : 0u;   // 2^-d
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = mul_f16x2(o[k], f | f << 16);
+        }
+        const int at = st * M::KV + j * (128 / CH) * 128;
+        *reinterpret_cast<uint4*>(put0 + at) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(put1 + at) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
       fence_proxy_async_smem();
-      mbar_arrive(&v_full[st]);
-      if (page >= 0) load_v();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
+      --left;
+      shift();
+      if (page >= 0) take(i + 2);
+      if (page >= 0) {
+        load();
+        ++left;
+      }
     }
   } else {
     // ---- softmax: row tid
@@ -437,28 +500,32 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       const int n = mine ? min(KV_BLOCK, pos - id * KV_BLOCK + 1) : 0;   // tokens that the row sees
       if (!warp_wait(&v_full[st], i >> 1) || !warp_wait(&s_full[st], i >> 1)) break;   // the scales, the products
       tc_fence_after();
-      uint32_t s[64];
-      tmem_ld32(lane_base + st * 64, s);
-      tmem_ld32(lane_base + st * 64 + 32, s + 32);
+      // two passes over S, 32 columns at a time (as a loop: see wait_long): the maximum, then the weights
       const float f = qf * ek_top[st];
       const uint64_t f2 = pack2(f, f);
-      tmem_wait_ld();
+      const bool whole = __all_sync(0xffffffffu, n == 0 || n == KV_BLOCK);
       float mx = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < KV_BLOCK; c += 32) {
+        uint32_t s[32];
+        tmem_ld32(lane_base + st * 64 + c, s);
+        tmem_wait_ld();
 #pragma unroll
-      for (int x = 0; x < 64; x += 4) {
-        const ulonglong2 ev = *reinterpret_cast<const ulonglong2*>(&ev_f[st][x]);
-        const float2 v0 = unpack2(fma2(pack2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), f2, ev.x));
-        const float2 v1 = unpack2(fma2(pack2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), f2, ev.y));
-        s[x] = __float_as_uint(v0.x), s[x + 1] = __float_as_uint(v0.y);
-        s[x + 2] = __float_as_uint(v1.x), s[x + 3] = __float_as_uint(v1.y);
+        for (int x = 0; x < 32; x += 4) {
+          const ulonglong2 ev = *reinterpret_cast<const ulonglong2*>(&ev_f[st][c + x]);
+          const float2 v0 = unpack2(fma2(pack2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), f2, ev.x));
+          const float2 v1 = unpack2(fma2(pack2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), f2, ev.y));
+          s[x] = __float_as_uint(v0.x), s[x + 1] = __float_as_uint(v0.y);
+          s[x + 2] = __float_as_uint(v1.x), s[x + 3] = __float_as_uint(v1.y);
+        }
+        if (!whole) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (c + x >= n) s[x] = __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 1])));
       }
-      if (!__all_sync(0xffffffffu, n == 0 || n == KV_BLOCK)) {
-#pragma unroll
-        for (int x = 0; x < 64; ++x)
-          if (x >= n) s[x] = __float_as_uint(-INFINITY);
-      }
-#pragma unroll
-      for (int x = 0; x < 64; x += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 1])));
       if (n == 0) mx = -INFINITY;
       if (m == -INFINITY) m = mx;   // nothing has been added for this row yet
       if (__any_sync(0xffffffffu, mx > m + AT_SLACK)) {
@@ -482,27 +549,35 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       const float base = m > -INFINITY ? m - P_SHIFT : 0.0f;
       const uint64_t nb2 = pack2(-base, -base);
       uint64_t add = 0;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t pk[16];
+#pragma unroll 1
+      for (int c = 0; c < KV_BLOCK; c += 32) {
+        uint32_t s[32], pk[16];
+        tmem_ld32(lane_base + st * 64 + c, s);
+        tmem_wait_ld();
 #pragma unroll
         for (int x = 0; x < 32; x += 4) {
-          const uint32_t* sx = s + hf * 32 + x;
-          const ulonglong2 iv = *reinterpret_cast<const ulonglong2*>(&ev_inv[st][hf * 32 + x]);
-          const float2 v0 = unpack2(add2(pack2(__uint_as_float(sx[0]), __uint_as_float(sx[1])), nb2));
-          const float2 v1 = unpack2(add2(pack2(__uint_as_float(sx[2]), __uint_as_float(sx[3])), nb2));
-          const float p0 = ex2(v0.x), p1 = ex2(v0.y), p2 = ex2(v1.x), p3 = ex2(v1.y);
+          const ulonglong2 ev = *reinterpret_cast<const ulonglong2*>(&ev_f[st][c + x]);
+          const ulonglong2 iv = *reinterpret_cast<const ulonglong2*>(&ev_inv[st][c + x]);
+          const float2 v0 = unpack2(add2(fma2(pack2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), f2, ev.x), nb2));
+          const float2 v1 =
+              unpack2(add2(fma2(pack2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), f2, ev.y), nb2));
+          float p0 = ex2(v0.x), p1 = ex2(v0.y), p2 = ex2(v1.x), p3 = ex2(v1.y);
+          if (!whole) {
+            p0 = c + x < n ? p0 : 0.0f, p1 = c + x + 1 < n ? p1 : 0.0f;
+            p2 = c + x + 2 < n ? p2 : 0.0f, p3 = c + x + 3 < n ? p3 : 0.0f;
+          }
           add = fma2(pack2(p0, p1), iv.x, fma2(pack2(p2, p3), iv.y, add));
           pk[x / 2] = n ? pack_f16x2(p0, p1) : 0u;
           pk[x / 2 + 1] = n ? pack_f16x2(p2, p3) : 0u;
         }
-        tmem_st16(lane_base + st * 64 + hf * 16, pk);
+        tmem_st16(lane_base + st * 64 + c / 2, pk);
       }
       const float2 sum = unpack2(add);
       if (n) l += sum.x + sum.y;
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&p_full[st]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[st]);
     }
     if (i > 0) warp_wait(&drain, 0);   // not o_done: the last two products with V may both be pending
     tc_fence_after();
@@ -530,7 +605,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == W_MMA) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(COLS) : "memory");
   }
