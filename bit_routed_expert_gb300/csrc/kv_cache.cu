@@ -5,111 +5,221 @@ namespace bre {
 
 namespace {
 
-// One warp per (token, head).  The warp whose token opens a run (the tokens in a row of one
-// block) stores the whole run and, for the keys, the block's channel-wise extremes.
-template <int D>
-__global__ void __launch_bounds__(128)
-    kv_append_kernel(uint8_t* pages, int8_t* bounds, int8_t* bexp, int H, KvTable tab, const uint16_t* __restrict__ k,
-                     const uint16_t* __restrict__ v, long long k_stride, long long v_stride,
-                     const int32_t* __restrict__ seq, const int32_t* __restrict__ pos, int T, int32_t* err) {
-  constexpr int PL = D / 32;   // channels a lane holds
-  pdl_wait();
-  const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int t0 = w / H, h = w % H;
-  if (t0 >= T) return;
-  const int s = __ldg(seq + t0), p0 = __ldg(pos + t0);
-  if (p0 < 0) return;
-  const int blk = p0 / KV_BLOCK;
-  auto in_run = [&](int t) {
-    const int p = __ldg(pos + t);
-    return __ldg(seq + t) == s && p >= 0 && p / KV_BLOCK == blk;
-  };
-  if (t0 > 0 && in_run(t0 - 1)) return;
-  const int page = kv_page(tab, s, blk, err);
-  if (page < 0) {
-    set_err(err, BRE_DEVERR_PAGE);   // a token to store needs a page
-    return;
+// A chunk of the call's tokens and one head per CTA.  The tokens in a row that belong to one block are
+// a run (padding entries among them do not end it); a run is stored by the CTA in whose chunk it starts, which sees all of its keys and so can
+// bring the block's bounds up to date without atomics.
+//
+// A lane holds eight channels, so D / 8 lanes hold a row and a warp two or four rows at a time: 16-byte loads,
+// 8-byte stores, a row's maximum by three or four shuffles.  Keys and values of four row groups are
+// loaded before the first is used.  A chunk of 64 tokens gives long calls whole blocks; with few tokens the
+// chunks shrink to one token and a call spreads over the GPU.
+constexpr int KA_WARPS = 4;
+
+// A row of eight channels a lane; LR lanes hold the row.
+template <int LR>
+struct RowCode {
+  uint2 codes;
+  int e;       // scale exponent
+  bool nan;
+  __device__ __forceinline__ explicit RowCode(const uint4& w) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t mx = 0;   // magnitudes of BF16 values compare like whole numbers
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx = __vmaxu2(mx, u[i] & 0x7FFF7FFFu);
+    mx = max(mx & 0xFFFFu, mx >> 16);
+#pragma unroll
+    for (int o = 1; o < LR; o *= 2) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    nan = mx > 0x7F80u;
+    e = row_exp(bf16_bits_to_f32(min(mx, 0x7F60u)));   // KV_MAX
+    const float down = pow2f(-e);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(u[i] << 16) * down;
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u) * down;
+    }
+    // (the conversion saturates what lies above KV_MAX)
+    codes = make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16, e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
+    if (nan) codes = make_uint2(0u, 0u);
   }
-  const size_t ph = (size_t)page * H + h;
-  uint8_t* pg = pages + ph * kv_page_bytes(D);
-  float hi[PL], lo[PL], amax = 0.0f;
-  for (int t = t0; t < T && in_run(t); ++t) {
-    const int slot = __ldg(pos + t) % KV_BLOCK;
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint16_t* row = kv ? v + t * v_stride : k + t * k_stride;
-      float x[PL], a = 0.0f;
-      bool nan = false;
-      for (int i = 0; i < PL; ++i) {
-        x[i] = kv_clamp(bf16_bits_to_f32(row[h * D + lane * PL + i]));
-        nan |= x[i] != x[i];
-        a = fmaxf(a, fabsf(x[i]));
+};
+
+template <int D>
+__global__ void __launch_bounds__(KA_WARPS * 32)
+    kv_append_kernel(uint8_t* __restrict__ pages, int8_t* __restrict__ bounds, int8_t* __restrict__ bexp, int H, KvTable tab,
+                     const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, long long k_stride, long long v_stride,
+                     const int32_t* __restrict__ seq, const int32_t* __restrict__ pos, int T, int chunk, int32_t* err) {
+  constexpr int LR = D / 8, RW = 32 / LR;       // lanes a row, rows a warp
+  constexpr int RC = RW * KA_WARPS, UN = 4;     // rows of the CTA at a time, of which UN steps are in flight
+  __shared__ float s_hi[KA_WARPS][D], s_lo[KA_WARPS][D], s_max[KA_WARPS];
+  __shared__ int s_end;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lr = lane % LR;
+  const int h = blockIdx.y, c0 = blockIdx.x * chunk, c1 = min(c0 + chunk, T);
+  for (int t = c0; t < c1;) {
+    const int s = __ldg(seq + t), p = __ldg(pos + t), blk = p / KV_BLOCK;
+    // this run's end: the first token of another block
+    __syncthreads();
+    if (tid == 0) s_end = T;
+    __syncthreads();
+    bool found = p < 0;
+    if (found && tid == 0) s_end = t + 1;
+    for (int i0 = t + 1; i0 < T && !found; i0 += KA_WARPS * 32) {
+      const int i = i0 + tid;
+      const int pi = i < T ? __ldg(pos + i) : -1;
+      const bool other = pi >= 0 && (__ldg(seq + i) != s || pi / KV_BLOCK != blk);
+      if (other) atomicMin(&s_end, i);
+      found = __syncthreads_or(other);
+    }
+    __syncthreads();
+    const int t0 = t, t1 = s_end;
+    t = t1;
+    if (p < 0) continue;
+    // a run that started in a chunk before belongs to it
+    int back = t0 - 1;
+    while (back >= 0 && __ldg(pos + back) < 0) --back;
+    if (back >= 0 && __ldg(seq + back) == s && __ldg(pos + back) / KV_BLOCK == blk) continue;
+    const int page = kv_page(tab, s, blk, tid == 0 ? err : nullptr);
+    if (page < 0) {
+      if (tid == 0) set_err(err, BRE_DEVERR_PAGE);   // a token to store needs a page
+      continue;
+    }
+    const size_t ph = (size_t)page * H + h;
+    uint8_t* pg = pages + ph * kv_page_bytes(D);
+    float hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
+    for (int r0 = t0 + warp * RW + lane / LR; r0 - lane / LR < t1; r0 += UN * RC) {
+      uint4 kw[UN], vw[UN];
+      int slot[UN];
+#pragma unroll
+      for (int j = 0; j < UN; ++j) {
+        const int r = r0 + j * RC;
+        const bool in = r < t1;
+        kw[j] = in ? __ldg(reinterpret_cast<const uint4*>(k + r * k_stride + h * D) + lr) : make_uint4(0, 0, 0, 0);
+        vw[j] = in ? __ldg(reinterpret_cast<const uint4*>(v + r * v_stride + h * D) + lr) : make_uint4(0, 0, 0, 0);
+        slot[j] = in ? __ldg(pos + r) : -1;
       }
-      for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-      nan = __any_sync(0xffffffffu, nan);
-      if (nan)
-        for (int i = 0; i < PL; ++i) x[i] = 0.0f;
-      const int e = row_exp(a);
-      uint8_t* dst = pg + kv * KV_BLOCK * D + slot * D + lane * PL;
-      for (int i = 0; i < PL; i += 2) {
-        const uint32_t c = e4m3x2(x[i] * pow2f(-e), x[i + 1] * pow2f(-e));
-        *reinterpret_cast<uint16_t*>(dst + i) = (uint16_t)c;
-        if (kv == 0) {
-          const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(c));
-          const float y[2] = {f.x * pow2f(e), f.y * pow2f(e)};
-          for (int j = 0; j < 2; ++j) {
-            hi[i + j] = t == t0 ? y[j] : fmaxf(hi[i + j], y[j]);
-            lo[i + j] = t == t0 ? y[j] : fminf(lo[i + j], y[j]);
-            amax = fmaxf(amax, fabsf(y[j]));
-          }
+#pragma unroll
+      for (int j = 0; j < UN; ++j) {
+        const RowCode<LR> kc(kw[j]), vc(vw[j]);
+        if (slot[j] < 0) continue;
+        slot[j] %= KV_BLOCK;
+        *reinterpret_cast<uint2*>(pg + slot[j] * D + lr * 8) = kc.codes;
+        *reinterpret_cast<uint2*>(pg + KV_BLOCK * D + slot[j] * D + lr * 8) = vc.codes;
+        if (lr == 0) {
+          pg[2 * KV_BLOCK * D + slot[j]] = (uint8_t)(kc.nan ? KV_NAN : kc.e + 127);
+          pg[2 * KV_BLOCK * D + KV_BLOCK + slot[j]] = (uint8_t)(vc.nan ? KV_NAN : vc.e + 127);
+        }
+        const float up = pow2f(kc.e);
+        const uint32_t c[2] = {kc.codes.x, kc.codes.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(c[i / 2] >> (16 * (i & 1)) & 0xFFFFu));
+          hi[2 * i] = fmaxf(hi[2 * i], f.x * up), hi[2 * i + 1] = fmaxf(hi[2 * i + 1], f.y * up);
+          lo[2 * i] = fminf(lo[2 * i], f.x * up), lo[2 * i + 1] = fminf(lo[2 * i + 1], f.y * up);
         }
       }
-      if (lane == 0) pg[2 * KV_BLOCK * D + kv * KV_BLOCK + slot] = (uint8_t)(nan ? KV_NAN : e + 127);
     }
-  }
-  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  int e = bound_exp_of(amax);
-  int8_t* bd = bounds + ph * 2 * D + lane * PL;
-  if (p0 % KV_BLOCK) {   // the block had begun before this call
-    const int oe = bexp[ph];
-    for (int i = 0; i < PL; ++i) {
-      hi[i] = fmaxf(hi[i], bd[i] * pow2f(oe));
-      lo[i] = fminf(lo[i], bd[D + i] * pow2f(oe));
+    // the warps' extremes, then the block's bounds
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int o = LR; o < 32; o *= 2) {
+        hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+        lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+      }
+    if (lane < LR)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s_hi[warp][lr * 8 + i] = hi[i], s_lo[warp][lr * 8 + i] = lo[i];
+    __syncthreads();
+    constexpr int ND = D / 128 ? D / 128 : 1;   // channels a thread
+    float ch = -INFINITY, cl = INFINITY, amax = 0.0f;
+    if (tid < D) {
+#pragma unroll
+      for (int w = 0; w < KA_WARPS; ++w) ch = fmaxf(ch, s_hi[w][tid]), cl = fminf(cl, s_lo[w][tid]);
+      amax = fmaxf(fabsf(ch), fabsf(cl));
     }
-    e = max(e, oe);
+    static_assert(ND == 1 && D <= KA_WARPS * 32, "a thread a channel");
+#pragma unroll
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (lane == 0) s_max[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < KA_WARPS; ++w) amax = fmaxf(amax, s_max[w]);
+    int e = bound_exp_of(amax);
+    int8_t* bd = bounds + ph * 2 * D + tid;
+    if (p % KV_BLOCK) {   // the block had begun before this call
+      const int oe = bexp[ph];
+      if (tid < D) ch = fmaxf(ch, bd[0] * pow2f(oe)), cl = fminf(cl, bd[D] * pow2f(oe));
+      e = max(e, oe);
+    }
+    __syncthreads();   // everyone has the old exponent
+    if (tid < D) {
+      bd[0] = (int8_t)ceilf(ch * pow2f(-e));
+      bd[D] = (int8_t)floorf(cl * pow2f(-e));
+    }
+    if (tid == 0) bexp[ph] = (int8_t)e;
   }
-  __syncwarp();
-  for (int i = 0; i < PL; ++i) {
-    bd[i] = (int8_t)ceilf(hi[i] * pow2f(-e));
-    bd[D + i] = (int8_t)floorf(lo[i] * pow2f(-e));
-  }
-  if (lane == 0) bexp[ph] = (int8_t)e;
 }
 
-// One warp per (token, head): codes times the row's scale, exact in BF16.
+// Codes times the row's scale, exact in BF16.  A lane takes 16 codes: D / 16 lanes a row; four rows' keys and
+// values of a warp in flight.
 template <int D>
 __global__ void __launch_bounds__(128)
     kv_read_kernel(const uint8_t* __restrict__ pages, int H, KvTable tab, const int32_t* __restrict__ seq,
                    const int32_t* __restrict__ pos, int T, uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                    int32_t* err) {
-  constexpr int PL = D / 32;
+  constexpr int LR = D / 16, UN = 4;
   pdl_wait();
-  const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int t = w / H, h = w % H;
-  if (t >= T) return;
-  const int p = __ldg(pos + t);
-  const int page = p < 0 ? -1 : kv_page(tab, __ldg(seq + t), p / KV_BLOCK, err);
-  if (p >= 0 && page < 0) set_err(err, BRE_DEVERR_PAGE);
-  const uint8_t* pg = pages + ((size_t)max(page, 0) * H + h) * kv_page_bytes(D);
-  for (int kv = 0; kv < 2; ++kv) {
-    uint16_t* out = kv ? v : k;
-    if (!out) continue;
-    const int slot = p % KV_BLOCK;
-    for (int i = 0; i < PL; ++i) {
-      float f = 0.0f;
-      if (page >= 0)
-        f = f16x2_to_f32x2(e4m3x2_to_f16x2(pg[kv * KV_BLOCK * D + slot * D + lane * PL + i])).x *
-            pow2f((int)pg[2 * KV_BLOCK * D + kv * KV_BLOCK + slot] - 127);
-      out[((size_t)t * H + h) * D + lane * PL + i] = (uint16_t)f32_to_bf16_rne(f);
+  pdl_launch_dependents();
+  // rows run over tokens first: the tokens of a block follow one another in a head's share of its page
+  const long long row0 = ((long long)blockIdx.x * 128 + threadIdx.x) / LR;
+  const int lr = threadIdx.x % LR, h = blockIdx.y;
+  const long long step = (long long)gridDim.x * (128 / LR);
+  for (long long r0 = row0; r0 < T; r0 += UN * step) {
+    int page[UN], slot[UN];
+#pragma unroll
+    for (int j = 0; j < UN; ++j) {
+      const long long t = r0 + j * step;
+      const int p = t < T ? __ldg(pos + t) : -1;
+      page[j] = p < 0 ? -1 : kv_page(tab, __ldg(seq + t), p / KV_BLOCK, err);
+      if (p >= 0 && page[j] < 0) set_err(err, BRE_DEVERR_PAGE);
+      slot[j] = p % KV_BLOCK;
+    }
+    uint4 kc[UN], vc[UN];
+    int ke[UN], ve[UN];
+#pragma unroll
+    for (int j = 0; j < UN; ++j) {
+      const uint8_t* pg = pages + ((size_t)max(page[j], 0) * H + h) * kv_page_bytes(D);
+      const bool in = page[j] >= 0;
+      kc[j] = in && k ? __ldg(reinterpret_cast<const uint4*>(pg + slot[j] * D) + lr) : make_uint4(0, 0, 0, 0);
+      vc[j] = in && v ? __ldg(reinterpret_cast<const uint4*>(pg + KV_BLOCK * D + slot[j] * D) + lr) : make_uint4(0, 0, 0, 0);
+      ke[j] = in ? (int)__ldg(pg + 2 * KV_BLOCK * D + slot[j]) : 127;
+      ve[j] = in ? (int)__ldg(pg + 2 * KV_BLOCK * D + KV_BLOCK + slot[j]) : 127;
+    }
+#pragma unroll
+    for (int j = 0; j < UN; ++j) {
+      const long long t = r0 + j * step;
+      if (t >= T) break;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint16_t* out = kv ? v : k;
+        if (!out) continue;
+        const uint4 c = kv ? vc[j] : kc[j];
+        const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+        const float f = pow2f((kv ? ve[j] : ke[j]) - 127);   // infinite for a NaN row, whose codes are zeros
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2(u[i] & 0xFFFFu)), b = f16x2_to_f32x2(e4m3x2_to_f16x2(u[i] >> 16));
+          o[2 * i] = pack_bf16x2(a.x * f, a.y * f), o[2 * i + 1] = pack_bf16x2(b.x * f, b.y * f);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)t * H + h) * D) + 2 * lr;
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
     }
   }
 }
@@ -121,9 +231,12 @@ cudaError_t launch_kv_append(const bre_kv_cache* c, const KvTokens& tk, const ui
   const int H = c->n_kv_heads;
   const KvTable tab{tk.table, tk.B, tk.N, c->n_pages};
   auto kern = c->head_dim == 128 ? kv_append_kernel<128> : kv_append_kernel<64>;
-  return launch_k(kern, dim3((unsigned)(((long long)tk.T * H + 3) / 4)), dim3(128), 0, s,
+  // tokens a CTA: whole blocks, as long as that leaves four CTAs to an SM
+  int chunk = KV_BLOCK;
+  while (chunk > 1 && (long long)tk.T * H < 4LL * device_sm_count() * chunk) chunk /= 2;
+  return launch_k(kern, dim3((unsigned)((tk.T + chunk - 1) / chunk), (unsigned)H), dim3(KA_WARPS * 32), 0, s,
                   static_cast<uint8_t*>(c->pages), c->bounds, c->bound_exp, H, tab, k, v, k_stride, v_stride, tk.seq,
-                  tk.pos, tk.T, err);
+                  tk.pos, tk.T, chunk, err);
 }
 
 cudaError_t launch_kv_read(const bre_kv_cache* c, const KvTokens& tk, uint16_t* k, uint16_t* v, int32_t* err,
@@ -131,7 +244,10 @@ cudaError_t launch_kv_read(const bre_kv_cache* c, const KvTokens& tk, uint16_t* 
   const int H = c->n_kv_heads;
   const KvTable tab{tk.table, tk.B, tk.N, c->n_pages};
   auto kern = c->head_dim == 128 ? kv_read_kernel<128> : kv_read_kernel<64>;
-  return launch_k(kern, dim3((unsigned)(((long long)tk.T * H + 3) / 4)), dim3(128), 0, s,
+  // 16 codes a thread; beyond 16 CTAs to an SM they go on to further rows
+  const long long ctas = ((long long)tk.T * (c->head_dim / 16) + 127) / 128;
+  const long long most = (16LL * device_sm_count() + H - 1) / H;
+  return launch_k(kern, dim3((unsigned)(ctas < most ? ctas : most), (unsigned)H), dim3(128), 0, s,
                   static_cast<const uint8_t*>(c->pages), H, tab, tk.seq, tk.pos, tk.T, k, v, err);
 }
 

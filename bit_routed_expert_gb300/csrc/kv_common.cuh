@@ -59,6 +59,12 @@ __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
   return make_float2(f16_bits_to_f32(h & 0xFFFFu), f16_bits_to_f32(h >> 16));
 }
 
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Thread-block clusters and distributed shared memory.
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");

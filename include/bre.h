@@ -321,8 +321,8 @@ typedef struct {
  * with the bounds that were there.  A position written again widens them only: they stay bounds.
  *   k, v: row t starts t * stride elements after the base and holds [n_kv_heads][D]; bases 16-byte
  *   aligned, strides multiples of 8.
- * The call's tokens of one block follow one another in the list, and no page is written for two
- * sequences.  A token to be stored whose block has no page sets BRE_DEVERR_PAGE. */
+ * The call's tokens of one block follow one another in the list (but for padding entries), and no page
+ * is written for two sequences.  A token to be stored whose block has no page sets BRE_DEVERR_PAGE. */
 bre_status kv_append(const bre_kv_cache *cache, const void *k_bf16, const void *v_bf16, int64_t k_stride,
                      int64_t v_stride, const int32_t *seq, const int32_t *pos, int T, const int32_t *table, int B,
                      int N, int32_t *dev_err, bre_stream_t stream);
