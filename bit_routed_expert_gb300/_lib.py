@@ -10,6 +10,7 @@ import torch
 from . import build as _build
 
 _lib = None
+_kv = None
 
 BRE_OK, BRE_ERR_ARG, BRE_ERR_UNSUPPORTED, BRE_ERR_CUDA, BRE_ERR_WORKSPACE = range(5)
 BRE_DEVERR_EXPERT_ID, BRE_DEVERR_ROW_ID, BRE_DEVERR_TIMEOUT, BRE_DEVERR_PAGE = 1, 2, 4, 8
@@ -80,6 +81,21 @@ def load(build_if_missing: bool = True):
             f.argtypes = args
         _lib = L
     return _lib
+
+
+def load_kv():
+    """The binding of the kv_* calls (kv_binding.cpp); raises if it is missing and cannot be built."""
+    global _kv
+    if _kv is None:
+        import importlib.util
+        load()
+        if not os.path.exists(_build.BINDING):
+            _build.build()
+        spec = importlib.util.spec_from_file_location("_kv", _build.BINDING)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        _kv = m
+    return _kv
 
 
 def check(rc: int, what: str):

@@ -261,10 +261,11 @@ class KvCache:
             raise ValueError("pages, bounds and bound_exp do not belong together")
         if p.dtype is not torch.uint8 or b.dtype is not torch.int8 or e.dtype is not torch.int8:
             raise ValueError("pages must be uint8, bounds and bound_exp int8")
-        _dev(p, "pages"), _dev(b, "bounds"), _dev(e, "bound_exp")
+        if not (p.is_cuda and b.is_cuda and e.is_cuda and p.is_contiguous() and b.is_contiguous() and e.is_contiguous()):
+            raise ValueError("pages, bounds and bound_exp must be contiguous CUDA tensors")
         self.n_pages, self.n_kv_heads, self.head_dim = n, H, D
         self._struct = BreKvCache(p.data_ptr(), b.data_ptr(), e.data_ptr(), n, H, D)
-        self._ref = C.byref(self._struct)
+        self._at = C.addressof(self._struct)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, device) -> "KvCache":
@@ -274,69 +275,22 @@ class KvCache:
                    torch.empty((n_pages, n_kv_heads), dtype=torch.int8, device=device))
 
 
-# The kv_* calls are made once or more a layer for every decoded token, so their marshalling is kept
-# to a few microseconds: plain integers for pointers, one condition for what is usually right (and
-# the reason looked for only where it is not), the raw current stream.
-def _rows(t: torch.Tensor, name: str, T: int, heads: int | None, D: int) -> int:
-    """Row stride (elements) of [T, heads, D] BF16 rows, which may be a slice of wider rows."""
-    n, h, d = t.shape
-    if n != T or d != D or (heads is not None and h != heads):
-        raise ValueError(f"{name} must be [{T}, {'heads' if heads is None else heads}, {D}], got {tuple(t.shape)}")
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != D and h > 1):
-        raise ValueError(f"{name}: a token's heads must follow one another without gaps")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype is not torch.bfloat16 and (t.element_size() != 2 or t.dtype is torch.float16):
-        raise ValueError(f"{name} must be bfloat16 (or its 16-bit patterns)")
-    return s0 if T > 1 else (h * D + 7) // 8 * 8
-
-
-def _like(t: torch.Tensor, name: str, dtype, shape) -> torch.Tensor:
-    if t.shape != shape or t.dtype is not dtype or not (t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)}, got {t.dtype} "
-                         f"{list(t.shape)} on {t.device}")
-    return t
-
-
-def _kv_tokens(seq, pos, table):
-    T, = seq.shape
-    B, N = table.shape
-    i32 = torch.int32
-    _like(seq, "seq", i32, (T,)), _like(pos, "pos", i32, (T,)), _like(table, "table", i32, (B, N))
-    return T, B, N
-
-
-def _stream(stream, t: torch.Tensor) -> int:
-    """Raw handle of `stream`, or of the current stream of t's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def kv_append(cache: KvCache, k, v, seq, pos, table, dev_err=None, stream=None):
     """Quantise and store the keys and values ([T, n_kv_heads, D] BF16, possibly slices of a fused
     projection's rows) of tokens seq[t], pos[t] (int32 [T]) and refresh the bounds of their blocks;
     table int32 [B, N] holds the page of each block of 64 positions of each sequence."""
-    T, B, N = _kv_tokens(seq, pos, table)
-    H, D = cache.n_kv_heads, cache.head_dim
-    ks, vs = _rows(k, "k", T, H, D), _rows(v, "v", T, H, D)
-    rc = _lib.load().kv_append(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, seq.data_ptr(), pos.data_ptr(), T,
-                               table.data_ptr(), B, N, _addr(dev_err), _stream(stream, seq))
+    rc = _lib.load_kv().append(cache._at, k, v, seq, pos, table, dev_err, _raw(stream))
     if rc:
         check(rc, "kv_append")
 
 
 def kv_read(cache: KvCache, seq, pos, table, k_out=None, v_out=None, dev_err=None, stream=None):
     """The stored keys and values of tokens seq[t], pos[t]: two BF16 tensors [T, n_kv_heads, D]."""
-    T, B, N = _kv_tokens(seq, pos, table)
-    shape, bf16 = (T, cache.n_kv_heads, cache.head_dim), torch.bfloat16
-    k_out = seq.new_empty(shape, dtype=bf16) if k_out is None else _like(k_out, "k_out", bf16, shape)
-    v_out = seq.new_empty(shape, dtype=bf16) if v_out is None else _like(v_out, "v_out", bf16, shape)
-    rc = _lib.load().kv_read(cache._ref, seq.data_ptr(), pos.data_ptr(), T, table.data_ptr(), B, N, k_out.data_ptr(),
-                             v_out.data_ptr(), _addr(dev_err), _stream(stream, seq))
+    rc, k_out, v_out = _lib.load_kv().read(cache._at, seq, pos, table, k_out, v_out, dev_err, _raw(stream))
     if rc:
         check(rc, "kv_read")
     return k_out, v_out
@@ -351,19 +305,8 @@ def kv_select(q, cache: KvCache, seq, pos, table, k: int, n_sink: int = 1, n_loc
     """For each token and kv head the k blocks to attend to: the first n_sink, the last n_local, and
     the best-scored others.  q [T, n_heads, D] BF16.  Returns (ids int32 [T, n_kv_heads, k], ascending,
     then -1; scores float32, then 0)."""
-    L = _lib.load()
-    T, B, N = _kv_tokens(seq, pos, table)
-    Hq, H, D = q.shape[1], cache.n_kv_heads, cache.head_dim
-    qs = _rows(q, "q", T, None, D)
-    if ws is None:
-        ws = seq.new_zeros(L.kv_select_workspace(T, Hq, H, D, B, N, k), dtype=torch.uint8)
-    shape = (T, H, k)
-    ids = seq.new_empty(shape) if ids is None else _like(ids, "ids", torch.int32, shape)
-    scores = (seq.new_empty(shape, dtype=torch.float32) if scores is None
-              else _like(scores, "scores", torch.float32, shape))
-    rc = L.kv_select(cache._ref, q.data_ptr(), qs, Hq, seq.data_ptr(), pos.data_ptr(), T, table.data_ptr(), B, N, k,
-                     n_sink, n_local, ids.data_ptr(), scores.data_ptr(), ws.data_ptr(), ws.numel(), _addr(dev_err),
-                     _stream(stream, seq))
+    rc, ids, scores = _lib.load_kv().select(cache._at, q, seq, pos, table, k, n_sink, n_local, ws, ids, scores, dev_err,
+                                            _raw(stream))
     if rc:
         check(rc, "kv_select")
     return ids, scores
@@ -378,21 +321,9 @@ def kv_attend(q, cache: KvCache, seq, pos, table, ids, scale: float | None = Non
     """Attention of q [T, n_heads, D] (BF16) over the blocks ids [T, n_kv_heads, k] lists, up to each
     token's own position; scale defaults to 1/sqrt(D).  Returns (out BF16 [T, n_heads, D], lse float32
     [T, n_heads]); rows that see nothing are 0 and -inf."""
-    L = _lib.load()
-    T, B, N = _kv_tokens(seq, pos, table)
-    Hq, H, D = q.shape[1], cache.n_kv_heads, cache.head_dim
-    qs = _rows(q, "q", T, None, D)
-    k = ids.shape[2]
-    _like(ids, "ids", torch.int32, (T, H, k))
-    if ws is None:
-        ws = seq.new_zeros(L.kv_attend_workspace(T, Hq, H, D, B, k), dtype=torch.uint8)
-    out = (seq.new_empty((T, Hq, D), dtype=torch.bfloat16) if out is None
-           else _like(out, "out", torch.bfloat16, (T, Hq, D)))
-    lse = (seq.new_empty((T, Hq), dtype=torch.float32) if lse is None
-           else _like(lse, "lse", torch.float32, (T, Hq)))
-    rc = L.kv_attend(cache._ref, q.data_ptr(), qs, Hq, seq.data_ptr(), pos.data_ptr(), T, table.data_ptr(), B, N,
-                     ids.data_ptr(), k, D ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(),
-                     ws.data_ptr(), ws.numel(), _addr(dev_err), _stream(stream, seq))
+    rc, out, lse = _lib.load_kv().attend(cache._at, q, seq, pos, table, ids,
+                                         cache.head_dim ** -0.5 if scale is None else scale, ws, out, lse, dev_err,
+                                         _raw(stream))
     if rc:
         check(rc, "kv_attend")
     return out, lse

@@ -1,4 +1,5 @@
-"""Build libbre.so (CUDA, sm_103a) in-tree with nvcc; translation units compile in parallel."""
+"""Build libbre.so (CUDA, sm_103a) in-tree with nvcc and _kv.so (the Python face of its kv_* calls, a C++ file
+against PyTorch's headers) with g++; translation units compile in parallel."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -12,6 +13,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libbre.so")
+BINDING = os.path.join(OUT_DIR, "_kv.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]
@@ -29,13 +31,38 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         [os.path.join(ROOT, "include", "bre.h"), __file__]
+
+
+def _compile_binding(obj: str) -> None:
+    import sysconfig
+
+    from torch.utils import cpp_extension
+    inc = [f"-I{p}" for p in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+                              os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), os.path.join(ROOT, "include"))]
+    import torch
+    r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+                        *inc, "-c", os.path.join(CSRC, "kv_binding.cpp"), "-o", obj], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on kv_binding.cpp:\n{r.stderr}")
+
+
+def _link_binding(obj: str) -> None:
+    from torch.utils import cpp_extension
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    libs = [a for p in cpp_extension.library_paths() for a in (f"-L{p}", f"-Wl,-rpath,{p}")]
+    r = subprocess.run(["g++", "-shared", "-o", tmp, obj, f"-L{OUT_DIR}", "-l:libbre.so", "-Wl,-rpath,$ORIGIN", *libs,
+                        "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _kv.so failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= max(os.path.getmtime(p) for p in _deps()):
+    newest = max(os.path.getmtime(p) for p in _deps())
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING)):
         return LIB
     cc = nvcc()
     objs = []
@@ -51,12 +78,16 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        bobj = os.path.join(OUT_DIR, "kv_binding.cpp.o")
+        binding = ex.submit(_compile_binding, bobj)
         objs = list(ex.map(compile_one, _sources()))
+        binding.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(bobj)
     return LIB
 
 

@@ -1,0 +1,227 @@
+// Python face of the kv_* calls.  They are made once or more a layer for every decoded token, where ctypes and
+// checks in Python cost more than the kernels (20 us a call against 5): here a call's arguments are
+// checked and passed on in about a microsecond, and outputs come from the caching allocator directly.
+// The functions take their arguments by position (api.py names and documents them); a wrong argument
+// raises ValueError, the library's status is returned as a number for api.py to raise.
+#include <Python.h>
+
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <initializer_list>
+#include <optional>
+#include <stdexcept>
+#include <string>
+#include <utility>
+
+#include "bre.h"
+
+namespace {
+
+using at::Tensor;
+
+[[noreturn]] void refuse(const std::string& what) { throw std::invalid_argument(what); }
+
+const Tensor& tensor(PyObject* o, const char* name) {
+  if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a tensor");
+  return THPVariable_Unpack(o);
+}
+
+std::string said(std::initializer_list<int64_t> shape) {
+  std::string s = "[";
+  for (int64_t d : shape) s += (s.size() > 1 ? ", " : "") + std::to_string(d);
+  return s + "]";
+}
+
+// A contiguous CUDA tensor of this type and shape.
+template <typename P = void>
+P* like(PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) {
+  const Tensor& t = tensor(o, name);
+  if (t.scalar_type() != type || t.sizes() != at::IntArrayRef(shape) || !t.is_cuda() || !t.is_contiguous())
+    refuse(std::string(name) + " must be a contiguous " + c10::toString(type) + " CUDA tensor " + said(shape));
+  return static_cast<P*>(t.data_ptr());
+}
+
+// Row stride (elements) of [T, heads, D] BF16 rows (or their 16-bit patterns), which may be a slice of wider
+// rows; heads < 0: any number, returned in *n_heads.
+const void* rows(PyObject* o, const char* name, int64_t T, int64_t heads, int64_t D, int64_t* stride, int* n_heads = nullptr) {
+  const Tensor& t = tensor(o, name);
+  if (t.dim() != 3 || t.size(0) != T || t.size(2) != D || (heads >= 0 && t.size(1) != heads))
+    refuse(std::string(name) + " must be " + said({T, heads, D}));
+  if (t.stride(2) != 1 || (t.size(1) > 1 && t.stride(1) != D))
+    refuse(std::string(name) + ": a token's heads must follow one another without gaps");
+  if (!t.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
+  if (t.element_size() != 2 || t.scalar_type() == at::kHalf) refuse(std::string(name) + " must be bfloat16");
+  *stride = T > 1 ? t.stride(0) : (t.size(1) * D + 7) / 8 * 8;
+  if (n_heads) *n_heads = (int)t.size(1);
+  return t.data_ptr();
+}
+
+// An owned reference.
+struct Ref {
+  PyObject* o;
+  explicit Ref(PyObject* p) : o(p) {}
+  Ref(Ref&& r) : o(r.o) { r.o = nullptr; }
+  ~Ref() { Py_XDECREF(o); }
+  void* data() const { return THPVariable_Unpack(o).data_ptr(); }
+};
+
+// The tokens of a call, the device and the stream.
+struct Call {
+  const bre_kv_cache* c;
+  const int32_t *seq, *pos, *table;
+  int T, B, N;
+  c10::Device device{c10::kCUDA, 0};
+  bre_stream_t stream;
+  int32_t* err;
+
+  Call(PyObject* cache, PyObject* seq_o, PyObject* pos_o, PyObject* table_o, PyObject* err_o, PyObject* stream_o) {
+    c = static_cast<const bre_kv_cache*>(PyLong_AsVoidPtr(cache));
+    if (!c) refuse("not a cache");
+    const Tensor& s = tensor(seq_o, "seq");
+    const Tensor& t = tensor(table_o, "table");
+    if (s.dim() != 1 || t.dim() != 2) refuse("seq must be [T] and table [B, N]");
+    T = (int)s.size(0), B = (int)t.size(0), N = (int)t.size(1);
+    seq = like<int32_t>(seq_o, "seq", at::kInt, {T});
+    pos = like<int32_t>(pos_o, "pos", at::kInt, {T});
+    table = like<int32_t>(table_o, "table", at::kInt, {B, N});
+    device = s.device();
+    err = err_o == Py_None ? nullptr : like<int32_t>(err_o, "dev_err", at::kInt, {1});
+    stream = reinterpret_cast<bre_stream_t>(stream_o == Py_None
+                                                ? (void*)c10::cuda::getCurrentCUDAStream(device.index()).stream()
+                                                : PyLong_AsVoidPtr(stream_o));
+  }
+  // The caller's output, or a new one.
+  Ref output(PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) const {
+    if (o == Py_None)
+      return Ref(THPVariable_Wrap(at::detail::empty_cuda(at::IntArrayRef(shape), type, device, std::nullopt)));
+    like(o, name, type, shape);
+    Py_INCREF(o);
+    return Ref(o);
+  }
+};
+
+// The caller's workspace (None where the call needs none).
+struct Workspace {
+  void* p = nullptr;
+  size_t n = 0;
+  Workspace(PyObject* o) {
+    if (o == Py_None) return;
+    const Tensor& t = tensor(o, "ws");
+    if (!t.is_cuda() || !t.is_contiguous() || t.scalar_type() != at::kByte) refuse("ws must be a contiguous uint8 CUDA tensor");
+    p = t.data_ptr();
+    n = (size_t)t.numel();
+  }
+};
+
+int integer(PyObject* o) {
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse("not a whole number");
+  }
+  return (int)v;
+}
+
+// (status, first output, second output)
+PyObject* answer(bre_status st, Ref& a, Ref& b) {
+  PyObject* r = PyTuple_New(3);
+  if (!r) throw std::bad_alloc();
+  PyTuple_SET_ITEM(r, 0, PyLong_FromLong(st));
+  PyTuple_SET_ITEM(r, 1, std::exchange(a.o, nullptr));
+  PyTuple_SET_ITEM(r, 2, std::exchange(b.o, nullptr));
+  return r;
+}
+
+template <typename F>
+PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
+  try {
+    if (given != wanted) refuse("wrong number of arguments");
+    return f();
+  } catch (const std::invalid_argument& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {   // cache k v seq pos table dev_err stream
+  return guarded(n, 8, [&] {
+    const Call call(a[0], a[3], a[4], a[5], a[6], a[7]);
+    int64_t ks, vs;
+    const void* k = rows(a[1], "k", call.T, call.c->n_kv_heads, call.c->head_dim, &ks);
+    const void* v = rows(a[2], "v", call.T, call.c->n_kv_heads, call.c->head_dim, &vs);
+    return PyLong_FromLong(kv_append(call.c, k, v, ks, vs, call.seq, call.pos, call.T, call.table, call.B, call.N, call.err,
+                                     call.stream));
+  });
+}
+
+PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {   // cache seq pos table k_out v_out dev_err stream
+  return guarded(n, 8, [&] {
+    const Call call(a[0], a[1], a[2], a[3], a[6], a[7]);
+    Ref k = call.output(a[4], "k_out", at::kBFloat16, {call.T, call.c->n_kv_heads, call.c->head_dim});
+    Ref v = call.output(a[5], "v_out", at::kBFloat16, {call.T, call.c->n_kv_heads, call.c->head_dim});
+    const bre_status st =
+        kv_read(call.c, call.seq, call.pos, call.T, call.table, call.B, call.N, k.data(), v.data(), call.err, call.stream);
+    return answer(st, k, v);
+  });
+}
+
+// cache q seq pos table k n_sink n_local ws ids scores dev_err stream
+PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&] {
+    const Call call(a[0], a[2], a[3], a[4], a[11], a[12]);
+    const int H = call.c->n_kv_heads, k = integer(a[5]), sink = integer(a[6]), local = integer(a[7]);
+    if (k < 0) refuse("k must not be negative");
+    int64_t qs;
+    int Hq;
+    const void* q = rows(a[1], "q", call.T, -1, call.c->head_dim, &qs, &Hq);
+    const Workspace ws(a[8]);
+    Ref ids = call.output(a[9], "ids", at::kInt, {call.T, H, k});
+    Ref sc = call.output(a[10], "scores", at::kFloat, {call.T, H, k});
+    const bre_status st = kv_select(call.c, q, qs, Hq, call.seq, call.pos, call.T, call.table, call.B, call.N, k, sink, local,
+                                    static_cast<int32_t*>(ids.data()), static_cast<float*>(sc.data()), ws.p, ws.n, call.err,
+                                    call.stream);
+    return answer(st, ids, sc);
+  });
+}
+
+// cache q seq pos table ids scale ws out lse dev_err stream
+PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&] {
+    const Call call(a[0], a[2], a[3], a[4], a[10], a[11]);
+    const int H = call.c->n_kv_heads, D = call.c->head_dim;
+    int64_t qs;
+    int Hq;
+    const void* q = rows(a[1], "q", call.T, -1, D, &qs, &Hq);
+    const Tensor& id = tensor(a[5], "ids");
+    if (id.dim() != 3) refuse("ids must be [T, n_kv_heads, k]");
+    const int k = (int)id.size(2);
+    const int32_t* ids = like<int32_t>(a[5], "ids", at::kInt, {call.T, H, k});
+    const double scale = PyFloat_AsDouble(a[6]);
+    if (scale == -1.0 && PyErr_Occurred()) {
+      PyErr_Clear();
+      refuse("scale must be a number");
+    }
+    const Workspace ws(a[7]);
+    Ref out = call.output(a[8], "out", at::kBFloat16, {call.T, Hq, D});
+    Ref lse = call.output(a[9], "lse", at::kFloat, {call.T, Hq});
+    const bre_status st = kv_attend(call.c, q, qs, Hq, call.seq, call.pos, call.T, call.table, call.B, call.N, ids, k,
+                                    (float)scale, out.data(), static_cast<float*>(lse.data()), ws.p, ws.n, call.err, call.stream);
+    return answer(st, out, lse);
+  });
+}
+
+PyMethodDef methods[] = {
+    {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_append)), METH_FASTCALL, nullptr},
+    {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_read)), METH_FASTCALL, nullptr},
+    {"select", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_select)), METH_FASTCALL, nullptr},
+    {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_attend)), METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kv", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__kv() { return PyModule_Create(&module); }
