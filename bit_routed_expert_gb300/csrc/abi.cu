@@ -241,7 +241,7 @@ bre_status kv_read(const bre_kv_cache* cache, const int32_t* seq, const int32_t*
                    int B, int N, void* k_out_bf16, void* v_out_bf16, int32_t* dev_err, bre_stream_t stream) {
   const bre_status st = kv_check(cache, seq, pos, T, table, B, N);
   if (st != BRE_OK || T == 0) return st;
-  if ((!k_out_bf16 && !v_out_bf16) || !aligned(k_out_bf16, 16) || !aligned(v_out_bf16, 16)) return BRE_ERR_ARG;
+  if ((!k_out_bf16 && !v_out_bf16) || !aligned(k_out_bf16, 32) || !aligned(v_out_bf16, 32)) return BRE_ERR_ARG;
   return cuda_status(launch_kv_read(cache, KvTokens{seq, pos, T, table, B, N}, static_cast<uint16_t*>(k_out_bf16),
                                     static_cast<uint16_t*>(v_out_bf16), dev_err,
                                     reinterpret_cast<cudaStream_t>(stream)));

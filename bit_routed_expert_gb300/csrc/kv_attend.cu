@@ -25,9 +25,14 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
+// CTAs to an SM.  The loads of a half block are all issued before its first product, so warps are what keeps
+// memory busy: 64 tokens x 32 blocks take 46 us with three CTAs (140 registers), 33 with four, 42 with five
+// (spills).  Both halves of 16 heads at D = 128 need the registers of two.
+constexpr int ar_ctas(int D, int NT) { return NT == 1 || D == 64 ? 4 : 2; }
+
 // NT: groups of eight query heads.
 template <int D, int NT>
-__global__ void __launch_bounds__(AR_WARPS * 32) kv_attend_rows_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(AR_WARPS * 32, ar_ctas(D, NT)) kv_attend_rows_kernel(const AttendArgs a) {
   constexpr int HB = D / 64;       // 64-channel halves of a key row
   constexpr int MT = D / 16;       // 16-channel row tiles of O^T
   constexpr int VW = D / 32;       // 4-channel words of a value row that a lane holds
@@ -309,8 +314,9 @@ cudaError_t launch_kv_attend(const bre_kv_cache* c, const KvTokens& tk, const ui
   if (tk.T >= 16LL * tk.B) return launch_kv_attend_tiles(a, D, s);
   // CTAs of a (token, head): halves of blocks for every warp, as long as the GPU has room for them
   const long long rows = (long long)tk.T * H;
+  const long long room = (long long)ar_ctas(D, G > 8 ? 2 : 1) * device_sm_count();
   int ranks = 1;
-  while (ranks < 8 && 2 * ranks * AR_WARPS <= 2 * k && rows * ranks * 2 <= 4LL * device_sm_count()) ranks *= 2;
+  while (ranks < 8 && 2 * ranks * AR_WARPS <= 2 * k && rows * ranks * 2 <= room) ranks *= 2;
   auto kern = D == 128 ? (G > 8 ? kv_attend_rows_kernel<128, 2> : kv_attend_rows_kernel<128, 1>)
                        : (G > 8 ? kv_attend_rows_kernel<64, 2> : kv_attend_rows_kernel<64, 1>);
   return launch_kc(kern, dim3((unsigned)(rows * ranks)), dim3(AR_WARPS * 32), ranks, 0, s, a);

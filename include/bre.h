@@ -327,7 +327,7 @@ bre_status kv_append(const bre_kv_cache *cache, const void *k_bf16, const void *
                      int64_t v_stride, const int32_t *seq, const int32_t *pos, int T, const int32_t *table, int B,
                      int N, int32_t *dev_err, bre_stream_t stream);
 
-/* Read tokens back: k_out, v_out [T][n_kv_heads][D] BF16 (either may be NULL), exactly the stored
+/* Read tokens back: k_out, v_out [T][n_kv_heads][D] BF16 (32-byte aligned; either may be NULL), exactly the stored
  * values; zeros for padding and for tokens without a page (which set BRE_DEVERR_PAGE). */
 bre_status kv_read(const bre_kv_cache *cache, const int32_t *seq, const int32_t *pos, int T, const int32_t *table,
                    int B, int N, void *k_out_bf16, void *v_out_bf16, int32_t *dev_err, bre_stream_t stream);
