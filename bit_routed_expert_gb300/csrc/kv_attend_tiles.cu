@@ -176,10 +176,10 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
   constexpr uint32_t COLS = 256;                   // tensor memory: S/P at 0 and 64, O at 128
   extern __shared__ unsigned char sm_raw[];
   __shared__ uint64_t blk_full[AT_RING], blk_empty[AT_RING], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
-      p_full[2], o_done, drain;
+      p_full[2], o_done, drain, sc_full[AT_RING];
   __shared__ Block ring[AT_RING];
-  __shared__ __align__(16) float ev_f[2][KV_BLOCK], ev_inv[2][KV_BLOCK];
-  __shared__ float q_factor[128], ek_top[2];
+  __shared__ __align__(16) float ev_f[AT_RING][KV_BLOCK], ev_inv[AT_RING][KV_BLOCK];
+  __shared__ float q_factor[128], ek_top[AT_RING];
   __shared__ uint32_t tmem_s;
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
   const int t0 = blockIdx.x * per, h = blockIdx.y, nt = min(per, a.T - t0), rows = nt * a.G;
 
   if (tid == 0) {
-    for (int i = 0; i < AT_RING; ++i) mbar_init(&blk_full[i], 1), mbar_init(&blk_empty[i], 4 + AT_CODES / 32 + 1);
+    for (int i = 0; i < AT_RING; ++i) mbar_init(&blk_full[i], 1), mbar_init(&sc_full[i], 4), mbar_init(&blk_empty[i], 4 + AT_CODES / 32 + 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 4);
       mbar_init(&k_empty[i], 1);
@@ -211,10 +211,10 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
   // queries: row r = (token r / G, head r % G) scaled by a power of two into FP16; K-major panels
   constexpr int PL = D / 32, QW = AT_THREADS / 32;
 #pragma unroll 1
-  for (int r0 = warp; r0 < 128; r0 += 4 * QW) {
-    uint32_t w[4][PL / 2];
+  for (int r0 = warp; r0 < 128; r0 += 10 * QW) {   // ten rows of a warp in flight: one round
+    uint32_t w[10][PL / 2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 10; ++j) {
       const int r = r0 + j * QW, tl = r / a.G;
       const uint32_t* qr = reinterpret_cast<const uint32_t*>(a.q + (long long)(t0 + tl) * a.q_stride +
                                                              (size_t)(h * a.G + r - tl * a.G) * D) + lane * (PL / 2);
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       for (int i = 0; i < PL / 2; ++i) w[j][i] = r < rows ? __ldg(qr + i) : 0u;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 10; ++j) {
       const int r = r0 + j * QW;
       if (r >= 128) break;
       uint32_t mx = 0;   // magnitudes of BF16 values compare like whole numbers; NaN and infinities count as 2^127
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
     uint64_t* const empty = values ? v_empty : k_empty;
     uint4 cur[NL], nxt[NL];
     int e2 = 0, e2n = 0;     // key scales of tokens lane and lane + 32: this block's, the next one's
-    int ev = 0, evn = 0;     // value scale of token dt
+    int ev = 0, evn = 0;     // value scale of token dt (keys' threads)
     int page = 0, n = 0;     // of the block that is loaded next
     const uint8_t* pg = nullptr;
     auto take = [&](int i) {
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       for (int j = 0; j < NL; ++j) nxt[j] = (dt + j * 128) / CH < n ? __ldg(src + j * 128) : make_uint4(0, 0, 0, 0);
       e2n = lane < n ? (int)__ldg(sc + lane) : 0;
       if (lane + 32 < n) e2n |= (int)__ldg(sc + 32 + lane) << 8;
-      if (values) evn = dt < n ? (int)__ldg(sc + KV_BLOCK + dt) : 127;
+      if (!values) evn = dt < n ? (int)__ldg(sc + KV_BLOCK + dt) : 127;
     };
     // where a thread puts its 16 values (token x0, channels 16 c ..; further loads are whole multiples of 8
     // tokens on): two swizzled pieces of 16 bytes.  The lanes of odd panels start with the second piece, so that
@@ -437,14 +437,20 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       // the block's largest key scale (a NaN row's does not count: its codes are zeros)
       const int ea = e2 & 255, eb = e2 >> 8;
       const int top = __reduce_max_sync(0xffffffffu, max(ea == KV_NAN ? 0 : ea, eb == KV_NAN ? 0 : eb));
-      // a free value stage also means that the softmax is done with the scales of two blocks before
       if (!warp_wait(&empty[st], (i >> 1) + 1)) break;
-      if (values && dt < KV_BLOCK) {
-        // a NaN row makes its token's logit NaN
-        const bool nan = (dt < 32 ? ea : eb) == KV_NAN || ev == KV_NAN;
-        ev_f[st][dt] = nan ? __int_as_float(0x7FC00000) : (float)(ev - 127);
-        ev_inv[st][dt] = pow2f(127 - min(ev, 253));
-        if (dt == 0) ek_top[st] = pow2f(max(top, 1) - 127);
+      if (!values) {
+        // the scales go to the softmax first.  Their place is free: S of two blocks ago has been formed, for which
+        // the weights of four blocks ago must have been used
+        const int sp = i % AT_RING;
+        if (dt < KV_BLOCK) {
+          // a NaN row makes its token's logit NaN
+          const bool nan = (dt < 32 ? ea : eb) == KV_NAN || ev == KV_NAN;
+          ev_f[sp][dt] = nan ? __int_as_float(0x7FC00000) : (float)(ev - 127);
+          ev_inv[sp][dt] = pow2f(127 - min(ev, 253));
+          if (dt == 0) ek_top[sp] = pow2f(max(top, 1) - 127);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_full[sp]);
       }
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
@@ -498,21 +504,23 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       if (lane == 0) mbar_arrive(&blk_empty[i % AT_RING]);
       if (page < 0) break;
       const int n = mine ? min(KV_BLOCK, pos - id * KV_BLOCK + 1) : 0;   // tokens that the row sees
-      if (!warp_wait(&v_full[st], i >> 1) || !warp_wait(&s_full[st], i >> 1)) break;   // the scales, the products
+      const int sp = i % AT_RING;
+      if (!warp_wait(&sc_full[sp], i / AT_RING) || !warp_wait(&s_full[st], i >> 1)) break;
       tc_fence_after();
+      const bool any = __any_sync(0xffffffffu, n > 0);   // else none of the warp's tokens lists the block
       // two passes over S, 32 columns at a time (as a loop: see wait_long): the maximum, then the weights
-      const float f = qf * ek_top[st];
+      const float f = qf * ek_top[sp];
       const uint64_t f2 = pack2(f, f);
       const bool whole = __all_sync(0xffffffffu, n == 0 || n == KV_BLOCK);
       float mx = -INFINITY;
 #pragma unroll 1
-      for (int c = 0; c < KV_BLOCK; c += 32) {
+      for (int c = any ? 0 : KV_BLOCK; c < KV_BLOCK; c += 32) {
         uint32_t s[32];
         tmem_ld32(lane_base + st * 64 + c, s);
         tmem_wait_ld();
 #pragma unroll
         for (int x = 0; x < 32; x += 4) {
-          const ulonglong2 ev = *reinterpret_cast<const ulonglong2*>(&ev_f[st][c + x]);
+          const ulonglong2 ev = *reinterpret_cast<const ulonglong2*>(&ev_f[sp][c + x]);
           const float2 v0 = unpack2(fma2(pack2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), f2, ev.x));
           const float2 v1 = unpack2(fma2(pack2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), f2, ev.y));
           s[x] = __float_as_uint(v0.x), s[x + 1] = __float_as_uint(v0.y);
@@ -552,20 +560,33 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
 #pragma unroll 1
       for (int c = 0; c < KV_BLOCK; c += 32) {
         uint32_t s[32], pk[16];
+        if (!any) {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) pk[x] = 0u;
+          tmem_st16(lane_base + st * 64 + c / 2, pk);
+          continue;
+        }
         tmem_ld32(lane_base + st * 64 + c, s);
         tmem_wait_ld();
 #pragma unroll
         for (int x = 0; x < 32; x += 4) {
-          const ulonglong2 ev = *reinterpret_cast<const ulonglong2*>(&ev_f[st][c + x]);
-          const ulonglong2 iv = *reinterpret_cast<const ulonglong2*>(&ev_inv[st][c + x]);
+          const ulonglong2 ev = *reinterpret_cast<const ulonglong2*>(&ev_f[sp][c + x]);
           const float2 v0 = unpack2(add2(fma2(pack2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), f2, ev.x), nb2));
           const float2 v1 =
               unpack2(add2(fma2(pack2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), f2, ev.y), nb2));
-          float p0 = ex2(v0.x), p1 = ex2(v0.y), p2 = ex2(v1.x), p3 = ex2(v1.y);
-          if (!whole) {
-            p0 = c + x < n ? p0 : 0.0f, p1 = c + x + 1 < n ? p1 : 0.0f;
-            p2 = c + x + 2 < n ? p2 : 0.0f, p3 = c + x + 3 < n ? p3 : 0.0f;
-          }
+          s[x] = __float_as_uint(ex2(v0.x)), s[x + 1] = __float_as_uint(ex2(v0.y));
+          s[x + 2] = __float_as_uint(ex2(v1.x)), s[x + 3] = __float_as_uint(ex2(v1.y));
+        }
+        if (!whole) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (c + x >= n) s[x] = 0u;
+        }
+#pragma unroll
+        for (int x = 0; x < 32; x += 4) {
+          const ulonglong2 iv = *reinterpret_cast<const ulonglong2*>(&ev_inv[sp][c + x]);
+          const float p0 = __uint_as_float(s[x]), p1 = __uint_as_float(s[x + 1]);
+          const float p2 = __uint_as_float(s[x + 2]), p3 = __uint_as_float(s[x + 3]);
           add = fma2(pack2(p0, p1), iv.x, fma2(pack2(p2, p3), iv.y, add));
           pk[x / 2] = n ? pack_f16x2(p0, p1) : 0u;
           pk[x / 2 + 1] = n ? pack_f16x2(p2, p3) : 0u;
@@ -593,13 +614,8 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       }
 #pragma unroll
       for (int x = 0; x < 8; ++x)
-        w[x] = l == 0.0f ? 0u
-                         : f32_to_bf16_rne(__uint_as_float(o[2 * x]) * inv) |
-                               f32_to_bf16_rne(__uint_as_float(o[2 * x + 1]) * inv) << 16;
-      if (live && ok) {
-        *reinterpret_cast<uint4*>(a.out + row * D + c) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(a.out + row * D + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-      }
+        w[x] = l == 0.0f ? 0u : pack_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
+      if (live && ok) st_v8(a.out + row * D + c, w);
     }
     if (live && ok && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : LN2 * ((m > -INFINITY ? m - P_SHIFT : 0.0f) + log2f(l));
   }

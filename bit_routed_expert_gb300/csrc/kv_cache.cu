@@ -164,13 +164,6 @@ __global__ void __launch_bounds__(KA_WARPS * 32)
   }
 }
 
-// 32 bytes at a 32-byte aligned address: whole sectors.
-__device__ __forceinline__ void st_v8(uint16_t* dst, const uint32_t (&o)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(o[0]), "r"(o[1]), "r"(o[2]),
-               "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-               : "memory");
-}
-
 // Codes times the row's scale, exact in BF16.  A lane takes 16 codes: D / 16 lanes a row, two rows'
 // keys and values of a lane in flight (more of them cost registers and so warps: 92 us against 71 for 131,072 tokens).
 template <int D>
