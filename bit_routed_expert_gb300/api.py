@@ -12,8 +12,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import (BRE_FMT_Q2_K, BRE_FMT_Q2_K_R16, BRE_FMT_Q8_0, BreKvCache, BreWeights, check, ptr,
-                   stream_handle)
+from ._lib import BRE_FMT_Q2_K, BRE_FMT_Q2_K_R16, BRE_FMT_Q8_0, BreWeights, check, ptr, stream_handle
 
 
 def _dev(t: torch.Tensor, name: str):
@@ -255,17 +254,8 @@ class KvCache:
     bound_exp: torch.Tensor
 
     def __post_init__(self):
-        p, b, e = self.pages, self.bounds, self.bound_exp
-        n, H, _, D = b.shape
-        if p.shape != (n, H, 2 * KV_BLOCK * (D + 1)) or e.shape != (n, H):
-            raise ValueError("pages, bounds and bound_exp do not belong together")
-        if p.dtype is not torch.uint8 or b.dtype is not torch.int8 or e.dtype is not torch.int8:
-            raise ValueError("pages must be uint8, bounds and bound_exp int8")
-        if not (p.is_cuda and b.is_cuda and e.is_cuda and p.is_contiguous() and b.is_contiguous() and e.is_contiguous()):
-            raise ValueError("pages, bounds and bound_exp must be contiguous CUDA tensors")
-        self.n_pages, self.n_kv_heads, self.head_dim = n, H, D
-        self._struct = BreKvCache(p.data_ptr(), b.data_ptr(), e.data_ptr(), n, H, D)
-        self._at = C.addressof(self._struct)
+        self.n_pages, self.n_kv_heads, self.head_dim, self._held, self._at = _lib.load_kv().cache(
+            self.pages, self.bounds, self.bound_exp)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, device) -> "KvCache":

@@ -259,6 +259,7 @@ bre_status kv_select(const bre_kv_cache* cache, const void* q_bf16, int64_t q_st
   if (st != BRE_OK || T == 0) return st;
   if ((st = kv_check_q(cache, q_bf16, q_stride, n_heads, k)) != BRE_OK) return st;
   if (!ids || n_sink < 0 || n_local < 0 || n_sink > k || n_local > k - n_sink) return BRE_ERR_ARG;
+  if (N > 131072) return BRE_ERR_UNSUPPORTED;   // the scores of a token lie in the shared memory of eight CTAs
   const size_t need = kv_select_ws_bytes(T, n_heads, cache->n_kv_heads, cache->head_dim, B, N, k);
   if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return BRE_ERR_WORKSPACE;
   return cuda_status(launch_kv_select(cache, KvTokens{seq, pos, T, table, B, N}, static_cast<const uint16_t*>(q_bf16),

@@ -20,6 +20,8 @@
 // is 2^15 times smaller, and then off by less than 2^-24 of the block's largest logit), the rest into the
 // logits' factor; a value's 2^ev goes into its weight (see kv_attend.cu).  O is rescaled only when a
 // row's maximum has grown by more than 2^7: the weights then still fit FP16.
+#include <atomic>
+
 #include "kv_attend.cuh"
 
 namespace bre {
@@ -629,9 +631,16 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
 
 template <int D>
 cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(kv_attend_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             TilesMem<D>::bytes);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> done{0};   // devices on which the kernel may have its shared memory
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(kv_attend_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               TilesMem<D>::bytes);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_release);
+  }
   const int per = 128 / a.G;
   return launch_k(kv_attend_tiles_kernel<D>, dim3((unsigned)((a.T + per - 1) / per), (unsigned)a.H), dim3(AT_THREADS),
                   TilesMem<D>::bytes, s, a);

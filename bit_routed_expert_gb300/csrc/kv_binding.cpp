@@ -214,7 +214,27 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// pages bounds bound_exp -> (n_pages, n_kv_heads, head_dim, bytes of a bre_kv_cache, their address)
+PyObject* py_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 3, [&]() -> PyObject* {
+    const Tensor &p = tensor(a[0], "pages"), &b = tensor(a[1], "bounds"), &e = tensor(a[2], "bound_exp");
+    if (b.dim() != 4 || b.size(2) != 2) refuse("bounds must be [n_pages, n_kv_heads, 2, head_dim]");
+    const int64_t N = b.size(0), H = b.size(1), D = b.size(3);
+    if (p.sizes() != at::IntArrayRef({N, H, 128 * (D + 1)}) || e.sizes() != at::IntArrayRef({N, H}))
+      refuse("pages, bounds and bound_exp do not belong together");
+    if (p.scalar_type() != at::kByte || b.scalar_type() != at::kChar || e.scalar_type() != at::kChar)
+      refuse("pages must be uint8, bounds and bound_exp int8");
+    for (const Tensor* t : {&p, &b, &e})
+      if (!t->is_cuda() || !t->is_contiguous()) refuse("pages, bounds and bound_exp must be contiguous CUDA tensors");
+    const bre_kv_cache c{p.data_ptr(), static_cast<int8_t*>(b.data_ptr()), static_cast<int8_t*>(e.data_ptr()), (int32_t)N, (int32_t)H,
+                         (int32_t)D};
+    PyObject* held = PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&c), sizeof(c));
+    return held ? Py_BuildValue("iiiNN", (int)N, (int)H, (int)D, held, PyLong_FromVoidPtr(PyBytes_AS_STRING(held))) : nullptr;
+  });
+}
+
 PyMethodDef methods[] = {
+    {"cache", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_cache)), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_append)), METH_FASTCALL, nullptr},
     {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_read)), METH_FASTCALL, nullptr},
     {"select", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_select)), METH_FASTCALL, nullptr},

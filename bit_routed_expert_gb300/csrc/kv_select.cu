@@ -8,6 +8,8 @@
 // 32-bit integers, whatever the order.
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "kv_common.cuh"
 
 namespace bre {
@@ -58,6 +60,7 @@ __device__ __forceinline__ int warp_top(const uint32_t* keys, int first, int n, 
   uint32_t lo = 1, hi = __reduce_max_sync(0xffffffffu, top) + 1u;
   if (want <= 0 || hi == 1u) return 0;
   if (__popc(__ballot_sync(0xffffffffu, top != 0u)) >= want) {
+    lo = __reduce_min_sync(0xffffffffu, top != 0u ? top : hi);
     uint32_t h = hi;   // as many lanes reach lo, fewer reach h
     while (h - lo > 1) {
       const uint32_t mid = lo + (h - lo) / 2;
@@ -69,7 +72,13 @@ __device__ __forceinline__ int warp_top(const uint32_t* keys, int first, int n, 
       if (c == want) break;
     }
   }
-  // count(>= lo) >= want unless lo = 1; count(>= hi) = above < want
+  if (lo == 1u) {   // more entries wanted than lanes have: between the smallest key and the largest
+    uint32_t least = hi;
+#pragma unroll
+    for (int j = 0; j < R; ++j) least = min(least, key[j] != 0u ? key[j] : hi);
+    lo = __reduce_min_sync(0xffffffffu, least);
+  }
+  // count(>= lo) >= want unless all entries are fewer; count(>= hi) = above < want
   auto count = [&](uint32_t v) {
     int c = 0;
 #pragma unroll
@@ -612,6 +621,18 @@ __global__ void __launch_bounds__(ST_WARPS * 32, 2) kv_select_tiles_kernel(const
 
 }  // namespace
 
+// Lets a kernel have so much dynamic shared memory; the call is made once a device.
+static cudaError_t allow_smem(const void* kern, int which, int bytes) {
+  static std::atomic<uint64_t> done[4];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done[which].load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done[which].fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 size_t kv_select_ws_bytes(int T, int Hq, int H, int D, int B, int N, int k) { return 0; }
 
 // Shared memory of the one-token kernel for stretches of `span` blocks.
@@ -623,12 +644,14 @@ cudaError_t launch_kv_select(const bre_kv_cache* c, const KvTokens& tk, const ui
   const int H = c->n_kv_heads, D = c->head_dim;
   const SelectArgs a{c->bounds, c->bound_exp, H,   Hq / H, KvTable{tk.table, tk.B, tk.N, c->n_pages},
                      q, q_stride, tk.seq, tk.pos, tk.T, k, n_sink, n_local, ids, scores, err};
-  if (tk.T >= 16LL * tk.B) {
+  // tiles: the lists of 32 tokens must fit (up to about 170 blocks a token)
+  const size_t most = device_max_smem_optin() - 2048;   // less the kernels' static shared memory
+  const size_t smem_t = select_tiles_smem(D, (k + 15) / 16 * 16);
+  if (tk.T >= 16LL * tk.B && smem_t <= most) {
     auto kern = D == 128 ? kv_select_tiles_kernel<128> : kv_select_tiles_kernel<64>;
-    const size_t smem = select_tiles_smem(D, (k + 15) / 16 * 16);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), D == 128, (int)most);
     if (e != cudaSuccess) return e;
-    return launch_k(kern, dim3((unsigned)((tk.T + ST_ROWS - 1) / ST_ROWS), (unsigned)H), dim3(ST_WARPS * 32), smem, s, a);
+    return launch_k(kern, dim3((unsigned)((tk.T + ST_ROWS - 1) / ST_ROWS), (unsigned)H), dim3(ST_WARPS * 32), smem_t, s, a);
   }
   // CTAs of a (token, head): while the GPU has room and a CTA keeps 64 blocks; more where the
   // stretch would not fit its shared memory
@@ -640,10 +663,8 @@ cudaError_t launch_kv_select(const bre_kv_cache* c, const KvTokens& tk, const ui
     ranks *= 2;
   const size_t smem = select_rows_smem((tk.N + ranks - 1) / ranks, k);
   auto kern = D == 128 ? kv_select_rows_kernel<128> : kv_select_rows_kernel<64>;
-  if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), 2 + (D == 128), (int)most);
+  if (e != cudaSuccess) return e;
   return launch_kc(kern, dim3((unsigned)(rows * ranks)), dim3(SR_WARPS * 32), ranks, smem, s, a);
 }
 

@@ -345,7 +345,7 @@ bre_status kv_read(const bre_kv_cache *cache, const int32_t *seq, const int32_t 
  *   scores [T][n_kv_heads][k] FP32 or NULL: their scores, then 0.
  *   q: as k in kv_append, [n_heads][D] a row.  ws: kv_select_workspace(...) bytes, zero-filled
  *   once after allocation (each call leaves it ready for the next).
- * Requires G <= 16, 1 <= k <= 256, n_sink + n_local <= k. */
+ * Requires G <= 16, 1 <= k <= 256, n_sink + n_local <= k, N <= 131,072 (8.4 million tokens). */
 size_t kv_select_workspace(int T, int n_heads, int n_kv_heads, int head_dim, int B, int N, int k);
 bre_status kv_select(const bre_kv_cache *cache, const void *q_bf16, int64_t q_stride, int n_heads, const int32_t *seq,
                      const int32_t *pos, int T, const int32_t *table, int B, int N, int k, int n_sink, int n_local,

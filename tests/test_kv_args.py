@@ -70,7 +70,7 @@ def test_select_refuses():
     assert select(q=None) == select(q=ODD) == select(qs=248) == select(qs=260) == select(ids=None) == BRE_ERR_ARG
     assert select(Hq=3, qs=192) == select(Hq=0) == select(k=0) == BRE_ERR_ARG
     assert select(sink=-1) == select(local=-1) == select(sink=3, local=2) == select(sink=5, local=0) == BRE_ERR_ARG
-    assert select(Hq=34, qs=34 * 64) == select(k=257) == BRE_ERR_UNSUPPORTED
+    assert select(Hq=34, qs=34 * 64) == select(k=257) == select(N=131073) == BRE_ERR_UNSUPPORTED
     need = _lib.load().kv_select_workspace(3, 4, 2, 64, 1, 1, 4)
     if need:
         assert select() == select(ws=P, wsb=need - 1) == select(ws=C.c_void_p((1 << 20) + 16), wsb=need)

@@ -226,6 +226,31 @@ def test_select_long_contexts(cuda_dev, T):
 
 
 @pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("k", [33, 150, 200, 256])
+def test_select_many(cuda_dev, T, k):
+    """Lists longer than a warp, than a prefill tile's shared memory, and than the blocks there are."""
+    D, H, G = 64, 1, 2
+    b = R.batch([2560], [1])
+    cache = R.filled(b, [2560], H, D)
+    g = torch.Generator().manual_seed(k)
+    for blocks in (100, 700, 1300):
+        n = R.Batch([0] * T, list(range(64 * blocks - T, 64 * blocks)),
+                    torch.randint(0, b.n_pages, (1, blocks), generator=g).to(torch.int32), b.n_pages)
+        check_select(cuda_dev, n, cache, R.rows(blocks, T, G, D), k, 3, 20)
+
+
+def test_select_longest_table(cuda_dev):
+    """131,072 blocks: the whole of eight CTAs' shared memory."""
+    D, H, G, blocks = 64, 1, 1, 131072
+    b = R.batch([2560], [1])
+    cache = R.filled(b, [2560], H, D)
+    g = torch.Generator().manual_seed(1)
+    n = R.Batch([0], [64 * blocks - 1], torch.randint(0, b.n_pages, (1, blocks), generator=g).to(torch.int32), b.n_pages)
+    for k in (16, 256):
+        check_select(cuda_dev, n, cache, R.rows(5, 1, G, D), k, 1, 2)
+
+
+@pytest.mark.parametrize("T", [1, 40])
 def test_select_blocks_without_pages(cuda_dev, T):
     D, H, G = 128, 2, 2
     lens = [1500, 900]
