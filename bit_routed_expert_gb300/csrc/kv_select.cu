@@ -330,29 +330,90 @@ struct SelectRowsMem {
   __host__ __device__ size_t bytes(int span) const { return 4 * ((size_t)pages(span) + span); }
 };
 
-// Sixteen whole numbers of the query's vector against sixteen bytes of bounds.
-__device__ __forceinline__ int dot16(const int (&u)[8], const uint4& b) {
-  int acc = 0;
-  acc = __dp2a_lo(u[0], (int)b.x, acc);
-  acc = __dp2a_hi(u[1], (int)b.x, acc);
-  acc = __dp2a_lo(u[2], (int)b.y, acc);
-  acc = __dp2a_hi(u[3], (int)b.y, acc);
-  acc = __dp2a_lo(u[4], (int)b.z, acc);
-  acc = __dp2a_hi(u[5], (int)b.z, acc);
-  acc = __dp2a_lo(u[6], (int)b.w, acc);
-  return __dp2a_hi(u[7], (int)b.w, acc);
+// Bytes 0, 1 (sel 0x4140) or 2, 3 (0x4342) of four whole numbers that were offset by 128 -> an FP16 pair.
+__device__ __forceinline__ uint32_t s8x2_to_f16x2(uint32_t biased, uint32_t sel) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(prmt(biased, 0x64646464u, sel)), "r"(0x64806480u));
+  return r;
+}
+
+// The `want` best of the entries first .. n - 1 (n <= 2 SR_WARPS 32) by the whole CTA, two entries a thread; else
+// as warp_top, without its bound: a step is two barriers that count.  For one token this is what takes least
+// time: 5,000 cycles for one warp's selection of 256 from code that runs once, 1,500 for this.
+template <typename Put>
+__device__ __forceinline__ int cta_top(const uint32_t* keys, int first, int n, int want, uint32_t (&s_red)[2][SR_WARPS],
+                                       Put put) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t key[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (2 * tid + j >= first && 2 * tid + j < n) key[j] = keys[key_at(2 * tid + j)];
+  __syncthreads();   // s_red is free
+  {
+    const uint32_t mx = __reduce_max_sync(0xffffffffu, max(key[0], key[1]));
+    const uint32_t mn = __reduce_min_sync(0xffffffffu, min(key[0] - 1u, key[1] - 1u));   // a key of 0 counts as the largest
+    if (lane == 0) s_red[0][warp] = mx, s_red[1][warp] = mn;
+  }
+  __syncthreads();
+  uint32_t hi = 0, lo = 0xFFFFFFFFu;
+#pragma unroll
+  for (int w = 0; w < SR_WARPS; ++w) hi = max(hi, s_red[0][w]), lo = min(lo, s_red[1][w]);
+  if (want <= 0 || hi == 0u) return 0;
+  lo += 1u, hi += 1u;
+  auto count = [&](uint32_t v) { return __syncthreads_count(key[0] >= v) + __syncthreads_count(key[1] >= v); };
+  // count(>= lo) = got, count(>= hi) = above < want
+  uint32_t thr = lo;
+  int above = 0, got = count(lo);
+  const int all = got;
+  while (got > want && hi - lo > 1) {
+    thr = lo + (hi - lo) / 2;
+    got = count(thr);
+    if (got > want) {
+      lo = thr;
+    } else if (got < want) {
+      hi = thr;
+      above = got;
+      got = want + 1;
+    }
+  }
+  const bool cut = got > want;   // hi - lo = 1: some of the entries equal to lo are left out
+  if (cut) thr = lo;
+  const uint32_t before = (1u << lane) - 1u;
+  bool take[2] = {key[0] > thr || (!cut && key[0] == thr), key[1] > thr || (!cut && key[1] == thr)};
+  if (cut) {
+    const uint32_t e0 = __ballot_sync(0xffffffffu, key[0] == thr), e1 = __ballot_sync(0xffffffffu, key[1] == thr);
+    __syncthreads();
+    if (lane == 0) s_red[0][warp] = __popc(e0) + __popc(e1);
+    __syncthreads();
+    int rank = __popc(e0 & before) + __popc(e1 & before);
+    for (int w = 0; w < warp; ++w) rank += s_red[0][w];
+    take[0] |= key[0] == thr && rank < want - above;
+    take[1] |= key[1] == thr && rank + (key[0] == thr) < want - above;
+  }
+  const uint32_t b0 = __ballot_sync(0xffffffffu, take[0]), b1 = __ballot_sync(0xffffffffu, take[1]);
+  __syncthreads();
+  if (lane == 0) s_red[1][warp] = __popc(b0) + __popc(b1);
+  __syncthreads();
+  int at = __popc(b0 & before) + __popc(b1 & before);
+  for (int w = 0; w < warp; ++w) at += s_red[1][w];
+  if (take[0]) put(at, 2 * tid, key[0]);
+  if (take[1]) put(at + take[0], 2 * tid + 1, key[1]);
+  return min(want, all);
 }
 
 template <int D>
 __global__ void __launch_bounds__(SR_WARPS * 32, 2) kv_select_rows_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint32_t sm[];
-  __shared__ __align__(16) short u[2 * D];
+  __shared__ __align__(16) __half u[2][2 * D];   // the query's vector; zeros
   __shared__ Forced f_s;
   __shared__ int eq_s;
+  __shared__ uint32_t s_red[2][SR_WARPS];
   const SelectRowsMem mem(a.k);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kk = mem.kk;
   const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
   const int row = blockIdx.x / ranks, t = row / a.H, h = row - t * a.H;
+  // the lists' unused places are entries that cannot be taken; the first CTA's are written by the others
+  for (int i = tid; i < SR_RANKS * key_at(kk); i += SR_WARPS * 32) sm[mem.all_k() + i] = 0u;
   cluster_arrive();
   pdl_wait();
   pdl_launch_dependents();
@@ -372,8 +433,12 @@ __global__ void __launch_bounds__(SR_WARPS * 32, 2) kv_select_rows_kernel(const 
     const int e = query_vector<W>(qr, D / 2, a.G, pl, mi);
     if (lane == 0) eq_s = e;
 #pragma unroll
-    for (int i = 0; i < 2 * W; ++i) u[2 * W * lane + i] = (short)pl[i], u[D + 2 * W * lane + i] = (short)-mi[i];
+    for (int i = 0; i < 2 * W; ++i) {
+      u[0][2 * W * lane + i] = __int2half_rn(pl[i]);
+      u[0][D + 2 * W * lane + i] = __int2half_rn(-mi[i]);
+    }
   } else if (warp == SR_WARPS - 2) {
+    for (int i = lane; i < D; i += 32) reinterpret_cast<uint32_t*>(u[1])[i] = 0u;
     const Forced f = forced_blocks(a, s, p, nb);
     if (lane == 0) f_s = f;
   } else {
@@ -382,31 +447,53 @@ __global__ void __launch_bounds__(SR_WARPS * 32, 2) kv_select_rows_kernel(const 
   __syncthreads();
   const Forced f = f_s;
 
-  // scores: 2 D / 16 lanes a block, eight loads in flight
-  constexpr int LB = 2 * D / 16, PW = 32 / LB;   // lanes a block, blocks a load
-  int uu[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) uu[j] = reinterpret_cast<const int*>(u)[(lane % LB) * 8 + j];
+  // scores, as in the prefill tiles but with the one vector in the first row of the product (the integer dot
+  // products dp2a and dp4a are a small fraction of the tensor cores' rate here): eight blocks a product, 32 of a
+  // warp in flight
+  constexpr int KS = 2 * D / 16, NT = 4;   // k steps, of which four cover 64 channels; products at a time
+  const int g = lane >> 2, t4 = lane & 3;
+  const __half* ul = u[g ? 1 : 0] + 16 * t4;
   // a warp's part: whole groups of 16, so that parts are lists of their own
   const int part = (n + 16 * SR_WARPS - 1) / (16 * SR_WARPS) * 16, w0 = min(warp * part, n), wn = min(part, n - w0);
-  for (int i0 = 0; i0 < wn; i0 += 8 * PW) {
-    uint4 bd[8];
-    int e[8];
+#pragma unroll 1
+  for (int i0 = 0; i0 < wn; i0 += 8 * NT) {
+    uint4 bd[NT][KS / 4];
+    int e[NT][2];   // of columns 2 t4, 2 t4 + 1
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = i0 + j * PW + lane / LB;
-      const int pg = i < wn ? page[w0 + i] : -1;
-      const size_t ph = (size_t)max(pg, 0) * a.H + h;
-      bd[j] = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.bounds + ph * 2 * D) + lane % LB) : make_uint4(0, 0, 0, 0);
-      e[j] = pg >= 0 ? (int)__ldg(a.bexp + ph) : -128;
+    for (int nt = 0; nt < NT; ++nt) {
+      const int i = i0 + 8 * nt + g, pg = i < wn ? page[w0 + i] : -1;
+      const int8_t* bp = a.bounds + ((size_t)max(pg, 0) * a.H + h) * 2 * D + 16 * t4;
+#pragma unroll
+      for (int cg = 0; cg < KS / 4; ++cg)
+        bd[nt][cg] = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(bp + 64 * cg)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int ic = i0 + 8 * nt + 2 * t4 + c, pc = g == 0 && ic < wn ? page[w0 + ic] : -1;
+        e[nt][c] = pc >= 0 ? (int)__ldg(a.bexp + (size_t)pc * a.H + h) : -128;
+      }
+    }
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[nt][j] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const uint2 uf = *reinterpret_cast<const uint2*>(ul + 64 * (ks / 4) + 4 * (ks % 4));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4& q = bd[nt][ks / 4];
+        const uint32_t w = (ks % 4 == 0 ? q.x : ks % 4 == 1 ? q.y : ks % 4 == 2 ? q.z : q.w) ^ 0x80808080u;
+        mma_f16_16816(acc[nt], uf.x, 0u, uf.y, 0u, s8x2_to_f16x2(w, 0x4140u), s8x2_to_f16x2(w, 0x4342u));
+      }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      int d = dot16(uu, bd[j]);
+    for (int nt = 0; nt < NT; ++nt) {
+      const int ic = i0 + 8 * nt + 2 * t4;
+      if (g == 0)
 #pragma unroll
-      for (int o = 1; o < LB; o *= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
-      const int i = i0 + j * PW + lane / LB;
-      if (i < wn && lane % LB == 0) keys[key_at(w0 + i)] = e[j] == -128 ? 0u : key_of_score((float)d * pow2f(e[j]));
+        for (int c = 0; c < 2; ++c)
+          if (ic + c < wn) keys[key_at(w0 + ic + c)] = e[nt][c] == -128 ? 0u : key_of_score(acc[nt][c] * pow2f(e[nt][c]));
     }
   }
   __syncthreads();
@@ -417,41 +504,50 @@ __global__ void __launch_bounds__(SR_WARPS * 32, 2) kv_select_rows_kernel(const 
   int* fin_b = reinterpret_cast<int*>(sm + mem.fin_b());
   uint32_t* lk = sm + mem.scratch(warp);
   int* lb = reinterpret_cast<int*>(lk + key_at(2 * kk));
+  auto push = [&](int place, int b, uint32_t key) {   // into the first CTA's lists
+    st_cluster_u32(sm + mem.all_k() + key_at(rank * kk + place), 0, key);
+    st_cluster_u32(sm + mem.all_b() + rank * kk + place, 0, (uint32_t)b);
+  };
   int got = 0;
+  uint32_t* loc_k = sm + mem.loc_k();
+  int* loc_b = reinterpret_cast<int*>(sm + mem.loc_b());
   if (n > SEL_CHUNK) {
-    uint32_t* loc_k = sm + mem.loc_k();
-    int* loc_b = reinterpret_cast<int*>(sm + mem.loc_b());
     got = warp_top_list(keys + key_at(w0), m0 - w0, min(wn, m1 - w0), [&](int i) { return b0 + w0 + i; }, want,
                         loc_k + warp * key_at(kk), loc_b + warp * kk, lk, lb);
     for (int i = got + lane; i < kk; i += 32) loc_k[key_at(warp * kk + i)] = 0u;
     __syncthreads();
-    if (warp == 0)
-      got = warp_top_list(loc_k, 0, SR_WARPS * kk, [&](int i) { return loc_b[i]; }, want, fin_k, fin_b, lk, lb);
-  } else if (warp == 0) {
-    got = warp_top_list(keys, m0, m1, [&](int i) { return b0 + i; }, want, fin_k, fin_b, lk, lb);
   }
   cluster_wait();   // the first CTA runs: its shared memory may be written
-  if (warp == 0) {
-    __syncwarp();
-    for (int i = lane; i < kk; i += 32) {
-      st_cluster_u32(sm + mem.all_k() + key_at(rank * kk + i), 0, i < got ? fin_k[key_at(i)] : 0u);
-      st_cluster_u32(sm + mem.all_b() + rank * kk + i, 0, i < got ? (uint32_t)fin_b[i] : 0u);
-    }
-  } else if (warp == 1) {
+  if (n <= SEL_CHUNK) {
+    got = cta_top(keys, m0, m1, want, s_red, [&](int p, int i, uint32_t key) { push(p, b0 + i, key); });
+  } else if (SR_WARPS * kk <= SEL_CHUNK) {
+    got = cta_top(loc_k, 0, SR_WARPS * kk, want, s_red, [&](int p, int i, uint32_t key) { push(p, loc_b[i], key); });
+  } else if (warp == 0) {
+    got = warp_top_list(loc_k, 0, SR_WARPS * kk, [&](int i) { return loc_b[i]; }, want, fin_k, fin_b, lk, lb);
+    for (int i = lane; i < got; i += 32) push(i, fin_b[i], fin_k[key_at(i)]);
+  }
+  if (warp == 1)
     for (int i = lane; i < f.slots(); i += 32) {
       const int b = f.block(i) - b0;
       if (b >= 0 && b < n) st_cluster_u32(sm + mem.forced() + i, 0, keys[key_at(b)]);
     }
-  }
   cluster_arrive();
   if (rank != 0) return;
   cluster_wait();
-  if (warp != 0) return;
-  if (ranks > 1) {
-    const int* all_b = reinterpret_cast<const int*>(sm + mem.all_b());
-    got = warp_top_list(sm + mem.all_k(), 0, ranks * kk, [&](int i) { return all_b[i]; }, want, fin_k, fin_b, lk, lb);
+  const uint32_t* all_k = sm + mem.all_k();
+  const int* all_b = reinterpret_cast<const int*>(sm + mem.all_b());
+  if (ranks == 1) {   // the one list is the result
+    if (warp == 0) write_lists(a, row, f, sm + mem.forced(), all_k, all_b, __shfl_sync(0xffffffffu, got, 0), eq_s);
+    return;
   }
-  write_lists(a, row, f, sm + mem.forced(), fin_k, fin_b, got, eq_s);
+  if (ranks * kk <= SEL_CHUNK) {
+    got = cta_top(all_k, 0, ranks * kk, want, s_red,
+                  [&](int p, int i, uint32_t key) { fin_k[key_at(p)] = key, fin_b[p] = all_b[i]; });
+    __syncthreads();
+  } else if (warp == 0) {
+    got = warp_top_list(all_k, 0, ranks * kk, [&](int i) { return all_b[i]; }, want, fin_k, fin_b, lk, lb);
+  }
+  if (warp == 0) write_lists(a, row, f, sm + mem.forced(), fin_k, fin_b, got, eq_s);
 }
 
 // ---------------------------------------------------------------------------
@@ -464,12 +560,6 @@ __global__ void __launch_bounds__(SR_WARPS * 32, 2) kv_select_rows_kernel(const 
 // sequence share the work; a tile that spans sequences goes through each of them in turn.
 constexpr int ST_WARPS = 16, ST_ROWS = 32, ST_NT = 2;   // ST_NT: column tiles (of 8 blocks) of a warp at a time
 constexpr int ST_LD = key_at(SEL_CHUNK) + 8;   // padded: the fragments' rows fall into different banks
-
-__device__ __forceinline__ uint32_t s8x2_to_f16x2(uint32_t biased, uint32_t sel) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(prmt(biased, 0x64646464u, sel)), "r"(0x64806480u));
-  return r;
-}
 
 // Shared memory: the fragments, the keys of a piece, its pages and units, the rows' lists (kk places, k
 // rounded up to whole groups of 16) and forced blocks' keys, the warps' scratch.
