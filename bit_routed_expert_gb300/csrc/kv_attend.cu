@@ -311,7 +311,13 @@ cudaError_t launch_kv_attend(const bre_kv_cache* c, const KvTokens& tk, const ui
   const int H = c->n_kv_heads, D = c->head_dim, G = Hq / H;
   const AttendArgs a{static_cast<const uint8_t*>(c->pages), H,     G,     KvTable{tk.table, tk.B, tk.N, c->n_pages},
                      q, q_stride, tk.seq, tk.pos, tk.T, ids, k, scale, out, lse, err};
-  if (tk.T >= 16LL * tk.B) return launch_kv_attend_tiles(a, D, s);
+  // Tiles of 128 rows pay where neighbours share their blocks (16 tokens a sequence on average) and where there are
+  // enough of them: a tile takes its 80 us (16 blocks a token, G = 8) however few there are.  Four kv heads, 16
+  // blocks, us by token / by tile: G = 8, D = 128: 512 tokens 82 / 94, 1,024 154 / 128; G = 16, D = 64: 512 69 / 70,
+  // 1,024 128 / 121; G = 2 (64 tokens a tile, whose lists differ more), D = 64: 512 39 / 167; 8,192 tokens, G = 8:
+  // 1,281 / 447.
+  const long long pairs = (long long)tk.T * H;
+  if (tk.T >= 16LL * tk.B && pairs >= 2048 && pairs * G >= 16384) return launch_kv_attend_tiles(a, D, s);
   // CTAs of a (token, head): halves of blocks for every warp, as long as the GPU has room for them
   const long long rows = (long long)tk.T * H;
   const long long room = (long long)ar_ctas(D, G > 8 ? 2 : 1) * device_sm_count();

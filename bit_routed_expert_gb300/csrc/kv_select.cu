@@ -735,10 +735,12 @@ cudaError_t launch_kv_select(const bre_kv_cache* c, const KvTokens& tk, const ui
   const int H = c->n_kv_heads, D = c->head_dim;
   const SelectArgs a{c->bounds, c->bound_exp, H,   Hq / H, KvTable{tk.table, tk.B, tk.N, c->n_pages},
                      q, q_stride, tk.seq, tk.pos, tk.T, k, n_sink, n_local, ids, scores, err};
-  // tiles: the lists of 32 tokens must fit (up to about 170 blocks a token)
+  // Tiles of 32 tokens: the lists must fit (up to about 170 blocks a token), the tokens mostly be of one sequence
+  // (16 a sequence on average), and there must be enough of them.  256 blocks, four kv heads, us by token / by tile:
+  // 128 tokens of one sequence 17 / 19, 256 31 / 19; 128 tokens of eight 17 / 22, 256 30 / 19; 64 of eight 9 / 34.
   const size_t most = device_max_smem_optin() - 2048;   // less the kernels' static shared memory
   const size_t smem_t = select_tiles_smem(D, (k + 15) / 16 * 16);
-  if (tk.T >= 16LL * tk.B && smem_t <= most) {
+  if (tk.T >= 16LL * tk.B && (long long)tk.T * H >= 640 && smem_t <= most) {
     auto kern = D == 128 ? kv_select_tiles_kernel<128> : kv_select_tiles_kernel<64>;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), D == 128, (int)most);
     if (e != cudaSuccess) return e;

@@ -33,6 +33,16 @@ def same_cache(c, pages, bounds, bexp):
     assert torch.equal(c.bound_exp.cpu(), bexp)
 
 
+def copies_for_tiles(T, H, G):
+    """How often a call's tokens have to be repeated for select and attend to go by tiles of many tokens, not token
+    by token (their launchers' rules); every copy then lies differently in its tiles."""
+    return -(-max(2048, 16384 // G + 1) // (T * H))
+
+
+def repeated(b, copies):
+    return R.Batch(b.seq * copies, b.pos * copies, b.table, b.n_pages)
+
+
 def blank(b, H, D):
     g = torch.Generator().manual_seed(5)   # what was in memory before must not matter
     return (torch.randint(0, 256, (b.n_pages, H, 128 * (D + 1)), generator=g, dtype=torch.uint8),
@@ -174,15 +184,20 @@ def test_append_and_read_outside_the_cache(cuda_dev):
 
 # ------------------------------------------------------------------ select
 
-def check_select(dev, b, cache, q, k, sink, local, **kw):
+def check_select(dev, b, cache, q, k, sink, local):
+    """Token by token, and in tiles."""
     pages, bounds, bexp = cache
     c = on(dev, pages, bounds, bexp)
-    e = err_word(dev)
-    ids, scores = kv_select(q.to(dev), c, *b.on(dev), k, n_sink=sink, n_local=local, dev_err=e, **kw)
     want, ws, err = R.select(q, bounds, bexp, b.seq, b.pos, b.table, k, sink, local)
-    assert torch.equal(ids.cpu(), want)
-    assert torch.equal(scores.cpu(), ws.float())
-    assert int(e) == (BRE_DEVERR_PAGE if err else 0)
+    T, H = len(b.seq), bounds.shape[1]
+    for copies in (1, copies_for_tiles(T, H, q.shape[1] // H)):
+        e = err_word(dev)
+        ids, scores = kv_select(q.to(dev).repeat(copies, 1, 1), c, *repeated(b, copies).on(dev), k, n_sink=sink,
+                                n_local=local, dev_err=e)
+        for i, s in zip(ids.cpu().split(T), scores.cpu().split(T)):
+            assert torch.equal(i, want)
+            assert torch.equal(s, ws.float())
+        assert int(e) == (BRE_DEVERR_PAGE if err else 0)
 
 
 SELECT = [([1], [1], 1, 4, 1, 1), ([64], [2], 2, 1, 0, 0), ([4000], [1], 4, 8, 1, 2), ([4000], [40], 4, 8, 1, 2),
@@ -290,9 +305,9 @@ def test_select_special_queries(cuda_dev, T):
 def test_select_query_slices_and_one_workspace(cuda_dev):
     """One workspace, zeroed once, for calls of different sizes; queries as slices of wider rows."""
     D, H, G = 64, 2, 4
-    ws = torch.zeros(max(kv_select_workspace(T, H * G, H, D, 4, 64, 16) for T in (1, 4, 200)), dtype=torch.uint8,
+    ws = torch.zeros(max(kv_select_workspace(T, H * G, H, D, 4, 64, 16) for T in (1, 4, 400)), dtype=torch.uint8,
                      device=cuda_dev)
-    for lens, new in (([4000], [1]), ([4000, 1000, 30, 2000], [1] * 4), ([3000], [200]), ([4000], [1])):
+    for lens, new in (([4000], [1]), ([4000, 1000, 30, 2000], [1] * 4), ([3000], [400]), ([4000], [1])):
         b = R.batch(lens, new, blocks=64)
         cache = R.filled(b, lens, H, D)
         wide = R.rows(4, len(b.seq), H * G + 3, D)
@@ -303,27 +318,27 @@ def test_select_query_slices_and_one_workspace(cuda_dev):
 
 # ------------------------------------------------------------------ attend
 
-def check_attend(dev, b, pages, q, ids, scale=None, cache=None, **kw):
-    H = pages.shape[1]
+def check_attend(dev, b, pages, q, ids, scale=None):
+    """Token by token, and in tiles."""
+    T, H = len(b.seq), pages.shape[1]
     D = q.shape[2]
     scale = D ** -0.5 if scale is None else scale
-    c = cache
-    if c is None:
-        c = on(dev, pages, torch.zeros((b.n_pages, H, 2, D), dtype=torch.int8),
-               torch.zeros((b.n_pages, H), dtype=torch.int8))
-    e = err_word(dev)
-    out, lse = kv_attend(q.to(dev), c, *b.on(dev), ids.to(dev), scale=scale, dev_err=e, **kw)
+    c = on(dev, pages, torch.zeros((b.n_pages, H, 2, D), dtype=torch.int8),
+           torch.zeros((b.n_pages, H), dtype=torch.int8))
     want, wl, mass, size, err = R.attend(q, pages, b.seq, b.pos, b.table, ids, scale)
-    assert int(e) == (BRE_DEVERR_PAGE if err else 0)
-    out, lse = out.cpu().double(), lse.cpu().double()
     d = (D * 2.0 ** -23 * size + 2.0 ** -20)
     tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2 * d)[..., None] * mass + 1e-30
-    assert bool((out - want).abs().le(tol).all()), float(((out - want).abs() / tol).max())
     empty = wl == -math.inf
-    assert torch.equal(lse == -math.inf, empty) and float(out[empty].abs().sum()) == 0
-    off = (lse - wl)[~empty].abs()
-    assert bool((off <= d[~empty] + 2.0 ** -22 * wl[~empty].abs()).all()), float(off.max())
-    return out
+    for copies in (1, copies_for_tiles(T, H, q.shape[1] // H)):
+        e = err_word(dev)
+        outs, lses = kv_attend(q.to(dev).repeat(copies, 1, 1), c, *repeated(b, copies).on(dev),
+                               ids.to(dev).repeat(copies, 1, 1), scale=scale, dev_err=e)
+        assert int(e) == (BRE_DEVERR_PAGE if err else 0)
+        for out, lse in zip(outs.cpu().double().split(T), lses.cpu().double().split(T)):
+            assert bool((out - want).abs().le(tol).all()), float(((out - want).abs() / tol).max())
+            assert torch.equal(lse == -math.inf, empty) and float(out[empty].abs().sum()) == 0
+            off = (lse - wl)[~empty].abs()
+            assert bool((off <= d[~empty] + 2.0 ** -22 * wl[~empty].abs()).all()), float(off.max())
 
 
 def some_ids(b, H, k, seed=0):
@@ -443,19 +458,21 @@ def test_attend_nan_stays_in_its_rows(cuda_dev, T):
         x[int(b.table[0, last // 64]), :, last % 64 + 1:] = 0xFF
     vc[int(b.table[0, 2]), 1, 4], vs[int(b.table[0, 2]), 1, 4] = 0, 255
     c = on(cuda_dev, pages, torch.zeros((b.n_pages, H, 2, D), dtype=torch.int8), torch.zeros((b.n_pages, H), dtype=torch.int8))
-    out, lse = kv_attend(q.to(cuda_dev), c, *b.on(cuda_dev), ids.to(cuda_dev), scale=0.125)
     want, wl, _, _, _ = R.attend(q, pages, b.seq, b.pos, b.table, ids, 0.125)
-    out, lse = out.cpu().double(), lse.cpu().double()
-    assert torch.equal(out.isnan(), want.isnan()) and torch.equal(lse.isnan(), wl.isnan())
     ok = ~want.isnan()
-    assert float((out - want)[ok].abs().max()) <= 2.0 ** -7 * float(clean[ok].abs().max())
+    for copies in (1, copies_for_tiles(T, H, G)):
+        outs, lses = kv_attend(q.to(cuda_dev).repeat(copies, 1, 1), c, *repeated(b, copies).on(cuda_dev),
+                               ids.to(cuda_dev).repeat(copies, 1, 1), scale=0.125)
+        for out, lse in zip(outs.cpu().double().split(T), lses.cpu().double().split(T)):
+            assert torch.equal(out.isnan(), want.isnan()) and torch.equal(lse.isnan(), wl.isnan())
+            assert float((out - want)[ok].abs().max()) <= 2.0 ** -7 * float(clean[ok].abs().max())
 
 
 def test_attend_query_slices_workspace_and_repeats(cuda_dev):
     """One workspace for calls of different sizes; the same call gives the same bits."""
     D, H, G = 128, 2, 4
-    sizes = (([2000], [1]), ([1000, 300], [1, 1]), ([600], [200]), ([2000], [1]))
-    ws = torch.zeros(max(kv_attend_workspace(T, H * G, H, D, 2, 12) for T in (1, 2, 200)), dtype=torch.uint8,
+    sizes = (([2000], [1]), ([1000, 300], [1, 1]), ([2200], [2100]), ([2000], [1]))
+    ws = torch.zeros(max(kv_attend_workspace(T, H * G, H, D, 2, 12) for T in (1, 2, 2100)), dtype=torch.uint8,
                      device=cuda_dev)
     for lens, new in sizes:
         b = R.batch(lens, new)
@@ -496,19 +513,22 @@ def test_pages_past_four_gigabytes(cuda_dev, T):
     at = [int(b.table[s, p // 64]) for s, p in zip(b.seq, b.pos)]
     assert torch.equal(ko.cpu().double(), torch.stack([kk[a, :, p % 64] for a, p in zip(at, b.pos)]))
     assert torch.equal(vo.cpu().double(), torch.stack([vv[a, :, p % 64] for a, p in zip(at, b.pos)]))
-    ids, _ = kv_select(q.to(cuda_dev), c, *on_dev, 4)
-    assert torch.equal(ids.cpu(), R.select(q, bounds, bexp, b.seq, b.pos, b.table, 4, 1, 2)[0])
-    out, _ = kv_attend(q.to(cuda_dev), c, *on_dev, ids)
-    want, _, mass, size, _ = R.attend(q, pages, b.seq, b.pos, b.table, ids.cpu(), D ** -0.5)
+    want_ids = R.select(q, bounds, bexp, b.seq, b.pos, b.table, 4, 1, 2)[0]
+    want, _, mass, size, _ = R.attend(q, pages, b.seq, b.pos, b.table, want_ids, D ** -0.5)
     tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2 * (D * 2.0 ** -23 * size + 2.0 ** -20))[..., None] * mass
-    assert bool(((out.cpu().double() - want).abs() <= tol).all())
+    for copies in (1, copies_for_tiles(T, H, G)):
+        on_dev = repeated(far, copies).on(cuda_dev)
+        ids, _ = kv_select(q.to(cuda_dev).repeat(copies, 1, 1), c, *on_dev, 4)
+        out, _ = kv_attend(q.to(cuda_dev).repeat(copies, 1, 1), c, *on_dev, ids)
+        assert all(torch.equal(i, want_ids) for i in ids.cpu().split(T))
+        assert all(bool(((o - want).abs() <= tol).all()) for o in out.cpu().double().split(T))
 
 
-@pytest.mark.parametrize("T", [1, 70])
-def test_a_step_on_another_stream_and_in_a_graph(cuda_dev, T):
+@pytest.mark.parametrize("T,G", [(1, 4), (70, 4), (1100, 8)])
+def test_a_step_on_another_stream_and_in_a_graph(cuda_dev, T, G):
     """append, select and attend of one step: on a side stream, and captured and replayed on new inputs."""
-    D, H, G, k = 64, 2, 4, 6
-    lens = [900]
+    D, H, k = 64, 2, 6
+    lens = [1200]
     b = R.batch(lens, [T])
     pages, bounds, bexp = R.filled(b, lens, H, D)
     c = on(cuda_dev, pages, bounds, bexp)
