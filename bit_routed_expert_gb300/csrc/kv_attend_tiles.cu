@@ -10,7 +10,8 @@
 // Fourteen warps:
 //   warps 0-3   softmax: a thread a row; S from tensor memory, weights back over it as FP16
 //   warps 4-7   turn the keys' codes into FP16 (exact) in 128-byte-swizzled shared memory
-//   warps 8-11  the values'; both have the next two blocks' codes under way into registers
+//   warps 8-11  the values'; two warps for the even blocks and two for the odd ones, so that a warp has twice the
+//               time for its waits and loads
 //   warp 12     merges the tokens' lists: the least next block over all tokens, and which tokens list it
 //   warp 13     issues the MMAs: S = Q K^T into tensor memory, O += P V with P read from tensor memory
 // K is K-major, V lies as it is in the cache (a token's channels in a row), which is the MN-major
@@ -189,11 +190,11 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
   const int t0 = blockIdx.x * per, h = blockIdx.y, nt = min(per, a.T - t0), rows = nt * a.G;
 
   if (tid == 0) {
-    for (int i = 0; i < AT_RING; ++i) mbar_init(&blk_full[i], 1), mbar_init(&sc_full[i], 4), mbar_init(&blk_empty[i], 4 + AT_CODES / 32 + 1);
+    for (int i = 0; i < AT_RING; ++i) mbar_init(&blk_full[i], 1), mbar_init(&sc_full[i], 2), mbar_init(&blk_empty[i], 4 + AT_CODES / 64 + 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 4);
+      mbar_init(&k_full[i], 2);
       mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 4);
+      mbar_init(&v_full[i], 2);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
         idr[j] = a.ids + ((size_t)(t0 + (live ? tl : 0)) * a.H + h) * a.k;
         advance(j);
       }
-      for (int i = 0;;) {
+      for (int i = 0, ends = 0;;) {
         const uint32_t key = __reduce_min_sync(0xffffffffu, min(min(cur[0], cur[1]), min(cur[2], cur[3])));
         Block b;
         b.page = -1;
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
           mbar_arrive(&blk_full[i % AT_RING]);
         }
         ++i;
-        if (key == 0xFFFFFFFFu) break;
+        if (key == 0xFFFFFFFFu && ++ends == 2) break;   // one for the even blocks' warps, one for the odd ones'
       }
     } else {
       // ---- MMA: kind::f16, FP32 sums, M = 128; second product with an MN-major B
@@ -378,79 +379,59 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       mbar_wait_bounded(&drain, 0, AT_WAIT);
     }
   } else if (warp >= 4) {
-    // ---- codes to FP16: 128 threads for the keys, 128 for the values, 16 codes (a 16-byte load) at a time.
-    // A warp works on its own rows; one arrival a warp.
-    constexpr int CH = D / 16, NL = KV_BLOCK * CH / 128;   // pieces a row, loads a thread
+    // ---- codes to FP16: 64 threads for the keys (values) of every other block, 16 codes (a 16-byte load) at a
+    // time.  A warp works on its own rows; one arrival a warp.
+    constexpr int CH = D / 16, NL = KV_BLOCK * CH / 64;   // pieces a row, loads a thread
     const bool values = warp >= 8;
-    const int dt = tid & 127;
-    uint64_t* const full = values ? v_full : k_full;
-    uint64_t* const empty = values ? v_empty : k_empty;
-    uint4 cur[NL], nxt[NL];
-    int e2 = 0, e2n = 0;     // key scales of tokens lane and lane + 32: this block's, the next one's
-    int ev = 0, evn = 0;     // value scale of token dt (keys' threads)
-    int page = 0, n = 0;     // of the block that is loaded next
-    const uint8_t* pg = nullptr;
-    auto take = [&](int i) {
-      if (!warp_wait(&blk_full[i % AT_RING], i / AT_RING)) {
-        page = -1;
-        return;
-      }
-      page = ring[i % AT_RING].page;
+    const int dt = tid & 63, st = (warp >> 1) & 1;        // st: parity of the blocks, and so the stage
+    uint64_t* const full = values ? &v_full[st] : &k_full[st];
+    uint64_t* const empty = values ? &v_empty[st] : &k_empty[st];
+    uint4 cur[NL];
+    int e2 = 0, ev = 0;     // key scales of tokens lane and lane + 32; value scale of token dt (keys' threads)
+    int n = 0;
+    // of tokens that no row sees (they may never have been written) neither codes nor scales are read
+    auto take_and_load = [&](int i) -> bool {
+      if (!warp_wait(&blk_full[i % AT_RING], i / AT_RING)) return false;
+      const int page = ring[i % AT_RING].page;
       n = ring[i % AT_RING].n;
       __syncwarp();
       if (lane == 0) mbar_arrive(&blk_empty[i % AT_RING]);
-      pg = a.pages + ((size_t)max(page, 0) * a.H + h) * kv_page_bytes(D);
-    };
-    // of tokens that no row sees (they may never have been written) neither codes nor scales are read
-    auto load = [&] {
+      if (page < 0) return false;
+      const uint8_t* pg = a.pages + ((size_t)page * a.H + h) * kv_page_bytes(D);
       const uint4* src = reinterpret_cast<const uint4*>(pg + (values ? KV_BLOCK * D : 0)) + dt;
       const uint8_t* sc = pg + 2 * KV_BLOCK * D;
 #pragma unroll
-      for (int j = 0; j < NL; ++j) nxt[j] = (dt + j * 128) / CH < n ? __ldg(src + j * 128) : make_uint4(0, 0, 0, 0);
-      e2n = lane < n ? (int)__ldg(sc + lane) : 0;
-      if (lane + 32 < n) e2n |= (int)__ldg(sc + 32 + lane) << 8;
-      if (!values) evn = dt < n ? (int)__ldg(sc + KV_BLOCK + dt) : 127;
+      for (int j = 0; j < NL; ++j) cur[j] = (dt + j * 64) / CH < n ? __ldg(src + j * 64) : make_uint4(0, 0, 0, 0);
+      if (!values) {
+        e2 = lane < n ? (int)__ldg(sc + lane) : 0;
+        if (lane + 32 < n) e2 |= (int)__ldg(sc + 32 + lane) << 8;
+        ev = dt < n ? (int)__ldg(sc + KV_BLOCK + dt) : 127;
+      }
+      return true;
     };
     // where a thread puts its 16 values (token x0, channels 16 c ..; further loads are whole multiples of 8
     // tokens on): two swizzled pieces of 16 bytes.  The lanes of odd panels start with the second piece, so that
     // eight lanes meet all banks.
     const int x0 = dt / CH, c = dt % CH;
     const bool second = (c / 4) & 1;
-    const int p0 = (values ? M::v : M::k) + (c / 4) * PANEL + x0 * 128 + (((2 * (c % 4)) ^ (x0 & 7)) << 4);
+    const int p0 = (values ? M::v : M::k) + st * M::KV + (c / 4) * PANEL + x0 * 128 + (((2 * (c % 4)) ^ (x0 & 7)) << 4);
     unsigned char* const put0 = sm + (second ? p0 ^ 16 : p0);
     unsigned char* const put1 = sm + (second ? p0 : p0 ^ 16);
-    auto shift = [&] {
-#pragma unroll
-      for (int j = 0; j < NL; ++j) cur[j] = nxt[j];
-      e2 = e2n, ev = evn;
-    };
-    int left = 0;   // blocks in registers
-    take(0);
-    if (page >= 0) {
-      load();
-      shift();
-      left = 1;
-      take(1);
-      if (page >= 0) load(), left = 2;
-    }
 #pragma unroll 1
-    for (int i = 0; left > 0; ++i) {
-      const int st = i & 1;
-      // the block's largest key scale (a NaN row's does not count: its codes are zeros)
-      const int ea = e2 & 255, eb = e2 >> 8;
-      const int top = __reduce_max_sync(0xffffffffu, max(ea == KV_NAN ? 0 : ea, eb == KV_NAN ? 0 : eb));
-      if (!warp_wait(&empty[st], (i >> 1) + 1)) break;
+    for (int i = st; take_and_load(i); i += 2) {
+      if (!warp_wait(empty, (i >> 1) + 1)) break;
+      int top = 0;
       if (!values) {
+        // the block's largest key scale (a NaN row's does not count: its codes are zeros)
+        const int ea = e2 & 255, eb = e2 >> 8;
+        top = __reduce_max_sync(0xffffffffu, max(ea == KV_NAN ? 0 : ea, eb == KV_NAN ? 0 : eb));
         // the scales go to the softmax first.  Their place is free: S of two blocks ago has been formed, for which
-        // the weights of four blocks ago must have been used
+        // the weights of four blocks ago must have been used.  A NaN row makes its token's logit NaN.
         const int sp = i % AT_RING;
-        if (dt < KV_BLOCK) {
-          // a NaN row makes its token's logit NaN
-          const bool nan = (dt < 32 ? ea : eb) == KV_NAN || ev == KV_NAN;
-          ev_f[sp][dt] = nan ? __int_as_float(0x7FC00000) : (float)(ev - 127);
-          ev_inv[sp][dt] = pow2f(127 - min(ev, 253));
-          if (dt == 0) ek_top[sp] = pow2f(max(top, 1) - 127);
-        }
+        const bool nan = (dt < 32 ? ea : eb) == KV_NAN || ev == KV_NAN;
+        ev_f[sp][dt] = nan ? __int_as_float(0x7FC00000) : (float)(ev - 127);
+        ev_inv[sp][dt] = pow2f(127 - min(ev, 253));
+        if (dt == 0) ek_top[sp] = pow2f(max(top, 1) - 127);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_full[sp]);
       }
@@ -465,27 +446,19 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
           o[2 * k + 1] = e4m3x2_to_f16x2(u[k] >> 16);
         }
         if (!values) {
-          const int x = x0 + j * (128 / CH);
+          const int x = x0 + j * (64 / CH);
           const int both = __shfl_sync(0xffffffffu, e2, x & 31);
           const int d = max(top - (x < 32 ? both & 255 : both >> 8), 0);
           const uint32_t f = d < 15 ? (uint32_t)(15 - d) << 10 : d < 25 ? 1u << (24 - d) : 0u;   // 2^-d
 #pragma unroll
           for (int k = 0; k < 8; ++k) o[k] = mul_f16x2(o[k], f | f << 16);
         }
-        const int at = st * M::KV + j * (128 / CH) * 128;
-        *reinterpret_cast<uint4*>(put0 + at) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(put1 + at) = make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint4*>(put0 + j * (64 / CH) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(put1 + j * (64 / CH) * 128) = make_uint4(o[4], o[5], o[6], o[7]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[st]);
-      --left;
-      shift();
-      if (page >= 0) take(i + 2);
-      if (page >= 0) {
-        load();
-        ++left;
-      }
+      if (lane == 0) mbar_arrive(full);
     }
   } else {
     // ---- softmax: row tid
