@@ -206,7 +206,8 @@ static bre_status kv_check(const bre_kv_cache* c, const int32_t* seq, const int3
       N <= 0 || !table || (T > 0 && (!seq || !pos)))
     return BRE_ERR_ARG;
   if (c->head_dim != 64 && c->head_dim != 128) return BRE_ERR_UNSUPPORTED;
-  if ((int64_t)T * c->n_kv_heads > INT32_MAX / 2 || N > INT32_MAX / 64) return BRE_ERR_UNSUPPORTED;
+  if (c->n_kv_heads > 65535 || (int64_t)T * c->n_kv_heads > INT32_MAX / 2 || N > INT32_MAX / 64)
+    return BRE_ERR_UNSUPPORTED;
   if (!aligned(c->pages, 16) || !aligned(c->bounds, 16) || !aligned(seq, 4) || !aligned(pos, 4) || !aligned(table, 4))
     return BRE_ERR_ARG;
   return BRE_OK;

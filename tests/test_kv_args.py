@@ -41,7 +41,7 @@ def attend(c=None, q=P, qs=256, Hq=4, T=3, ids=P, k=4, scale=1.0, out=P, ws=None
 BAD_CACHES = [({"pages": 0}, BRE_ERR_ARG), ({"bounds": 0}, BRE_ERR_ARG), ({"bound_exp": 0}, BRE_ERR_ARG),
               ({"n_pages": 0}, BRE_ERR_ARG), ({"n_kv_heads": 0}, BRE_ERR_ARG), ({"n_pages": -1}, BRE_ERR_ARG),
               ({"head_dim": 96}, BRE_ERR_UNSUPPORTED), ({"head_dim": 0}, BRE_ERR_UNSUPPORTED),
-              ({"head_dim": 256}, BRE_ERR_UNSUPPORTED), ({"pages": (1 << 20) + 8}, BRE_ERR_ARG),
+              ({"head_dim": 256}, BRE_ERR_UNSUPPORTED), ({"n_kv_heads": 65536}, BRE_ERR_UNSUPPORTED), ({"pages": (1 << 20) + 8}, BRE_ERR_ARG),
               ({"bounds": (1 << 20) + 4}, BRE_ERR_ARG)]
 
 
