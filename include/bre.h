@@ -357,7 +357,8 @@ bre_status kv_select(const bre_kv_cache *cache, const void *q_bf16, int64_t q_st
  *   s_x = scale * q . key_x,  out = sum_x exp(s_x) value_x / sum_x exp(s_x),  lse = log sum_x exp(s_x)
  * A row that sees no token gives zeros and lse = -inf; one that sees a token whose key or value row
  * is NaN gives NaN and lse = NaN.  Logits, maxima and sums are FP32; the
- * probabilities enter the second product as FP16 (relative error 2^-11), the codes exactly.
+ * probabilities enter the second product as FP16 (relative error 2^-11 for those within 2^-22 of the
+ * row's largest, the value's scale counted in; absolute below), the codes exactly.
  *   ids [T][n_kv_heads][k] int32, any order; out [T][n_heads][D] BF16, 32-byte aligned; lse [T][n_heads] FP32 or
  *   NULL (natural logarithm).  ws: as in kv_select, kv_attend_workspace(...) bytes.  Requires G <= 16, k <= 256. */
 size_t kv_attend_workspace(int T, int n_heads, int n_kv_heads, int head_dim, int B, int k);
