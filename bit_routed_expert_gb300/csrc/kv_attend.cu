@@ -310,7 +310,7 @@ cudaError_t launch_kv_attend(const bre_kv_cache* c, const KvTokens& tk, const ui
                              cudaStream_t s) {
   const int H = c->n_kv_heads, D = c->head_dim, G = Hq / H;
   const AttendArgs a{static_cast<const uint8_t*>(c->pages), H,     G,     KvTable{tk.table, tk.B, tk.N, c->n_pages},
-                     q, q_stride, tk.seq, tk.pos, tk.T, ids, k, scale, out, lse, err};
+                     q, q_stride, tk.seq, tk.pos, tk.T, ids, k, scale, out, lse, err, 0};
   // Tiles of 128 rows pay where neighbours share their blocks (16 tokens a sequence on average) and where there are
   // enough of them: a tile takes its 80 us (16 blocks a token, G = 8) however few there are.  Four kv heads, 16
   // blocks, us by token / by tile: G = 8, D = 128: 512 tokens 82 / 94, 1,024 154 / 128; G = 16, D = 64: 512 69 / 70,

@@ -34,6 +34,7 @@ struct AttendArgs {
   uint16_t* out;
   float* lse;
   int32_t* err;
+  long long wait;   // budget (cycles) of the tile kernel's waits where one is set
 };
 
 // 128 rows (tokens times query heads) at a time (kv_attend_tiles.cu)

@@ -34,7 +34,7 @@ constexpr int AT_THREADS = 128 + AT_CODES + 64;
 constexpr int W_MERGE = (128 + AT_CODES) / 32, W_MMA = W_MERGE + 1;
 constexpr int AT_RING = 4;                          // blocks that the merging warp may be ahead
 constexpr float AT_SLACK = 7.0f;                    // growth of a row's maximum (log2) that needs no rescaling
-constexpr long long AT_WAIT = 4000000000LL;         // cycles before a wait gives up (~2 s)
+constexpr long long AT_WAIT = 4000000000LL;         // cycles before a wait gives up (~2 s), if no budget is set
 
 struct Block {
   int page, id, n, pad;    // n: tokens that some row sees; page < 0: the end
@@ -172,7 +172,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-template <int D>
+// PATIENT: the waits have the default budget; else the one that was set (a budget that is not a constant costs 5 %
+// of the kernel's time, even where only the out-of-line wait knows it).
+template <int D, bool PATIENT>
 __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const AttendArgs a) {
   using M = TilesMem<D>;
   constexpr int PANEL_Q = 128 * 128, PANEL = KV_BLOCK * 128;
@@ -251,7 +253,8 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
 
   bool ok = true;   // no wait of this thread has given up
   auto wait = [&](uint64_t* bar, int phase) {
-    if (ok && !try_wait_ms(bar, phase & 1) && !wait_long(bar, phase & 1)) {
+    if (ok && (PATIENT ? !try_wait_ms(bar, phase & 1) && !wait_long(bar, phase & 1)
+                       : !mbar_wait_bounded(bar, phase & 1, a.wait))) {
       ok = false;
       set_err(a.err, BRE_DEVERR_TIMEOUT);
     }
@@ -602,27 +605,30 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
   }
 }
 
-template <int D>
+template <int D, bool PATIENT>
 cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};   // devices on which the kernel may have its shared memory
   int dev = 0;
   cudaGetDevice(&dev);
   const uint64_t bit = 1ull << (dev & 63);
   if (!(done.load(std::memory_order_acquire) & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(kv_attend_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(kv_attend_tiles_kernel<D, PATIENT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                TilesMem<D>::bytes);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_release);
   }
   const int per = 128 / a.G;
-  return launch_k(kv_attend_tiles_kernel<D>, dim3((unsigned)((a.T + per - 1) / per), (unsigned)a.H), dim3(AT_THREADS),
+  return launch_k(kv_attend_tiles_kernel<D, PATIENT>, dim3((unsigned)((a.T + per - 1) / per), (unsigned)a.H), dim3(AT_THREADS),
                   TilesMem<D>::bytes, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attend_tiles(const AttendArgs& a, int D, cudaStream_t s) {
-  return D == 128 ? launch<128>(a, s) : launch<64>(a, s);
+cudaError_t launch_kv_attend_tiles(const AttendArgs& args, int D, cudaStream_t s) {
+  AttendArgs a = args;
+  a.wait = ffn_wait_budget(0);   // 0: none set
+  if (a.wait) return D == 128 ? launch<128, false>(a, s) : launch<64, false>(a, s);
+  return D == 128 ? launch<128, true>(a, s) : launch<64, true>(a, s);
 }
 
 }  // namespace bre

@@ -368,8 +368,8 @@ bre_status kv_attend(const bre_kv_cache *cache, const void *q_bf16, int64_t q_st
                      bre_stream_t stream);
 
 /* Budget, in SM clock cycles, of the bounded waits inside the expert FFN kernels
- * (moe_expert_ffn, both paths) for calls made after this one, from any thread of the process;
- * 0 restores the defaults (about 1 s on the decode path, 2 s on the grouped-GEMM path).  A wait
+ * (moe_expert_ffn, both paths) and kv_attend's tile kernel for calls made after this one, from any
+ * thread of the process; 0 restores the defaults (about 1 s on the decode path, 2 s on the others).  A wait
  * that runs out sets BRE_DEVERR_TIMEOUT in the call's dev_err; the kernel then waits, with the
  * default budget, for the copies and tensor-core operations it has in flight, frees its tensor
  * memory and returns, and that call's outputs are invalid.  The next call on the same workspace

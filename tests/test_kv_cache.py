@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import kv_reference as R
-from bit_routed_expert_gb300 import (BreError, KvCache, StepGraph, kv_append, kv_attend, kv_attend_workspace, kv_read,
+from bit_routed_expert_gb300 import (BreError, KvCache, StepGraph, _lib, kv_append, kv_attend, kv_attend_workspace, kv_read,
                                      kv_select, kv_select_workspace)
 from bit_routed_expert_gb300._lib import BRE_DEVERR_PAGE
 
@@ -600,3 +600,27 @@ def test_binding_refuses(cuda_dev):
     none = [torch.zeros(0, dtype=torch.int32, device=cuda_dev)] * 2
     out, lse = kv_attend(q[:0], c, *none, table, ids[:0])
     assert out.shape == (0, 4, 64) and kv_read(c, *none, table)[0].shape == (0, 2, 64)
+
+
+def test_attend_wait_budget_runs_out_then_the_next_call_is_clean(cuda_dev):
+    """The tile kernel's waits with a budget of one cycle: the call returns and sets the bit; the next call, with
+    the default budget, gives the bits of the one before."""
+    D, H, G, k = 64, 2, 8, 6
+    b = R.batch([1200], [1100])
+    pages, bounds, bexp = R.filled(b, [1200], H, D)
+    c = on(cuda_dev, pages, bounds, bexp)
+    q, ids, tokens = R.rows(3, 1100, H * G, D).to(cuda_dev), some_ids(b, H, k).to(cuda_dev), b.on(cuda_dev)
+    e = err_word(cuda_dev)
+    out, lse = kv_attend(q, c, *tokens, ids, dev_err=e)
+    assert int(e) == 0
+    L = _lib.load()
+    try:
+        assert L.bre_set_ffn_wait_limit(1) == _lib.BRE_OK
+        kv_attend(q, c, *tokens, ids, dev_err=e)
+        torch.cuda.synchronize()
+    finally:
+        assert L.bre_set_ffn_wait_limit(0) == _lib.BRE_OK
+    assert int(e) == _lib.BRE_DEVERR_TIMEOUT
+    e.zero_()
+    again, lse2 = kv_attend(q, c, *tokens, ids, dev_err=e)
+    assert int(e) == 0 and torch.equal(again, out) and torch.equal(lse2, lse)
