@@ -10,9 +10,15 @@ namespace {
 // bring the block's bounds up to date without atomics.
 //
 // A lane holds eight channels, so D / 8 lanes hold a row and a warp two or four rows at a time: 16-byte loads,
-// 8-byte stores, a row's maximum by three or four shuffles.  Keys and values of four row groups are
-// loaded before the first is used.  A chunk of 64 tokens gives long calls whole blocks; with few tokens the
-// chunks shrink to one token and a call spreads over the GPU.
+// 8-byte stores, a row's maximum by three or four shuffles.  A chunk of 64 tokens gives long calls whole
+// blocks; with few tokens the chunks shrink to one token and a call spreads over the GPU.
+//
+// A call is a chain of loads that wait for one another, and for long calls half of its time is arithmetic
+// (4.8 million warp instructions for 8,192 tokens of 8 heads of 128).  So the chain is kept short: positions,
+// then the page's number beside the first rows, then two rows a lane in flight, each replaced as it is used; 9.8 us
+// for those tokens, against 11.2 us with the rows asked for once the run and its page were known.  Four rows a lane
+// take 119 registers: 9.6 us there, but 15.6 against 13.0 us for 6,418 ragged tokens of 4 heads of 64; six CTAs an SM
+// instead of five 10.5 us.
 constexpr int KA_WARPS = 4;
 
 // A row of eight channels a lane; LR lanes hold the row.
@@ -35,8 +41,9 @@ struct RowCode {
     float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(u[i] << 16) * down;
-      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u) * down;
+      const float2 y = __fmul2_rn(make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u)),
+                                  make_float2(down, down));
+      x[2 * i] = y.x, x[2 * i + 1] = y.y;
     }
     // (the conversion saturates what lies above KV_MAX)
     codes = make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16, e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
@@ -45,80 +52,111 @@ struct RowCode {
 };
 
 template <int D>
-__global__ void __launch_bounds__(KA_WARPS * 32)
+__global__ void __launch_bounds__(KA_WARPS * 32, 5)
     kv_append_kernel(uint8_t* __restrict__ pages, int8_t* __restrict__ bounds, int8_t* __restrict__ bexp, int H, KvTable tab,
                      const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, long long k_stride, long long v_stride,
                      const int32_t* __restrict__ seq, const int32_t* __restrict__ pos, int T, int chunk, int32_t* err) {
   constexpr int LR = D / 8, RW = 32 / LR;       // lanes a row, rows a warp
-  constexpr int RC = RW * KA_WARPS, UN = 4;     // rows of the CTA at a time, of which UN steps are in flight
+  constexpr int RC = RW * KA_WARPS, UN = 2;     // rows of the CTA at a time, of which UN steps are in flight
   __shared__ float s_hi[KA_WARPS][D], s_lo[KA_WARPS][D], s_max[KA_WARPS];
-  __shared__ int s_end;
+  __shared__ int s_other[2][KA_WARPS];
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lr = lane % LR;
   const int h = blockIdx.y, c0 = blockIdx.x * chunk, c1 = min(c0 + chunk, T);
+  int par = 0;   // of s_other: the barrier of one pass also keeps the next but one from overtaking it
   for (int t = c0; t < c1;) {
+    // What the run needs is read in two steps, each of loads that do not wait for one another: first the
+    // positions, then the page's number, the first rows and (page known) the old bounds.
     const int s = __ldg(seq + t), p = __ldg(pos + t), blk = p / KV_BLOCK;
-    // this run's end: the first token of another block
-    __syncthreads();
-    if (tid == 0) s_end = T;
-    __syncthreads();
-    bool found = p < 0;
-    if (found && tid == 0) s_end = t + 1;
-    for (int i0 = t + 1; i0 < T && !found; i0 += KA_WARPS * 32) {
-      const int i = i0 + tid;
-      const int pi = i < T ? __ldg(pos + i) : -1;
-      const bool other = pi >= 0 && (__ldg(seq + i) != s || pi / KV_BLOCK != blk);
-      if (other) atomicMin(&s_end, i);
-      found = __syncthreads_or(other);
+    const int bs = t ? __ldg(seq + t - 1) : 0, bp = t ? __ldg(pos + t - 1) : 0;
+    const int q0 = t + warp * RW + lane / LR;   // this lane's first row
+    int slot[UN], sq[UN];
+#pragma unroll
+    for (int j = 0; j < UN; ++j) {
+      const int r = q0 + j * RC;
+      slot[j] = r < T ? __ldg(pos + r) : -1, sq[j] = r < T ? __ldg(seq + r) : -1;
     }
-    __syncthreads();
-    const int t0 = t, t1 = s_end;
-    t = t1;
-    if (p < 0) continue;
+    int i = t + 1 + tid;
+    int pi = i < T ? __ldg(pos + i) : -1, si = i < T ? __ldg(seq + i) : -1;
+    if (p < 0) {
+      ++t;
+      continue;
+    }
     // a run that started in a chunk before belongs to it
-    int back = t0 - 1;
-    while (back >= 0 && __ldg(pos + back) < 0) --back;
-    if (back >= 0 && __ldg(seq + back) == s && __ldg(pos + back) / KV_BLOCK == blk) continue;
-    const int page = kv_page(tab, s, blk, tid == 0 ? err : nullptr);
+    bool mine = t == 0 || bp < 0 || bs != s || bp / KV_BLOCK != blk;
+    if (t && bp < 0) {
+      int back = t - 2;
+      while (back >= 0 && __ldg(pos + back) < 0) --back;
+      mine = back < 0 || __ldg(seq + back) != s || __ldg(pos + back) / KV_BLOCK != blk;
+    }
+    const int page = mine ? kv_page(tab, s, blk, tid == 0 ? err : nullptr) : -1;
+    uint4 kw[UN], vw[UN];
+#pragma unroll
+    for (int j = 0; j < UN; ++j) {   // (rows of the block behind another block's are of another run: not stored below)
+      const int r = q0 + j * RC;
+      const bool in = mine && slot[j] >= 0 && sq[j] == s && slot[j] / KV_BLOCK == blk;
+      kw[j] = in ? __ldg(reinterpret_cast<const uint4*>(k + r * k_stride + h * D) + lr) : make_uint4(0, 0, 0, 0);
+      vw[j] = in ? __ldg(reinterpret_cast<const uint4*>(v + r * v_stride + h * D) + lr) : make_uint4(0, 0, 0, 0);
+    }
+    // the run's end: the first token of another block
+    int t1 = T;
+    for (int i0 = t + 1;;) {
+      const uint32_t other = __ballot_sync(0xffffffffu, pi >= 0 && (si != s || pi / KV_BLOCK != blk));
+      if (lane == 0) s_other[par][warp] = other ? i0 + warp * 32 + __ffs(other) - 1 : T;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < KA_WARPS; ++w) t1 = min(t1, s_other[par][w]);
+      par ^= 1;
+      i0 += KA_WARPS * 32;
+      if (t1 < T || i0 >= T) break;
+      i = i0 + tid;
+      pi = i < T ? __ldg(pos + i) : -1, si = i < T ? __ldg(seq + i) : -1;
+    }
+    t = t1;
+    if (!mine) continue;
     if (page < 0) {
       if (tid == 0) set_err(err, BRE_DEVERR_PAGE);   // a token to store needs a page
       continue;
     }
     const size_t ph = (size_t)page * H + h;
     uint8_t* pg = pages + ph * kv_page_bytes(D);
+    int8_t* bd = bounds + ph * 2 * D + tid;
+    const bool begun = p % KV_BLOCK != 0;   // before this call
+    int oe = -127, oh = 0, ol = 0;
+    if (begun) {
+      oe = bexp[ph];
+      if (tid < D) oh = bd[0], ol = bd[D];
+    }
     float hi[8], lo[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
-    for (int r0 = t0 + warp * RW + lane / LR; r0 - lane / LR < t1; r0 += UN * RC) {
-      uint4 kw[UN], vw[UN];
-      int slot[UN];
+    for (int c = 0; c < 8; ++c) hi[c] = -INFINITY, lo[c] = INFINITY;
+    for (int r0 = q0; r0 - lane / LR < t1; r0 += UN * RC) {
 #pragma unroll
       for (int j = 0; j < UN; ++j) {
-        const int r = r0 + j * RC;
+        const RowCode<LR> kc(kw[j]), vc(vw[j]);
+        const int at = r0 + j * RC < t1 ? slot[j] : -1;
+        // a later row takes the registers: its loads run while the others are stored
+        const int r = r0 + (UN + j) * RC;
         const bool in = r < t1;
         kw[j] = in ? __ldg(reinterpret_cast<const uint4*>(k + r * k_stride + h * D) + lr) : make_uint4(0, 0, 0, 0);
         vw[j] = in ? __ldg(reinterpret_cast<const uint4*>(v + r * v_stride + h * D) + lr) : make_uint4(0, 0, 0, 0);
         slot[j] = in ? __ldg(pos + r) : -1;
-      }
-#pragma unroll
-      for (int j = 0; j < UN; ++j) {
-        const RowCode<LR> kc(kw[j]), vc(vw[j]);
-        if (slot[j] < 0) continue;
-        slot[j] %= KV_BLOCK;
-        *reinterpret_cast<uint2*>(pg + slot[j] * D + lr * 8) = kc.codes;
-        *reinterpret_cast<uint2*>(pg + KV_BLOCK * D + slot[j] * D + lr * 8) = vc.codes;
+        if (at < 0) continue;
+        const int sl = at % KV_BLOCK;
+        *reinterpret_cast<uint2*>(pg + sl * D + lr * 8) = kc.codes;
+        *reinterpret_cast<uint2*>(pg + KV_BLOCK * D + sl * D + lr * 8) = vc.codes;
         if (lr == 0) {
-          pg[2 * KV_BLOCK * D + slot[j]] = (uint8_t)(kc.nan ? KV_NAN : kc.e + 127);
-          pg[2 * KV_BLOCK * D + KV_BLOCK + slot[j]] = (uint8_t)(vc.nan ? KV_NAN : vc.e + 127);
+          pg[2 * KV_BLOCK * D + sl] = (uint8_t)(kc.nan ? KV_NAN : kc.e + 127);
+          pg[2 * KV_BLOCK * D + KV_BLOCK + sl] = (uint8_t)(vc.nan ? KV_NAN : vc.e + 127);
         }
         const float up = pow2f(kc.e);
         const uint32_t c[2] = {kc.codes.x, kc.codes.y};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(c[i / 2] >> (16 * (i & 1)) & 0xFFFFu));
-          hi[2 * i] = fmaxf(hi[2 * i], f.x * up), hi[2 * i + 1] = fmaxf(hi[2 * i + 1], f.y * up);
-          lo[2 * i] = fminf(lo[2 * i], f.x * up), lo[2 * i + 1] = fminf(lo[2 * i + 1], f.y * up);
+        for (int x = 0; x < 4; ++x) {
+          const float2 f = __fmul2_rn(f16x2_to_f32x2(e4m3x2_to_f16x2(c[x / 2] >> (16 * (x & 1)) & 0xFFFFu)), make_float2(up, up));
+          hi[2 * x] = fmaxf(hi[2 * x], f.x), hi[2 * x + 1] = fmaxf(hi[2 * x + 1], f.y);
+          lo[2 * x] = fminf(lo[2 * x], f.x), lo[2 * x + 1] = fminf(lo[2 * x + 1], f.y);
         }
       }
     }
@@ -149,13 +187,10 @@ __global__ void __launch_bounds__(KA_WARPS * 32)
 #pragma unroll
     for (int w = 0; w < KA_WARPS; ++w) amax = fmaxf(amax, s_max[w]);
     int e = bound_exp_of(amax);
-    int8_t* bd = bounds + ph * 2 * D + tid;
-    if (p % KV_BLOCK) {   // the block had begun before this call
-      const int oe = bexp[ph];
-      if (tid < D) ch = fmaxf(ch, bd[0] * pow2f(oe)), cl = fminf(cl, bd[D] * pow2f(oe));
+    if (begun) {   // (the old exponent was read before the barriers, so it may be overwritten)
+      ch = fmaxf(ch, oh * pow2f(oe)), cl = fminf(cl, ol * pow2f(oe));
       e = max(e, oe);
     }
-    __syncthreads();   // everyone has the old exponent
     if (tid < D) {
       bd[0] = (int8_t)ceilf(ch * pow2f(-e));
       bd[D] = (int8_t)floorf(cl * pow2f(-e));
