@@ -211,7 +211,6 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  pdl_launch_dependents();
 
   // queries: row r = (token r / G, head r % G) scaled by a power of two into FP16; K-major panels
   constexpr int PL = D / 32, QW = AT_THREADS / 32;
@@ -248,6 +247,10 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
+  // Only now, when this CTA has its tensor memory: one thread's signal counts for the CTA, and a following launch of
+  // this kernel takes its tensor memory before it waits for this grid.  Signalled earlier, it could take columns that a
+  // CTA of this grid still waits for, and each would wait for the other.
+  pdl_launch_dependents();
   tc_fence_after();
   const uint32_t tmem = tmem_s;
 
