@@ -151,8 +151,10 @@ template <typename Block>
 __device__ __forceinline__ int warp_top_piece(int have, const uint32_t* keys, int first, int n, Block block_of, int want,
                                               uint32_t* ok, int* ob, uint32_t* lk, int* lb) {
   const bool join = have > 0;
-  if (join)
+  if (join) {
     for (int i = threadIdx.x & 31; i < have; i += 32) lk[key_at(i)] = ok[key_at(i)], lb[i] = ob[i];
+    __syncwarp();   // the second selection reads them in other lanes; the first may find nothing and return at once
+  }
   const int got = warp_top_any(keys, first, n, want, [&](int p, int i, uint32_t key) {
     if (join)
       lk[key_at(have + p)] = key, lb[have + p] = block_of(i);
