@@ -248,14 +248,27 @@ KV_BLOCK = 64   # tokens of a cache page, and of a block of the selection
 class KvCache:
     """A paged key/value cache on the device (layout: bre_kv_cache in include/bre.h): pages uint8
     [n_pages, n_kv_heads, 128 D + 128], bounds int8 [n_pages, n_kv_heads, 2, D], bound_exp int8
-    [n_pages, n_kv_heads].  Which page holds which block of a sequence is the caller's table."""
+    [n_pages, n_kv_heads].  Which page holds which block of a sequence is the caller's table.
+    The calls take the fields as they are: a cache grows by assigning larger tensors to all three, and
+    a copy (copy.deepcopy, pickle) is a cache of its own."""
     pages: torch.Tensor
     bounds: torch.Tensor
     bound_exp: torch.Tensor
 
     def __post_init__(self):
-        self.n_pages, self.n_kv_heads, self.head_dim, self._held, self._at = _lib.load_kv().cache(
-            self.pages, self.bounds, self.bound_exp)
+        _lib.load_kv().check(self)
+
+    @property
+    def n_pages(self) -> int:
+        return self.bounds.shape[0]
+
+    @property
+    def n_kv_heads(self) -> int:
+        return self.bounds.shape[1]
+
+    @property
+    def head_dim(self) -> int:
+        return self.bounds.shape[3]
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, device) -> "KvCache":
@@ -273,14 +286,14 @@ def kv_append(cache: KvCache, k, v, seq, pos, table, dev_err=None, stream=None):
     """Quantise and store the keys and values ([T, n_kv_heads, D] BF16, possibly slices of a fused
     projection's rows) of tokens seq[t], pos[t] (int32 [T]) and refresh the bounds of their blocks;
     table int32 [B, N] holds the page of each block of 64 positions of each sequence."""
-    rc = _lib.load_kv().append(cache._at, k, v, seq, pos, table, dev_err, _raw(stream))
+    rc = _lib.load_kv().append(cache, k, v, seq, pos, table, dev_err, _raw(stream))
     if rc:
         check(rc, "kv_append")
 
 
 def kv_read(cache: KvCache, seq, pos, table, k_out=None, v_out=None, dev_err=None, stream=None):
     """The stored keys and values of tokens seq[t], pos[t]: two BF16 tensors [T, n_kv_heads, D]."""
-    rc, k_out, v_out = _lib.load_kv().read(cache._at, seq, pos, table, k_out, v_out, dev_err, _raw(stream))
+    rc, k_out, v_out = _lib.load_kv().read(cache, seq, pos, table, k_out, v_out, dev_err, _raw(stream))
     if rc:
         check(rc, "kv_read")
     return k_out, v_out
@@ -295,7 +308,7 @@ def kv_select(q, cache: KvCache, seq, pos, table, k: int, n_sink: int = 1, n_loc
     """For each token and kv head the k blocks to attend to: the first n_sink, the last n_local, and
     the best-scored others.  q [T, n_heads, D] BF16.  Returns (ids int32 [T, n_kv_heads, k], ascending,
     then -1; scores float32, then 0)."""
-    rc, ids, scores = _lib.load_kv().select(cache._at, q, seq, pos, table, k, n_sink, n_local, ws, ids, scores, dev_err,
+    rc, ids, scores = _lib.load_kv().select(cache, q, seq, pos, table, k, n_sink, n_local, ws, ids, scores, dev_err,
                                             _raw(stream))
     if rc:
         check(rc, "kv_select")
@@ -311,9 +324,7 @@ def kv_attend(q, cache: KvCache, seq, pos, table, ids, scale: float | None = Non
     """Attention of q [T, n_heads, D] (BF16) over the blocks ids [T, n_kv_heads, k] lists, up to each
     token's own position; scale defaults to 1/sqrt(D).  Returns (out BF16 [T, n_heads, D], lse float32
     [T, n_heads]); rows that see nothing are 0 and -inf."""
-    rc, out, lse = _lib.load_kv().attend(cache._at, q, seq, pos, table, ids,
-                                         cache.head_dim ** -0.5 if scale is None else scale, ws, out, lse, dev_err,
-                                         _raw(stream))
+    rc, out, lse = _lib.load_kv().attend(cache, q, seq, pos, table, ids, scale, ws, out, lse, dev_err, _raw(stream))
     if rc:
         check(rc, "kv_attend")
     return out, lse

@@ -9,6 +9,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <initializer_list>
 #include <optional>
 #include <stdexcept>
@@ -34,6 +35,49 @@ std::string said(std::initializer_list<int64_t> shape) {
   return s + "]";
 }
 
+// An owned reference.
+struct Ref {
+  PyObject* o;
+  explicit Ref(PyObject* p) : o(p) {}
+  Ref(Ref&& r) : o(r.o) { r.o = nullptr; }
+  ~Ref() { Py_XDECREF(o); }
+  void* data() const { return THPVariable_Unpack(o).data_ptr(); }
+};
+
+PyObject *name_pages, *name_bounds, *name_bound_exp;   // interned by the module's start
+
+// A KvCache as its fields are at the time of the call: they may have been assigned since it was made (a cache that
+// grows), and a copy has tensors of its own.  Nothing of it is kept from one call for the next.
+struct Cache {
+  Ref pages, bounds, bound_exp;
+  int64_t n, heads, dim;
+
+  static Ref field(PyObject* cache, PyObject* name) {
+    PyObject* o = PyObject_GetAttr(cache, name);
+    if (!o) {
+      PyErr_Clear();
+      refuse("not a cache");
+    }
+    return Ref(o);
+  }
+  explicit Cache(PyObject* cache)
+      : pages(field(cache, name_pages)), bounds(field(cache, name_bounds)), bound_exp(field(cache, name_bound_exp)) {
+    const Tensor &p = tensor(pages.o, "pages"), &b = tensor(bounds.o, "bounds"), &e = tensor(bound_exp.o, "bound_exp");
+    if (b.dim() != 4 || b.size(2) != 2) refuse("bounds must be [n_pages, n_kv_heads, 2, head_dim]");
+    n = b.size(0), heads = b.size(1), dim = b.size(3);
+    if (p.sizes() != at::IntArrayRef({n, heads, 128 * (dim + 1)}) || e.sizes() != at::IntArrayRef({n, heads}))
+      refuse("pages, bounds and bound_exp do not belong together");
+    if (p.scalar_type() != at::kByte || b.scalar_type() != at::kChar || e.scalar_type() != at::kChar)
+      refuse("pages must be uint8, bounds and bound_exp int8");
+    for (const Tensor* t : {&p, &b, &e})
+      if (!t->is_cuda() || !t->is_contiguous()) refuse("pages, bounds and bound_exp must be contiguous CUDA tensors");
+  }
+  bre_kv_cache native() const {
+    return {pages.data(),   static_cast<int8_t*>(bounds.data()), static_cast<int8_t*>(bound_exp.data()), (int32_t)n, (int32_t)heads,
+            (int32_t)dim};
+  }
+};
+
 // A contiguous CUDA tensor of this type and shape.
 template <typename P = void>
 P* like(PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) {
@@ -58,27 +102,18 @@ const void* rows(PyObject* o, const char* name, int64_t T, int64_t heads, int64_
   return t.data_ptr();
 }
 
-// An owned reference.
-struct Ref {
-  PyObject* o;
-  explicit Ref(PyObject* p) : o(p) {}
-  Ref(Ref&& r) : o(r.o) { r.o = nullptr; }
-  ~Ref() { Py_XDECREF(o); }
-  void* data() const { return THPVariable_Unpack(o).data_ptr(); }
-};
-
 // The tokens of a call, the device and the stream.
 struct Call {
-  const bre_kv_cache* c;
+  Cache cache;
+  bre_kv_cache c;
   const int32_t *seq, *pos, *table;
   int T, B, N;
   c10::Device device{c10::kCUDA, 0};
   bre_stream_t stream;
   int32_t* err;
 
-  Call(PyObject* cache, PyObject* seq_o, PyObject* pos_o, PyObject* table_o, PyObject* err_o, PyObject* stream_o) {
-    c = static_cast<const bre_kv_cache*>(PyLong_AsVoidPtr(cache));
-    if (!c) refuse("not a cache");
+  Call(PyObject* cache_o, PyObject* seq_o, PyObject* pos_o, PyObject* table_o, PyObject* err_o, PyObject* stream_o)
+      : cache(cache_o), c(cache.native()) {
     const Tensor& s = tensor(seq_o, "seq");
     const Tensor& t = tensor(table_o, "table");
     if (s.dim() != 1 || t.dim() != 2) refuse("seq must be [T] and table [B, N]");
@@ -151,9 +186,9 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {   // cache k 
   return guarded(n, 8, [&] {
     const Call call(a[0], a[3], a[4], a[5], a[6], a[7]);
     int64_t ks, vs;
-    const void* k = rows(a[1], "k", call.T, call.c->n_kv_heads, call.c->head_dim, &ks);
-    const void* v = rows(a[2], "v", call.T, call.c->n_kv_heads, call.c->head_dim, &vs);
-    return PyLong_FromLong(kv_append(call.c, k, v, ks, vs, call.seq, call.pos, call.T, call.table, call.B, call.N, call.err,
+    const void* k = rows(a[1], "k", call.T, call.c.n_kv_heads, call.c.head_dim, &ks);
+    const void* v = rows(a[2], "v", call.T, call.c.n_kv_heads, call.c.head_dim, &vs);
+    return PyLong_FromLong(kv_append(&call.c, k, v, ks, vs, call.seq, call.pos, call.T, call.table, call.B, call.N, call.err,
                                      call.stream));
   });
 }
@@ -161,10 +196,10 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {   // cache k 
 PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {   // cache seq pos table k_out v_out dev_err stream
   return guarded(n, 8, [&] {
     const Call call(a[0], a[1], a[2], a[3], a[6], a[7]);
-    Ref k = call.output(a[4], "k_out", at::kBFloat16, {call.T, call.c->n_kv_heads, call.c->head_dim});
-    Ref v = call.output(a[5], "v_out", at::kBFloat16, {call.T, call.c->n_kv_heads, call.c->head_dim});
+    Ref k = call.output(a[4], "k_out", at::kBFloat16, {call.T, call.c.n_kv_heads, call.c.head_dim});
+    Ref v = call.output(a[5], "v_out", at::kBFloat16, {call.T, call.c.n_kv_heads, call.c.head_dim});
     const bre_status st =
-        kv_read(call.c, call.seq, call.pos, call.T, call.table, call.B, call.N, k.data(), v.data(), call.err, call.stream);
+        kv_read(&call.c, call.seq, call.pos, call.T, call.table, call.B, call.N, k.data(), v.data(), call.err, call.stream);
     return answer(st, k, v);
   });
 }
@@ -173,15 +208,15 @@ PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {   // cache seq 
 PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 13, [&] {
     const Call call(a[0], a[2], a[3], a[4], a[11], a[12]);
-    const int H = call.c->n_kv_heads, k = integer(a[5]), sink = integer(a[6]), local = integer(a[7]);
+    const int H = call.c.n_kv_heads, k = integer(a[5]), sink = integer(a[6]), local = integer(a[7]);
     if (k < 0) refuse("k must not be negative");
     int64_t qs;
     int Hq;
-    const void* q = rows(a[1], "q", call.T, -1, call.c->head_dim, &qs, &Hq);
+    const void* q = rows(a[1], "q", call.T, -1, call.c.head_dim, &qs, &Hq);
     const Workspace ws(a[8]);
     Ref ids = call.output(a[9], "ids", at::kInt, {call.T, H, k});
     Ref sc = call.output(a[10], "scores", at::kFloat, {call.T, H, k});
-    const bre_status st = kv_select(call.c, q, qs, Hq, call.seq, call.pos, call.T, call.table, call.B, call.N, k, sink, local,
+    const bre_status st = kv_select(&call.c, q, qs, Hq, call.seq, call.pos, call.T, call.table, call.B, call.N, k, sink, local,
                                     static_cast<int32_t*>(ids.data()), static_cast<float*>(sc.data()), ws.p, ws.n, call.err,
                                     call.stream);
     return answer(st, ids, sc);
@@ -192,7 +227,7 @@ PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&] {
     const Call call(a[0], a[2], a[3], a[4], a[10], a[11]);
-    const int H = call.c->n_kv_heads, D = call.c->head_dim;
+    const int H = call.c.n_kv_heads, D = call.c.head_dim;
     int64_t qs;
     int Hq;
     const void* q = rows(a[1], "q", call.T, -1, D, &qs, &Hq);
@@ -200,7 +235,7 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (id.dim() != 3) refuse("ids must be [T, n_kv_heads, k]");
     const int k = (int)id.size(2);
     const int32_t* ids = like<int32_t>(a[5], "ids", at::kInt, {call.T, H, k});
-    const double scale = PyFloat_AsDouble(a[6]);
+    const double scale = a[6] == Py_None ? std::pow((double)D, -0.5) : PyFloat_AsDouble(a[6]);
     if (scale == -1.0 && PyErr_Occurred()) {
       PyErr_Clear();
       refuse("scale must be a number");
@@ -208,33 +243,22 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Workspace ws(a[7]);
     Ref out = call.output(a[8], "out", at::kBFloat16, {call.T, Hq, D});
     Ref lse = call.output(a[9], "lse", at::kFloat, {call.T, Hq});
-    const bre_status st = kv_attend(call.c, q, qs, Hq, call.seq, call.pos, call.T, call.table, call.B, call.N, ids, k,
+    const bre_status st = kv_attend(&call.c, q, qs, Hq, call.seq, call.pos, call.T, call.table, call.B, call.N, ids, k,
                                     (float)scale, out.data(), static_cast<float*>(lse.data()), ws.p, ws.n, call.err, call.stream);
     return answer(st, out, lse);
   });
 }
 
-// pages bounds bound_exp -> (n_pages, n_kv_heads, head_dim, bytes of a bre_kv_cache, their address)
-PyObject* py_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 3, [&]() -> PyObject* {
-    const Tensor &p = tensor(a[0], "pages"), &b = tensor(a[1], "bounds"), &e = tensor(a[2], "bound_exp");
-    if (b.dim() != 4 || b.size(2) != 2) refuse("bounds must be [n_pages, n_kv_heads, 2, head_dim]");
-    const int64_t N = b.size(0), H = b.size(1), D = b.size(3);
-    if (p.sizes() != at::IntArrayRef({N, H, 128 * (D + 1)}) || e.sizes() != at::IntArrayRef({N, H}))
-      refuse("pages, bounds and bound_exp do not belong together");
-    if (p.scalar_type() != at::kByte || b.scalar_type() != at::kChar || e.scalar_type() != at::kChar)
-      refuse("pages must be uint8, bounds and bound_exp int8");
-    for (const Tensor* t : {&p, &b, &e})
-      if (!t->is_cuda() || !t->is_contiguous()) refuse("pages, bounds and bound_exp must be contiguous CUDA tensors");
-    const bre_kv_cache c{p.data_ptr(), static_cast<int8_t*>(b.data_ptr()), static_cast<int8_t*>(e.data_ptr()), (int32_t)N, (int32_t)H,
-                         (int32_t)D};
-    PyObject* held = PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&c), sizeof(c));
-    return held ? Py_BuildValue("iiiNN", (int)N, (int)H, (int)D, held, PyLong_FromVoidPtr(PyBytes_AS_STRING(held))) : nullptr;
+// cache -> None: refuses what is no cache
+PyObject* py_check(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 1, [&]() -> PyObject* {
+    const Cache c(a[0]);
+    Py_RETURN_NONE;
   });
 }
 
 PyMethodDef methods[] = {
-    {"cache", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_cache)), METH_FASTCALL, nullptr},
+    {"check", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_check)), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_append)), METH_FASTCALL, nullptr},
     {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_read)), METH_FASTCALL, nullptr},
     {"select", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_select)), METH_FASTCALL, nullptr},
@@ -244,4 +268,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kv", nullptr, -1, methods, nullpt
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__kv() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__kv() {
+  name_pages = PyUnicode_InternFromString("pages");
+  name_bounds = PyUnicode_InternFromString("bounds");
+  name_bound_exp = PyUnicode_InternFromString("bound_exp");
+  return name_pages && name_bounds && name_bound_exp ? PyModule_Create(&module) : nullptr;
+}

@@ -1,9 +1,13 @@
 """Cases of the key/value cache calls that answered wrongly once, against the definitions in 64 bits."""
+import copy
+import pickle
+
 import pytest
 import torch
 
 import kv_reference as R
-from test_kv_cache import check_select
+from bit_routed_expert_gb300 import KvCache, kv_append, kv_attend, kv_read, kv_select
+from test_kv_cache import check_select, on
 
 pytestmark = pytest.mark.gpu
 
@@ -20,3 +24,52 @@ def test_select_last_piece_holds_only_forced_blocks(cuda_dev, blocks, sink, loca
     n = R.Batch([0] * T, list(range(64 * blocks - T, 64 * blocks)),
                 torch.randint(0, b.n_pages, (1, blocks), generator=g).to(torch.int32), b.n_pages)
     check_select(cuda_dev, n, cache, R.rows(blocks, T, G, D), k, sink, local)
+
+
+def own(c):
+    return c.pages.cpu(), c.bounds.cpu(), c.bound_exp.cpu()
+
+
+def test_a_cache_that_grew_and_a_copy_use_their_own_tensors(cuda_dev):
+    """append, read, select and attend after the fields were assigned, and on a deep copy and an unpickled cache."""
+    D, H, G = 64, 2, 2
+    b = R.batch([100], [30])
+    small = R.filled(b, [100], H, D)
+    old = on(cuda_dev, *small)
+    held = [old.pages, old.bounds, old.bound_exp]
+    c = on(cuda_dev, *small)
+    c.pages, c.bounds, c.bound_exp = (torch.cat([x, x.flip(0)]) for x in held)
+    assert c.n_pages == 2 * b.n_pages
+    table = torch.where(b.table >= 0, b.table + b.n_pages, b.table)   # pages that only the larger cache has
+    n = R.Batch(b.seq, b.pos, table, 2 * b.n_pages)
+    k, v, q = R.rows(1, 30, H, D), R.rows(2, 30, H, D), R.rows(3, 30, H * G, D)
+    for other in (copy.deepcopy(c), pickle.loads(pickle.dumps(c)), c):
+        want, before = own(other), own(c)
+        e = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+        kv_append(other, k.to(cuda_dev), v.to(cuda_dev), *n.on(cuda_dev), dev_err=e)
+        assert not R.append(*want, k, v, n.seq, n.pos, table)
+        assert all(torch.equal(x, y) for x, y in zip(own(other), want)) and int(e) == 0
+        if other is not c:
+            assert all(torch.equal(x, y) for x, y in zip(own(c), before))
+        kk, _ = R.values(want[0], D)
+        got, _ = kv_read(other, *n.on(cuda_dev))
+        assert torch.equal(got.cpu().double(), torch.stack([kk[int(table[0, p // 64]), :, p % 64] for p in n.pos]))
+        ids, _ = kv_select(q.to(cuda_dev), other, *n.on(cuda_dev), 3)
+        assert torch.equal(ids.cpu(), R.select(q, *want[1:], n.seq, n.pos, table, 3, 1, 2)[0])
+        out, _ = kv_attend(q.to(cuda_dev), other, *n.on(cuda_dev), ids)
+        o, _, mass, size, _ = R.attend(q, want[0], n.seq, n.pos, table, ids.cpu(), D ** -0.5)
+        tol = 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2 * (D * 2.0 ** -23 * size + 2.0 ** -20))[..., None] * mass
+        assert bool(((out.cpu().double() - o).abs() <= tol).all())
+    assert all(torch.equal(x.cpu(), y) for x, y in zip(held, small))
+
+
+def test_fields_that_do_not_belong_together_are_refused(cuda_dev):
+    """A cache half way through its growth."""
+    c = KvCache.empty(3, 2, 64, cuda_dev)
+    c.pages = torch.cat([c.pages, c.pages])
+    tokens = R.batch([3], [3]).on(cuda_dev)
+    with pytest.raises(ValueError, match="belong together"):
+        kv_read(c, *tokens)
+    c.pages = c.pages[:3].cpu()
+    with pytest.raises(ValueError, match="CUDA"):
+        kv_read(c, *tokens)
