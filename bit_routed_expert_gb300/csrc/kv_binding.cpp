@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -71,6 +72,20 @@ struct Cache {
       refuse("pages must be uint8, bounds and bound_exp int8");
     for (const Tensor* t : {&p, &b, &e})
       if (!t->is_cuda() || !t->is_contiguous()) refuse("pages, bounds and bound_exp must be contiguous CUDA tensors");
+    device(nullptr, 0);
+  }
+  // The cache's device; refuses tensors among a call's other arguments that are not there.
+  c10::Device device(PyObject* const* a, Py_ssize_t n) const {
+    const c10::Device d = THPVariable_Unpack(pages.o).device();
+    auto there = [&](PyObject* o) {
+      const c10::Device x = THPVariable_Unpack(o).device();
+      if (x != d) refuse("all tensors must be on the CUDA device of the cache's pages, " + d.str() + ": there is one on " + x.str());
+    };
+    there(bounds.o);
+    there(bound_exp.o);
+    for (Py_ssize_t i = 0; i < n; ++i)   // (THPVariable_Check takes long over what is no tensor)
+      if (a[i] != Py_None && !PyLong_CheckExact(a[i]) && !PyFloat_CheckExact(a[i]) && THPVariable_Check(a[i])) there(a[i]);
+    return d;
   }
   bre_kv_cache native() const {
     return {pages.data(),   static_cast<int8_t*>(bounds.data()), static_cast<int8_t*>(bound_exp.data()), (int32_t)n, (int32_t)heads,
@@ -102,18 +117,25 @@ const void* rows(PyObject* o, const char* name, int64_t T, int64_t heads, int64_
   return t.data_ptr();
 }
 
-// The tokens of a call, the device and the stream.
+// A call's cache, tokens and stream.  The cache's device, which every tensor among the arguments must be on, is the
+// current one while the call lasts (streams, attributes and launches go by it).
 struct Call {
   Cache cache;
+  c10::Device device;
+  c10::cuda::OptionalCUDAGuard guard;
   bre_kv_cache c;
   const int32_t *seq, *pos, *table;
   int T, B, N;
-  c10::Device device{c10::kCUDA, 0};
   bre_stream_t stream;
   int32_t* err;
 
-  Call(PyObject* cache_o, PyObject* seq_o, PyObject* pos_o, PyObject* table_o, PyObject* err_o, PyObject* stream_o)
-      : cache(cache_o), c(cache.native()) {
+  // a: the call's n arguments, of which the first is the cache, `tokens` and the two after it seq, pos and table, the
+  // last but one dev_err and the last the stream
+  Call(PyObject* const* a, Py_ssize_t n, int tokens)
+      : cache(a[0]), device(cache.device(a + 1, n - 1)), c(cache.native()) {
+    if (c10::cuda::current_device() != device.index()) guard.set_device(device);   // (a guard costs about a microsecond)
+    PyObject *const seq_o = a[tokens], *const pos_o = a[tokens + 1], *const table_o = a[tokens + 2];
+    PyObject *const err_o = a[n - 2], *const stream_o = a[n - 1];
     const Tensor& s = tensor(seq_o, "seq");
     const Tensor& t = tensor(table_o, "table");
     if (s.dim() != 1 || t.dim() != 2) refuse("seq must be [T] and table [B, N]");
@@ -121,7 +143,6 @@ struct Call {
     seq = like<int32_t>(seq_o, "seq", at::kInt, {T});
     pos = like<int32_t>(pos_o, "pos", at::kInt, {T});
     table = like<int32_t>(table_o, "table", at::kInt, {B, N});
-    device = s.device();
     err = err_o == Py_None ? nullptr : like<int32_t>(err_o, "dev_err", at::kInt, {1});
     stream = reinterpret_cast<bre_stream_t>(stream_o == Py_None
                                                 ? (void*)c10::cuda::getCurrentCUDAStream(device.index()).stream()
@@ -184,7 +205,7 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
 
 PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {   // cache k v seq pos table dev_err stream
   return guarded(n, 8, [&] {
-    const Call call(a[0], a[3], a[4], a[5], a[6], a[7]);
+    const Call call(a, n, 3);
     int64_t ks, vs;
     const void* k = rows(a[1], "k", call.T, call.c.n_kv_heads, call.c.head_dim, &ks);
     const void* v = rows(a[2], "v", call.T, call.c.n_kv_heads, call.c.head_dim, &vs);
@@ -195,7 +216,7 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {   // cache k 
 
 PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {   // cache seq pos table k_out v_out dev_err stream
   return guarded(n, 8, [&] {
-    const Call call(a[0], a[1], a[2], a[3], a[6], a[7]);
+    const Call call(a, n, 1);
     Ref k = call.output(a[4], "k_out", at::kBFloat16, {call.T, call.c.n_kv_heads, call.c.head_dim});
     Ref v = call.output(a[5], "v_out", at::kBFloat16, {call.T, call.c.n_kv_heads, call.c.head_dim});
     const bre_status st =
@@ -207,7 +228,7 @@ PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {   // cache seq 
 // cache q seq pos table k n_sink n_local ws ids scores dev_err stream
 PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 13, [&] {
-    const Call call(a[0], a[2], a[3], a[4], a[11], a[12]);
+    const Call call(a, n, 2);
     const int H = call.c.n_kv_heads, k = integer(a[5]), sink = integer(a[6]), local = integer(a[7]);
     if (k < 0) refuse("k must not be negative");
     int64_t qs;
@@ -226,7 +247,7 @@ PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // cache q seq pos table ids scale ws out lse dev_err stream
 PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&] {
-    const Call call(a[0], a[2], a[3], a[4], a[10], a[11]);
+    const Call call(a, n, 2);
     const int H = call.c.n_kv_heads, D = call.c.head_dim;
     int64_t qs;
     int Hq;

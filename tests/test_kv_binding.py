@@ -1,6 +1,7 @@
 """The Python face of the key/value cache calls on the host (no GPU): what reaches the library, what is refused."""
 import copy
 import pickle
+from unittest import mock
 
 import pytest
 import torch
@@ -75,3 +76,53 @@ def test_no_cache_is_refused():
             binding.check(bad)
         with pytest.raises(ValueError, match="not a cache"):
             binding.read(bad, 0, 0, 0, None, None, None, None)
+
+
+def fake(device, *shape, dtype=torch.int32):
+    """A tensor that says that it is on `device`, without memory."""
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def fake_call(name, cache_devices=("cuda:0",) * 3, **where):
+    """One call whose tensors are all on cuda:0 but for those named in `where`."""
+    at = lambda n: where.get(n, "cuda:0")  # noqa: E731
+    # (a fake tensor would begin with a real one on its device, where there are devices)
+    with mock.patch("torch.cuda.is_available", lambda: False), torch._subclasses.fake_tensor.FakeTensorMode():
+        d = cache_devices
+        c = KvCache(fake(d[0], 3, 2, 128 * 65, dtype=torch.uint8), fake(d[1], 3, 2, 2, 64, dtype=torch.int8),
+                    fake(d[2], 3, 2, dtype=torch.int8))
+        tokens = fake(at("seq"), 5), fake(at("pos"), 5), fake(at("table"), 1, 3)
+        rows = lambda n, h: fake(at(n), 5, h, 64, dtype=torch.bfloat16)  # noqa: E731
+        err = fake(at("dev_err"), 1)
+        ids = fake(at("ids"), 5, 2, 4)
+        if name == "append":
+            kv_append(c, rows("k", 2), rows("v", 2), *tokens, dev_err=err)
+        elif name == "read":
+            kv_read(c, *tokens, k_out=rows("k_out", 2), v_out=rows("v_out", 2), dev_err=err)
+        elif name == "select":
+            kv_select(rows("q", 4), c, *tokens, 4, ids=ids, scores=fake(at("scores"), 5, 2, 4, dtype=torch.float32),
+                      ws=fake(at("ws"), 0, dtype=torch.uint8), dev_err=err)
+        else:
+            kv_attend(rows("q", 4), c, *tokens, ids, out=rows("out", 4), ws=fake(at("ws"), 0, dtype=torch.uint8),
+                      lse=fake(at("lse"), 5, 4, dtype=torch.float32), dev_err=err)
+
+
+ARGUMENTS = {"append": ["k", "v"], "read": ["k_out", "v_out"], "select": ["q", "ids", "scores", "ws"],
+             "attend": ["q", "ids", "out", "lse", "ws"]}
+
+
+@pytest.mark.parametrize("device", ["cuda:1", "cpu"])
+@pytest.mark.parametrize("name", list(ARGUMENTS))
+def test_tensors_on_another_device_are_refused(name, device):
+    """Before anything looks at an address: a launch would take one device's pointers to another."""
+    for arg in ARGUMENTS[name] + ["seq", "pos", "table", "dev_err"]:
+        with pytest.raises(ValueError, match="device of the cache's pages, cuda:0: there is one on " + device):
+            fake_call(name, **{arg: device})
+
+
+def test_a_cache_on_two_devices_is_refused():
+    for i in range(1, 3):
+        d = ["cuda:0"] * 3
+        d[i] = "cuda:1"
+        with pytest.raises(ValueError, match="device of the cache's pages"):
+            fake_call("append", cache_devices=d)
