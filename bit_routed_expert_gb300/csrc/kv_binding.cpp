@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <cstdint>
 #include <initializer_list>
 #include <optional>
 #include <stdexcept>
@@ -36,6 +37,22 @@ std::string said(std::initializer_list<int64_t> shape) {
   return s + "]";
 }
 
+// The library counts in 32 bits.
+int int32(int64_t v, const char* name) {
+  if (v < INT32_MIN || v > INT32_MAX) refuse(std::string(name) + " is outside 32 bits: " + std::to_string(v));
+  return (int)v;
+}
+int integer(PyObject* o, const char* name) {
+  int over = 0;
+  const long long v = PyLong_AsLongLongAndOverflow(o, &over);
+  if (v == -1 && PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse(std::string(name) + " must be a whole number");
+  }
+  if (over) refuse(std::string(name) + " is outside 32 bits");
+  return int32(v, name);
+}
+
 // An owned reference.
 struct Ref {
   PyObject* o;
@@ -51,7 +68,7 @@ PyObject *name_pages, *name_bounds, *name_bound_exp;   // interned by the module
 // grows), and a copy has tensors of its own.  Nothing of it is kept from one call for the next.
 struct Cache {
   Ref pages, bounds, bound_exp;
-  int64_t n, heads, dim;
+  int n, heads, dim;
 
   static Ref field(PyObject* cache, PyObject* name) {
     PyObject* o = PyObject_GetAttr(cache, name);
@@ -65,8 +82,8 @@ struct Cache {
       : pages(field(cache, name_pages)), bounds(field(cache, name_bounds)), bound_exp(field(cache, name_bound_exp)) {
     const Tensor &p = tensor(pages.o, "pages"), &b = tensor(bounds.o, "bounds"), &e = tensor(bound_exp.o, "bound_exp");
     if (b.dim() != 4 || b.size(2) != 2) refuse("bounds must be [n_pages, n_kv_heads, 2, head_dim]");
-    n = b.size(0), heads = b.size(1), dim = b.size(3);
-    if (p.sizes() != at::IntArrayRef({n, heads, 128 * (dim + 1)}) || e.sizes() != at::IntArrayRef({n, heads}))
+    n = int32(b.size(0), "n_pages"), heads = int32(b.size(1), "n_kv_heads"), dim = int32(b.size(3), "head_dim");
+    if (p.sizes() != at::IntArrayRef({n, heads, 128 * (dim + 1LL)}) || e.sizes() != at::IntArrayRef({n, heads}))
       refuse("pages, bounds and bound_exp do not belong together");
     if (p.scalar_type() != at::kByte || b.scalar_type() != at::kChar || e.scalar_type() != at::kChar)
       refuse("pages must be uint8, bounds and bound_exp int8");
@@ -88,8 +105,7 @@ struct Cache {
     return d;
   }
   bre_kv_cache native() const {
-    return {pages.data(),   static_cast<int8_t*>(bounds.data()), static_cast<int8_t*>(bound_exp.data()), (int32_t)n, (int32_t)heads,
-            (int32_t)dim};
+    return {pages.data(), static_cast<int8_t*>(bounds.data()), static_cast<int8_t*>(bound_exp.data()), n, heads, dim};
   }
 };
 
@@ -113,7 +129,7 @@ const void* rows(PyObject* o, const char* name, int64_t T, int64_t heads, int64_
   if (!t.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
   if (t.element_size() != 2 || t.scalar_type() == at::kHalf) refuse(std::string(name) + " must be bfloat16");
   *stride = T > 1 ? t.stride(0) : (t.size(1) * D + 7) / 8 * 8;
-  if (n_heads) *n_heads = (int)t.size(1);
+  if (n_heads) *n_heads = int32(t.size(1), "the number of heads");
   return t.data_ptr();
 }
 
@@ -132,14 +148,15 @@ struct Call {
   // a: the call's n arguments, of which the first is the cache, `tokens` and the two after it seq, pos and table, the
   // last but one dev_err and the last the stream
   Call(PyObject* const* a, Py_ssize_t n, int tokens)
-      : cache(a[0]), device(cache.device(a + 1, n - 1)), c(cache.native()) {
-    if (c10::cuda::current_device() != device.index()) guard.set_device(device);   // (a guard costs about a microsecond)
+      : cache(a[0]), device(cache.device(a + 1, n - 1)) {
     PyObject *const seq_o = a[tokens], *const pos_o = a[tokens + 1], *const table_o = a[tokens + 2];
     PyObject *const err_o = a[n - 2], *const stream_o = a[n - 1];
     const Tensor& s = tensor(seq_o, "seq");
     const Tensor& t = tensor(table_o, "table");
     if (s.dim() != 1 || t.dim() != 2) refuse("seq must be [T] and table [B, N]");
-    T = (int)s.size(0), B = (int)t.size(0), N = (int)t.size(1);
+    T = int32(s.size(0), "T"), B = int32(t.size(0), "B"), N = int32(t.size(1), "N");
+    if (c10::cuda::current_device() != device.index()) guard.set_device(device);   // (a guard costs about a microsecond)
+    c = cache.native();
     seq = like<int32_t>(seq_o, "seq", at::kInt, {T});
     pos = like<int32_t>(pos_o, "pos", at::kInt, {T});
     table = like<int32_t>(table_o, "table", at::kInt, {B, N});
@@ -170,15 +187,6 @@ struct Workspace {
     n = (size_t)t.numel();
   }
 };
-
-int integer(PyObject* o) {
-  const long v = PyLong_AsLong(o);
-  if (v == -1 && PyErr_Occurred()) {
-    PyErr_Clear();
-    refuse("not a whole number");
-  }
-  return (int)v;
-}
 
 // (status, first output, second output)
 PyObject* answer(bre_status st, Ref& a, Ref& b) {
@@ -228,8 +236,9 @@ PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {   // cache seq 
 // cache q seq pos table k n_sink n_local ws ids scores dev_err stream
 PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 13, [&] {
+    const int k = integer(a[5], "k"), sink = integer(a[6], "n_sink"), local = integer(a[7], "n_local");
     const Call call(a, n, 2);
-    const int H = call.c.n_kv_heads, k = integer(a[5]), sink = integer(a[6]), local = integer(a[7]);
+    const int H = call.c.n_kv_heads;
     if (k < 0) refuse("k must not be negative");
     int64_t qs;
     int Hq;
@@ -254,7 +263,7 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* q = rows(a[1], "q", call.T, -1, D, &qs, &Hq);
     const Tensor& id = tensor(a[5], "ids");
     if (id.dim() != 3) refuse("ids must be [T, n_kv_heads, k]");
-    const int k = (int)id.size(2);
+    const int k = int32(id.size(2), "k");
     const int32_t* ids = like<int32_t>(a[5], "ids", at::kInt, {call.T, H, k});
     const double scale = a[6] == Py_None ? std::pow((double)D, -0.5) : PyFloat_AsDouble(a[6]);
     if (scale == -1.0 && PyErr_Occurred()) {

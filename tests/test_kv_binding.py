@@ -126,3 +126,30 @@ def test_a_cache_on_two_devices_is_refused():
         d[i] = "cuda:1"
         with pytest.raises(ValueError, match="device of the cache's pages"):
             fake_call("append", cache_devices=d)
+
+
+@pytest.mark.parametrize("kw", [{"k": 2 ** 32 + 4}, {"n_sink": 2 ** 32}, {"n_local": 2 ** 32 + 1}, {"k": -2 ** 31 - 1},
+                                {"k": 2 ** 64 + 4}, {"n_sink": -2 ** 63 - 1}])
+def test_numbers_outside_32_bits_are_refused(kw):
+    """Not cut to the 32 bits that the library takes, where 2^32 + 4 would be 4."""
+    with torch._subclasses.fake_tensor.FakeTensorMode(), mock.patch("torch.cuda.is_available", lambda: False):
+        c = KvCache(fake("cuda:0", 3, 2, 128 * 65, dtype=torch.uint8), fake("cuda:0", 3, 2, 2, 64, dtype=torch.int8),
+                    fake("cuda:0", 3, 2, dtype=torch.int8))
+        tokens = fake("cuda:0", 5), fake("cuda:0", 5), fake("cuda:0", 1, 3)
+        args = {"k": 4, "n_sink": 1, "n_local": 1, **kw}
+        with pytest.raises(ValueError, match=next(iter(kw)) + " is outside 32 bits"):
+            kv_select(fake("cuda:0", 5, 4, 64, dtype=torch.bfloat16), c, *tokens, args.pop("k"), **args)
+        with pytest.raises(ValueError, match="k must be a whole number"):
+            kv_select(fake("cuda:0", 5, 4, 64, dtype=torch.bfloat16), c, *tokens, 4.0)
+
+
+@pytest.mark.parametrize("T,B,N,name", [(2 ** 32 + 1, 1, 3, "T"), (5, 2 ** 32 + 1, 3, "B"), (5, 1, 2 ** 32 + 3, "N")])
+def test_sizes_outside_32_bits_are_refused(T, B, N, name):
+    with torch._subclasses.fake_tensor.FakeTensorMode(), mock.patch("torch.cuda.is_available", lambda: False):
+        c = KvCache(fake("cuda:0", 3, 2, 128 * 65, dtype=torch.uint8), fake("cuda:0", 3, 2, 2, 64, dtype=torch.int8),
+                    fake("cuda:0", 3, 2, dtype=torch.int8))
+        with pytest.raises(ValueError, match=name + " is outside 32 bits"):
+            kv_read(c, fake("cuda:0", T), fake("cuda:0", T), fake("cuda:0", B, N))
+        with pytest.raises(ValueError, match="n_pages is outside 32 bits"):
+            KvCache(fake("cuda:0", 2 ** 32 + 3, 2, 128 * 65, dtype=torch.uint8),
+                    fake("cuda:0", 2 ** 32 + 3, 2, 2, 64, dtype=torch.int8), fake("cuda:0", 2 ** 32 + 3, 2, dtype=torch.int8))
