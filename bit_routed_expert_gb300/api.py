@@ -278,6 +278,9 @@ class KvCache:
                    torch.empty((n_pages, n_kv_heads), dtype=torch.int8, device=device))
 
 
+# Of the kv_* calls: `stream` (default: the current one) is where the call runs.  What it reads must be ready
+# there and stay allocated until it has run, as under torch.cuda.stream; outputs that are not passed are allocated there,
+# and to be used on the current stream once that has waited for `stream`.
 def _raw(stream):
     return None if stream is None else stream.cuda_stream
 

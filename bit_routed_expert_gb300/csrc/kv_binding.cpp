@@ -143,6 +143,7 @@ struct Call {
   const int32_t *seq, *pos, *table;
   int T, B, N;
   bre_stream_t stream;
+  std::optional<c10::cuda::CUDAStream> current;   // where it is not the call's
   int32_t* err;
 
   // a: the call's n arguments, of which the first is the cache, `tokens` and the two after it seq, pos and table, the
@@ -161,14 +162,30 @@ struct Call {
     pos = like<int32_t>(pos_o, "pos", at::kInt, {T});
     table = like<int32_t>(table_o, "table", at::kInt, {B, N});
     err = err_o == Py_None ? nullptr : like<int32_t>(err_o, "dev_err", at::kInt, {1});
-    stream = reinterpret_cast<bre_stream_t>(stream_o == Py_None
-                                                ? (void*)c10::cuda::getCurrentCUDAStream(device.index()).stream()
-                                                : PyLong_AsVoidPtr(stream_o));
+    const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(device.index());
+    cudaStream_t on = now.stream();
+    if (stream_o != Py_None) {
+      on = static_cast<cudaStream_t>(PyLong_AsVoidPtr(stream_o));
+      if (PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse("not a stream");
+      }
+      if (on != now.stream()) current = now;
+    }
+    stream = reinterpret_cast<bre_stream_t>(on);
   }
-  // The caller's output, or a new one.
+  // The caller's output, or a new one.  For a call on another stream than the current one it is allocated there:
+  // memory of the current stream may be in use by work that the other stream does not wait for.  The
+  // caller, who is on the current stream, is a user of it too.
   Ref output(PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) const {
-    if (o == Py_None)
-      return Ref(THPVariable_Wrap(at::detail::empty_cuda(at::IntArrayRef(shape), type, device, std::nullopt)));
+    if (o == Py_None) {
+      if (!current) return Ref(THPVariable_Wrap(at::detail::empty_cuda(at::IntArrayRef(shape), type, device, std::nullopt)));
+      const c10::cuda::CUDAStreamGuard there(
+          c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), device.index()));
+      const Tensor t = at::detail::empty_cuda(at::IntArrayRef(shape), type, device, std::nullopt);
+      t.record_stream(*current);
+      return Ref(THPVariable_Wrap(t));
+    }
     like(o, name, type, shape);
     Py_INCREF(o);
     return Ref(o);

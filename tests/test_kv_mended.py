@@ -73,3 +73,35 @@ def test_fields_that_do_not_belong_together_are_refused(cuda_dev):
     c.pages = c.pages[:3].cpu()
     with pytest.raises(ValueError, match="CUDA"):
         kv_read(c, *tokens)
+
+
+def test_new_outputs_of_a_call_on_another_stream_are_allocated_there(cuda_dev):
+    """Memory that the current stream has just given back may still be read by what runs there."""
+    D, H, G, T = 64, 2, 4, 8192
+    b = R.batch([T], [T])
+    c = on(cuda_dev, *R.filled(b, [T], H, D))
+    tokens = b.on(cuda_dev)
+    q = R.rows(3, T, H * G, D).to(cuda_dev)
+    ids = torch.zeros((T, H, 2), dtype=torch.int32, device=cuda_dev)
+    first = [*kv_read(c, *tokens), *kv_select(q, c, *tokens, 8), *kv_attend(q, c, *tokens, ids)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    made = []
+    for call in (lambda: kv_read(c, *tokens, stream=side), lambda: kv_select(q, c, *tokens, 8, stream=side),
+                 lambda: kv_attend(q, c, *tokens, ids, stream=side)):
+        free = [torch.empty_like(x) for x in first[len(made):len(made) + 2]]
+        places = [x.data_ptr() for x in free]
+        del free
+        out = call()
+        assert not {x.data_ptr() for x in out} & set(places)
+        made += out
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(made, first))
+    # given back while the current stream still works: not handed out again before it is done
+    torch.cuda._sleep(200_000_000)
+    places = {x.data_ptr() for x in made}
+    shapes = [(x.shape, x.dtype) for x in made]
+    del made, out
+    with torch.cuda.stream(side):
+        assert not {torch.empty(s, dtype=d, device=cuda_dev).data_ptr() for s, d in shapes} & places
+    torch.cuda.synchronize()
