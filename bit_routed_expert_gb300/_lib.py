@@ -84,12 +84,13 @@ def load(build_if_missing: bool = True):
 
 
 def load_kv():
-    """The binding of the kv_* calls (kv_binding.cpp); raises if it is missing and cannot be built."""
+    """The binding of the kv_* calls (kv_binding.cpp); raises if it is missing, or built against another PyTorch or
+    Python, and cannot be built."""
     global _kv
     if _kv is None:
         import importlib.util
         load()
-        if not os.path.exists(_build.BINDING):
+        if not _build.binding_is_current():
             _build.build()
         spec = importlib.util.spec_from_file_location("_kv", _build.BINDING)
         m = importlib.util.module_from_spec(spec)

@@ -14,6 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libbre.so")
 BINDING = os.path.join(OUT_DIR, "_kv.so")
+BUILT_FOR = os.path.join(OUT_DIR, "_kv.built_for")   # the PyTorch and Python that BINDING was built against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]
@@ -33,6 +34,23 @@ def _sources():
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         [os.path.join(ROOT, "include", "bre.h"), __file__]
+
+
+def _versions() -> str:
+    import sysconfig
+
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_is_current() -> bool:
+    """Whether BINDING is there and was built against the PyTorch and Python that run: against others it may load
+    and read tensors wrongly."""
+    try:
+        with open(BUILT_FOR) as f:
+            return os.path.exists(BINDING) and f.read() == _versions()
+    except OSError:
+        return False
 
 
 def _compile_binding(obj: str) -> None:
@@ -56,13 +74,18 @@ def _link_binding(obj: str) -> None:
                         "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of _kv.so failed:\n{r.stderr}")
+    if os.path.exists(BUILT_FOR):
+        os.remove(BUILT_FOR)   # it does not stand beside a binding of another version for a moment
     os.replace(tmp, BINDING)
+    with open(BUILT_FOR + f".{os.getpid()}.tmp", "w") as f:
+        f.write(_versions())
+    os.replace(f.name, BUILT_FOR)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     newest = max(os.path.getmtime(p) for p in _deps())
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING)):
+    if not force and binding_is_current() and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING)):
         return LIB
     cc = nvcc()
     objs = []

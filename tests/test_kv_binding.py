@@ -153,3 +153,28 @@ def test_sizes_outside_32_bits_are_refused(T, B, N, name):
         with pytest.raises(ValueError, match="n_pages is outside 32 bits"):
             KvCache(fake("cuda:0", 2 ** 32 + 3, 2, 128 * 65, dtype=torch.uint8),
                     fake("cuda:0", 2 ** 32 + 3, 2, 2, 64, dtype=torch.int8), fake("cuda:0", 2 ** 32 + 3, 2, dtype=torch.int8))
+
+
+def test_a_binding_of_another_version_is_built_again(monkeypatch, tmp_path):
+    """Not loaded: it reads PyTorch's own structures."""
+    from bit_routed_expert_gb300 import build
+    right = build.binding_is_current() and open(build.BUILT_FOR).read()
+    assert right and torch.__version__ in right
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_kv.so"))
+    monkeypatch.setattr(build, "BUILT_FOR", str(tmp_path / "_kv.built_for"))
+    monkeypatch.setattr(_lib, "_kv", None)
+
+    def built(*a, **kw):
+        raise RuntimeError("built again")
+
+    monkeypatch.setattr(build, "build", built)
+    for so, version in ((False, None), (True, None), (True, right + "x"), (True, "torch 1.0"), (False, right)):
+        for name, there in (("_kv.so", so), ("_kv.built_for", version)):
+            (tmp_path / name).unlink(missing_ok=True)
+            if there:
+                (tmp_path / name).write_text(there if isinstance(there, str) else "")
+        assert not build.binding_is_current()
+        with pytest.raises(RuntimeError, match="built again"):
+            _lib.load_kv()
+    (tmp_path / "_kv.so").write_text("")
+    assert build.binding_is_current()
