@@ -17,9 +17,10 @@
 // K is K-major, V lies as it is in the cache (a token's channels in a row), which is the MN-major
 // form of the second product's operand.  S and P share two buffers, K and V have two stages each.
 //
-// Scales: a key's 2^ek goes into its FP16 values relative to the block's largest (exact unless it
-// is 2^15 times smaller, and then off by less than 2^-24 of the block's largest logit), the rest into the
-// logits' factor; a value's 2^ev goes into its weight (see kv_attend.cu).  O is rescaled only when a
+// Scales: a key's 2^ek goes into its FP16 values relative to the block's largest as far as that is exact, down
+// to 2^-15 (codes are multiples of 2^-9, FP16 values of 2^-24), the rest into the logits' factor: one for the block
+// or, where some key is smaller still, one a token.  (The largest key may be one that a row does not even see.)  A
+// value's 2^ev goes into its weight (see kv_attend.cu).  O is rescaled only when a
 // row's maximum has grown by more than 2^7: the weights then still fit FP16.
 #include <atomic>
 
@@ -183,8 +184,8 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
   __shared__ uint64_t blk_full[AT_RING], blk_empty[AT_RING], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
       p_full[2], o_done, drain, sc_full[AT_RING];
   __shared__ Block ring[AT_RING];
-  __shared__ __align__(16) float ev_f[AT_RING][KV_BLOCK], ev_inv[AT_RING][KV_BLOCK];
-  __shared__ float q_factor[128], ek_top[AT_RING];
+  __shared__ __align__(16) float ev_f[AT_RING][KV_BLOCK], ev_inv[AT_RING][KV_BLOCK], ek_f[AT_RING][KV_BLOCK];
+  __shared__ float q_factor[128], ek_top[AT_RING];   // ek_top: 2^(largest key exponent); 0: the tokens' own in ek_f
   __shared__ uint32_t tmem_s;
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -437,7 +438,13 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
         const bool nan = (dt < 32 ? ea : eb) == KV_NAN || ev == KV_NAN;
         ev_f[sp][dt] = nan ? __int_as_float(0x7FC00000) : (float)(ev - 127);
         ev_inv[sp][dt] = pow2f(127 - min(ev, 253));
-        if (dt == 0) ek_top[sp] = pow2f(max(top, 1) - 127);
+        // tokens whose own scales reach below what FP16 holds relative to the largest (a byte of 0: not read)
+        const bool wide = __any_sync(0xffffffffu, (ea && top - ea > 15) || (eb && top - eb > 15));
+        if (wide) {
+          const int ek = dt < 32 ? ea : eb;
+          ek_f[sp][dt] = pow2f(ek == KV_NAN ? 0 : ek + min(top - ek, 15) - 127);
+        }
+        if (dt == 0) ek_top[sp] = wide ? 0.0f : pow2f(max(top, 1) - 127);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_full[sp]);
       }
@@ -455,7 +462,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
           const int x = x0 + j * (64 / CH);
           const int both = __shfl_sync(0xffffffffu, e2, x & 31);
           const int d = max(top - (x < 32 ? both & 255 : both >> 8), 0);
-          const uint32_t f = d < 15 ? (uint32_t)(15 - d) << 10 : d < 25 ? 1u << (24 - d) : 0u;   // 2^-d
+          const uint32_t f = d < 15 ? (uint32_t)(15 - d) << 10 : 1u << 9;   // 2^-min(d, 15)
 #pragma unroll
           for (int k = 0; k < 8; ++k) o[k] = mul_f16x2(o[k], f | f << 16);
         }
@@ -490,8 +497,21 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       tc_fence_after();
       const bool any = __any_sync(0xffffffffu, n > 0);   // else none of the warp's tokens lists the block
       // two passes over S, 32 columns at a time (as a loop: see wait_long): the maximum, then the weights
-      const float f = qf * ek_top[sp];
+      const float kt = ek_top[sp];
+      const float f = kt != 0.0f ? qf * kt : 1.0f;
       const uint64_t f2 = pack2(f, f);
+      if (kt == 0.0f && any) {   // S times its tokens' own factors, in place
+#pragma unroll 1
+        for (int c = 0; c < KV_BLOCK; c += 16) {
+          uint32_t s[16];
+          tmem_ld16(lane_base + st * 64 + c, s);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * qf * ek_f[sp][c + x]);
+          tmem_st16(lane_base + st * 64 + c, s);
+        }
+        tmem_wait_st();
+      }
       const bool whole = __all_sync(0xffffffffu, n == 0 || n == KV_BLOCK);
       float mx = -INFINITY;
 #pragma unroll 1

@@ -7,7 +7,7 @@ import torch
 
 import kv_reference as R
 from bit_routed_expert_gb300 import KvCache, kv_append, kv_attend, kv_read, kv_select
-from test_kv_cache import check_select, on
+from test_kv_cache import check_attend, check_select, on, some_ids
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +105,24 @@ def test_new_outputs_of_a_call_on_another_stream_are_allocated_there(cuda_dev):
     with torch.cuda.stream(side):
         assert not {torch.empty(s, dtype=d, device=cuda_dev).data_ptr() for s, d in shapes} & places
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("up", [14, 15, 16, 24, 40, 100])
+def test_attend_beside_a_key_of_another_size(cuda_dev, up, D):
+    """One key of every block is 2^up times the others: for the rows that see it, orthogonal to their queries; the
+    tokens before it in the last block do not see it.  The other keys count in full either way."""
+    H, G, T, slot = 2, 4, 40, 15
+    lens = [400]
+    b = R.batch(lens, [T])
+    pages, _, _ = R.filled(b, lens, H, D)
+    kc, _, ks, _ = R.views(pages, D)
+    kc[:, :, slot, 1:] = 0
+    kc[:, :, slot, 0] = 0x7E
+    ks[:, :, slot] += up
+    q = R.rows(21, T, H * G, D)
+    q[:, :, 0] = 0.0
+    check_attend(cuda_dev, b, pages, q, some_ids(b, H, 5))
+    ks -= 60   # and all keys small, the queries large
+    q *= 2.0 ** 60
+    check_attend(cuda_dev, b, pages, q, some_ids(b, H, 5))
