@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(AR_WARPS * 32, ar_ctas(D, NT)) kv_attend_rows_
     l[nt][0] = l[nt][1] = 0.0f;
   }
 
+  bool large = false;   // a value scale above EV_LARGE has been met
   const int step = ranks * AR_WARPS, items = 2 * a.k;
   const int32_t* idr = a.ids + (size_t)row * a.k;
   for (int base = rank * AR_WARPS + warp; base < items; base += 32 * step) {
@@ -178,6 +179,12 @@ __global__ void __launch_bounds__(AR_WARPS * 32, ar_ctas(D, NT)) kv_attend_rows_
           kf2[mt][r] = pow2f(ek[mt][r] - 127);
           evf[mt][r] = ek[mt][r] == KV_NAN || ev[mt][r] == KV_NAN ? __int_as_float(0x7FC00000) : (float)(ev[mt][r] - 127);
         }
+      bool beyond = false;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) beyond |= ev[mt][r] > EV_LARGE;   // (NaN rows as well; unseen tokens have 127)
+      large |= __any_sync(0xffffffffu, beyond);
       // weights; sc[mt][2 r + c] is token 16 mt + 8 r + g, head 2 t4 + c
       uint32_t pb[NT][2][2];
 #pragma unroll
@@ -200,8 +207,15 @@ __global__ void __launch_bounds__(AR_WARPS * 32, ar_ctas(D, NT)) kv_attend_rows_
           mx[c] = fmaxf(mx[c], m[nt][c]);
           const float base_m = mx[c] > -INFINITY ? mx[c] - P_SHIFT : 0.0f;   // NaN logits have no maximum
           const float r0 = ex2(m[nt][c] - P_SHIFT - base_m);
+          l[nt][c] = scale_sum(l[nt][c], m[nt][c] - P_SHIFT - base_m);
           m[nt][c] = mx[c];
-          l[nt][c] *= r0;
+          float without = l[nt][c];
+          if (large) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) without += exp2f(sc[nt][mt][2 * r + c] - base_m - evf[mt][r]);
+          }
 #pragma unroll
           for (int i = 0; i < MT; ++i) o[nt][i][c] *= r0, o[nt][i][2 + c] *= r0;
 #pragma unroll
@@ -212,6 +226,7 @@ __global__ void __launch_bounds__(AR_WARPS * 32, ar_ctas(D, NT)) kv_attend_rows_
               v = ex2(v - base_m);
               l[nt][c] = fmaf(v, pow2f(127 - ev[mt][r]), l[nt][c]);
             }
+          if (large) l[nt][c] = without;
         }
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -273,7 +288,7 @@ __global__ void __launch_bounds__(AR_WARPS * 32, ar_ctas(D, NT)) kv_attend_rows_
       for (int w = 0; w < AR_WARPS; ++w) M = fmaxf(M, part_m[w][threadIdx.x]);
       const float b = M > -INFINITY ? M : 0.0f;
 #pragma unroll
-      for (int w = 0; w < AR_WARPS; ++w) ll = fmaf(ex2(part_m[w][threadIdx.x] - b), part_l[w][threadIdx.x], ll);
+      for (int w = 0; w < AR_WARPS; ++w) ll += scale_sum(part_l[w][threadIdx.x], part_m[w][threadIdx.x] - b);
       mm = M;
     }
     __syncthreads();
@@ -290,9 +305,9 @@ __global__ void __launch_bounds__(AR_WARPS * 32, ar_ctas(D, NT)) kv_attend_rows_
     for (int j = 0; j < parts; ++j) M = fmaxf(M, at(&part_m[j & 3][head], &part_m[0][head], j));
     const float b = M > -INFINITY ? M : 0.0f;
     for (int j = 0; j < parts; ++j) {
-      const float w = ex2(at(&part_m[j & 3][head], &part_m[0][head], j) - b);
-      v = fmaf(w, at(&part_o[j & 3][head][c], &part_o[0][head][c], j), v);
-      z = fmaf(w, at(&part_l[j & 3][head], &part_l[0][head], j), z);
+      const float d = at(&part_m[j & 3][head], &part_m[0][head], j) - b;
+      v = fmaf(ex2(d), at(&part_o[j & 3][head][c], &part_o[0][head][c], j), v);
+      z += scale_sum(at(&part_l[j & 3][head], &part_l[0][head], j), d);
     }
     const size_t r = (size_t)row * a.G + head;
     a.out[r * D + c] = (uint16_t)f32_to_bf16_rne(z == 0.0f ? 0.0f : v / z);

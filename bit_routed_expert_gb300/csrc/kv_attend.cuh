@@ -19,6 +19,18 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// Weights are 2^(logit + ev) against their own maximum, ev the exponent of the value's scale; the sum of exponentials
+// gets the factor 2^-ev back.  A weight that vanishes beside a value of another size still counts in that sum.
+// While no value scale is above this byte no term within 2^-40 of the sum is lost (ev is -64 at least, 26 at most: a
+// weight is above 2^-126 if its term is); from the first larger one on (values beyond 3 * 10^10; infinities have
+// ev = 119) the sum's terms are formed without ev.
+constexpr int EV_LARGE = 153;
+// l * 2^d for d <= 0, where 2^d alone may vanish although l is large (sums are held relative to the weights' maximum).
+__device__ __forceinline__ float scale_sum(float l, float d) {
+  const float h = ex2(0.5f * d);
+  return l * h * h;
+}
+
 struct AttendArgs {
   const uint8_t* pages;
   int H, G;

@@ -173,6 +173,65 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// A row's part of one block as in the main loop of the softmax, in steps that are right for scales of any size: the
+// logits of S times the query's factor, then times the keys' own; terms of the sum formed without the values'
+// exponents ev.  By a whole warp; S, O: this warp's tensor memory; kt: the factor of the keys of tokens 0-31 and
+// 32-63, where it is positive, else it is in ek for each; m, l: the row's maximum and sum -> the new ones.  A tile
+// goes on this way from its first block whose keys are far apart or that has a value scale above EV_LARGE, in a loop
+// of its own behind the main one (402 us for the 8,192-token chunk; called in the main loop 412 to 445, where it is
+// never taken).
+template <int D>
+__device__ __forceinline__ float2 careful_block(uint32_t S, uint32_t O, bool have_o, float2 kt, const float* ek, const float* ev,
+                                             float qf, int n, float m, float l) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < KV_BLOCK; c += 16) {
+    uint32_t s[16];
+    tmem_ld16(S + c, s);
+    tmem_wait_ld();
+    const float k = c < 32 ? kt.x : kt.y;
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      const float v = c + x < n ? fmaf(__uint_as_float(s[x]) * qf, k > 0.0f ? k : ek[c + x], ev[c + x]) : -INFINITY;
+      mx = fmaxf(mx, v);
+      s[x] = __float_as_uint(v);
+    }
+    tmem_st16(S + c, s);
+  }
+  tmem_wait_st();
+  const float nm = fmaxf(m, mx), d = m > -INFINITY ? m - nm : 0.0f;
+  if (have_o && __any_sync(0xffffffffu, d < 0.0f)) {
+    const float sc = ex2(d);
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+      uint32_t o[16];
+      tmem_ld16(O + c, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * sc);
+      tmem_st16(O + c, o);
+    }
+    tmem_wait_st();
+  }
+  l = scale_sum(l, d);
+  const float base = nm > -INFINITY ? nm - P_SHIFT : 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < KV_BLOCK; c += 32) {
+    uint32_t s[32], pk[16];
+    tmem_ld32(S + c, s);
+    tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < 32; x += 2) {
+      const float v0 = __uint_as_float(s[x]) - base, v1 = __uint_as_float(s[x + 1]) - base;
+      if (c + x < n) l += exp2f(v0 - ev[c + x]);
+      if (c + x + 1 < n) l += exp2f(v1 - ev[c + x + 1]);
+      pk[x / 2] = pack_f16x2(ex2(v0), ex2(v1));
+    }
+    tmem_st16(S + c / 2, pk);
+  }
+  return make_float2(nm, l);
+}
+
 // PATIENT: the waits have the default budget; else the one that was set (a budget that is not a constant costs 5 %
 // of the kernel's time, even where only the out-of-line wait knows it).
 template <int D, bool PATIENT>
@@ -185,7 +244,8 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       p_full[2], o_done, drain, sc_full[AT_RING];
   __shared__ Block ring[AT_RING];
   __shared__ __align__(16) float ev_f[AT_RING][KV_BLOCK], ev_inv[AT_RING][KV_BLOCK], ek_f[AT_RING][KV_BLOCK];
-  __shared__ float q_factor[128], ek_top[AT_RING];   // ek_top: 2^(largest key exponent); 0: the tokens' own in ek_f
+  __shared__ float q_factor[128];
+  __shared__ float2 ek_top[AT_RING];   // one half by each warp, see careful_block
   __shared__ uint32_t tmem_s;
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -440,11 +500,12 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
         ev_inv[sp][dt] = pow2f(127 - min(ev, 253));
         // tokens whose own scales reach below what FP16 holds relative to the largest (a byte of 0: not read)
         const bool wide = __any_sync(0xffffffffu, (ea && top - ea > 15) || (eb && top - eb > 15));
-        if (wide) {
+        const bool large = __any_sync(0xffffffffu, ev > EV_LARGE);   // (of this warp's half; NaN rows as well)
+        if (wide || large) {
           const int ek = dt < 32 ? ea : eb;
           ek_f[sp][dt] = pow2f(ek == KV_NAN ? 0 : ek + min(top - ek, 15) - 127);
         }
-        if (dt == 0) ek_top[sp] = wide ? 0.0f : pow2f(max(top, 1) - 127);
+        if (lane == 0) reinterpret_cast<float*>(&ek_top[sp])[dt >> 5] = wide || large ? 0.0f : pow2f(max(top, 1) - 127);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_full[sp]);
       }
@@ -481,7 +542,8 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
     const float qf = q_factor[r];
     const uint32_t lane_base = tmem + ((uint32_t)warp << 21);   // lanes 32 warp ..
     float m = -INFINITY, l = 0.0f;   // m: the maximum that the weights are held against
-    int i = 0;
+    bool rare = false;               // a block that is not for this loop: see careful_block
+    int i = 0, n = 0;
     for (;; ++i) {
       const int st = i & 1;
       if (!warp_wait(&blk_full[i % AT_RING], i / AT_RING)) break;
@@ -491,27 +553,19 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       __syncwarp();
       if (lane == 0) mbar_arrive(&blk_empty[i % AT_RING]);
       if (page < 0) break;
-      const int n = mine ? min(KV_BLOCK, pos - id * KV_BLOCK + 1) : 0;   // tokens that the row sees
+      n = mine ? min(KV_BLOCK, pos - id * KV_BLOCK + 1) : 0;   // tokens that the row sees
       const int sp = i % AT_RING;
       if (!warp_wait(&sc_full[sp], i / AT_RING) || !warp_wait(&s_full[st], i >> 1)) break;
       tc_fence_after();
       const bool any = __any_sync(0xffffffffu, n > 0);   // else none of the warp's tokens lists the block
       // two passes over S, 32 columns at a time (as a loop: see wait_long): the maximum, then the weights
-      const float kt = ek_top[sp];
-      const float f = kt != 0.0f ? qf * kt : 1.0f;
-      const uint64_t f2 = pack2(f, f);
-      if (kt == 0.0f && any) {   // S times its tokens' own factors, in place
-#pragma unroll 1
-        for (int c = 0; c < KV_BLOCK; c += 16) {
-          uint32_t s[16];
-          tmem_ld16(lane_base + st * 64 + c, s);
-          tmem_wait_ld();
-#pragma unroll
-          for (int x = 0; x < 16; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * qf * ek_f[sp][c + x]);
-          tmem_st16(lane_base + st * 64 + c, s);
-        }
-        tmem_wait_st();
+      const float2 kt = ek_top[sp];
+      if (fminf(kt.x, kt.y) == 0.0f) {
+        rare = true;
+        break;
       }
+      const float f = qf * kt.x;
+      const uint64_t f2 = pack2(f, f);
       const bool whole = __all_sync(0xffffffffu, n == 0 || n == KV_BLOCK);
       float mx = -INFINITY;
 #pragma unroll 1
@@ -541,9 +595,9 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
         // some row's weights would outgrow FP16: all rows of the warp take their new maximum
         if (!warp_wait(&o_done, i - 1)) break;
         tc_fence_after();
-        const float nm = fmaxf(m, mx), sc = m > -INFINITY ? ex2(m - nm) : 1.0f;
+        const float nm = fmaxf(m, mx), d = m > -INFINITY ? m - nm : 0.0f, sc = ex2(d);
         m = nm;
-        l *= sc;
+        l = scale_sum(l, d);
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           uint32_t o[16];
@@ -600,6 +654,27 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[st]);
+    }
+    // the rest of the tile's blocks from the first rare one on
+    while (rare && ok) {
+      const int st = i & 1, sp = i % AT_RING;
+      if (i > 0 && !warp_wait(&o_done, i - 1)) break;   // O may be rescaled
+      tc_fence_after();
+      const float2 ml = careful_block<D>(lane_base + st * 64, lane_base + 128, i > 0, ek_top[sp], ek_f[sp], ev_f[sp], qf, n, m, l);
+      m = ml.x, l = ml.y;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[st]);
+      ++i;
+      if (!warp_wait(&blk_full[i % AT_RING], i / AT_RING)) break;
+      const Block& b = ring[i % AT_RING];
+      const int page = b.page;
+      n = live && (b.mask[tl >> 5] >> (tl & 31) & 1u) ? min(KV_BLOCK, pos - b.id * KV_BLOCK + 1) : 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&blk_empty[i % AT_RING]);
+      if (page < 0 || !warp_wait(&sc_full[i % AT_RING], i / AT_RING) || !warp_wait(&s_full[i & 1], i >> 1)) break;
+      tc_fence_after();
     }
     if (i > 0) warp_wait(&drain, 0);   // not o_done: the last two products with V may both be pending
     tc_fence_after();

@@ -126,3 +126,23 @@ def test_attend_beside_a_key_of_another_size(cuda_dev, up, D):
     ks -= 60   # and all keys small, the queries large
     q *= 2.0 ** 60
     check_attend(cuda_dev, b, pages, q, some_ids(b, H, 5))
+
+
+@pytest.mark.parametrize("where", ["first", "last", "everywhere"])
+@pytest.mark.parametrize("big", [50, 80, 110, 119])
+def test_attend_beside_a_value_of_another_size(cuda_dev, big, where):
+    """Value rows of zeros (the least scale, 2^-64) and a few whose scale is 2^big, up to that of infinities, which
+    saturate: every token counts in the sum of the weights whatever its value's scale."""
+    D, H, G, T = 64, 2, 4, 40
+    lens = [400]
+    b = R.batch(lens, [T])
+    pages, _, _ = R.filled(b, lens, H, D)
+    _, vc, _, vs = R.views(pages, D)
+    g = torch.Generator().manual_seed(big)
+    zero = torch.rand(vs.shape, generator=g) < 0.5
+    vc[zero], vs[zero] = 0, 63
+    block = {"first": [0], "last": [5], "everywhere": range(7)}[where]
+    for i in block:
+        vs[int(b.table[0, i]), :, ::9] = 127 + big
+    ids = torch.arange(6, dtype=torch.int32).expand(T, H, 6).contiguous()
+    check_attend(cuda_dev, b, pages, R.rows(21, T, H * G, D), ids)
