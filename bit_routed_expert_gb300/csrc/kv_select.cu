@@ -28,6 +28,10 @@ __device__ __forceinline__ float score_of_key(uint32_t key) {
   return __uint_as_float(key ^ (~(uint32_t)((int32_t)key >> 31) | 0x80000000u));
 }
 
+// Scores are held as the whole number times 2^(bound_exp - SCORE_DOWN): below 2^24 times 2^122, they would be beyond
+// FP32's range for keys near the ends of theirs, and infinities do not compare.
+constexpr int SCORE_DOWN = 32;
+
 // Keys lie in shared memory with four unused words after every 16: a lane reads 4, 8 or 16 of them
 // in a row by 16-byte loads that meet no bank twice.
 __host__ __device__ constexpr int key_at(int i) { return i + 4 * (i >> 4); }
@@ -280,12 +284,13 @@ __device__ __forceinline__ Forced forced_blocks(const SelectArgs& a, int s, int 
 __device__ __forceinline__ void write_lists(const SelectArgs& a, size_t row, const Forced& f, const uint32_t* forced_k,
                                             const uint32_t* mid_k, const int* mid_b, int n_mid, int eq) {
   const int lane = threadIdx.x & 31, slots = f.slots();
-  const float up = pow2f(eq);
+  const int e1 = (eq + SCORE_DOWN) / 2;   // in two factors: their product may be beyond FP32 where the score is not
+  const float up1 = pow2f(e1), up2 = pow2f(eq + SCORE_DOWN - e1);
   int32_t* ids = a.ids + row * a.k;
   float* scores = a.scores ? a.scores + row * a.k : nullptr;
   auto put = [&](int p, int b, uint32_t key) {
     ids[p] = b;
-    if (scores) scores[p] = score_of_key(key) * up;
+    if (scores) scores[p] = score_of_key(key) * up1 * up2;
   };
   int at = 0;
   for (int i0 = 0; i0 < slots || i0 == 0; i0 += 32) {
@@ -496,7 +501,7 @@ __global__ void __launch_bounds__(SR_WARPS * 32, 2) kv_select_rows_kernel(const 
       if (g == 0)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          if (ic + c < wn) keys[key_at(w0 + ic + c)] = e[nt][c] == -128 ? 0u : key_of_score(acc[nt][c] * pow2f(e[nt][c]));
+          if (ic + c < wn) keys[key_at(w0 + ic + c)] = e[nt][c] == -128 ? 0u : key_of_score(acc[nt][c] * pow2f(e[nt][c] - SCORE_DOWN));
     }
   }
   __syncthreads();
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(ST_WARPS * 32, 2) kv_select_tiles_kernel(const
   uint4* af = reinterpret_cast<uint4*>(sm_raw);                        // [2 row tiles][KS][32 lanes]
   uint32_t* keys = reinterpret_cast<uint32_t*>(sm_raw + ST_ROWS * 2 * D * 2);   // [ST_ROWS][ST_LD]
   int* page = reinterpret_cast<int*>(keys + ST_ROWS * ST_LD);          // [SEL_CHUNK]
-  float* unit = reinterpret_cast<float*>(page + SEL_CHUNK);            // [SEL_CHUNK] 2^bound_exp, 0: no page
+  float* unit = reinterpret_cast<float*>(page + SEL_CHUNK);            // [SEL_CHUNK] 2^(bound_exp - SCORE_DOWN), 0: no page
   const int kk = (a.k + 15) / 16 * 16;
   uint32_t* best_k = reinterpret_cast<uint32_t*>(unit + SEL_CHUNK);    // [ST_ROWS][key_at(kk)]
   int* best_b = reinterpret_cast<int*>(best_k + ST_ROWS * key_at(kk)); // [ST_ROWS][kk]
@@ -639,7 +644,7 @@ __global__ void __launch_bounds__(ST_WARPS * 32, 2) kv_select_tiles_kernel(const
       for (int i = tid; i < SEL_CHUNK; i += ST_WARPS * 32) {
         const int pg = i < nc ? kv_page(a.tab, s, base + i, a.err) : -1;
         page[i] = pg;
-        unit[i] = pg >= 0 ? pow2f(__ldg(a.bexp + (size_t)pg * a.H + h)) : 0.0f;
+        unit[i] = pg >= 0 ? pow2f(__ldg(a.bexp + (size_t)pg * a.H + h) - SCORE_DOWN) : 0.0f;
       }
       __syncthreads();
       for (int c0 = warp * 8 * ST_NT; c0 < nc; c0 += ST_WARPS * 8 * ST_NT) {

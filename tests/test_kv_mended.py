@@ -146,3 +146,19 @@ def test_attend_beside_a_value_of_another_size(cuda_dev, big, where):
         vs[int(b.table[0, i]), :, ::9] = 127 + big
     ids = torch.arange(6, dtype=torch.int32).expand(T, H, 6).contiguous()
     check_attend(cuda_dev, b, pages, R.rows(21, T, H * G, D), ids)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("shift", [50, 90, 119])
+def test_select_compares_scores_beyond_the_range(cuda_dev, T, shift):
+    """Keys so large (infinities are stored as 448 * 2^119) that a score without the query's factor is beyond FP32: the
+    blocks still compare as whole numbers do, and with small queries the scores themselves are within the range."""
+    D, H, G = 64, 1, 4
+    lens = [1000]
+    b = R.batch(lens, [T])
+    pages, bounds, bexp = R.filled(b, lens, H, D)
+    bexp += shift
+    q = R.rows(2, T, G, D)
+    check_select(cuda_dev, b, (pages, bounds, bexp), q * 2.0 ** -shift, 6, 1, 1)
+    q[:, :, :D // 2] = 0.0
+    check_select(cuda_dev, b, (pages, bounds, bexp), q * 2.0 ** -50, 6, 0, 1)
