@@ -280,6 +280,7 @@ bre_status kv_attend(const bre_kv_cache* cache, const void* q_bf16, int64_t q_st
   bre_status st = kv_check(cache, seq, pos, T, table, B, N);
   if (st != BRE_OK || T == 0) return st;
   if ((st = kv_check_q(cache, q_bf16, q_stride, n_heads, k)) != BRE_OK) return st;
+  if (N > (1 << 25) - 2) return BRE_ERR_UNSUPPORTED;   // block numbers share 32 bits with a tile's 128 tokens
   if (!ids || !out_bf16 || !aligned(out_bf16, 32) || !(scale - scale == 0.0f)) return BRE_ERR_ARG;
   const size_t need = kv_attend_ws_bytes(T, n_heads, cache->n_kv_heads, cache->head_dim, B, k);
   if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return BRE_ERR_WORKSPACE;

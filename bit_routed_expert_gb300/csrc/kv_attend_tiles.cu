@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
         while (ptr[j] < a.k) {
           const int b = __ldg(idr[j] + ptr[j]++);
           if (b >= 0 && b <= pos[j] / KV_BLOCK) {
-            cur[j] = run[j] | (uint32_t)min(b, (1 << 25) - 2);
+            cur[j] = run[j] | (uint32_t)min(b, (1 << 25) - 2);   // (larger tables are refused: that block is outside)
             break;
           }
         }

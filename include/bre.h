@@ -360,7 +360,8 @@ bre_status kv_select(const bre_kv_cache *cache, const void *q_bf16, int64_t q_st
  * probabilities enter the second product as FP16 (relative error 2^-11 for those within 2^-22 of the
  * row's largest, the value's scale counted in; absolute below), the codes exactly.
  *   ids [T][n_kv_heads][k] int32, any order; out [T][n_heads][D] BF16, 32-byte aligned; lse [T][n_heads] FP32 or
- *   NULL (natural logarithm).  ws: as in kv_select, kv_attend_workspace(...) bytes.  Requires G <= 16, k <= 256. */
+ *   NULL (natural logarithm).  ws: as in kv_select, kv_attend_workspace(...) bytes.  Requires G <= 16, k <= 256,
+ *   N <= 2^25 - 2. */
 size_t kv_attend_workspace(int T, int n_heads, int n_kv_heads, int head_dim, int B, int k);
 bre_status kv_attend(const bre_kv_cache *cache, const void *q_bf16, int64_t q_stride, int n_heads, const int32_t *seq,
                      const int32_t *pos, int T, const int32_t *table, int B, int N, const int32_t *ids, int k,
