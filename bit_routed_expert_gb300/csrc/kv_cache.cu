@@ -51,6 +51,46 @@ struct RowCode {
   }
 };
 
+// Padding may be long (a graph of a fixed number of tokens): what looks beyond it takes KA_LOOK entries a lane at a time.
+constexpr int KA_LOOK = 8;
+
+// By a whole warp: the last index <= i whose entry is no padding, -1 if there is none.
+__device__ __forceinline__ int last_real(const int32_t* __restrict__ pos, int i) {
+  const int lane = threadIdx.x & 31;
+  for (; i >= 0; i -= KA_LOOK * 32) {
+    int p[KA_LOOK];
+#pragma unroll
+    for (int j = 0; j < KA_LOOK; ++j) p[j] = i - 32 * j - lane >= 0 ? __ldg(pos + i - 32 * j - lane) : -1;
+#pragma unroll
+    for (int j = 0; j < KA_LOOK; ++j) {
+      const uint32_t real = __ballot_sync(0xffffffffu, p[j] >= 0);
+      if (real) return i - 32 * j - (__ffs(real) - 1);
+    }
+  }
+  return -1;
+}
+
+// By a whole warp, of the entries first .. first + 32 KA_LOOK - 1 (< T): the first of another block (else T), and the
+// last before it that is of this one, plus 1 (else 0).
+__device__ __forceinline__ int2 run_end(const int32_t* __restrict__ seq, const int32_t* __restrict__ pos, int first, int T,
+                                        int s, int blk) {
+  const int lane = threadIdx.x & 31;
+  int p[KA_LOOK], q[KA_LOOK], last = 0;
+#pragma unroll
+  for (int j = 0; j < KA_LOOK; ++j) {
+    const int i = first + 32 * j + lane;
+    p[j] = i < T ? __ldg(pos + i) : -1, q[j] = i < T ? __ldg(seq + i) : -1;
+  }
+#pragma unroll
+  for (int j = 0; j < KA_LOOK; ++j) {
+    const uint32_t other = __ballot_sync(0xffffffffu, p[j] >= 0 && (q[j] != s || p[j] / KV_BLOCK != blk));
+    const uint32_t own = __ballot_sync(0xffffffffu, p[j] >= 0) & ((other & -other) - 1u);   // (all if there is no other)
+    if (own) last = first + 32 * j + 32 - __clz(own);
+    if (other) return make_int2(first + 32 * j + __ffs(other) - 1, last);
+  }
+  return make_int2(T, last);
+}
+
 template <int D>
 __global__ void __launch_bounds__(KA_WARPS * 32, 5)
     kv_append_kernel(uint8_t* __restrict__ pages, int8_t* __restrict__ bounds, int8_t* __restrict__ bexp, int H, KvTable tab,
@@ -59,12 +99,12 @@ __global__ void __launch_bounds__(KA_WARPS * 32, 5)
   constexpr int LR = D / 8, RW = 32 / LR;       // lanes a row, rows a warp
   constexpr int RC = RW * KA_WARPS, UN = 2;     // rows of the CTA at a time, of which UN steps are in flight
   __shared__ float s_hi[KA_WARPS][D], s_lo[KA_WARPS][D], s_max[KA_WARPS];
-  __shared__ int s_other[2][KA_WARPS];
+  __shared__ int2 s_end[2][KA_WARPS];
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lr = lane % LR;
   const int h = blockIdx.y, c0 = blockIdx.x * chunk, c1 = min(c0 + chunk, T);
-  int par = 0;   // of s_other: the barrier of one pass also keeps the next but one from overtaking it
+  int par = 0;   // of s_end: the barrier of one pass also keeps the next but one from overtaking it
   for (int t = c0; t < c1;) {
     // What the run needs is read in two steps, each of loads that do not wait for one another: first the
     // positions, then the page's number, the first rows and (page known) the old bounds.
@@ -77,17 +117,17 @@ __global__ void __launch_bounds__(KA_WARPS * 32, 5)
       const int r = q0 + j * RC;
       slot[j] = r < T ? __ldg(pos + r) : -1, sq[j] = r < T ? __ldg(seq + r) : -1;
     }
-    int i = t + 1 + tid;
-    int pi = i < T ? __ldg(pos + i) : -1, si = i < T ? __ldg(seq + i) : -1;
-    if (p < 0) {
-      ++t;
+    const int i = t + 1 + tid;
+    const int pi = i < T ? __ldg(pos + i) : -1, si = i < T ? __ldg(seq + i) : -1;
+    if (p < 0) {   // on to the next entry that is no padding
+      const uint32_t real = __ballot_sync(0xffffffffu, t + 1 + lane < c1 && __ldg(pos + t + 1 + lane) >= 0);
+      t += real ? __ffs(real) : 33;
       continue;
     }
     // a run that started in a chunk before belongs to it
     bool mine = t == 0 || bp < 0 || bs != s || bp / KV_BLOCK != blk;
     if (t && bp < 0) {
-      int back = t - 2;
-      while (back >= 0 && __ldg(pos + back) < 0) --back;
+      const int back = last_real(pos, t - 2);
       mine = back < 0 || __ldg(seq + back) != s || __ldg(pos + back) / KV_BLOCK != blk;
     }
     const int page = mine ? kv_page(tab, s, blk, tid == 0 ? err : nullptr) : -1;
@@ -99,19 +139,25 @@ __global__ void __launch_bounds__(KA_WARPS * 32, 5)
       kw[j] = in ? __ldg(reinterpret_cast<const uint4*>(k + r * k_stride + h * D) + lr) : make_uint4(0, 0, 0, 0);
       vw[j] = in ? __ldg(reinterpret_cast<const uint4*>(v + r * v_stride + h * D) + lr) : make_uint4(0, 0, 0, 0);
     }
-    // the run's end: the first token of another block
-    int t1 = T;
-    for (int i0 = t + 1;;) {
+    // the run's end: the first token of another block; and its last own token, as padding may follow
+    int t1 = T, t2 = t + 1;
+    {
       const uint32_t other = __ballot_sync(0xffffffffu, pi >= 0 && (si != s || pi / KV_BLOCK != blk));
-      if (lane == 0) s_other[par][warp] = other ? i0 + warp * 32 + __ffs(other) - 1 : T;
+      const uint32_t own = __ballot_sync(0xffffffffu, pi >= 0) & ((other & -other) - 1u);   // (all if there is no other)
+      const int i0 = t + 1 + warp * 32;
+      if (lane == 0) s_end[par][warp] = make_int2(other ? i0 + __ffs(other) - 1 : T, own ? i0 + 32 - __clz(own) : 0);
+    }
+    for (int i0 = t + 1 + KA_WARPS * 32;; i0 += KA_WARPS * KA_LOOK * 32) {
       __syncthreads();
 #pragma unroll
-      for (int w = 0; w < KA_WARPS; ++w) t1 = min(t1, s_other[par][w]);
+      for (int w = 0; w < KA_WARPS; ++w) {
+        const int2 end = s_end[par][w];
+        if (t1 == T) t1 = end.x, t2 = max(t2, end.y);
+      }
       par ^= 1;
-      i0 += KA_WARPS * 32;
       if (t1 < T || i0 >= T) break;
-      i = i0 + tid;
-      pi = i < T ? __ldg(pos + i) : -1, si = i < T ? __ldg(seq + i) : -1;
+      const int2 end = run_end(seq, pos, i0 + warp * KA_LOOK * 32, T, s, blk);
+      if (lane == 0) s_end[par][warp] = end;
     }
     t = t1;
     if (!mine) continue;
@@ -131,14 +177,14 @@ __global__ void __launch_bounds__(KA_WARPS * 32, 5)
     float hi[8], lo[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) hi[c] = -INFINITY, lo[c] = INFINITY;
-    for (int r0 = q0; r0 - lane / LR < t1; r0 += UN * RC) {
+    for (int r0 = q0; r0 - lane / LR < t2; r0 += UN * RC) {
 #pragma unroll
       for (int j = 0; j < UN; ++j) {
         const RowCode<LR> kc(kw[j]), vc(vw[j]);
-        const int at = r0 + j * RC < t1 ? slot[j] : -1;
+        const int at = r0 + j * RC < t2 ? slot[j] : -1;
         // a later row takes the registers: its loads run while the others are stored
         const int r = r0 + (UN + j) * RC;
-        const bool in = r < t1;
+        const bool in = r < t2;
         kw[j] = in ? __ldg(reinterpret_cast<const uint4*>(k + r * k_stride + h * D) + lr) : make_uint4(0, 0, 0, 0);
         vw[j] = in ? __ldg(reinterpret_cast<const uint4*>(v + r * v_stride + h * D) + lr) : make_uint4(0, 0, 0, 0);
         slot[j] = in ? __ldg(pos + r) : -1;

@@ -162,3 +162,25 @@ def test_select_compares_scores_beyond_the_range(cuda_dev, T, shift):
     check_select(cuda_dev, b, (pages, bounds, bexp), q * 2.0 ** -shift, 6, 1, 1)
     q[:, :, :D // 2] = 0.0
     check_select(cuda_dev, b, (pages, bounds, bexp), q * 2.0 ** -50, 6, 0, 1)
+
+
+@pytest.mark.parametrize("D,H", [(64, 3), (128, 1)])
+@pytest.mark.parametrize("before,between,behind", [(0, 0, 4000), (4000, 0, 0), (1300, 1, 1300), (70, 130, 1025), (33, 257, 31)])
+def test_append_among_long_padding(cuda_dev, D, H, before, between, behind):
+    """Padding before, between the tokens of (and between) blocks, and behind; chunks that are all padding."""
+    lens, new = [150, 70], [90, 70]
+    b = R.batch(lens, new)
+    seq, pos = [0] * before, [-1] * before
+    for i, (s, p) in enumerate(zip(b.seq, b.pos)):
+        gap = between if i % 37 == 5 else 0
+        seq += [s] + [1] * gap
+        pos += [p] + [-1] * gap
+    n = R.Batch(seq + [0] * behind, pos + [-1] * behind, b.table, b.n_pages)
+    T = len(n.seq)
+    pages, bounds, bexp = R.filled(b, lens, H, D)
+    k, v = R.rows(1, T, H, D), R.rows(2, T, H, D)
+    c = on(cuda_dev, pages, bounds, bexp)
+    kv_append(c, k.to(cuda_dev), v.to(cuda_dev), *n.on(cuda_dev))
+    real = [i for i in range(T) if n.pos[i] >= 0]   # padding between a block's tokens changes nothing
+    assert not R.append(pages, bounds, bexp, k[real], v[real], b.seq, b.pos, b.table)
+    assert all(torch.equal(x, y) for x, y in zip(own(c), (pages, bounds, bexp)))
