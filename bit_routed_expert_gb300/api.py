@@ -310,7 +310,7 @@ def kv_select(q, cache: KvCache, seq, pos, table, k: int, n_sink: int = 1, n_loc
               scores=None, dev_err=None, stream=None):
     """For each token and kv head the k blocks to attend to: the first n_sink, the last n_local, and
     the best-scored others.  q [T, n_heads, D] BF16.  Returns (ids int32 [T, n_kv_heads, k], ascending,
-    then -1; scores float32, then 0)."""
+    then -1; scores float32, then 0).  ws: not used, as kv_select_workspace is 0 for every size."""
     rc, ids, scores = _lib.load_kv().select(cache, q, seq, pos, table, k, n_sink, n_local, ws, ids, scores, dev_err,
                                             _raw(stream))
     if rc:
@@ -326,7 +326,7 @@ def kv_attend(q, cache: KvCache, seq, pos, table, ids, scale: float | None = Non
               dev_err=None, stream=None):
     """Attention of q [T, n_heads, D] (BF16) over the blocks ids [T, n_kv_heads, k] lists, up to each
     token's own position; scale defaults to 1/sqrt(D).  Returns (out BF16 [T, n_heads, D], lse float32
-    [T, n_heads]); rows that see nothing are 0 and -inf."""
+    [T, n_heads]); rows that see nothing are 0 and -inf.  ws: not used, as kv_attend_workspace is 0."""
     rc, out, lse = _lib.load_kv().attend(cache, q, seq, pos, table, ids, scale, ws, out, lse, dev_err, _raw(stream))
     if rc:
         check(rc, "kv_attend")

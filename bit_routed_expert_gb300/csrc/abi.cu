@@ -248,44 +248,35 @@ bre_status kv_read(const bre_kv_cache* cache, const int32_t* seq, const int32_t*
                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 
-size_t kv_select_workspace(int T, int n_heads, int n_kv_heads, int head_dim, int B, int N, int k) {
-  if (T <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || B <= 0 || N <= 0 || k <= 0) return 0;
-  return kv_select_ws_bytes(T, n_heads, n_kv_heads, head_dim, B, N, k);
-}
+// (neither call needs a workspace; the arguments are kept for callers that pass one)
+size_t kv_select_workspace(int, int, int, int, int, int, int) { return 0; }
 
 bre_status kv_select(const bre_kv_cache* cache, const void* q_bf16, int64_t q_stride, int n_heads, const int32_t* seq,
                      const int32_t* pos, int T, const int32_t* table, int B, int N, int k, int n_sink, int n_local,
-                     int32_t* ids, float* scores, void* ws, size_t ws_bytes, int32_t* dev_err, bre_stream_t stream) {
+                     int32_t* ids, float* scores, void*, size_t, int32_t* dev_err, bre_stream_t stream) {
   bre_status st = kv_check(cache, seq, pos, T, table, B, N);
   if (st != BRE_OK || T == 0) return st;
   if ((st = kv_check_q(cache, q_bf16, q_stride, n_heads, k)) != BRE_OK) return st;
   if (!ids || n_sink < 0 || n_local < 0 || n_sink > k || n_local > k - n_sink) return BRE_ERR_ARG;
   if (N > 131072) return BRE_ERR_UNSUPPORTED;   // the scores of a token lie in the shared memory of eight CTAs
-  const size_t need = kv_select_ws_bytes(T, n_heads, cache->n_kv_heads, cache->head_dim, B, N, k);
-  if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return BRE_ERR_WORKSPACE;
   return cuda_status(launch_kv_select(cache, KvTokens{seq, pos, T, table, B, N}, static_cast<const uint16_t*>(q_bf16),
-                                      q_stride, n_heads, k, n_sink, n_local, ids, scores, ws, dev_err,
+                                      q_stride, n_heads, k, n_sink, n_local, ids, scores, dev_err,
                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 
-size_t kv_attend_workspace(int T, int n_heads, int n_kv_heads, int head_dim, int B, int k) {
-  if (T <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || B <= 0 || k <= 0) return 0;
-  return kv_attend_ws_bytes(T, n_heads, n_kv_heads, head_dim, B, k);
-}
+size_t kv_attend_workspace(int, int, int, int, int, int) { return 0; }
 
 bre_status kv_attend(const bre_kv_cache* cache, const void* q_bf16, int64_t q_stride, int n_heads, const int32_t* seq,
                      const int32_t* pos, int T, const int32_t* table, int B, int N, const int32_t* ids, int k,
-                     float scale, void* out_bf16, float* lse, void* ws, size_t ws_bytes, int32_t* dev_err,
+                     float scale, void* out_bf16, float* lse, void*, size_t, int32_t* dev_err,
                      bre_stream_t stream) {
   bre_status st = kv_check(cache, seq, pos, T, table, B, N);
   if (st != BRE_OK || T == 0) return st;
   if ((st = kv_check_q(cache, q_bf16, q_stride, n_heads, k)) != BRE_OK) return st;
   if (N > (1 << 25) - 2) return BRE_ERR_UNSUPPORTED;   // block numbers share 32 bits with a tile's 128 tokens
   if (!ids || !out_bf16 || !aligned(out_bf16, 32) || !(scale - scale == 0.0f)) return BRE_ERR_ARG;
-  const size_t need = kv_attend_ws_bytes(T, n_heads, cache->n_kv_heads, cache->head_dim, B, k);
-  if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return BRE_ERR_WORKSPACE;
   return cuda_status(launch_kv_attend(cache, KvTokens{seq, pos, T, table, B, N}, static_cast<const uint16_t*>(q_bf16),
-                                      q_stride, n_heads, ids, k, scale, static_cast<uint16_t*>(out_bf16), lse, ws,
+                                      q_stride, n_heads, ids, k, scale, static_cast<uint16_t*>(out_bf16), lse,
                                       dev_err, reinterpret_cast<cudaStream_t>(stream)));
 }
 

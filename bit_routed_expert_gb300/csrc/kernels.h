@@ -88,14 +88,10 @@ cudaError_t launch_kv_append(const bre_kv_cache* c, const KvTokens& tk, const ui
                              long long k_stride, long long v_stride, int32_t* err, cudaStream_t s);
 cudaError_t launch_kv_read(const bre_kv_cache* c, const KvTokens& tk, uint16_t* k, uint16_t* v, int32_t* err,
                            cudaStream_t s);
-size_t kv_select_ws_bytes(int T, int Hq, int H, int D, int B, int N, int k);
 cudaError_t launch_kv_select(const bre_kv_cache* c, const KvTokens& tk, const uint16_t* q, long long q_stride, int Hq,
-                             int k, int n_sink, int n_local, int32_t* ids, float* scores, void* ws, int32_t* err,
-                             cudaStream_t s);
-size_t kv_attend_ws_bytes(int T, int Hq, int H, int D, int B, int k);
+                             int k, int n_sink, int n_local, int32_t* ids, float* scores, int32_t* err, cudaStream_t s);
 cudaError_t launch_kv_attend(const bre_kv_cache* c, const KvTokens& tk, const uint16_t* q, long long q_stride, int Hq,
-                             const int32_t* ids, int k, float scale, uint16_t* out, float* lse, void* ws, int32_t* err,
-                             cudaStream_t s);
+                             const int32_t* ids, int k, float scale, uint16_t* out, float* lse, int32_t* err, cudaStream_t s);
 
 // tiled tensor map over global memory: dims innermost first, strides (bytes) of dims 1..rank-1
 bool encode_tiled(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,

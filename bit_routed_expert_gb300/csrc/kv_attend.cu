@@ -318,11 +318,8 @@ __global__ void __launch_bounds__(AR_WARPS * 32, ar_ctas(D, NT)) kv_attend_rows_
 
 }  // namespace
 
-size_t kv_attend_ws_bytes(int T, int Hq, int H, int D, int B, int k) { return 0; }
-
 cudaError_t launch_kv_attend(const bre_kv_cache* c, const KvTokens& tk, const uint16_t* q, long long q_stride, int Hq,
-                             const int32_t* ids, int k, float scale, uint16_t* out, float* lse, void* ws, int32_t* err,
-                             cudaStream_t s) {
+                             const int32_t* ids, int k, float scale, uint16_t* out, float* lse, int32_t* err, cudaStream_t s) {
   const int H = c->n_kv_heads, D = c->head_dim, G = Hq / H;
   const AttendArgs a{static_cast<const uint8_t*>(c->pages), H,     G,     KvTable{tk.table, tk.B, tk.N, c->n_pages},
                      q, q_stride, tk.seq, tk.pos, tk.T, ids, k, scale, out, lse, err, 0};

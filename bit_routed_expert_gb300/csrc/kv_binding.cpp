@@ -192,7 +192,7 @@ struct Call {
   }
 };
 
-// The caller's workspace (None where the call needs none).
+// The caller's workspace (no call needs one).
 struct Workspace {
   void* p = nullptr;
   size_t n = 0;

@@ -731,14 +731,11 @@ static cudaError_t allow_smem(const void* kern, int which, int bytes) {
   return e;
 }
 
-size_t kv_select_ws_bytes(int T, int Hq, int H, int D, int B, int N, int k) { return 0; }
-
 // Shared memory of the one-token kernel for stretches of `span` blocks.
 static size_t select_rows_smem(int span, int k) { return SelectRowsMem(k).bytes(span); }
 
 cudaError_t launch_kv_select(const bre_kv_cache* c, const KvTokens& tk, const uint16_t* q, long long q_stride, int Hq,
-                             int k, int n_sink, int n_local, int32_t* ids, float* scores, void* ws, int32_t* err,
-                             cudaStream_t s) {
+                             int k, int n_sink, int n_local, int32_t* ids, float* scores, int32_t* err, cudaStream_t s) {
   const int H = c->n_kv_heads, D = c->head_dim;
   const SelectArgs a{c->bounds, c->bound_exp, H,   Hq / H, KvTable{tk.table, tk.B, tk.N, c->n_pages},
                      q, q_stride, tk.seq, tk.pos, tk.T, k, n_sink, n_local, ids, scores, err};

@@ -15,7 +15,7 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from bit_routed_expert_gb300 import (BRE_FMT_Q8_0, FfnWeights, KvCache, MoeLayer, StepGraph, kv_append, kv_attend,  # noqa: E402
-                                     kv_attend_workspace, kv_select, kv_select_workspace, moe_residual_norm)
+                                     kv_select, moe_residual_norm)
 from bit_routed_expert_gb300 import api, synth  # noqa: E402
 
 
@@ -38,9 +38,6 @@ class SparseLayer:
         N = -(-max_len // api.KV_BLOCK)
         self.cache = KvCache.empty(B * N, K, D, dev)
         self.table = torch.randperm(B * N, generator=g, device=dev).to(torch.int32).view(B, N).contiguous()
-        # what a serving loop keeps from call to call
-        self.select_ws = torch.zeros(kv_select_workspace(T_max, H, K, D, B, N, self.TOP), dtype=torch.uint8, device=dev)
-        self.attend_ws = torch.zeros(kv_attend_workspace(T_max, H, K, D, B, self.TOP), dtype=torch.uint8, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
 
     def forward(self, x, seq, pos):
@@ -50,8 +47,8 @@ class SparseLayer:
         qkv = (u @ self.w_qkv).view(T, H + 2 * K, D)
         q, k, v = qkv[:, :H], qkv[:, H:H + K], qkv[:, H + K:]   # slices: the calls take row strides
         kv_append(self.cache, k, v, seq, pos, self.table, dev_err=self.err)
-        ids, _ = kv_select(q, self.cache, seq, pos, self.table, self.TOP, ws=self.select_ws, dev_err=self.err)
-        att, _ = kv_attend(q, self.cache, seq, pos, self.table, ids, ws=self.attend_ws, dev_err=self.err)
+        ids, _ = kv_select(q, self.cache, seq, pos, self.table, self.TOP, dev_err=self.err)
+        att, _ = kv_attend(q, self.cache, seq, pos, self.table, ids, dev_err=self.err)
         x, u = moe_residual_norm(x, att.reshape(T, H * D) @ self.w_o, 1.0)
         out, _ = self.moe.forward(u)
         return moe_residual_norm(x, out, 2.0 ** -0.5, want_norm=False)[0]

@@ -343,9 +343,8 @@ bre_status kv_read(const bre_kv_cache *cache, const int32_t *seq, const int32_t 
  * the others by score, highest first, lowest block first among equals, k in all.
  *   ids [T][n_kv_heads][k] int32: the blocks taken, ascending, then -1;
  *   scores [T][n_kv_heads][k] FP32 or NULL: their scores, then 0.
- *   q: as k in kv_append, [n_heads][D] a row.  ws: kv_select_workspace(...) bytes, zero-filled
- *   once after allocation (each call leaves it ready for the next); NULL where that is 0, as it
- *   is for every size now.
+ *   q: as k in kv_append, [n_heads][D] a row.  ws, ws_bytes: not looked at; kv_select_workspace is 0
+ *   for every size.
  * Requires G <= 16, 1 <= k <= 256, n_sink + n_local <= k, N <= 131,072 (8.4 million tokens). */
 size_t kv_select_workspace(int T, int n_heads, int n_kv_heads, int head_dim, int B, int N, int k);
 bre_status kv_select(const bre_kv_cache *cache, const void *q_bf16, int64_t q_stride, int n_heads, const int32_t *seq,
@@ -360,7 +359,7 @@ bre_status kv_select(const bre_kv_cache *cache, const void *q_bf16, int64_t q_st
  * probabilities enter the second product as FP16 (relative error 2^-11 for those within 2^-22 of the
  * row's largest, the value's scale counted in; absolute below), the codes exactly.
  *   ids [T][n_kv_heads][k] int32, any order; out [T][n_heads][D] BF16, 32-byte aligned; lse [T][n_heads] FP32 or
- *   NULL (natural logarithm).  ws: as in kv_select, kv_attend_workspace(...) bytes.  Requires G <= 16, k <= 256,
+ *   NULL (natural logarithm).  ws, ws_bytes: as in kv_select.  Requires G <= 16, k <= 256,
  *   N <= 2^25 - 2. */
 size_t kv_attend_workspace(int T, int n_heads, int n_kv_heads, int head_dim, int B, int k);
 bre_status kv_attend(const bre_kv_cache *cache, const void *q_bf16, int64_t q_stride, int n_heads, const int32_t *seq,

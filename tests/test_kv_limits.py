@@ -20,3 +20,12 @@ def test_attend_block_numbers_fit_their_25_bits(N):
     entry 2^25 - 1 would be read as it."""
     assert attend(N, 3) == BRE_ERR_UNSUPPORTED
     assert attend(2 ** 25 - 2, 0) == BRE_OK
+
+
+def test_no_call_needs_a_workspace():
+    """The arguments stay for callers that pass one: 0 bytes for every size, and what is passed is not looked at."""
+    L = _lib.load()
+    for T in (0, 1, 5, 8192, 1 << 20):
+        for G in (1, 16):
+            assert L.kv_select_workspace(T, 4 * G, 4, 128, 64, 131072, 256) == 0
+            assert L.kv_attend_workspace(T, 4 * G, 4, 128, 64, 256) == 0
