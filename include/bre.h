@@ -318,7 +318,9 @@ typedef struct {
  * NaN is stored as a NaN row; magnitudes above 448 * 2^119 (infinities too) saturate.
  * The bounds of every block written to are brought up to date (a NaN row counts as zeros there):
  * from this call's keys alone where its first token of the block is at slot 0, else together
- * with the bounds that were there.  A position written again widens them only: they stay bounds.
+ * with the bounds that were there.  A position written again widens them only, so they stay bounds; but where
+ * slot 0 is written again they are those of this call's keys alone: later slots that are kept are then
+ * not covered until they too are written again.
  *   k, v: row t starts t * stride elements after the base and holds [n_kv_heads][D]; bases 16-byte
  *   aligned, strides multiples of 8.
  * The call's tokens of one block follow one another in the list (but for padding entries), and no page

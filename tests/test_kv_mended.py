@@ -184,3 +184,21 @@ def test_append_among_long_padding(cuda_dev, D, H, before, between, behind):
     real = [i for i in range(T) if n.pos[i] >= 0]   # padding between a block's tokens changes nothing
     assert not R.append(pages, bounds, bexp, k[real], v[real], b.seq, b.pos, b.table)
     assert all(torch.equal(x, y) for x, y in zip(own(c), (pages, bounds, bexp)))
+
+
+def test_writing_slot_0_again_starts_the_bounds_anew(cuda_dev):
+    """The bounds are then those of that call's keys alone (a page is used again; a rejected block is decoded again); a
+    later slot written again widens them."""
+    D, H = 64, 2
+    b = R.batch([20], [20])
+    pages, bounds, bexp = R.filled(b, [20], H, D)
+    c = on(cuda_dev, pages, bounds, bexp)
+    for a, z, gain in ((0, 20, 8.0), (0, 3, 0.5), (3, 6, 2.0)):
+        k = R.rows(a + z, z - a, H, D, gain=gain)
+        n = R.Batch(b.seq[a:z], b.pos[a:z], b.table, b.n_pages)
+        kv_append(c, k.to(cuda_dev), k.to(cuda_dev), *n.on(cuda_dev))
+        R.append(pages, bounds, bexp, k, k, n.seq, n.pos, n.table)
+        assert all(torch.equal(x, y) for x, y in zip(own(c), (pages, bounds, bexp)))
+    kk = R.values(pages, D)[0][int(b.table[0, 0])]
+    hi = bounds[int(b.table[0, 0]), :, 0].double() * 2.0 ** bexp[int(b.table[0, 0])].double()[:, None]
+    assert bool((kk[:, :6].amax(1) <= hi).all()) and not bool((kk[:, :20].amax(1) <= hi).all())
