@@ -173,16 +173,36 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Whether a key row that is not all zeros lies more than 2^15 below the block's largest scale `top`.  By a whole warp,
+// with the scales of tokens lane and lane + 32 (0: not there).  Zero rows, whose scale is the least one, are exact in
+// FP16 beside anything.  Out of line, as it is called for few blocks.
+__device__ __noinline__ bool far_apart(const uint8_t* keys, int D, int ea, int eb, int top) {
+  constexpr int LEAST = KV_EXP_MIN + 127;
+  bool far = false;
+  for (int half = 0; half < 2; ++half) {
+    const int e = half ? eb : ea;
+    if (e == 0 || top - e <= 15) continue;
+    uint32_t codes = e == LEAST ? 0u : 1u;
+    const uint4* row = reinterpret_cast<const uint4*>(keys + ((threadIdx.x & 31) + 32 * half) * D);
+    for (int i = 0; codes == 0u && i < D / 16; ++i) {
+      const uint4 w = __ldg(row + i);
+      codes = (w.x | w.y | w.z | w.w) & 0x7F7F7F7Fu;
+    }
+    far |= codes != 0u;
+  }
+  __syncwarp();
+  return __any_sync(0xffffffffu, far);
+}
+
 // A row's part of one block as in the main loop of the softmax, in steps that are right for scales of any size: the
-// logits of S times the query's factor, then times the keys' own; terms of the sum formed without the values'
-// exponents ev.  By a whole warp; S, O: this warp's tensor memory; kt: the factor of the keys of tokens 0-31 and
-// 32-63, where it is positive, else it is in ek for each; m, l: the row's maximum and sum -> the new ones.  A tile
-// goes on this way from its first block whose keys are far apart or that has a value scale above EV_LARGE, in a loop
-// of its own behind the main one (402 us for the 8,192-token chunk; called in the main loop 412 to 445, where it is
-// never taken).
-template <int D>
-__device__ __forceinline__ float2 careful_block(uint32_t S, uint32_t O, bool have_o, float2 kt, const float* ek, const float* ev,
-                                             float qf, int n, float m, float l) {
+// logits are S times the query's factor, then times the keys' own; terms of the sum are formed without the values'
+// exponents ev.  A tile goes on this way from its first block whose keys are far apart or that has a value scale above
+// EV_LARGE, in a loop of its own behind the main one (called in the main loop, where it is never taken, it cost 3 to
+// 12 % of the kernel's time).
+//
+// The logits plus ev in place of S, -inf beyond n; their maximum.  By a whole warp; kt: the factor of the keys of
+// tokens 0-31 and 32-63, where it is positive, else it is in ek for each.
+__device__ __forceinline__ float careful_logits(uint32_t S, float2 kt, const float* ek, const float* ev, float qf, int n) {
   float mx = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < KV_BLOCK; c += 16) {
@@ -199,22 +219,12 @@ __device__ __forceinline__ float2 careful_block(uint32_t S, uint32_t O, bool hav
     tmem_st16(S + c, s);
   }
   tmem_wait_st();
-  const float nm = fmaxf(m, mx), d = m > -INFINITY ? m - nm : 0.0f;
-  if (have_o && __any_sync(0xffffffffu, d < 0.0f)) {
-    const float sc = ex2(d);
-#pragma unroll 1
-    for (int c = 0; c < D; c += 16) {
-      uint32_t o[16];
-      tmem_ld16(O + c, o);
-      tmem_wait_ld();
-#pragma unroll
-      for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * sc);
-      tmem_st16(O + c, o);
-    }
-    tmem_wait_st();
-  }
-  l = scale_sum(l, d);
-  const float base = nm > -INFINITY ? nm - P_SHIFT : 0.0f;
+  return mx;
+}
+// The weights against the maximum m over those logits; what they add to the row's sum.
+__device__ __forceinline__ float careful_weights(uint32_t S, const float* ev, float m, int n) {
+  const float base = m > -INFINITY ? m - P_SHIFT : 0.0f;
+  float sum = 0.0f;
 #pragma unroll 1
   for (int c = 0; c < KV_BLOCK; c += 32) {
     uint32_t s[32], pk[16];
@@ -223,13 +233,27 @@ __device__ __forceinline__ float2 careful_block(uint32_t S, uint32_t O, bool hav
 #pragma unroll
     for (int x = 0; x < 32; x += 2) {
       const float v0 = __uint_as_float(s[x]) - base, v1 = __uint_as_float(s[x + 1]) - base;
-      if (c + x < n) l += exp2f(v0 - ev[c + x]);
-      if (c + x + 1 < n) l += exp2f(v1 - ev[c + x + 1]);
+      if (c + x < n) sum += exp2f(v0 - ev[c + x]);
+      if (c + x + 1 < n) sum += exp2f(v1 - ev[c + x + 1]);
       pk[x / 2] = pack_f16x2(ex2(v0), ex2(v1));
     }
     tmem_st16(S + c / 2, pk);
   }
-  return make_float2(nm, l);
+  return sum;
+}
+// O of a whole warp's rows times sc.
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t O, float sc) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(O + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * sc);
+    tmem_st16(O + c, o);
+  }
+  tmem_wait_st();
 }
 
 // PATIENT: the waits have the default budget; else the one that was set (a budget that is not a constant costs 5 %
@@ -245,7 +269,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
   __shared__ Block ring[AT_RING];
   __shared__ __align__(16) float ev_f[AT_RING][KV_BLOCK], ev_inv[AT_RING][KV_BLOCK], ek_f[AT_RING][KV_BLOCK];
   __shared__ float q_factor[128];
-  __shared__ float2 ek_top[AT_RING];   // one half by each warp, see careful_block
+  __shared__ float2 ek_top[AT_RING];   // factor of a block's keys, one half by each warp; 0: see careful_logits
   __shared__ uint32_t tmem_s;
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -456,6 +480,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
     uint4 cur[NL];
     int e2 = 0, ev = 0;     // key scales of tokens lane and lane + 32; value scale of token dt (keys' threads)
     int n = 0;
+    const uint8_t* keys = nullptr;
     // of tokens that no row sees (they may never have been written) neither codes nor scales are read
     auto take_and_load = [&](int i) -> bool {
       if (!warp_wait(&blk_full[i % AT_RING], i / AT_RING)) return false;
@@ -465,6 +490,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
       if (lane == 0) mbar_arrive(&blk_empty[i % AT_RING]);
       if (page < 0) return false;
       const uint8_t* pg = a.pages + ((size_t)page * a.H + h) * kv_page_bytes(D);
+      if (!values) keys = pg;
       const uint4* src = reinterpret_cast<const uint4*>(pg + (values ? KV_BLOCK * D : 0)) + dt;
       const uint8_t* sc = pg + 2 * KV_BLOCK * D;
 #pragma unroll
@@ -499,7 +525,8 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
         ev_f[sp][dt] = nan ? __int_as_float(0x7FC00000) : (float)(ev - 127);
         ev_inv[sp][dt] = pow2f(127 - min(ev, 253));
         // tokens whose own scales reach below what FP16 holds relative to the largest (a byte of 0: not read)
-        const bool wide = __any_sync(0xffffffffu, (ea && top - ea > 15) || (eb && top - eb > 15));
+        bool wide = __any_sync(0xffffffffu, (ea && top - ea > 15) || (eb && top - eb > 15));
+        if (wide) wide = far_apart(keys, D, ea, eb, top);
         const bool large = __any_sync(0xffffffffu, ev > EV_LARGE);   // (of this warp's half; NaN rows as well)
         if (wide || large) {
           const int ek = dt < 32 ? ea : eb;
@@ -542,7 +569,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
     const float qf = q_factor[r];
     const uint32_t lane_base = tmem + ((uint32_t)warp << 21);   // lanes 32 warp ..
     float m = -INFINITY, l = 0.0f;   // m: the maximum that the weights are held against
-    bool rare = false;               // a block that is not for this loop: see careful_block
+    bool rare = false;               // a block that is not for this loop: see careful_logits
     int i = 0, n = 0;
     for (;; ++i) {
       const int st = i & 1;
@@ -598,16 +625,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
         const float nm = fmaxf(m, mx), d = m > -INFINITY ? m - nm : 0.0f, sc = ex2(d);
         m = nm;
         l = scale_sum(l, d);
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
-          tmem_ld16(lane_base + 128 + c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * sc);
-          tmem_st16(lane_base + 128 + c, o);
-        }
-        tmem_wait_st();
+        rescale<D>(lane_base + 128, sc);
       }
       const float base = m > -INFINITY ? m - P_SHIFT : 0.0f;
       const uint64_t nb2 = pack2(-base, -base);
@@ -658,10 +676,17 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
     // the rest of the tile's blocks from the first rare one on
     while (rare && ok) {
       const int st = i & 1, sp = i % AT_RING;
-      if (i > 0 && !warp_wait(&o_done, i - 1)) break;   // O may be rescaled
-      tc_fence_after();
-      const float2 ml = careful_block<D>(lane_base + st * 64, lane_base + 128, i > 0, ek_top[sp], ek_f[sp], ev_f[sp], qf, n, m, l);
-      m = ml.x, l = ml.y;
+      const float mx = careful_logits(lane_base + st * 64, ek_top[sp], ek_f[sp], ev_f[sp], qf, n);
+      if (m == -INFINITY) m = mx;
+      if (__any_sync(0xffffffffu, mx > m + AT_SLACK)) {
+        if (!warp_wait(&o_done, i - 1)) break;
+        tc_fence_after();
+        const float nm = fmaxf(m, mx), d = m > -INFINITY ? m - nm : 0.0f;
+        m = nm;
+        l = scale_sum(l, d);
+        rescale<D>(lane_base + 128, ex2(d));
+      }
+      l += careful_weights(lane_base + st * 64, ev_f[sp], m, n);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();

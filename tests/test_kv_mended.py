@@ -202,3 +202,31 @@ def test_writing_slot_0_again_starts_the_bounds_anew(cuda_dev):
     kk = R.values(pages, D)[0][int(b.table[0, 0])]
     hi = bounds[int(b.table[0, 0]), :, 0].double() * 2.0 ** bexp[int(b.table[0, 0])].double()[:, None]
     assert bool((kk[:, :6].amax(1) <= hi).all()) and not bool((kk[:, :20].amax(1) <= hi).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("codes", ["zeros", "minus zeros", "one code", "mixed"])
+def test_attend_beside_keys_of_the_least_scale(cuda_dev, codes, D):
+    """Key rows of zeros have the least scale and are exact beside anything; others of that scale count where the queries
+    are as large as these keys are small."""
+    H, G, T = 2, 4, 40
+    lens = [400]
+    b = R.batch(lens, [T])
+    pages, _, _ = R.filled(b, lens, H, D)
+    kc, _, ks, _ = R.views(pages, D)
+    row = torch.zeros(64, D, dtype=torch.uint8)
+    if codes == "minus zeros":
+        row[:] = 0x80
+    elif codes == "one code":
+        row[:, D - 1] = 0x7E
+    elif codes == "mixed":
+        row[20, 0], row[50, 5] = 0x38, 0xB8
+    for i, x in enumerate((0, 7, 20, 31, 32, 50, 63)):
+        kc[:, :, x], ks[:, :, x] = row[x], 63
+    q = R.rows(21, T, H * G, D)
+    check_attend(cuda_dev, b, pages, q, some_ids(b, H, 5))
+    q[:, :, :D // 2] = 0.0
+    kc[:, :, :, D // 2:D - 1] &= 0x80   # only the last channel meets the queries: the small rows' logits are theirs
+    near = torch.tensor([x not in (0, 7, 20, 31, 32, 50, 63) for x in range(64)])
+    kc[:, :, near, D - 1] = 0
+    check_attend(cuda_dev, b, pages, q * 2.0 ** 55, some_ids(b, H, 5))
