@@ -26,8 +26,7 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   return d;
 }
 // CTAs to an SM.  The loads of a half block are all issued before its first product, so warps are what keeps
-// memory busy: 64 tokens x 32 blocks take 46 us with three CTAs (140 registers), 33 with four, 42 with five
-// (spills).  Both halves of 16 heads at D = 128 need the registers of two.
+// memory busy: 64 tokens x 32 blocks take 41 us with three CTAs, 30 with four, 47 with five (spills).  Both halves of 16 heads at D = 128 need the registers of two.
 constexpr int ar_ctas(int D, int NT) { return NT == 1 || D == 64 ? 4 : 2; }
 
 // NT: groups of eight query heads.
@@ -323,11 +322,14 @@ cudaError_t launch_kv_attend(const bre_kv_cache* c, const KvTokens& tk, const ui
   const int H = c->n_kv_heads, D = c->head_dim, G = Hq / H;
   const AttendArgs a{static_cast<const uint8_t*>(c->pages), H,     G,     KvTable{tk.table, tk.B, tk.N, c->n_pages},
                      q, q_stride, tk.seq, tk.pos, tk.T, ids, k, scale, out, lse, err, 0};
-  // Tiles of 128 rows pay where neighbours share their blocks (16 tokens a sequence on average) and where there are
-  // enough of them: a tile takes its 80 us (16 blocks a token, G = 8) however few there are.  Four kv heads, 16
-  // blocks, us by token / by tile: G = 8, D = 128: 512 tokens 82 / 94, 1,024 154 / 128; G = 16, D = 64: 512 69 / 70,
-  // 1,024 128 / 121; G = 2 (64 tokens a tile, whose lists differ more), D = 64: 512 39 / 167; 8,192 tokens, G = 8:
-  // 1,281 / 447.
+  // Tiles of 128 rows pay where neighbours share their blocks (16 tokens on average for each of the table's sequences,
+  // whether the call has tokens of all of them or not) and where there are enough of them: a tile takes its 50 to 70 us
+  // (16 blocks a token, G = 8 or 16) however few there are.  Four kv heads, 16 of 256 blocks, us by token / by
+  // tile: G = 8, D = 128: 256 tokens 43 / 71, 512 82 / 75, 1,024 154 / 98, 8,192 1,195 / 544; G = 8, D = 64: 512
+  // 49 / 68, 1,024 91 / 84; G = 16, D = 64: 256 39 / 48, 512 73 / 58; G = 4, D = 128: 512 72 / 127, 1,024 134 / 137,
+  // 2,048 262 / 167; G = 2 (64 tokens a tile, whose lists differ more), D = 64: 1,024 76 / 161, 2,048 147 / 171, 4,096
+  // 290 / 194; G = 1, D = 64: 4,096 284 / 239.  At the rule's edges it takes the slower kernel for G = 8, D = 64 (512
+  // tokens) and G = 2, D = 64 (2,048).
   const long long pairs = (long long)tk.T * H;
   if (tk.T >= 16LL * tk.B && pairs >= 2048 && pairs * G >= 16384) return launch_kv_attend_tiles(a, D, s);
   // CTAs of a (token, head): halves of blocks for every warp, as long as the GPU has room for them

@@ -14,10 +14,10 @@ namespace {
 // blocks; with few tokens the chunks shrink to one token and a call spreads over the GPU.
 //
 // A call is a chain of loads that wait for one another, and for long calls half of its time is arithmetic
-// (4.8 million warp instructions for 8,192 tokens of 8 heads of 128).  So the chain is kept short: positions,
+// (4.8 million warp instructions for 8,192 tokens of 4 heads of 128).  So the chain is kept short: positions,
 // then the page's number beside the first rows, then two rows a lane in flight, each replaced as it is used; 9.8 us
 // for those tokens, against 11.2 us with the rows asked for once the run and its page were known.  Four rows a lane
-// take 119 registers: 9.6 us there, but 15.6 against 13.0 us for 6,418 ragged tokens of 4 heads of 64; six CTAs an SM
+// take 119 registers: 9.6 us there, but 15.6 against 13.0 us for 6,418 ragged tokens of 8 heads of 64; six CTAs an SM
 // instead of five 10.5 us.
 constexpr int KA_WARPS = 4;
 

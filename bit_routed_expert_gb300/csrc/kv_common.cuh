@@ -3,7 +3,7 @@
 // A page holds KV_BLOCK consecutive tokens of one sequence.  For each of its key/value heads, in
 // this order and without gaps: KV_BLOCK key rows of D E4M3 codes, KV_BLOCK value rows, KV_BLOCK
 // key scales, KV_BLOCK value scales (E8M0, one byte a row).  A head's share of a page is one
-// contiguous, 16-byte aligned piece of 128 D + 128 bytes, so it moves in one bulk copy.
+// contiguous, 16-byte aligned piece of 128 D + 128 bytes, read and written in 8- and 16-byte pieces.
 //
 // One power-of-two scale a row, not one for every 32 channels: E4M3 carries an exponent itself,
 // and against the row's largest value it keeps four significant bits down to 2^-14 of it, so a

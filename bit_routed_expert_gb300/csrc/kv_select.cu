@@ -740,7 +740,7 @@ cudaError_t launch_kv_select(const bre_kv_cache* c, const KvTokens& tk, const ui
   const SelectArgs a{c->bounds, c->bound_exp, H,   Hq / H, KvTable{tk.table, tk.B, tk.N, c->n_pages},
                      q, q_stride, tk.seq, tk.pos, tk.T, k, n_sink, n_local, ids, scores, err};
   // Tiles of 32 tokens: the lists must fit (up to about 170 blocks a token), the tokens mostly be of one sequence
-  // (16 a sequence on average), and there must be enough of them.  256 blocks, four kv heads, us by token / by tile:
+  // (16 on average for each of the table's sequences, whether the call has tokens of all of them or not), and there must be enough of them.  256 blocks, four kv heads, us by token / by tile:
   // 128 tokens of one sequence 17 / 19, 256 31 / 19; 128 tokens of eight 17 / 22, 256 30 / 19; 64 of eight 9 / 34.
   const size_t most = device_max_smem_optin() - 2048;   // less the kernels' static shared memory
   const size_t smem_t = select_tiles_smem(D, (k + 15) / 16 * 16);

@@ -289,7 +289,9 @@ bre_status engram_inject(const uint8_t *table, int64_t n_rows, const int64_t *ro
  * pos[t]; a negative position is a padding entry: it stores nothing, selects nothing and its
  * outputs are zeros.  table [B][N]: the page of each block of 64 consecutive positions of a
  * sequence; a negative entry means that the block has no page (not yet, or given back).
- * seq, pos and table are int32 device arrays.
+ * seq, pos and table are int32 device arrays.  kv_select and kv_attend choose between a kernel that goes token by
+ * token and one that takes many neighbours at a time by T / B, the tokens a sequence of the table: a long chunk of a few
+ * of many sequences runs faster (attention up to three times) with a table of those sequences' rows alone.
  *
  *   pages [n_pages][n_kv_heads][128 D + 128] bytes, D = head_dim: for each head of a page 64 key
  *     rows of D E4M3 codes (OCP: bias 7, no infinities; the NaN codes do not occur), 64 value rows,
@@ -357,9 +359,11 @@ bre_status kv_select(const bre_kv_cache *cache, const void *q_bf16, int64_t q_st
  * the blocks that ids lists for its kv head (-1: none; a block listed twice counts twice),
  *   s_x = scale * q . key_x,  out = sum_x exp(s_x) value_x / sum_x exp(s_x),  lse = log sum_x exp(s_x)
  * A row that sees no token gives zeros and lse = -inf; one that sees a token whose key or value row
- * is NaN gives NaN and lse = NaN.  Logits, maxima and sums are FP32; the
- * probabilities enter the second product as FP16 (relative error 2^-11 for those within 2^-22 of the
- * row's largest, the value's scale counted in; absolute below), the codes exactly.
+ * is NaN gives NaN and lse = NaN.  Logits, maxima and sums are FP32, where a logit is held with the exponent of
+ * its token's value scale added (rounded to 2^-24 of the two); the codes enter both products exactly.  A query
+ * enters as FP16 times a power of two that takes its head's largest magnitude to 63.5 .. 127: exactly down
+ * to 2^-23 of that, off by 2^-31 of it at most below.  The probabilities enter the second product as FP16 (relative
+ * error 2^-11 for those within 2^-22 of the row's largest, the value's scale counted in; absolute below).
  *   ids [T][n_kv_heads][k] int32, any order; out [T][n_heads][D] BF16, 32-byte aligned; lse [T][n_heads] FP32 or
  *   NULL (natural logarithm).  ws, ws_bytes: as in kv_select.  Requires G <= 16, k <= 256,
  *   N <= 2^25 - 2. */
