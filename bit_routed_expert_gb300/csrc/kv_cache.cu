@@ -238,8 +238,10 @@ __global__ void __launch_bounds__(KA_WARPS * 32, 5)
       e = max(e, oe);
     }
     if (tid < D) {
-      bd[0] = (int8_t)ceilf(ch * pow2f(-e));
-      bd[D] = (int8_t)floorf(cl * pow2f(-e));
+      // (beside a key 2^115 larger a channel may vanish in the product, yet its bounds lie on their sides of 0)
+      const float down = pow2f(-e), hi = ceilf(ch * down), lo = floorf(cl * down);
+      bd[0] = (int8_t)(ch > 0.0f ? fmaxf(hi, 1.0f) : hi);
+      bd[D] = (int8_t)(cl < 0.0f ? fminf(lo, -1.0f) : lo);
     }
     if (tid == 0) bexp[ph] = (int8_t)e;
   }

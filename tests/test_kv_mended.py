@@ -230,3 +230,24 @@ def test_attend_beside_keys_of_the_least_scale(cuda_dev, codes, D):
     near = torch.tensor([x not in (0, 7, 20, 31, 32, 50, 63) for x in range(64)])
     kc[:, :, near, D - 1] = 0
     check_attend(cuda_dev, b, pages, q * 2.0 ** 55, some_ids(b, H, 5))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("step", [1, 7, 20])
+def test_bounds_hold_beside_a_key_of_another_size(cuda_dev, D, step):
+    """An infinity (stored as 448 * 2^119) among keys of 2^-34: the other channels' bounds are 1 and -1 of its unit, not 0."""
+    H = 2
+    b = R.batch([20], [20])
+    pages, bounds, bexp = R.filled(b, [20], H, D)
+    c = on(cuda_dev, pages, bounds, bexp)
+    k = R.rows(3, 20, H, D, gain=2.0 ** -34)
+    k[9, 1, 5], k[11, 0, 6] = float("inf"), float("-inf")
+    k[:, :, 7], k[:, :, 8], k[:, :, 9] = k[:, :, 7].abs(), -k[:, :, 8].abs(), 0.0
+    for i in range(0, 20, step):
+        n = R.Batch(b.seq[i:i + step], b.pos[i:i + step], b.table, b.n_pages)
+        kv_append(c, k[i:i + step].to(cuda_dev), k[i:i + step].to(cuda_dev), *n.on(cuda_dev))
+        R.append(pages, bounds, bexp, k[i:i + step], k[i:i + step], n.seq, n.pos, n.table)
+    assert all(torch.equal(x, y) for x, y in zip(own(c), (pages, bounds, bexp)))
+    kk, u = R.values(pages, D)[0][int(b.table[0, 0])], 2.0 ** bexp[int(b.table[0, 0])].double()[:, None]
+    assert bool((kk[:, :20].amax(1) <= bounds[int(b.table[0, 0]), :, 0] * u).all())
+    assert bool((kk[:, :20].amin(1) >= bounds[int(b.table[0, 0]), :, 1] * u).all())
