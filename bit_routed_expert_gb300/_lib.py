@@ -13,11 +13,11 @@ _lib = None
 _kv = None
 
 BRE_OK, BRE_ERR_ARG, BRE_ERR_UNSUPPORTED, BRE_ERR_CUDA, BRE_ERR_WORKSPACE = range(5)
-BRE_DEVERR_EXPERT_ID, BRE_DEVERR_ROW_ID, BRE_DEVERR_TIMEOUT, BRE_DEVERR_PAGE = 1, 2, 4, 8
+BRE_DEVERR_EXPERT_ID, BRE_DEVERR_ROW_ID, BRE_DEVERR_TIMEOUT, BRE_DEVERR_PAGE, BRE_DEVERR_FULL = 1, 2, 4, 8, 16
 BRE_FMT_Q2_K, BRE_FMT_Q8_0, BRE_FMT_Q2_K_R16 = 1, 2, 3
 
 # exported symbol -> (restype, argtypes)
-_P, _I, _I64, _SZ, _F = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_float
+_P, _I, _I64, _SZ, _F, _D = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_float, C.c_double
 SIGNATURES = {
     "bre_status_string": (C.c_char_p, [_I]),
     "moe_route_workspace": (_SZ, [_I, _I]),
@@ -39,6 +39,14 @@ SIGNATURES = {
     "kv_select": (_I, [_P, _P, _I64, _I, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P, _P]),
     "kv_attend_workspace": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "kv_attend": (_I, [_P, _P, _I64, _I, _P, _P, _I, _P, _I, _I, _P, _I, _F, _P, _P, _P, _SZ, _P, _P]),
+    "kv_attend_tree_workspace": (_SZ, [_I, _I, _I, _I]),
+    "kv_attend_tree": (_I, [_P, _P, _I64, _I, _P, _P, _I, _P, _I, _I, _P, _P, _I, _F, _P, _P, _P, _SZ, _P, _P]),
+    "kv_rotate": (_I, [_P, _I64, _I, _P, _I64, _I, _I, _P, _I, _P, _I, _F, _I, _I, _I, _P, _I64, _P, _I64, _P]),
+    "bre_rope_turns": (_I, [_I, _D, _I, _D, _D, _D, _D, _P, _P]),
+    "kv_compact": (_I, [_P, _P, _I, _I, _P, _P, _I, _P, _P, _P, _P]),
+    "kv_fork": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P]),
+    "kv_resize_workspace": (_SZ, [_I, _I, _I]),
+    "kv_resize": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _SZ, _P, _P]),
     "bre_dequant": (_I, [_I, _P, _I64, _P, _P]),
     "bre_repack_q2k_r16": (_I, [_P, _P, _I, _I, _I, _I64, _I64, _P]),
     "bre_set_ffn_wait_limit": (_I, [_I64]),

@@ -333,6 +333,83 @@ def kv_attend(q, cache: KvCache, seq, pos, table, ids, scale: float | None = Non
     return out, lse
 
 
+def kv_attend_tree_workspace(T: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return _lib.load().kv_attend_tree_workspace(T, n_heads, n_kv_heads, head_dim)
+
+
+def kv_attend_tree(q, cache: KvCache, seq, pos, table, start=None, mask=None, scale: float | None = None, ws=None, out=None,
+                   lse=None, dev_err=None, stream=None):
+    """Attention of q [T, n_heads, D] (BF16) over the whole cached context.  mask None: causal, every token
+    x <= pos[t].  Else the sequence's first start[b] tokens (int32 [B]) and, of those drafted behind them, the ones whose bit
+    x - start[b] of mask[t] is set (int64 [T, words], 64 bits a word).  Returns (out, lse) as kv_attend.
+    ws: uint8 [kv_attend_tree_workspace(...)], one for calls that may run at the same time each; a new one if None."""
+    rc, out, lse = _lib.load_kv().attend_tree(cache, q, seq, pos, table, start, mask, scale, ws, out, lse, dev_err, _raw(stream))
+    if rc:
+        check(rc, "kv_attend_tree")
+    return out, lse
+
+
+ROPE_SCALINGS = ("linear", "base", "ramp", "bands")   # BRE_ROPE_* from 1 on (include/bre.h has the formulas)
+
+
+def rope_turns(rot_dim: int, theta: float = 10000.0, scaling: str | None = None, factor: float = 1.0, low: float = 1.0,
+               high: float | None = None, length: float = 0.0, device="cpu"):
+    """The frequencies of kv_rotate for rot_dim channels: (turns int64 [rot_dim / 2] on `device`, gain).  scaling, for contexts
+    `factor` times as long as the `length` trained on: "linear", "base", "ramp" or "bands"."""
+    if scaling is not None and scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be None or one of {ROPE_SCALINGS}")
+    how = 0 if scaling is None else 1 + ROPE_SCALINGS.index(scaling)
+    if high is None:
+        high = 4.0 if scaling == "bands" else 32.0
+    turns = torch.empty(max(rot_dim // 2, 1), dtype=torch.int64)
+    gain = C.c_float()
+    check(_lib.load().bre_rope_turns(rot_dim, theta, how, factor, low, high, length, ptr(turns), C.byref(gain)), "bre_rope_turns")
+    return turns.to(device), gain.value
+
+
+def kv_rotate(q, k, pos, turns, gain: float = 1.0, offset: int = 0, interleaved: bool = False, backward: bool = False, q_out=None,
+              k_out=None, stream=None):
+    """Rotary positions: channels offset .. offset + 2 len(turns) - 1 of every head of q [T, n_heads, D] and k [T, n_kv_heads, D]
+    (BF16, possibly slices of a projection's rows; k may be None) turn by pos[t] * turns (int64, rope_turns), as two halves
+    or, interleaved, as neighbours.  backward: the transposed rotation, for gradients.  Returns (q_out, k_out): new tensors
+    unless given; q_out=q, k_out=k works in place."""
+    rc, q_out, k_out = _lib.load_kv().rotate(q, k, pos, turns, gain, offset, interleaved, backward, q_out, k_out, _raw(stream))
+    if rc:
+        check(rc, "kv_rotate")
+    return q_out, k_out
+
+
+def kv_compact(cache: KvCache, table, start, nodes, count, length=None, dev_err=None, stream=None):
+    """Keep tokens start[b] + nodes[b, j], j < count[b], of every sequence and move them together behind start[b]; the bounds of
+    their blocks are made anew.  start, count int32 [B], nodes int32 [B, A] ascending; count < 0 leaves a sequence alone.
+    Returns the new lengths, int32 [B]."""
+    rc, length, _ = _lib.load_kv().compact(cache, table, start, nodes, count, length, dev_err, _raw(stream))
+    if rc:
+        check(rc, "kv_compact")
+    return length
+
+
+def kv_fork(cache: KvCache, refs, table, parent, length, dev_err=None, stream=None):
+    """Row b of the table becomes the blocks of the first length[b] tokens of what row parent[b] was (a negative parent: none);
+    refs int32 [n_pages] counts the entries that name each page.  In place; nothing of the cache is copied."""
+    rc = _lib.load_kv().fork(cache, refs, table, parent, length, dev_err, _raw(stream))
+    if rc:
+        check(rc, "kv_fork")
+
+
+def kv_resize_workspace(n_pages: int, B: int, N: int) -> int:
+    return _lib.load().kv_resize_workspace(n_pages, B, N)
+
+
+def kv_resize(cache: KvCache, refs, table, start, end, ws=None, dev_err=None, stream=None):
+    """Give every sequence pages of its own for positions start[b] .. end[b] - 1 (a shared block that start[b] lies
+    inside of is copied) and take back those behind; the lowest free pages (refs 0) first.  end < 0 leaves a row alone.
+    ws: uint8 [kv_resize_workspace(...)]; a new one if None."""
+    rc = _lib.load_kv().resize(cache, refs, table, start, end, ws, dev_err, _raw(stream))
+    if rc:
+        check(rc, "kv_resize")
+
+
 class MoeLayer:
     """One MoE layer resident on the device, with its workspaces; forward() runs
     route + permute (one call) -> expert FFN (routed + shared) -> combine."""

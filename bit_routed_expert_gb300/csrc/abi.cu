@@ -1,5 +1,6 @@
 // extern "C" entry points of libbre: host-side argument checks, then the launchers.
 #include <atomic>
+#include <cmath>
 
 #include <cuda_runtime.h>
 
@@ -278,6 +279,110 @@ bre_status kv_attend(const bre_kv_cache* cache, const void* q_bf16, int64_t q_st
   return cuda_status(launch_kv_attend(cache, KvTokens{seq, pos, T, table, B, N}, static_cast<const uint16_t*>(q_bf16),
                                       q_stride, n_heads, ids, k, scale, static_cast<uint16_t*>(out_bf16), lse,
                                       dev_err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kv_attend_tree_workspace(int T, int n_heads, int n_kv_heads, int head_dim) {
+  return T > 0 && n_heads > 0 && n_kv_heads > 0 && head_dim > 0 ? kv_tree_ws_bytes(T, n_heads, n_kv_heads, head_dim) : 0;
+}
+
+bre_status kv_attend_tree(const bre_kv_cache* cache, const void* q_bf16, int64_t q_stride, int n_heads, const int32_t* seq,
+                          const int32_t* pos, int T, const int32_t* table, int B, int N, const int32_t* start,
+                          const uint64_t* mask, int words, float scale, void* out_bf16, float* lse, void* ws, size_t ws_bytes,
+                          int32_t* dev_err, bre_stream_t stream) {
+  bre_status st = kv_check(cache, seq, pos, T, table, B, N);
+  if (st != BRE_OK || T == 0) return st;
+  if ((st = kv_check_q(cache, q_bf16, q_stride, n_heads, 1)) != BRE_OK) return st;
+  if (mask && (!start || words <= 0 || !aligned(mask, 8) || !aligned(start, 4))) return BRE_ERR_ARG;
+  if (mask && words > 1024) return BRE_ERR_UNSUPPORTED;
+  if (!out_bf16 || !aligned(out_bf16, 32) || !aligned(lse, 4) || !(scale - scale == 0.0f)) return BRE_ERR_ARG;
+  const size_t need = kv_tree_ws_bytes(T, n_heads, cache->n_kv_heads, cache->head_dim);
+  if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return BRE_ERR_WORKSPACE;
+  TreeArgs a{};
+  a.cache = cache;
+  a.tk = KvTokens{seq, pos, T, table, B, N};
+  a.q = static_cast<const uint16_t*>(q_bf16), a.q_stride = q_stride, a.Hq = n_heads;
+  a.start = mask ? start : nullptr, a.mask = mask, a.words = mask ? words : 0;
+  a.scale = scale, a.out = static_cast<uint16_t*>(out_bf16), a.lse = lse, a.ws = ws, a.err = dev_err;
+  return cuda_status(launch_kv_attend_tree(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bre_status kv_rotate(const void* q_bf16, int64_t q_stride, int n_heads, const void* k_bf16, int64_t k_stride, int n_kv_heads,
+                     int head_dim, const int32_t* pos, int T, const uint64_t* turns, int n_pairs, float gain, int offset,
+                     int interleaved, int backward, void* q_out_bf16, int64_t q_out_stride, void* k_out_bf16,
+                     int64_t k_out_stride, bre_stream_t stream) {
+  if (T < 0 || n_heads <= 0 || head_dim <= 0 || n_pairs <= 0 || offset < 0 || (int64_t)offset + 2LL * n_pairs > head_dim)
+    return BRE_ERR_ARG;
+  if (head_dim % 8 || head_dim > 256) return BRE_ERR_UNSUPPORTED;
+  if (n_kv_heads < 0) return BRE_ERR_ARG;
+  if ((int64_t)n_heads + n_kv_heads > INT32_MAX / 512) return BRE_ERR_UNSUPPORTED;
+  if (!turns || !aligned(turns, 8) || !(gain - gain == 0.0f)) return BRE_ERR_ARG;
+  if (T == 0) return BRE_OK;   // (rows of no tokens may have no address)
+  if (!k_bf16 ? k_out_bf16 != nullptr || n_kv_heads != 0 : n_kv_heads == 0) return BRE_ERR_ARG;
+  auto rows_ok = [&](const void* in, int64_t in_stride, const void* out, int64_t out_stride, int heads) {
+    return in && out && aligned(in, 2) && aligned(out, 2) && in_stride >= (int64_t)heads * head_dim &&
+           out_stride >= (int64_t)heads * head_dim;
+  };
+  if (!pos || !aligned(pos, 4) || !rows_ok(q_bf16, q_stride, q_out_bf16, q_out_stride, n_heads) ||
+      (k_bf16 && !rows_ok(k_bf16, k_stride, k_out_bf16, k_out_stride, n_kv_heads)))
+    return BRE_ERR_ARG;
+  const RotateRows q{static_cast<const uint16_t*>(q_bf16), static_cast<uint16_t*>(q_out_bf16), q_stride, q_out_stride, n_heads};
+  RotateRows k{};
+  if (k_bf16)
+    k = {static_cast<const uint16_t*>(k_bf16), static_cast<uint16_t*>(k_out_bf16), k_stride, k_out_stride, n_kv_heads};
+  return cuda_status(launch_kv_rotate(q, k, head_dim, pos, T, turns, n_pairs, gain, offset, interleaved != 0, backward != 0,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bre_status bre_rope_turns(int rot_dim, double theta, int scaling, double factor, double low, double high, double length,
+                          uint64_t* turns, float* gain) {
+  if (rot_dim <= 0 || rot_dim % 2 || !turns || !gain || !(theta > 1.0) || std::isinf(theta)) return BRE_ERR_ARG;
+  if (scaling < BRE_ROPE_PLAIN || scaling > BRE_ROPE_BANDS) return BRE_ERR_UNSUPPORTED;
+  if (scaling != BRE_ROPE_PLAIN && (!(factor > 0.0) || std::isinf(factor))) return BRE_ERR_ARG;
+  if (scaling >= BRE_ROPE_RAMP && (!(length > 0.0) || std::isinf(length) || !(low > 0.0) || !(high > low) || std::isinf(high)))
+    return BRE_ERR_ARG;
+  return rope_turns(rot_dim, theta, scaling, factor, low, high, length, turns, gain) ? BRE_OK : BRE_ERR_ARG;
+}
+
+// What the page calls check beside the cache.
+static bre_status kv_check_pages(const bre_kv_cache* c, const int32_t* refs, const int32_t* table, int B, int N,
+                                 const int32_t* one, const int32_t* two) {
+  const bre_status st = kv_check(c, nullptr, nullptr, 0, table, B, N);
+  if (st != BRE_OK) return st;
+  if (!refs || !one || !two || !aligned(refs, 4) || !aligned(one, 4) || !aligned(two, 4)) return BRE_ERR_ARG;
+  if ((int64_t)B * N > INT32_MAX || c->n_kv_heads > 65534) return BRE_ERR_UNSUPPORTED;
+  return BRE_OK;
+}
+
+bre_status kv_compact(const bre_kv_cache* cache, const int32_t* table, int B, int N, const int32_t* start, const int32_t* nodes,
+                      int A, const int32_t* count, int32_t* length, int32_t* dev_err, bre_stream_t stream) {
+  const bre_status st = kv_check(cache, nullptr, nullptr, 0, table, B, N);
+  if (st != BRE_OK) return st;
+  if (!start || !count || A < 0 || (A > 0 && !nodes) || !aligned(start, 4) || !aligned(nodes, 4) || !aligned(count, 4) ||
+      !aligned(length, 4))
+    return BRE_ERR_ARG;
+  return cuda_status(launch_kv_compact(cache, table, B, N, start, nodes, A, count, length, dev_err,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+bre_status kv_fork(const bre_kv_cache* cache, int32_t* refs, int32_t* table, int B, int N, const int32_t* parent,
+                   const int32_t* length, int32_t* dev_err, bre_stream_t stream) {
+  const bre_status st = kv_check_pages(cache, refs, table, B, N, parent, length);
+  if (st != BRE_OK) return st;
+  if (B > KV_FORK_MAX_B) return BRE_ERR_UNSUPPORTED;
+  return cuda_status(launch_kv_fork(cache->n_pages, refs, table, B, N, parent, length, dev_err,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kv_resize_workspace(int n_pages, int B, int N) {
+  return n_pages > 0 && B > 0 && N > 0 ? kv_resize_ws_bytes(n_pages, B, N) : 0;
+}
+
+bre_status kv_resize(const bre_kv_cache* cache, int32_t* refs, int32_t* table, int B, int N, const int32_t* start,
+                     const int32_t* end, void* ws, size_t ws_bytes, int32_t* dev_err, bre_stream_t stream) {
+  const bre_status st = kv_check_pages(cache, refs, table, B, N, start, end);
+  if (st != BRE_OK) return st;
+  if (!ws || ws_bytes < kv_resize_ws_bytes(cache->n_pages, B, N) || !aligned(ws, 16)) return BRE_ERR_WORKSPACE;
+  return cuda_status(launch_kv_resize(cache, refs, table, B, N, start, end, ws, dev_err, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 bre_status bre_set_ffn_wait_limit(int64_t cycles) {

@@ -93,6 +93,47 @@ cudaError_t launch_kv_select(const bre_kv_cache* c, const KvTokens& tk, const ui
 cudaError_t launch_kv_attend(const bre_kv_cache* c, const KvTokens& tk, const uint16_t* q, long long q_stride, int Hq,
                              const int32_t* ids, int k, float scale, uint16_t* out, float* lse, int32_t* err, cudaStream_t s);
 
+// rotary positions: the rows of one tensor (heads = 0: none), in and out
+struct RotateRows {
+  const uint16_t* in;
+  uint16_t* out;
+  long long in_stride, out_stride;
+  int heads;
+};
+cudaError_t launch_kv_rotate(const RotateRows& q, const RotateRows& k, int D, const int32_t* pos, int T, const uint64_t* turns,
+                             int pairs, float gain, int offset, bool interleaved, bool backward, cudaStream_t s);
+bool rope_turns(int rot_dim, double theta, int scaling, double factor, double low, double high, double length,
+                uint64_t* turns, float* gain);
+
+// attention over the whole cached context and a tree behind it
+struct TreeArgs {
+  const bre_kv_cache* cache;
+  KvTokens tk;
+  const uint16_t* q;
+  long long q_stride;
+  int Hq;
+  const int32_t* start;    // [B] and
+  const uint64_t* mask;    // [T][words], or both NULL
+  int words;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  void* ws;
+  int32_t* err;
+};
+size_t kv_tree_ws_bytes(int T, int Hq, int H, int D);
+cudaError_t launch_kv_attend_tree(const TreeArgs& a, cudaStream_t s);
+
+// pages of the cache
+cudaError_t launch_kv_compact(const bre_kv_cache* c, const int32_t* table, int B, int N, const int32_t* start,
+                              const int32_t* nodes, int A, const int32_t* count, int32_t* length, int32_t* err, cudaStream_t s);
+constexpr int KV_FORK_MAX_B = 49152;   // a column of the table lies in shared memory
+cudaError_t launch_kv_fork(int n_pages, int32_t* refs, int32_t* table, int B, int N, const int32_t* parent,
+                           const int32_t* length, int32_t* err, cudaStream_t s);
+size_t kv_resize_ws_bytes(int n_pages, int B, int N);
+cudaError_t launch_kv_resize(const bre_kv_cache* c, int32_t* refs, int32_t* table, int B, int N, const int32_t* start,
+                             const int32_t* end, void* ws, int32_t* err, cudaStream_t s);
+
 // tiled tensor map over global memory: dims innermost first, strides (bytes) of dims 1..rank-1
 bool encode_tiled(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
                   const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swizzle);

@@ -59,6 +59,7 @@ typedef enum {
 #define BRE_DEVERR_ROW_ID 2    /* an Engram row id outside [0, n_rows): row decoded as +0 */
 #define BRE_DEVERR_TIMEOUT 4   /* a bounded device wait gave up; outputs of that CTA are invalid */
 #define BRE_DEVERR_PAGE 8      /* a sequence, block or page outside the cache or the page table */
+#define BRE_DEVERR_FULL 16     /* fewer free pages than blocks that needed one */
 
 typedef enum { BRE_FMT_Q2_K = 1, BRE_FMT_Q8_0 = 2, BRE_FMT_Q2_K_R16 = 3 } bre_fmt;
 
@@ -372,6 +373,99 @@ bre_status kv_attend(const bre_kv_cache *cache, const void *q_bf16, int64_t q_st
                      const int32_t *pos, int T, const int32_t *table, int B, int N, const int32_t *ids, int k,
                      float scale, void *out_bf16, float *lse, void *ws, size_t ws_bytes, int32_t *dev_err,
                      bre_stream_t stream);
+
+/* Attention over the whole cached context and a tree of drafted tokens behind it: for each query head of token t of
+ * sequence b = seq[t], over the tokens x <= pos[t] of the sequence that have a page and for which
+ *   mask NULL: nothing more (causal attention over all that is cached: single tokens, prompts, chunks of them)
+ *   else:      x < start[b], or bit j % 64 of mask[t][j / 64] is set, j = x - start[b] < 64 words,
+ * s_x, out and lse as in kv_attend, empty and NaN rows too; a query that holds a NaN or an infinity gives NaN.  The
+ * drafted tokens were stored by kv_append at positions start[b] + j in the order of the tree's nodes; a node's bits are its
+ * ancestors' and its own.  (Their rotary positions go by the depth in the tree, not by their place.)  The call's tokens of one
+ * sequence should follow one another in the list: then each key is read once for all of them.
+ * Logits, maxima and sums are FP32, the logits with their value's scale as in kv_attend.  A query enters as the sum of two E4M3
+ * numbers times a power of two that takes its head's largest magnitude to 224 .. 448: exactly down to 2^-10 of that, off
+ * by 2^-19 of it at most below.  The probabilities enter the second product as FP16, as in kv_attend.
+ *   start [B] int32 (negative counts as 0) and mask [T][words] uint64, or both NULL; out, lse as in kv_attend.
+ *   ws: kv_attend_tree_workspace(T, ...) bytes of scratch, 256-byte aligned, which need no initialisation; calls that
+ *   share it must be ordered (two graphs that may run at the same time need one each).
+ * Requires G <= 16, words <= 1024. */
+size_t kv_attend_tree_workspace(int T, int n_heads, int n_kv_heads, int head_dim);
+bre_status kv_attend_tree(const bre_kv_cache* cache, const void* q_bf16, int64_t q_stride, int n_heads, const int32_t* seq,
+                          const int32_t* pos, int T, const int32_t* table, int B, int N, const int32_t* start,
+                          const uint64_t* mask, int words, float scale, void* out_bf16, float* lse, void* ws, size_t ws_bytes,
+                          int32_t* dev_err, bre_stream_t stream);
+
+/* Rotary positions: of each head of every row, channels offset .. offset + 2 n_pairs - 1 turn in pairs (a_i, b_i),
+ *   angle = 2 pi frac(pos[t] * turns[i] / 2^64),  c = gain cos(angle),  s = gain sin(angle)
+ *   (a, b) -> (a c - b s, a s + b c);  backward: (a c + b s, b c - a s), the transposed map, which takes the outputs'
+ *   gradients to the inputs' (and, with gain 1, undoes the rotation)
+ * in FP32, rounded once to BF16; the other channels pass unchanged.  The angle is exact for every position (whole numbers
+ * that wrap at a full turn) up to the rounding of turns and 2^-25 of half a turn.  Pairs: interleaved 0: a_i = channel
+ * offset + i, b_i = offset + n_pairs + i; else offset + 2 i and offset + 2 i + 1.  A row with a negative position gives zeros.
+ *   q, q_out [T][n_heads][D], k, k_out [T][n_kv_heads][D]: BF16, rows `stride` elements apart; k NULL: queries only;
+ *   an output may be its input (with the same stride) but may not overlap it otherwise.  pos [T] int32,
+ *   turns [n_pairs] uint64 on the device (bre_rope_turns).
+ * Requires D % 8 == 0, D <= 256, n_pairs >= 1, offset + 2 n_pairs <= D. */
+bre_status kv_rotate(const void* q_bf16, int64_t q_stride, int n_heads, const void* k_bf16, int64_t k_stride, int n_kv_heads,
+                     int head_dim, const int32_t* pos, int T, const uint64_t* turns, int n_pairs, float gain, int offset,
+                     int interleaved, int backward, void* q_out_bf16, int64_t q_out_stride, void* k_out_bf16,
+                     int64_t k_out_stride, bre_stream_t stream);
+
+/* The frequencies of kv_rotate: turns (HOST, [rot_dim / 2]) in units of 2^-64 full turns a position, and the gain.  With
+ * f_i = theta^(-2 i / rot_dim) radians a position, for contexts `factor` times as long as the `length` trained on:
+ *   BRE_ROPE_PLAIN   f_i
+ *   BRE_ROPE_LINEAR  f_i / factor
+ *   BRE_ROPE_BASE    f_i of the base theta * factor^(rot_dim / (rot_dim - 2))
+ *   BRE_ROPE_RAMP    r f_i / factor + (1 - r) f_i, r = clamp((i - a) / max(b - a, 0.001), 0, 1), where
+ *                    p(n) = rot_dim ln(length / (2 pi n)) / (2 ln theta) is the pair that makes n turns in `length`,
+ *                    a = max(floor(p(high)), 0), b = min(ceil(p(low)), rot_dim / 2 - 1); gain = 0.1 ln(factor) + 1
+ *   BRE_ROPE_BANDS   (1 - w) f_i / factor + w f_i, w = clamp((length f_i / (2 pi) - low) / (high - low), 0, 1)
+ * The gain of the others (and for factor <= 1) is 1.  low and high are turns in `length` (usual: 1 and 32 for the ramp,
+ * 1 and 4 for bands) and, like length, only looked at for those two.  Host arithmetic in 64 bits; no GPU is needed. */
+#define BRE_ROPE_PLAIN 0
+#define BRE_ROPE_LINEAR 1
+#define BRE_ROPE_BASE 2
+#define BRE_ROPE_RAMP 3
+#define BRE_ROPE_BANDS 4
+bre_status bre_rope_turns(int rot_dim, double theta, int scaling, double factor, double low, double high, double length,
+                          uint64_t* turns, float* gain);
+
+/* Pages.  refs [n_pages] int32, kept by the caller beside the table: how many table entries name the page; 0: it is free.
+ * kv_fork and kv_resize keep it so.  table is updated in place.  A page that several sequences share must not be
+ * written: kv_resize comes before kv_append.  Entries that name no page of the cache set BRE_DEVERR_PAGE and count as
+ * none.  Every result is the same whatever the order in which the GPU works.
+ *
+ * Keep some of the tokens behind start[b] and move them together: for every sequence b with count[b] >= 0, token
+ * start[b] + j becomes what token start[b] + nodes[b][j] was, j < count[b] (the path of a tree that was accepted; the
+ * tokens of a context that an eviction keeps), and length[b] = start[b] + count[b]; count[b] < 0: the sequence is left as
+ * it is, length[b] = start[b].  The bounds of the blocks from start[b] / 64 up to length[b] are made anew from the keys
+ * of the tokens before length[b].  nodes [B][A] int32 ascend; a list that does not, a count above A, a start below 0 or a
+ * token without a page sets BRE_DEVERR_PAGE and leaves that sequence as it is, with length[b] = start[b].
+ *   start, count [B]; length [B] int32 out, or NULL.  None of the blocks may be shared. */
+bre_status kv_compact(const bre_kv_cache* cache, const int32_t* table, int B, int N, const int32_t* start, const int32_t* nodes,
+                      int A, const int32_t* count, int32_t* length, int32_t* dev_err, bre_stream_t stream);
+
+/* Every sequence continues another one (a step of a beam search, or several answers to one prompt): row b of the table
+ * becomes the first ceil(length[b] / 64) entries of what row parent[b] was before the call, then -1; refs follow, and
+ * pages that no row names any more are free.  parent[b] < 0 or length[b] <= 0: the row is emptied.  parent[b] = b with a
+ * length that covers its blocks leaves it as it is.  parent[b] >= B sets BRE_DEVERR_PAGE and leaves the row as it is.
+ * Only the table and refs change, so no key is copied.  Requires B <= 49,152. */
+bre_status kv_fork(const bre_kv_cache* cache, int32_t* refs, int32_t* table, int B, int N, const int32_t* parent,
+                   const int32_t* length, int32_t* dev_err, bre_stream_t stream);
+
+/* Pages of their own for positions start[b] .. end[b] - 1 of every sequence, which are to be written, and none behind
+ * them.  For every b with end[b] >= 0: blocks from ceil(end[b] / 64) on lose their pages; of the blocks from
+ * start[b] / 64 up to there, one that has no page, or whose page had more than one reference before the call, gets
+ * a free one: the pages that had no reference before the call, lowest first, in the order of b and then of the blocks.  The
+ * block that start[b] lies inside of (start[b] % 64 > 0) gets a copy of its former page's contents.  Blocks below it are not
+ * looked at.  end[b] < 0: the row is left as it is.  If there are too few free pages BRE_DEVERR_FULL is set and
+ * the blocks that come last stay as they were; end[b] > 64 N sets BRE_DEVERR_PAGE and counts as 64 N.
+ * (start = end = length[b] gives back what lies behind the length.)  start [B] (negative counts as 0), end [B] int32.
+ *   ws: kv_resize_workspace(...) bytes of scratch, 16-byte aligned, no initialisation; as kv_attend_tree's.
+ * Requires B * N < 2^31. */
+size_t kv_resize_workspace(int n_pages, int B, int N);
+bre_status kv_resize(const bre_kv_cache* cache, int32_t* refs, int32_t* table, int B, int N, const int32_t* start,
+                     const int32_t* end, void* ws, size_t ws_bytes, int32_t* dev_err, bre_stream_t stream);
 
 /* Budget, in SM clock cycles, of the bounded waits inside the expert FFN kernels
  * (moe_expert_ffn, both paths) and kv_attend's tile kernel for calls made after this one, from any
