@@ -25,6 +25,7 @@
 #include <atomic>
 
 #include "kv_attend.cuh"
+#include "kv_tc.cuh"
 
 namespace bre {
 
@@ -35,7 +36,6 @@ constexpr int AT_THREADS = 128 + AT_CODES + 64;
 constexpr int W_MERGE = (128 + AT_CODES) / 32, W_MMA = W_MERGE + 1;
 constexpr int AT_RING = 4;                          // blocks that the merging warp may be ahead
 constexpr float AT_SLACK = 7.0f;                    // growth of a row's maximum (log2) that needs no rescaling
-constexpr long long AT_WAIT = 4000000000LL;         // cycles before a wait gives up (~2 s), if no budget is set
 
 struct Block {
   int page, id, n, pad;    // n: tokens that some row sees; page < 0: the end
@@ -48,130 +48,6 @@ struct TilesMem {
   static constexpr int q = 0, k = q + Q, v = k + 2 * KV, end = v + 2 * KV;
   static constexpr int bytes = end + 1024;   // the swizzled tiles start on 1024 bytes
 };
-
-// Shared-memory descriptors of 128-byte-swizzled tiles: K-major (rows of 64 values, eight rows 1024 bytes
-// apart from the next eight), and MN-major (rows of 64 values along M or N; the next 64 of them `panel`
-// bytes on, the next eight of K 1024 bytes on).
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-         ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, uint32_t panel) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-#define BRE_R8(f, b) f(b), f(b + 1), f(b + 2), f(b + 3), f(b + 4), f(b + 5), f(b + 6), f(b + 7)
-// 32 consecutive columns of this thread's tensor-memory lane; the values are there after tmem_wait_ld.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
-#define BRE_OUT(i) "=r"(r[i])
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : BRE_R8(BRE_OUT, 0), BRE_R8(BRE_OUT, 8), BRE_R8(BRE_OUT, 16), BRE_R8(BRE_OUT, 24)
-      : "r"(addr));
-#undef BRE_OUT
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
-#define BRE_OUT(i) "=r"(r[i])
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : BRE_R8(BRE_OUT, 0), BRE_R8(BRE_OUT, 8)
-      : "r"(addr));
-#undef BRE_OUT
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
-#define BRE_IN(i) "r"(r[i])
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-      BRE_R8(BRE_IN, 0), BRE_R8(BRE_IN, 8)
-      : "memory");
-#undef BRE_IN
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// The first try of a wait is inline, the bounded loop is not: with four roles in one kernel the
-// instruction caches are what runs short first.
-// A try suspends the warp for up to a millisecond: fourteen warps, half of them waiting, would otherwise take
-// the workers' issue slots.
-__device__ __forceinline__ bool try_wait_ms(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-      : "memory");
-  return ok != 0;
-}
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!try_wait_ms(bar, parity))
-    if (clock64() - t0 > AT_WAIT) return false;
-  return true;
-}
-
-// True in one lane.  The MMA warp stays together and lets one lane issue, so that the compiler keeps descriptors
-// and addresses in uniform registers, where the MMA instructions want them.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
-// Two FP32 values at a time.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 
 // Whether a key row that is not all zeros lies more than 2^15 below the block's largest scale `top`.  By a whole warp,
 // with the scales of tokens lane and lane + 32 (0: not there).  Zero rows, whose scale is the least one, are exact in
