@@ -9,17 +9,19 @@
 // order of the context (the same numbers whatever the order in which CTAs finish).  The host knows neither
 // lengths nor runs: every CTA adds up the work of all tiles itself and finds its place.
 //
-// Fourteen warps:
+// Fifteen warps:
 //   warps 0-3, 4-7  softmax, a thread a row: two tiles' rows of the same block, or, where there is one tile, its
 //                   rows of the even and of the odd blocks, each with a running maximum, sum and output of its own
-//   warps 8-11      queries into two E4M3 terms; the values' codes into FP16 (exact) in 128-byte-swizzled shared memory
+//   warps 8-11      queries into two E4M3 terms; the values' codes into FP16 in 128-byte-swizzled shared memory
 //   warp 12         walks through the share, looks up pages and starts the copies (TMA: keys swizzled, values as they lie)
-//   warp 13         issues the MMAs: S = Q K^T into tensor memory, O += P V with P read from tensor memory
+//   warps 13, 14    issue the MMAs: S = Q K^T into tensor memory; O += P V with P read from tensor memory
 //
 // The keys' codes are an MMA operand as they lie in the cache.  A BF16 query is q = 2^e (a + b), a and b E4M3: a is
 // q's nearest code, b the rest's, so that the two products add up to that of q itself (see bre.h for what is lost).  Two
 // products of 8-bit operands take the tensor cores as long as one of 16-bit ones, and the keys need no conversion.  A key's
-// scale multiplies its logit and a value's scale goes into its weight (see kv_attend.cu), both by token.
+// scale multiplies its logit.  A value's scale goes into its FP16 value relative to the block's largest, which is exact down to
+// 2^-15 of that, and the largest one into the block's weights; where a row is further below, or the scale is above
+// EV_LARGE, every token's own goes into its weight (see kv_attend.cu), by slower code.
 #include <atomic>
 
 #include "kv_attend.cuh"
@@ -29,22 +31,26 @@ namespace bre {
 
 namespace {
 
-constexpr int TT_THREADS = 448;
+constexpr int TT_THREADS = 480;
 constexpr int TT_WARPS = TT_THREADS / 32;
-constexpr int W_CONV = 8, W_LOAD = 12, W_TREE_MMA = 13;
-constexpr int TT_RING = 8;               // descriptors between the walking warp and the others
-constexpr int TT_K = 6, TT_V = 6;        // blocks of keys, of values on their way
-constexpr int TT_V16 = 3;                // blocks of converted values
+constexpr int W_CONV = 8, W_LOAD = 12, W_S = 13, W_O = 14;
+// Depths of the rings (powers of 2): keys with what the S warp is told, values with what the converting warps are told;
+// converted values; what either softmax group is told; scales; units' logit factors.  The last two need no barriers: a
+// softmax group has one of every two blocks, and the end of every unit, and lags behind by TT_GROUP of these and
+// by the TT_V that the converting warps may be apart.
+constexpr int TT_K = 4, TT_V = 4, TT_V16 = 4, TT_GROUP = 4, TT_SC = 16, TT_QF = 8;
 constexpr int TT_MAX_CTAS = 160;
 constexpr float TT_SLACK = 7.0f;         // growth of a row's maximum (log2) that needs no rescaling
 // Costs of the shares: a block for one tile, for two tiles, and what a unit takes beside its blocks.
 constexpr int COST_ONE = 2, COST_TWO = 3, COST_UNIT = 6;
 
-enum : int { F_BLOCK = 1, F_FIRST = 2, F_FULL = 4, F_END = 8, F_EXIT = 16, F_TWO = 32, F_SOME = 64 };
+enum : int { F_BLOCK = 1, F_FIRST = 2, F_FULL = 4, F_END = 8, F_EXIT = 16, F_TWO = 32, F_SOME = 64, F_ODD = 128, F_NEW = 256 };
 
-// What the walking warp tells the others: a block, or the end of a unit's part.
+// What the walking warp tells the others: a block (F_ODD: of the second group, where there is one tile; F_NEW: the first
+// of its group in the unit), or the end of a unit's part.
 struct Item {
-  int t0, n, h, blk, flags, slot, begin, pad;   // slot < 0: the whole unit, its outputs are final
+  int t0, n, h, blk;              // tokens, kv head; block (at the end: how many there were)
+  int flags, slot, begin, kb;     // slot < 0: the whole unit, its outputs are final; running number of the block
 };
 
 // Where the parts of a unit that several CTAs share are to be found (written by the CTA that holds its first block).
@@ -108,6 +114,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Bit x - 64 blk set: the token sees slot x (of the 64 of a block).
 __device__ __forceinline__ uint64_t seen_bits(const uint64_t* __restrict__ mask, int words, int start, int pos, int blk) {
   const long long x0 = (long long)blk * KV_BLOCK;
@@ -135,6 +147,13 @@ __device__ __forceinline__ bool other_run(int s, int p, int s2, int p2) {
   return (p < 0) != (p2 < 0) || (p >= 0 && s != s2);
 }
 
+// Two counters; which one is not known when the program is compiled, and an array would lie in memory.
+struct Pair {
+  int a, b;
+  __device__ __forceinline__ int operator[](int i) const { return i ? b : a; }
+  __device__ __forceinline__ void add(int i) { a += i ^ 1, b += i; }
+};
+
 struct Unit {
   int blocks, step;   // of a tile and one kv head: blocks, cost of one
   __device__ __forceinline__ Unit(int n, int top, int N, int per_one) {
@@ -147,147 +166,352 @@ struct Unit {
   // the first block that counts from x on or later
   __device__ __forceinline__ int first_from(long long x) const {
     if (x <= 0) return 0;
-    const long long i = (x - COST_UNIT + step - 1) / step;
-    return i < 1 ? 1 : i > blocks ? blocks : (int)i;
+    if (x > at(blocks - 1)) return blocks;   // (what follows fits 32 bits: a unit has at most 2^25 blocks)
+    return max(((int)x - COST_UNIT + step - 1) / step, 1);
   }
 };
+
+// a / b; hardly ever of numbers that need the long division
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return a <= 0x7FFFFFFFLL && b <= 0x7FFFFFFFLL ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 
 struct PlanMem {
   int run[TT_WARPS], top[TT_WARPS];
   uint32_t cut[TT_WARPS];
   long long sum[TT_WARPS];
-  long long found_at;   // cost before the tile in which the share begins
-  int found;            // that tile's first token
+  long long lo, hi, per;   // this CTA's share, costs lo .. hi (none if hi <= lo); length of a share
+  long long found_at;      // cost before the tile in which the share begins
+  int found;               // that tile's first token
 };
 
-// Adds up the cost of all tiles; on the second pass (lo >= 0) finds the tile that holds cost lo.  By the whole CTA.
-__device__ long long plan_pass(const TreeParams& a, PlanMem& m, long long lo) {
+// The cost of all tiles, summed up by the whole CTA, a thread a token; and where the CTA's share begins.  Rolled up as far as it
+// goes: the code runs once, and fetching it takes longer than running it.
+__device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, per_one = 128 / a.G;
-  int run = -1, top = INT32_MIN;   // of the last token so far: first token of its run; largest position of its tile
-  long long sum = 0;
-  for (int base = 0; base < a.T; base += TT_THREADS) {
-    const int t = base + tid;
-    const bool in = t < a.T;
-    const int s = in ? __ldg(a.seq + t) : 0, p = in ? __ldg(a.pos + t) : -1;
-    const bool begins = in && (t == 0 || other_run(s, p, __ldg(a.seq + t - 1), __ldg(a.pos + t - 1)));
-    const bool cut_next = in && (t == a.T - 1 || other_run(s, p, __ldg(a.seq + t + 1), __ldg(a.pos + t + 1)));
-    int r = begins ? t : -1;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int x = __shfl_up_sync(0xffffffffu, r, o);
-      if (lane >= o) r = max(r, x);
-    }
-    if (lane == 31) m.run[warp] = r;
-    __syncthreads();
-    for (int w = 0; w < TT_WARPS; ++w) {
-      if (w < warp) r = max(r, m.run[w]);
-    }
-    r = max(r, run);
-    const int idx = (t - r) % a.per;
-    const bool first = in && idx == 0;
-    // the largest position since the tile's first token
-    int v = p;
-    uint32_t cut = first;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int x = __shfl_up_sync(0xffffffffu, v, o);
-      const uint32_t c = __shfl_up_sync(0xffffffffu, cut, o);
-      if (lane >= o) {
-        if (!cut) v = max(v, x);
-        cut |= c;
+  long long lo = -1;
+  for (int pass = 0;; ++pass) {   // a second pass, where the list is longer than the CTA, finds the place of the share
+    int run = -1, top = INT32_MIN;   // of the last token so far: first token of its run; largest position of its tile
+    long long sum = 0, mine = 0, at = 0;
+    int from = 0;
+#pragma unroll 1
+    for (int base = 0; base < a.T; base += TT_THREADS) {
+      const int t = base + tid;
+      const bool in = t < a.T;
+      const int s = in ? __ldg(a.seq + t) : 0, p = in ? __ldg(a.pos + t) : -1;
+      const int sb = in && t ? __ldg(a.seq + t - 1) : 0, pb = in && t ? __ldg(a.pos + t - 1) : -1;
+      const int sn = t + 1 < a.T ? __ldg(a.seq + t + 1) : 0, pn = t + 1 < a.T ? __ldg(a.pos + t + 1) : -1;
+      int r = in && (t == 0 || other_run(s, p, sb, pb)) ? t : -1;
+#pragma unroll 1
+      for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, r, o);
+        if (lane >= o) r = max(r, x);
       }
+      if (lane == 31) m.run[warp] = r;
+      __syncthreads();
+#pragma unroll 1
+      for (int w = 0; w < warp; ++w) r = max(r, m.run[w]);
+      r = max(r, run);
+      const int idx = (t - r) % a.per;
+      // the largest position since the tile's first token
+      int v = p;
+      uint32_t cut = in && idx == 0;
+#pragma unroll 1
+      for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, v, o);
+        const uint32_t c = __shfl_up_sync(0xffffffffu, cut, o);
+        if (lane >= o) {
+          if (!cut) v = max(v, x);
+          cut |= c;
+        }
+      }
+      if (lane == 31) m.top[warp] = v, m.cut[warp] = cut;
+      __syncthreads();
+      int before = top;
+#pragma unroll 1
+      for (int w = 0; w < warp; ++w) before = m.cut[w] ? m.top[w] : max(before, m.top[w]);
+      if (!cut) v = max(v, before);
+      long long c = 0;
+      if (in && (t == a.T - 1 || other_run(s, p, sn, pn) || idx == a.per - 1))   // a tile's last token
+        c = Unit(idx + 1, v, a.tab.N, per_one).cost() * a.H;
+      const long long own = c;
+#pragma unroll 1
+      for (int o = 1; o < 32; o *= 2) {
+        const long long x = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += x;
+      }
+      if (lane == 31) m.sum[warp] = c;
+      __syncthreads();
+      long long all = sum;
+#pragma unroll 1
+      for (int w = 0; w < TT_WARPS; ++w) {
+        if (w < warp) c += m.sum[w];
+        all += m.sum[w];
+        run = max(run, m.run[w]);   // the chunk's last token carries on
+        top = m.cut[w] ? m.top[w] : max(top, m.top[w]);
+      }
+      mine = own, at = sum + c - own, from = t - idx;
+      sum = all;
+      if (pass && lo >= at && lo < at + mine) m.found = from, m.found_at = at;
+      __syncthreads();
     }
-    if (lane == 31) m.top[warp] = v, m.cut[warp] = cut;
-    __syncthreads();
-    int before = top;
-    for (int w = 0; w < TT_WARPS; ++w)
-      if (w < warp) before = m.cut[w] ? m.top[w] : max(before, m.top[w]);
-    if (!cut) v = max(v, before);
-    long long c = 0;
-    if (cut_next || (in && idx == a.per - 1)) c = Unit(idx + 1, v, a.tab.N, per_one).cost() * a.H;
-    const long long mine = c;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const long long x = __shfl_up_sync(0xffffffffu, c, o);
-      if (lane >= o) c += x;
-    }
-    if (lane == 31) m.sum[warp] = c;
-    __syncthreads();
-    long long all = sum;
-    for (int w = 0; w < TT_WARPS; ++w) {
-      if (w < warp) c += m.sum[w];
-      all += m.sum[w];
-    }
-    const long long at = sum + c - mine;
-    if (lo >= 0 && mine > 0 && lo >= at && lo < at + mine) m.found = t - idx, m.found_at = at;
-    // the chunk's last token carries on
-    run = max(run, -1);
-    for (int w = 0; w < TT_WARPS; ++w) {
-      run = max(run, m.run[w]);
-      top = m.cut[w] ? m.top[w] : max(top, m.top[w]);
-    }
-    sum = all;
-    __syncthreads();
+    if (pass) break;
+    // No share is shorter than the step from a unit's first block to its second: every CTA between those of a unit's first
+    // and last block then holds a block of it.
+    const long long most = quotient(sum, COST_UNIT + COST_TWO);
+    const long long per = quotient(sum, most < 1 ? 1 : most < (long long)gridDim.x ? most : (long long)gridDim.x) + 1;
+    lo = per * blockIdx.x;
+    if (tid == 0) m.lo = lo, m.hi = min(lo + per, sum), m.per = per;
+    const bool one = a.T <= TT_THREADS;
+    if (one && lo >= at && lo < at + mine) m.found = from, m.found_at = at;
+    if (one || lo >= sum) break;
   }
-  return sum;
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
 // The attention kernel
 // ---------------------------------------------------------------------------
 
-// The part of a block in a row's sum of exponentials formed without the values' scales: where a value's scale is above
-// EV_LARGE the weights, which have it, may vanish although their terms do not.  By a whole warp.
-__device__ __noinline__ float careful_sum(uint32_t S, const float* kf, const float* ev, float f, float base, uint64_t seen) {
-  float sum = 0.0f;
+// A row's part of one block that not every row sees as a whole, or whose values' scales differ too much, or are too large,
+// for the ordinary way: every token has an exponent ev of its own in its weight, and the terms of the sum of exponentials
+// are formed without it (they may be of any size where the weight has vanished).  By a whole warp.
+//
+// The largest logit plus ev.
+__device__ __noinline__ float careful_max(uint32_t S, const float* kf, const float* ev, float f, uint64_t seen) {
+  float mx = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < KV_BLOCK; c += 16) {
     uint32_t s[16];
     tmem_ld16(S + c, s);
     tmem_wait_ld();
 #pragma unroll
-    for (int x = 0; x < 16; ++x) {
-      const float v = fmaf(__uint_as_float(s[x]) * kf[c + x], f, ev[c + x]);
-      if (seen >> (c + x) & 1ull) sum += exp2f(v - base - ev[c + x]);
+    for (int x = 0; x < 16; ++x)
+      if (seen >> (c + x) & 1ull) mx = fmaxf(mx, fmaf(__uint_as_float(s[x]) * kf[c + x], f, ev[c + x]));
+  }
+  return mx;
+}
+// The weights against base; the sum of the terms.
+__device__ __noinline__ float careful_weights(uint32_t S, const float* kf, const float* ev, float f, float base, uint64_t seen) {
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < KV_BLOCK; c += 32) {
+    uint32_t s[32], pk[16];
+    tmem_ld32(S + c, s);
+    tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < 32; x += 2) {
+      float v0 = fmaf(__uint_as_float(s[x]) * kf[c + x], f, ev[c + x]) - base;
+      float v1 = fmaf(__uint_as_float(s[x + 1]) * kf[c + x + 1], f, ev[c + x + 1]) - base;
+      if (!(seen >> (c + x) & 1ull)) v0 = -INFINITY;
+      if (!(seen >> (c + x + 1) & 1ull)) v1 = -INFINITY;
+      if (seen >> (c + x) & 1ull) sum += exp2f(v0 - ev[c + x]);
+      if (seen >> (c + x + 1) & 1ull) sum += exp2f(v1 - ev[c + x + 1]);
+      pk[x / 2] = pack_f16x2(ex2(v0), ex2(v1));
     }
+    tmem_st16(S + c / 2, pk);
   }
   return sum;
 }
 
-// PATIENT: the waits have the default budget (see kv_attend_tiles.cu).
+// What runs once a unit, or seldom, is out of line: the loops over the blocks shall stay close together.
+//
+// Queries of a unit's rows (of up to two tiles) into two E4M3 terms, by four warps; factors: of the rows' logits.
+template <int D>
+__device__ __noinline__ void load_queries(const TreeParams& a, const Item& x, unsigned char* sq, int buf0, float* factors) {
+  using M = TreeMem<D>;
+  constexpr int CL = D / 32, UN = 8;   // channels a lane, rows of a warp in flight
+  const int lane = threadIdx.x & 31, rows = x.n * a.G, per_one = 128 / a.G;
+  const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // a row's factor is not negative: see the maximum
+#pragma unroll 1
+  for (int r0 = (threadIdx.x >> 5) - W_CONV; r0 < rows; r0 += 4 * UN) {
+    uint32_t w[UN][CL / 2];
+#pragma unroll
+    for (int j = 0; j < UN; ++j) {
+      const int r = r0 + 4 * j, tl = r / a.G;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + (long long)(x.t0 + tl) * a.q_stride +
+                                                              (size_t)(x.h * a.G + r - tl * a.G) * D) + lane * (CL / 2);
+#pragma unroll
+      for (int i = 0; i < CL / 2; ++i) w[j][i] = r < rows ? __ldg(src + i) ^ flip : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < UN; ++j) {
+      const int r = r0 + 4 * j;
+      if (r >= rows) break;
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < CL / 2; ++i) mx = __vmaxu2(mx, w[j][i] & 0x7FFF7FFFu);
+      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
+      // least e with max|q| <= 448 * 2^e
+      const int bits = (int)(min(mx, 0x7F7Fu) << 16);
+      const int e = max((bits >> 23) - 127 - 8 + ((bits & 0x7FFFFF) > 0x600000 ? 1 : 0), -118);
+      const float down = pow2f(-e);
+      uint32_t hi = 0, rest = 0;
+#pragma unroll
+      for (int i = 0; i < CL / 2; ++i) {
+        const float u = __uint_as_float(w[j][i] << 16) * down, v = __uint_as_float(w[j][i] & 0xFFFF0000u) * down;
+        const uint32_t c = e4m3x2(u, v);
+        const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(c));
+        hi |= c << (16 * i);
+        rest |= e4m3x2(u - f.x, v - f.y) << (16 * i);
+      }
+      // tile and row in it: a tile holds whole tokens
+      const int tile = r >= per_one * a.G, rr = r - tile * per_one * a.G;
+      unsigned char* dst = sq + (buf0 + tile) * 2 * M::TERM + swizzled<D>(rr, lane * CL / 16) + lane * CL % 16;
+      if constexpr (CL == 4) {
+        *reinterpret_cast<uint32_t*>(dst) = hi;
+        *reinterpret_cast<uint32_t*>(dst + M::TERM) = rest;
+      } else {
+        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)hi;
+        *reinterpret_cast<uint16_t*>(dst + M::TERM) = (uint16_t)rest;
+      }
+      if (lane == 0) factors[tile * 128 + rr] = mx > 0x7F7Fu ? __int_as_float(0x7FC00000) : fabsf(a.scale) * LOG2E * pow2f(e);
+    }
+  }
+}
+// Slots of a block that some row of the unit sees.  By a whole warp.
+__device__ __noinline__ uint64_t seen_by_some(const TreeParams& a, const Item& x) {
+  uint64_t seen = 0;
+#pragma unroll 1
+  for (int i = threadIdx.x & 31; i < x.n; i += 32)
+    seen |= seen_bits(a.mask ? a.mask + (size_t)(x.t0 + i) * a.words : nullptr, a.words, x.begin, __ldg(a.pos + x.t0 + i), x.blk);
+  __syncwarp();
+  return (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(seen >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)seen);
+}
+// Whether a row more than 2^15 below the block's largest scale is not all zeros; c0, c1: scales of tokens lane and lane + 32
+// (0: does not count).  By a whole warp.
+template <int D>
+__device__ __noinline__ bool far_below(const unsigned char* raw, int c0, int c1, int top) {
+  bool far = false;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const int c = i ? c1 : c0;
+    if (c == 0 || top - c <= 15) continue;
+#pragma unroll 1
+    for (int j = 0; j < D / 16; ++j) {
+      const uint4 w = reinterpret_cast<const uint4*>(raw + ((threadIdx.x & 31) + 32 * i) * D)[j];
+      far |= ((w.x | w.y | w.z | w.w) & 0x7F7F7F7Fu) != 0;
+    }
+  }
+  __syncwarp();
+  return __any_sync(0xffffffffu, far);
+}
+// The outputs of row r of group w: of two tiles each group has its rows; of one tile (O, O + 128: either group's part of
+// every row, times c0 and c1) each joins half of the channels.
+template <int D>
+__device__ __noinline__ void store_rows(const TreeParams& a, const Item& x, uint32_t O, int r, int w, float m, float l, float c0,
+                                        float c1) {
+  const bool two = x.flags & F_TWO, some = x.flags & F_SOME, halves = some && !two, both = halves && x.blk > 1;
+  const int per_one = 128 / a.G, tr = r / a.G, row = (two ? w * per_one * a.G : 0) + r, tok = row / a.G;
+  const bool my = tr < per_one && tok < x.n && (two || some || w == 0);
+  if (!__any_sync(0xffffffffu, my)) return;
+  const size_t at = ((size_t)(x.t0 + tok) * a.H + x.h) * a.G + (row - tok * a.G);
+  const size_t part = (size_t)x.slot * a.rows + row;
+  if (my && (two || w == 0)) {
+    if (x.slot >= 0) a.ml[part] = make_float2(m, l);
+    else if (a.lse) a.lse[at] = l == 0.0f ? -INFINITY : LN2 * ((m > -INFINITY ? m - P_SHIFT : 0.0f) + log2f(l));
+  }
+  if (two) O += w * 128;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int cb = halves ? w * (D / 2) : 0, ce = halves ? cb + D / 2 : D;
+#pragma unroll 1
+  for (int c = cb; c < ce; c += 16) {
+    uint32_t o[16], o1[16], b[8];
+    if (some) tmem_ld16(O + c, o);
+    if (both) tmem_ld16(O + 128 + c, o1);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = some ? __uint_as_float(o[i]) * c0 : 0.0f;
+      if (both) v = fmaf(__uint_as_float(o1[i]), c1, v);
+      o[i] = __float_as_uint(v);
+    }
+    if (!my) continue;
+    if (x.slot >= 0) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<uint4*>(a.part + part * D + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = l == 0.0f ? 0u : pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+      st_v8(a.out + at * D + c, b);
+    }
+  }
+}
+// O of a whole warp's rows times sc.
+template <int D>
+__device__ __noinline__ void rescale(uint32_t O, float sc) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(O + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sc);
+    tmem_st16(O + c, o);
+  }
+}
+
+// A warp's waits.  In line and short: five roles' code competes for the SM's instruction cache.  A try suspends the warp for
+// a few hundred cycles, so that TRIES take a second or so; where a budget is set (PATIENT false) a wait polls.  A wait that runs out
+// makes every later one of the warp give up at once; who has waited for a ring's slot must look at `left` before using it.
+constexpr int TRIES = 1 << 23;
+template <bool PATIENT>
+struct Waits {
+  int left;   // tries of a wait; 0: some wait has given up
+  __device__ __forceinline__ void operator()(uint64_t* bar, int phase) {
+#define BRE_WAIT(how)                                                                                                     \
+  asm volatile(                                                                                                           \
+      "{\n\t.reg .pred p;\n\t.reg .s32 n;\n\tmov.s32 n, %0;\n"                                                             \
+      "AGAIN:\n\tmbarrier." how ".parity.shared::cta.b64 p, [%1], %2;\n\tvote.sync.all.pred p, p, 0xffffffff;\n\t"        \
+      "@p bra THERE;\n\tsub.s32 n, n, 1;\n\tsetp.gt.s32 p, n, 0;\n\t@p bra AGAIN;\n\tmov.s32 %0, 0;\n"                   \
+      "THERE:\n\t}"                                                                                                       \
+      : "+r"(left)                                                                                                        \
+      : "r"(smem_u32(bar)), "r"((uint32_t)phase & 1u)                                                                     \
+      : "memory")
+    if (PATIENT) BRE_WAIT("try_wait");
+    else BRE_WAIT("test_wait");
+#undef BRE_WAIT
+  }
+};
+
+struct TreeBars {
+  uint64_t k_full[TT_K], k_empty[TT_K], v_full[TT_V], v_empty[TT_V], v16_full[TT_V16], v16_empty[TT_V16];
+  uint64_t gr_full[2][TT_GROUP], gr_empty[2][TT_GROUP], s_full[2][2], p_full[2][2], o_done[2][2], q_full[2], q_empty[2];
+  uint64_t swap_in, swap_out, drain;
+};
+
 template <int D, bool PATIENT>
 __global__ void __launch_bounds__(TT_THREADS, 1)
-    kv_tree_kernel(const TreeParams a, const __grid_constant__ CUtensorMap key_map) {
+    kv_tree_kernel(const __grid_constant__ TreeParams a, const __grid_constant__ CUtensorMap key_map) {
   using M = TreeMem<D>;
   constexpr uint32_t COLS = 512;   // tensor memory: S / P of either softmax group twice at 0 .. 255, their O at 256 and 384
   constexpr int PANEL = KV_BLOCK * 128;
   extern __shared__ unsigned char sm_raw[];
-  __shared__ uint64_t it_full[TT_RING], it_empty[TT_RING], sc_full[TT_RING], k_full[TT_K], k_empty[TT_K], v_full[TT_V], v_empty[TT_V],
-      v16_full[TT_V16], v16_empty[TT_V16], s_full[2][2], p_full[2][2], o_done[2], q_full[2], q_empty[2], seg_done, swap_in, swap_out, drain;
-  __shared__ Item ring[TT_RING];
-  __shared__ __align__(16) float kf[TT_RING][KV_BLOCK], ev_f[TT_RING][KV_BLOCK], ev_inv[TT_RING][KV_BLOCK];
-  __shared__ int large[TT_RING];           // some value's scale is above EV_LARGE
-  __shared__ float q_factor[2][128];
-  __shared__ float2 swap[2][128];          // a row's maximum and sum in either softmax group
+  __shared__ TreeBars bar;
+  __shared__ Item to_v[TT_V], group[2][TT_GROUP];
+  __shared__ int to_s[TT_K], to_o[TT_V16];
+  __shared__ __align__(16) float kf[TT_SC][KV_BLOCK], ev_f[TT_SC][KV_BLOCK];   // keys' scales; the values' exponents
+  __shared__ float ev_top[TT_SC];                  // the exponent that all weights of a block have; NaN: each has its own
+  __shared__ float q_factor[TT_QF][2][128];
+  __shared__ float2 swap[2][128];                  // a row's maximum and sum in either softmax group
   __shared__ PlanMem plan;
   __shared__ uint32_t tmem_s;
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per_one = 128 / a.G;           // tokens of one tile of rows
 
-  if (tid == 0) {
-    for (int i = 0; i < TT_RING; ++i) mbar_init(&it_full[i], 1), mbar_init(&it_empty[i], 13), mbar_init(&sc_full[i], 1);
-    for (int i = 0; i < TT_K; ++i) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
-    for (int i = 0; i < TT_V; ++i) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 4);
-    for (int i = 0; i < TT_V16; ++i) mbar_init(&v16_full[i], 4), mbar_init(&v16_empty[i], 1);
-    for (int i = 0; i < 2; ++i) {
-      for (int j = 0; j < 2; ++j) mbar_init(&s_full[i][j], 1), mbar_init(&p_full[i][j], 4);
-      mbar_init(&o_done[i], 1), mbar_init(&q_full[i], 4), mbar_init(&q_empty[i], 1);
-    }
-    mbar_init(&seg_done, 1), mbar_init(&drain, 1), mbar_init(&swap_in, 8), mbar_init(&swap_out, 8);
+  static_assert(TT_K == 4 && TT_V == 4 && TT_V16 == 4 && TT_GROUP == 4, "barriers are set up in one loop");
+  if (tid < 4) {
+    const int i = tid, g = i & 1, j = i >> 1;
+    mbar_init(&bar.k_full[i], 1), mbar_init(&bar.k_empty[i], 1), mbar_init(&bar.v_full[i], 1), mbar_init(&bar.v_empty[i], 4);
+    mbar_init(&bar.v16_full[i], 4), mbar_init(&bar.v16_empty[i], 1);
+    mbar_init(&bar.gr_full[0][i], 1), mbar_init(&bar.gr_full[1][i], 1), mbar_init(&bar.gr_empty[0][i], 4), mbar_init(&bar.gr_empty[1][i], 4);
+    mbar_init(&bar.s_full[g][j], 1), mbar_init(&bar.p_full[g][j], 4), mbar_init(&bar.o_done[g][j], 1);
+    if (j == 0) mbar_init(&bar.q_full[g], 4), mbar_init(&bar.q_empty[g], 1);
+    if (i == 0) mbar_init(&bar.swap_in, 8), mbar_init(&bar.swap_out, 8), mbar_init(&bar.drain, 2);
+    fence_mbar_init();
   }
-  fence_mbar_init();
-  if (warp == W_TREE_MMA) {
+  if (warp == W_S) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_s)), "n"(COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -299,47 +523,47 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   const uint32_t tmem = tmem_s;
   pdl_wait();
 
-  // this CTA's share: costs lo .. hi
-  const long long total = plan_pass(a, plan, -1);
-  // No share is shorter than the step from a unit's first block to its second: every CTA between those of a unit's first and
-  // last block then holds a block of it.
-  const long long most = total / (COST_UNIT + COST_TWO);
-  const long long ctas = most < 1 ? 1 : most < (long long)gridDim.x ? most : (long long)gridDim.x;
-  auto share = [&](long long c) { return total * c / ctas; };
-  const bool works = blockIdx.x < ctas;
-  const long long lo = works ? share(blockIdx.x) : 0, hi = works ? share(blockIdx.x + 1) : 0;
-  if (works) plan_pass(a, plan, lo);
-
-  bool ok = true;   // no wait of this thread has given up
-  auto wait = [&](uint64_t* bar, int phase) {
-    if (ok && (PATIENT ? !try_wait_ms(bar, phase & 1) && !wait_long(bar, phase & 1) : !mbar_wait_bounded(bar, phase & 1, a.wait))) {
-      ok = false;
-      set_err(a.err, BRE_DEVERR_TIMEOUT);
-    }
-    return ok;
-  };
-  auto warp_wait = [&](uint64_t* bar, int phase) { return ok = __all_sync(0xffffffffu, wait(bar, phase)); };
+  make_plan(a, plan);
+  const bool works = plan.lo < plan.hi;
+  Waits<PATIENT> wait{PATIENT ? TRIES : (int)min(max(a.wait / 32, 1LL), (long long)INT32_MAX)};
 
   if (!works) {
     if (tid == 0) a.join[blockIdx.x].parts = 0;
   } else if (warp == W_LOAD) {
     // ---- walk: tiles from plan.found on, kv heads, blocks
+    const int per_one = 128 / a.G;
     int it = 0, kb = 0;
     Join join{0, 0, 0, 0};
-    auto publish = [&](const Item& x) {
-      if (!warp_wait(&it_empty[it % TT_RING], it / TT_RING + 1)) return false;
-      if (lane == 0) {
-        ring[it % TT_RING] = x;
-        mbar_arrive(&it_full[it % TT_RING]);
+    // to the S warp and to the converting warps; page < 0: nothing to copy
+    auto publish = [&](const Item& x, int page) {
+      const int st = it & 3;
+      wait(&bar.k_empty[st], (it >> 2) + 1);
+      wait(&bar.v_empty[st], (it >> 2) + 1);
+      if (wait.left && lane == 0) {
+        to_s[st] = x.flags;
+        to_v[st] = x;
+        if (page >= 0) {
+          const long long ph = (long long)page * a.H + x.h;
+          mbar_arrive_expect_tx(&bar.k_full[st], M::K);
+          tma_load_3d(sm + M::k + st * M::K, &key_map, 0, 0, (int)ph, &bar.k_full[st]);
+          mbar_arrive_expect_tx(&bar.v_full[st], M::V);
+          bulk_g2s(sm + M::v + st * M::V, a.pages + ph * kv_page_bytes(D) + KV_BLOCK * D, M::V, &bar.v_full[st]);
+        } else {
+          mbar_arrive(&bar.k_full[st]);
+          mbar_arrive(&bar.v_full[st]);
+        }
       }
-      ++it;
-      return true;
+      __syncwarp();
+      if (wait.left) ++it;
     };
+    const long long lo = plan.lo, hi = plan.hi, share = plan.per;
     long long at = plan.found_at;
-    for (int t0 = plan.found; t0 < a.T && at < hi && ok;) {
+#pragma unroll 1
+    for (int t0 = plan.found; t0 < a.T && at < hi && wait.left;) {
       // the tile: tokens in a row of one run; their number, largest and smallest position
       const int s = __ldg(a.seq + t0), p0 = __ldg(a.pos + t0);
       int n = 0, top = INT32_MIN, low = INT32_MAX;
+#pragma unroll 1
       for (int i = 0; i < a.per; i += 32) {
         const int t = t0 + i + lane;
         const bool in = i + lane < a.per && t < a.T;
@@ -354,7 +578,10 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       const Unit unit(n, top, a.tab.N, per_one);
       const int begin = a.start && (unsigned)s < (unsigned)a.tab.B ? max(__ldg(a.start + s), 0) : 0;
       const int two = n > per_one ? F_TWO : 0;
-      for (int h = 0; h < a.H && ok; ++h, at += unit.cost()) {
+      // blocks below this one are seen as a whole by all rows
+      const int whole = (int)(min((long long)low + 1, a.mask ? (long long)begin : (long long)low + 1) / KV_BLOCK);
+#pragma unroll 1
+      for (int h = 0; h < a.H && wait.left; ++h, at += unit.cost()) {
         if (at + unit.cost() <= lo) continue;
         if (at >= hi) break;
         const int b0 = unit.first_from(lo - at), b1 = unit.first_from(hi - at);
@@ -364,483 +591,392 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
           slot = 2 * blockIdx.x;
         } else if (b1 < unit.blocks) {
           slot = 2 * blockIdx.x + 1;
-          // the CTA that holds the unit's last block
-          const long long x = at + unit.at(unit.blocks - 1);
-          long long c = x * ctas / total;
-          while (c + 1 < ctas && share(c + 1) <= x) ++c;
-          while (c > 0 && share(c) > x) --c;
-          join = Join{t0, n, h, (int)c - (int)blockIdx.x + 1};
+          // up to the CTA that holds the unit's last block
+          join = Join{t0, n, h, (int)quotient(at + unit.at(unit.blocks - 1), share) - (int)blockIdx.x + 1};
         }
         if (top >= 0 && top / KV_BLOCK >= a.tab.N && b0 == 0 && lane == 0) set_err(a.err, BRE_DEVERR_PAGE);
-        int some = 0;
-        for (int g = b0; g < b1 && top >= 0 && ok; g += 32) {
+        int jb = 0;
+#pragma unroll 1
+        for (int g = b0; g < b1 && top >= 0 && wait.left; g += 32) {
           const int my = g + lane < b1 ? kv_page(a.tab, s, g + lane, a.err) : -1;
-          for (uint32_t todo = __ballot_sync(0xffffffffu, my >= 0); todo && ok; todo &= todo - 1) {
-            const int src = __ffs(todo) - 1, page = __shfl_sync(0xffffffffu, my, src), blk = g + src;
-            const long long x1 = (long long)blk * KV_BLOCK + KV_BLOCK - 1;
-            const bool full = x1 <= low && (!a.mask || x1 < begin);
-            const int ks = kb % TT_K, vs = kb % TT_V;
-            if (!warp_wait(&k_empty[ks], kb / TT_K + 1) || !warp_wait(&v_empty[vs], kb / TT_V + 1)) break;
-            if (lane == 0) {
-              const long long ph = (long long)page * a.H + h;
-              mbar_arrive_expect_tx(&k_full[ks], M::K);
-              tma_load_3d(sm + M::k + ks * M::K, &key_map, 0, 0, (int)ph, &k_full[ks]);
-              mbar_arrive_expect_tx(&v_full[vs], M::V);
-              bulk_g2s(sm + M::v + vs * M::V, a.pages + ph * kv_page_bytes(D) + KV_BLOCK * D, M::V, &v_full[vs]);
-            }
-            ++kb;
-            if (!publish(Item{t0, n, h, blk, F_BLOCK | (some ? 0 : F_FIRST) | (full ? F_FULL : 0) | two, slot, begin, 0})) break;
-            some = F_SOME;
+#pragma unroll 1
+          for (uint32_t todo = __ballot_sync(0xffffffffu, my >= 0); todo && wait.left; todo &= todo - 1) {
+            const int src = __ffs(todo) - 1, blk = g + src;
+            const int flags = F_BLOCK | (jb ? 0 : F_FIRST) | (blk < whole ? F_FULL : 0) | two | (jb & 1 ? F_ODD : 0) |
+                              (jb < (two ? 1 : 2) ? F_NEW : 0);
+            publish(Item{t0, n, h, blk, flags, slot, begin, kb}, __shfl_sync(0xffffffffu, my, src));
+            ++kb, ++jb;
           }
         }
-        if (ok) publish(Item{t0, n, h, 0, F_END | two | some, slot, begin, 0});
+        publish(Item{t0, n, h, jb, F_END | two | (jb ? F_SOME : 0), slot, begin, kb}, -1);
       }
       t0 += n;
     }
-    if (ok) publish(Item{0, 0, 0, 0, F_EXIT, -1, 0, 0});
+    publish(Item{0, 0, 0, 0, F_EXIT, -1, 0, 0}, -1);
     if (lane == 0) a.join[blockIdx.x] = join;
-    if (!ok) {   // copies that are on their way still write to this CTA's shared memory
-      for (int i = max(0, kb - TT_K); i < kb; ++i) mbar_wait_bounded(&k_full[i % TT_K], i / TT_K & 1, AT_WAIT);
-      for (int i = max(0, kb - TT_V); i < kb; ++i) mbar_wait_bounded(&v_full[i % TT_V], i / TT_V & 1, AT_WAIT);
-    }
-  } else if (warp == W_TREE_MMA) {
-    // ---- MMA.  S of a block is formed up to two products ahead of its P V.
-    const uint32_t id_s = (1u << 4) | ((uint32_t)(KV_BLOCK >> 3) << 17) | ((128u >> 4) << 24);   // E4M3, FP32 sums, M = 128
-    const uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);   // FP16; V is MN-major
+    if (!wait.left)   // copies that are on their way still write to this CTA's shared memory
+      for (int i = max(0, it - 4); i < it; ++i) {
+        mbar_wait_bounded(&bar.k_full[i & 3], i >> 2 & 1, AT_WAIT);
+        mbar_wait_bounded(&bar.v_full[i & 3], i >> 2 & 1, AT_WAIT);
+      }
+  } else if (warp == W_S) {
+    // ---- S = Q K^T: E4M3 operands, FP32 sums, M = 128
+    const uint32_t id_s = (1u << 4) | ((uint32_t)(KV_BLOCK >> 3) << 17) | ((128u >> 4) << 24);
     const uint64_t q0 = desc_codes<D>(smem_u32(sm + M::q)), k0 = desc_codes<D>(smem_u32(sm + M::k));
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    int live = 0, qb = 0;           // the unit's query buffers; the next one-tile unit's buffer
+    Pair cs{0, 0}, uses{0, 0};      // S of either group, units of either query buffer so far
+#pragma unroll 1
+    for (int it = 0;; ++it) {
+      const int ks = it & 3;
+      wait(&bar.k_full[ks], it >> 2);
+      if (!wait.left) break;
+      // (a warp reduction: what the MMAs' operands are formed from is then in uniform registers, where they want it)
+      const int flags = (int)__reduce_or_sync(0xffffffffu, (uint32_t)to_s[ks]), two = flags & F_TWO ? 1 : 0;
+      if (!(flags & F_BLOCK)) {
+        if (flags & F_EXIT) break;
+        if (elect_one()) {
+          if (flags & F_SOME && live & 1) mma_commit(&bar.q_empty[0]);
+          if (flags & F_SOME && live & 2) mma_commit(&bar.q_empty[1]);
+          mbar_arrive(&bar.k_empty[ks]);
+        }
+        __syncwarp();
+        if (flags & F_SOME) {
+          uses.a += live & 1, uses.b += live >> 1;
+          if (!two) qb ^= 1;
+        }
+        continue;
+      }
+      if (flags & F_FIRST) {
+        live = two ? 3 : 1 << qb;
+        if (live & 1) wait(&bar.q_full[0], uses.a);
+        if (live & 2) wait(&bar.q_full[1], uses.b);
+      }
+#pragma unroll 1
+      for (int g = 0; g <= two; ++g) {
+        const int w = two ? g : flags & F_ODD ? 1 : 0, qt = two ? g : qb, c = cs[w], buf = c & 1;
+        wait(&bar.o_done[w][buf], (c >> 1) + 1);   // the weights that lay in S's columns have been used
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t st = tm + w * 128 + buf * 64;
+          const uint64_t qd = q0 + ((qt * 2 * M::TERM) >> 4), kd = k0 + ((ks * M::K) >> 4);
+#pragma unroll
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              mma_codes(st, qd + ((term * M::TERM + kk * 32) >> 4), kd + ((kk * 32) >> 4), id_s, term + kk > 0);
+          mma_commit(&bar.s_full[w][buf]);
+          if (g == two) mma_commit(&bar.k_empty[ks]);
+        }
+        __syncwarp();
+        cs.add(w);
+      }
+    }
+    // products that are under way still use tensor and shared memory
+    if (elect_one()) mma_commit(&bar.drain);
+    __syncwarp();
+  } else if (warp == W_O) {
+    // ---- O += P V: FP16 operands, P from tensor memory, V MN-major
+    const uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
     const uint64_t v0 = desc_mn_major(smem_u32(sm + M::v16), PANEL);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    int kb = 0, vb = 0;            // blocks whose S, whose last P V have been issued
-    int cs[2] = {0, 0}, cp[2] = {0, 0};   // S and P V of either group so far
-    int started[2] = {0, 0};       // products P V of this unit
-    int qb = 0, uses[2] = {0, 0};  // the next one-tile unit's query buffer; uses of the buffers
-    int queue = 0, queued = 0;     // groups (and whether they are a block's last) that wait for their P V: two bits each
-    auto pv = [&]() {
-      const int w = queue & 1, last = queue >> 1 & 1;
-      queue >>= 2, --queued;
-      const int buf = cp[w] & 1, st = vb % TT_V16;
-      if (!warp_wait(&v16_full[st], vb / TT_V16) || !warp_wait(&p_full[w][buf], cp[w] >> 1)) return;
-      tc_fence_after();
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < KV_BLOCK / 16; ++kk)
-          mma_ts(tm + 256 + w * 128, tm + w * 128 + buf * 64 + kk * 8, v0 + ((st * M::V16 + kk * 2048) >> 4), id_o,
-                 kk > 0 ? 1u : started[w] > 0);
-        mma_commit(&o_done[w]);
-        if (last) mma_commit(&v16_empty[st]);
-      }
-      __syncwarp();
-      ++cp[w], started[w] = 1;
-      if (last) ++vb;
-    };
-    int jb = 0, live = 0;          // blocks of this unit; query buffers that it uses
-    int base[2] = {0, 0}, segs = 0;   // S of either group before this unit; units that had blocks
+    Pair cp{0, 0};
 #pragma unroll 1
-    for (int it = 0; ok; ++it) {
-      if (!warp_wait(&it_full[it % TT_RING], it / TT_RING)) break;
-      const int flags = ring[it % TT_RING].flags;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&it_empty[it % TT_RING]);
+    for (int kb = 0;; ++kb) {
+      const int st = kb & 3;
+      wait(&bar.v16_full[st], kb >> 2);
+      if (!wait.left) break;
+      const int flags = (int)__reduce_or_sync(0xffffffffu, (uint32_t)to_o[st]), two = flags & F_TWO ? 1 : 0;
       if (flags & F_EXIT) break;
-      if (flags & F_BLOCK) {
-        if (flags & F_FIRST) {
-          jb = 0, live = flags & F_TWO ? 3 : 1 << qb;
-          for (int i = 0; i < 2; ++i)
-            if (live >> i & 1) warp_wait(&q_full[i], uses[i]);
-        }
-        const int ks = kb % TT_K;
-        if (!warp_wait(&k_full[ks], kb / TT_K)) break;
-        for (int g = 0; g < (flags & F_TWO ? 2 : 1); ++g) {
-          const int w = flags & F_TWO ? g : jb & 1, qt = flags & F_TWO ? g : qb, buf = cs[w] & 1;
-          // the weights that lay in S's columns must have been used (P V of the group's product before the last)
-          if (cs[w] - base[w] > 1 && !warp_wait(&o_done[w], cs[w] - 2)) break;
-          tc_fence_after();
-          if (elect_one()) {
+#pragma unroll 1
+      for (int g = 0; g <= two; ++g) {
+        const int w = two ? g : flags & F_ODD ? 1 : 0, c = cp[w], buf = c & 1;
+        wait(&bar.p_full[w][buf], c >> 1);
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t o = tm + 256 + w * 128, pt = tm + w * 128 + buf * 64, more = flags & F_NEW ? 0u : 1u;
+          const uint64_t vd = v0 + ((st * M::V16) >> 4);
 #pragma unroll
-            for (int term = 0; term < 2; ++term)
-#pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)
-                mma_codes(tm + w * 128 + buf * 64, q0 + (((qt * 2 + term) * M::TERM + kk * 32) >> 4),
-                          k0 + ((ks * M::K + kk * 32) >> 4), id_s, term + kk > 0);
-            mma_commit(&s_full[w][buf]);
-            if (!(flags & F_TWO) || g) mma_commit(&k_empty[ks]);
-          }
-          __syncwarp();
-          ++cs[w];
-          queue |= (w | (!(flags & F_TWO) || g ? 2 : 0)) << (2 * queued++);
-          if (queued > 2) pv();
+          for (int kk = 0; kk < KV_BLOCK / 16; ++kk) mma_ts(o, pt + kk * 8, vd + ((kk * 2048) >> 4), id_o, kk > 0 ? 1u : more);
+          mma_commit(&bar.o_done[w][buf]);
+          if (g == two) mma_commit(&bar.v16_empty[st]);
         }
-        ++kb, ++jb;
-      }
-      if (flags & F_END) {
-        while (queued && ok) pv();
-        started[0] = started[1] = 0;
-        if (flags & F_SOME) {
-          if (elect_one()) {
-            mma_commit(&seg_done);
-            for (int i = 0; i < 2; ++i)
-              if (live >> i & 1) mma_commit(&q_empty[i]);
-          }
-          __syncwarp();
-          // all of the unit's products have completed before the next one's begin: a wait for a product is then never
-          // two phases from its barrier's state
-          if (!warp_wait(&seg_done, segs)) break;
-          ++segs;
-          for (int i = 0; i < 2; ++i) uses[i] += live >> i & 1, base[i] = cs[i];
-          if (!(flags & F_TWO)) qb ^= 1;
-        }
+        __syncwarp();
+        cp.add(w);
       }
     }
-    if (!ok) {   // products that are under way still use tensor and shared memory
-      if (elect_one()) mma_commit(&drain);
-      __syncwarp();
-      mbar_wait_bounded(&drain, 0, AT_WAIT);
-    }
-  } else if (warp >= W_CONV && warp < W_LOAD) {
+    if (elect_one()) mma_commit(&bar.drain);
+    __syncwarp();
+  } else if (warp >= W_CONV) {
     // ---- queries to two terms; codes of values to FP16
     constexpr int CH = D / 16, NP = KV_BLOCK * CH / 128;   // 16-code pieces of a row, pieces a thread
     const int cw = warp - W_CONV, dt = cw * 32 + lane;
-    int kb = 0, qb = 0, uses[2] = {0, 0}, last = 0;
+    // where a thread's pieces go: two swizzled ones of 16 bytes each; the lanes of odd panels start with the second, so that
+    // eight lanes meet all banks.  (The rows of a thread are whole multiples of 8 apart.)
+    const int c = dt % CH, x0 = dt / CH;
+    const bool second = (c / 4) & 1;
+    const int o0 = (c / 4) * PANEL + x0 * 128 + (((2 * (c % 4)) ^ (x0 & 7)) << 4), first = second ? o0 ^ 16 : o0;
+    int qb = 0, units = 0, last = 0, kb = 0;
+    Pair uses{0, 0}, gr{0, 0};
 #pragma unroll 1
-    for (int it = 0; ok; ++it) {
-      const int slot = it % TT_RING;
-      if (!warp_wait(&it_full[slot], it / TT_RING)) break;
-      const Item x = ring[slot];
-      if (x.flags & F_EXIT) break;
-      if (x.flags & F_FIRST) {
-        // rows of up to two tiles; the buffers are free when the S of their former unit have been formed
-        last = x.flags & F_TWO ? 3 : 1 << qb;
-        for (int i = 0; i < 2; ++i)
-          if (last >> i & 1) warp_wait(&q_empty[i], uses[i] + 1);
-        if (!ok) break;
-        constexpr int CL = D / 32, UN = 8;   // channels a lane, rows of a warp in flight
-        const int rows = x.n * a.G;
+    for (int it = 0;; ++it) {
+      const int vs = it & 3;
+      wait(&bar.v_full[vs], it >> 2);
+      if (!wait.left) break;
+      const int flags = to_v[vs].flags, two = flags & F_TWO;
+      // the groups that hear of it
+      const int who = !(flags & F_BLOCK) || two ? 3 : flags & F_ODD ? 2 : 1;
+      auto tell = [&]() {   // by one warp
 #pragma unroll 1
-        for (int r0 = cw; r0 < rows; r0 += 4 * UN) {
-          uint32_t w[UN][CL / 2];
-#pragma unroll
-          for (int j = 0; j < UN; ++j) {
-            const int r = r0 + 4 * j, tl = r / a.G;
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + (long long)(x.t0 + tl) * a.q_stride +
-                                                                    (size_t)(x.h * a.G + r - tl * a.G) * D) + lane * (CL / 2);
-#pragma unroll
-            for (int i = 0; i < CL / 2; ++i) w[j][i] = r < rows ? __ldg(src + i) : 0u;
-          }
-#pragma unroll
-          for (int j = 0; j < UN; ++j) {
-            const int r = r0 + 4 * j;
-            if (r >= rows) break;
-            uint32_t mx = 0;
-#pragma unroll
-            for (int i = 0; i < CL / 2; ++i) mx = __vmaxu2(mx, w[j][i] & 0x7FFF7FFFu);
-            mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
-            // least e with max|q| <= 448 * 2^e
-            const int bits = (int)(min(mx, 0x7F7Fu) << 16);
-            const int e = max((bits >> 23) - 127 - 8 + ((bits & 0x7FFFFF) > 0x600000 ? 1 : 0), -118);
-            const float down = pow2f(-e);
-            uint32_t hi = 0, rest = 0;
-#pragma unroll
-            for (int i = 0; i < CL / 2; ++i) {
-              const float u = __uint_as_float(w[j][i] << 16) * down, v = __uint_as_float(w[j][i] & 0xFFFF0000u) * down;
-              const uint32_t c = e4m3x2(u, v);
-              const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(c));
-              hi |= c << (16 * i);
-              rest |= e4m3x2(u - f.x, v - f.y) << (16 * i);
-            }
-            // tile and row in it: a tile holds whole tokens
-            const int tile = r >= per_one * a.G, rr = r - tile * per_one * a.G, buf = x.flags & F_TWO ? tile : qb;
-            unsigned char* dst = sm + M::q + buf * 2 * M::TERM + swizzled<D>(rr, lane * CL / 16) + lane * CL % 16;
-            if constexpr (CL == 4) {
-              *reinterpret_cast<uint32_t*>(dst) = hi;
-              *reinterpret_cast<uint32_t*>(dst + M::TERM) = rest;
-            } else {
-              *reinterpret_cast<uint16_t*>(dst) = (uint16_t)hi;
-              *reinterpret_cast<uint16_t*>(dst + M::TERM) = (uint16_t)rest;
-            }
-            if (lane == 0) q_factor[buf][rr] = mx > 0x7F7Fu ? __int_as_float(0x7FC00000) : a.scale * LOG2E * pow2f(e);
+        for (int g = 0; g < 2; ++g) {
+          if (!(who >> g & 1)) continue;
+          const int n = gr[g];
+          wait(&bar.gr_empty[g][n & 3], (n >> 2) + 1);
+          if (!wait.left) break;
+          if (lane == 0) {
+            group[g][n & 3] = to_v[vs];
+            mbar_arrive(&bar.gr_full[g][n & 3]);
           }
         }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0)
-          for (int i = 0; i < 2; ++i)
-            if (last >> i & 1) mbar_arrive(&q_full[i]);
-      }
-      if (x.flags & F_BLOCK) {
-        const int vs = kb % TT_V, st = kb % TT_V16;
+      };
+      if (flags & F_BLOCK) {
+        if (flags & F_FIRST) {
+          // rows of up to two tiles; the buffers are free when the S of their former unit have been formed
+          last = two ? 3 : 1 << qb;
+          if (last & 1) wait(&bar.q_empty[0], uses.a + 1);
+          if (last & 2) wait(&bar.q_empty[1], uses.b + 1);
+          load_queries<D>(a, to_v[vs], sm + M::q, two ? 0 : qb, &q_factor[units % TT_QF][0][0]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (last & 1) mbar_arrive(&bar.q_full[0]);
+            if (last & 2) mbar_arrive(&bar.q_full[1]);
+          }
+        }
+        const int st = kb & 3, sp = kb % TT_SC;
         // slots that some row sees (others may never have been written: their values become zeros)
         uint64_t seen = ~0ull;
-        if (!(x.flags & F_FULL)) {
-          seen = 0;
-          for (int i = lane; i < x.n; i += 32)
-            seen |= seen_bits(a.mask ? a.mask + (size_t)(x.t0 + i) * a.words : nullptr, a.words, x.begin, __ldg(a.pos + x.t0 + i), x.blk);
-          seen = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(seen >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)seen);
-        }
-        if (!warp_wait(&v_full[vs], kb / TT_V)) break;
+        if (!(flags & F_FULL)) seen = seen_by_some(a, to_v[vs]);
         const unsigned char* raw = sm + M::v + vs * M::V;
-        if (kb % 4 == cw) {   // this block's scales
-          bool over = false;
+        const uint8_t* scales = raw + KV_BLOCK * D;
+        // the largest scale of the block's values (of a NaN row and of one that no row sees: does not count)
+        const int e0 = scales[KV_BLOCK + lane], e1 = scales[KV_BLOCK + 32 + lane];
+        const int c0 = e0 == KV_NAN || !((uint32_t)seen >> lane & 1u) ? 0 : e0;
+        const int c1 = e1 == KV_NAN || !((uint32_t)(seen >> 32) >> lane & 1u) ? 0 : e1;
+        const int top = max(__reduce_max_sync(0xffffffffu, max(c0, c1)), 1);
+        const int least = __reduce_min_sync(0xffffffffu, min(c0 ? c0 : 255, c1 ? c1 : 255));
+        bool careful = top > EV_LARGE;
+        if (top - least > 15) careful |= far_below<D>(raw, c0, c1, top);
+        if ((kb & 3) == cw) {   // this block's scales for the softmax
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int c = lane + 32 * i, ek = raw[KV_BLOCK * D + c], ev = raw[KV_BLOCK * D + KV_BLOCK + c];
-            kf[slot][c] = pow2f(min(ek, 253) - 127);
-            ev_f[slot][c] = ek == KV_NAN || ev == KV_NAN ? __int_as_float(0x7FC00000) : (float)(ev - 127);
-            ev_inv[slot][c] = pow2f(127 - min(ev, 253));
-            over |= ev > EV_LARGE && (seen >> c & 1ull);
+            const int x = lane + 32 * i, ek = scales[x], ev = i ? e1 : e0;
+            kf[sp][x] = ek == KV_NAN || ev == KV_NAN ? __int_as_float(0x7FC00000) : pow2f(ek - 127);
+            ev_f[sp][x] = (float)((careful ? ev : top) - 127);
           }
-          over = __any_sync(0xffffffffu, over);
-          if (lane == 0) large[slot] = over;
+          if (lane == 0) ev_top[sp] = careful ? __int_as_float(0x7FC00000) : (float)(top - 127);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sc_full[slot]);
+          tell();
         }
         uint4 cur[NP];
+        uint32_t up[NP];   // 2^(the row's scale - the largest), at least 2^-15
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          const int x0 = (dt + j * 128) / CH;
-          cur[j] = seen >> x0 & 1ull ? reinterpret_cast<const uint4*>(raw)[dt + j * 128] : make_uint4(0, 0, 0, 0);
+          cur[j] = reinterpret_cast<const uint4*>(raw)[dt + j * 128];
+          const int d = min(max(top - (int)scales[KV_BLOCK + x0 + j * (128 / CH)], 0), 15);
+          up[j] = careful ? 0x3C003C00u : (d < 15 ? (uint32_t)(15 - d) << 10 : 1u << 9) * 0x10001u;
         }
-        if (!warp_wait(&v16_empty[st], kb / TT_V16 + 1)) break;
-        // two swizzled pieces of 16 bytes; the lanes of odd panels start with the second, so that eight lanes meet all banks
-        const int c = dt % CH;
-        const bool second = (c / 4) & 1;
+        if (!(flags & F_FULL)) {
+#pragma unroll
+          for (int j = 0; j < NP; ++j)
+            if (!(seen >> (x0 + j * (128 / CH)) & 1ull)) cur[j] = make_uint4(0, 0, 0, 0);
+        }
+        wait(&bar.v16_empty[st], (kb >> 2) + 1);
+        unsigned char* const to = sm + M::v16 + st * M::V16 + first;
+        const int other = first & 16 ? -16 : 16;
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          const int x0 = (dt + j * 128) / CH;
-          const int p0 = M::v16 + st * M::V16 + (c / 4) * PANEL + x0 * 128 + (((2 * (c % 4)) ^ (x0 & 7)) << 4);
           const uint32_t u[4] = {second ? cur[j].z : cur[j].x, second ? cur[j].w : cur[j].y, second ? cur[j].x : cur[j].z,
                                  second ? cur[j].y : cur[j].w};
           uint32_t o[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            o[2 * k] = e4m3x2_to_f16x2(u[k] & 0xFFFFu);
-            o[2 * k + 1] = e4m3x2_to_f16x2(u[k] >> 16);
+            o[2 * k] = mul_f16x2(e4m3x2_to_f16x2(u[k] & 0xFFFFu), up[j]);
+            o[2 * k + 1] = mul_f16x2(e4m3x2_to_f16x2(u[k] >> 16), up[j]);
           }
-          *reinterpret_cast<uint4*>(sm + (second ? p0 ^ 16 : p0)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(sm + (second ? p0 : p0 ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+          *reinterpret_cast<uint4*>(to + j * (128 / CH) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(to + j * (128 / CH) * 128 + other) = make_uint4(o[4], o[5], o[6], o[7]);
         }
         fence_proxy_async_smem();
+        if (dt == 0) to_o[st] = flags;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&v16_full[st]), mbar_arrive(&v_empty[vs]);
+        if (lane == 0) mbar_arrive(&bar.v16_full[st]);
         ++kb;
+      } else {
+        if (cw == 0) tell();
+        if (flags & F_EXIT) {
+          const int st = kb & 3;
+          wait(&bar.v16_empty[st], (kb >> 2) + 1);
+          if (dt == 0) to_o[st] = F_EXIT;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.v16_full[st]);
+          break;
+        }
+        if (flags & F_SOME) {
+          ++units, uses.a += last & 1, uses.b += last >> 1;
+          if (!two) qb ^= 1;
+        }
       }
-      if (x.flags & F_END && cw == 0 && lane == 0) mbar_arrive(&sc_full[slot]);   // (one arrival for each use of a slot)
-      if (x.flags & F_END && x.flags & F_SOME) {
-        for (int i = 0; i < 2; ++i) uses[i] += last >> i & 1;
-        if (!(x.flags & F_TWO)) qb ^= 1;
-      }
+      gr.a += who & 1, gr.b += who >> 1;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&it_empty[slot]);
+      if (lane == 0) mbar_arrive(&bar.v_empty[vs]);
     }
-  } else if (warp < W_CONV) {
+  } else {
     // ---- softmax: row r of group w
     const int w = warp >> 2, r = tid & 127;
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);   // lanes 32 (warp % 4) ..
-    const uint32_t O = lane_base + 256 + w * 128;
-    int qb = 0, done = 0, segs = 0;   // products of this group; units that had blocks
-    float m = -INFINITY, l = 0.0f, f = 0.0f;
-    int jb = 0, mine = 0, pos = -1;   // blocks of this unit, those of this group; the row's position
+    int units = 0, swaps = 0, done = 0, mine = 0;   // units that had blocks, of one tile; products of the group, of this unit
+    float m = -INFINITY, l = 0.0f, f = 0.0f;        // m: the maximum that the weights are held against
     int tl = 0;
-    bool live = false, warp_live = false;
+    bool warp_live = false;
 #pragma unroll 1
-    for (int it = 0; ok; ++it) {
-      const int slot = it % TT_RING;
-      if (!warp_wait(&it_full[slot], it / TT_RING)) break;
-      const int flags = ring[slot].flags;
-      if (flags & F_EXIT) break;
-      if (flags & F_FIRST) jb = 0;
-      if (flags & F_BLOCK && (flags & F_TWO || (jb & 1) == w)) {
-        const int buf = done & 1;
+    for (int it = 0;; ++it) {
+      wait(&bar.gr_full[w][it & 3], it >> 2);
+      if (!wait.left) break;
+      const Item& x = group[w][it & 3];
+      const int flags = x.flags;
+      if (flags & F_BLOCK) {
+        const int buf = done & 1, sp = x.kb % TT_SC;
         const uint32_t S = lane_base + w * 128 + buf * 64;
-        if (mine == 0) {
-          const int tr = r / a.G;
+        if (flags & F_NEW) {
+          const int per_one = 128 / a.G, tr = r / a.G;
           tl = (flags & F_TWO ? w * per_one : 0) + tr;
-          live = tr < per_one && tl < ring[slot].n;
-          pos = live ? __ldg(a.pos + ring[slot].t0 + tl) : -1;
+          const bool live = tr < per_one && tl < x.n;
+          if (!live) tl = -1;
           warp_live = __any_sync(0xffffffffu, live);
         }
-        if (!warp_wait(&sc_full[slot], it / TT_RING)) break;
-        if (!warp_wait(&s_full[w][buf], done >> 1)) break;
+        wait(&bar.s_full[w][buf], done >> 1);
         tc_fence_after();
-        if (mine == 0) f = q_factor[flags & F_TWO ? w : qb][r];
+        // (S has been formed from the queries, so all of their factors are there; what comes of other rows does not matter)
+        if (flags & F_NEW) f = tl >= 0 ? q_factor[units % TT_QF][flags & F_TWO ? w : 0][r] : 0.0f;
         if (warp_live) {
-          uint32_t s[64];
-          tmem_ld32(S, s);
-          tmem_ld32(S + 32, s + 32);
-          uint64_t seen = live ? ~0ull : 0ull;
-          if (!(flags & F_FULL) && live)
-            seen = seen_bits(a.mask ? a.mask + (size_t)(ring[slot].t0 + tl) * a.words : nullptr, a.words, ring[slot].begin, pos,
-                             ring[slot].blk);
-          const uint64_t f2 = pack2(f, f);
-          tmem_wait_ld();
-          float mx = -INFINITY;
+          const float top = ev_top[sp];
+          if (flags & F_FULL && top == top) {
+            // the ordinary way: every row sees the whole block, and the block's values have one scale
+            uint32_t s[64];   // S, then S times the keys' scales
+            tmem_ld32(S, s);
+            tmem_ld32(S + 32, s + 32);
+            tmem_wait_ld();
+            float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
-          for (int x = 0; x < 64; x += 4) {
-            const ulonglong2 kk = *reinterpret_cast<const ulonglong2*>(&kf[slot][x]);
-            const ulonglong2 ev = *reinterpret_cast<const ulonglong2*>(&ev_f[slot][x]);
-            const float2 v0 = unpack2(fma2(mul2(pack2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), kk.x), f2, ev.x));
-            const float2 v1 = unpack2(fma2(mul2(pack2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), kk.y), f2, ev.y));
-            s[x] = __float_as_uint(v0.x), s[x + 1] = __float_as_uint(v0.y);
-            s[x + 2] = __float_as_uint(v1.x), s[x + 3] = __float_as_uint(v1.y);
-          }
-          if (!(flags & F_FULL)) {
-#pragma unroll
-            for (int x = 0; x < 64; ++x)
-              if (!(seen >> x & 1ull)) s[x] = __float_as_uint(-INFINITY);
-          }
-#pragma unroll
-          for (int x = 0; x < 64; x += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 1])));
-          if (!live) mx = -INFINITY;
-          if (m == -INFINITY) m = mx;   // nothing has been added for this row yet
-          if (__any_sync(0xffffffffu, mx > m + TT_SLACK)) {
-            // some row's weights would outgrow FP16: all rows of the warp take their new maximum.  (P V of the product
-            // before the last has completed: S of this one was formed after it.)
-            if (mine > 0 && !warp_wait(&o_done[w], done - 1)) break;
-            tc_fence_after();
-            const float nm = fmaxf(m, mx), d = m > -INFINITY ? m - nm : 0.0f, sc = ex2(d);
-            m = nm;
-            l = scale_sum(l, d);
-            if (mine > 0) {
+            for (int c = 0; c < 64; c += 4) {
+              const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&kf[sp][c]);
+              const float2 v0 = unpack2(mul2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), k.x));
+              const float2 v1 = unpack2(mul2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), k.y));
+              mx = max3(mx, v0.x, v0.y), my = max3(my, v1.x, v1.y);
+              s[c] = __float_as_uint(v0.x), s[c + 1] = __float_as_uint(v0.y);
+              s[c + 2] = __float_as_uint(v1.x), s[c + 3] = __float_as_uint(v1.y);
+            }
+            mx = fmaf(fmaxf(mx, my), f, top);   // (f is not negative; a query that gives NaN has a NaN maximum)
+            if (m == -INFINITY) m = mx;         // nothing has been added for this row yet
+            if (__builtin_expect(__any_sync(0xffffffffu, mx > m + TT_SLACK), 0)) {
+              // some row's weights would outgrow FP16: all rows of the warp take their new maximum
+              if (mine > 0) wait(&bar.o_done[w][buf ^ 1], (done - 1) >> 1);
+              tc_fence_after();
+              const float then = fmaxf(m, mx), d = m > -INFINITY ? m - then : 0.0f, sc = ex2(d);
+              l = scale_sum(l, d);
+              m = then;
+              if (mine > 0) {
+                const uint32_t O = lane_base + 256 + w * 128;
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                tmem_ld16(O + c, o);
-                tmem_wait_ld();
+                for (int c = 0; c < D; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(O + c, o);
+                  tmem_wait_ld();
 #pragma unroll
-                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * sc);
-                tmem_st16(O + c, o);
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sc);
+                  tmem_st16(O + c, o);
+                }
               }
             }
-          }
-          const float base = m > -INFINITY ? m - P_SHIFT : 0.0f;
-          if (large[slot]) l += careful_sum(S, kf[slot], ev_f[slot], f, base, seen);
-          const uint64_t nb2 = pack2(-base, -base);
-          uint64_t add = 0;
-          uint32_t pk[32];
+            const float add = top - (m > -INFINITY ? m - P_SHIFT : 0.0f);
+            const uint64_t f2 = pack2(f, f), add2 = pack2(add, add);
+            float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-          for (int x = 0; x < 64; x += 4) {
-            const ulonglong2 iv = *reinterpret_cast<const ulonglong2*>(&ev_inv[slot][x]);
-            const float2 v0 = unpack2(add2(pack2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), nb2));
-            const float2 v1 = unpack2(add2(pack2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), nb2));
-            const float p0 = ex2(v0.x), p1 = ex2(v0.y), p2 = ex2(v1.x), p3 = ex2(v1.y);
-            add = fma2(pack2(p0, p1), iv.x, fma2(pack2(p2, p3), iv.y, add));
-            pk[x / 2] = pack_f16x2(p0, p1), pk[x / 2 + 1] = pack_f16x2(p2, p3);
+            for (int half = 0; half < 64; half += 32) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                const float2 y = unpack2(fma2(pack2(__uint_as_float(s[half + c]), __uint_as_float(s[half + c + 1])), f2, add2));
+                const float p0 = ex2(y.x), p1 = ex2(y.y);
+                sum0 += p0, sum1 += p1;
+                pk[c / 2] = pack_f16x2(p0, p1);
+              }
+              tmem_st16(S + half / 2, pk);
+            }
+            l = fmaf(sum0 + sum1, ex2(-top), l);
+          } else {
+            const uint64_t seen = tl < 0 ? 0ull : flags & F_FULL ? ~0ull
+                : seen_bits(a.mask ? a.mask + (size_t)(x.t0 + tl) * a.words : nullptr, a.words, x.begin, __ldg(a.pos + x.t0 + tl), x.blk);
+            const float mx = careful_max(S, kf[sp], ev_f[sp], f, seen);
+            if (m == -INFINITY) m = mx;
+            if (__any_sync(0xffffffffu, mx > m + TT_SLACK)) {
+              if (mine > 0) wait(&bar.o_done[w][buf ^ 1], (done - 1) >> 1);
+              tc_fence_after();
+              const float then = fmaxf(m, mx), d = m > -INFINITY ? m - then : 0.0f;
+              l = scale_sum(l, d);
+              m = then;
+              if (mine > 0) rescale<D>(lane_base + 256 + w * 128, ex2(d));
+            }
+            l += careful_weights(S, kf[sp], ev_f[sp], f, m > -INFINITY ? m - P_SHIFT : 0.0f, seen);
           }
-          const float2 sum = unpack2(add);
-          if (!large[slot]) l += sum.x + sum.y;
-          tmem_st16(S, pk);
-          tmem_st16(S + 16, pk + 16);
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[w][buf]);
+        if (lane == 0) mbar_arrive(&bar.p_full[w][buf]), mbar_arrive(&bar.gr_empty[w][it & 3]);
         ++done, ++mine;
+        continue;
       }
-      if (flags & F_BLOCK) ++jb;
-      if (flags & F_END) {
-        const Item x = ring[slot];
-        const int count = x.n * a.G;
-        if (flags & F_SOME) {
-          if (!warp_wait(&seg_done, segs)) break;
-          tc_fence_after();
-        }
-        if (flags & F_TWO || !(flags & F_SOME)) {
-          // rows of its own; of a unit without blocks the first group answers for one tile
-          const int tr = r / a.G, row = (flags & F_TWO ? w * per_one : 0) * a.G + r;
-          const bool my = tr < per_one && row < count && (flags & F_TWO || w == 0);
-          const bool any = flags & F_SOME;
-          if (my && x.slot >= 0) a.ml[(size_t)x.slot * a.rows + row] = make_float2(any ? m : -INFINITY, any ? l : 0.0f);
-          const int tok = row / a.G;
-          const size_t at = ((size_t)(x.t0 + tok) * a.H + x.h) * a.G + (row - tok * a.G);
-          const float inv = 1.0f / l;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16], b[8];
-            if (any) {
-              tmem_ld16(O + c, o);
-              tmem_wait_ld();
-            }
-            if (!my) continue;
-            if (x.slot >= 0) {
-              float* dst = a.part + ((size_t)x.slot * a.rows + row) * D + c;
-#pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<uint4*>(dst + i) = any ? make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]) : make_uint4(0, 0, 0, 0);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                b[i] = !any || l == 0.0f ? 0u : pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-              st_v8(a.out + at * D + c, b);
-            }
-          }
-          if (my && x.slot < 0 && a.lse)
-            a.lse[at] = !any || l == 0.0f ? -INFINITY : LN2 * ((m > -INFINITY ? m - P_SHIFT : 0.0f) + log2f(l));
-        } else {
-          // the two groups have a part of every row each: either joins half of the channels
-          swap[w][r] = make_float2(m, l);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&swap_in);
-          if (!warp_wait(&swap_in, segs)) break;
-          const float2 y0 = swap[0][r], y1 = swap[1][r];
-          const bool both = jb > 1;   // else the second group has nothing, its O least of all
-          const float top = fmaxf(y0.x, y1.x), ref = top > -INFINITY ? top : 0.0f;
-          const float c0 = ex2(y0.x - ref), c1 = both ? ex2(y1.x - ref) : 0.0f;
-          const float sum = scale_sum(y0.y, y0.x - ref) + (both ? scale_sum(y1.y, y1.x - ref) : 0.0f);
-          const bool my = r < count;
-          if (my && x.slot >= 0 && w == 0) a.ml[(size_t)x.slot * a.rows + r] = make_float2(top, sum);
-          const int tok = r / a.G;
-          const size_t at = ((size_t)(x.t0 + tok) * a.H + x.h) * a.G + (r - tok * a.G);
-          const float inv = 1.0f / sum;
-          const bool warp_my = __any_sync(0xffffffffu, my);
-#pragma unroll 1
-          for (int c = w * (D / 2); warp_my && c < (w + 1) * (D / 2); c += 16) {
-            uint32_t o[16], o1[16], b[8];
-            tmem_ld16(lane_base + 256 + c, o);
-            if (both) tmem_ld16(lane_base + 384 + c, o1);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float v = __uint_as_float(o[i]) * c0;
-              if (both) v = fmaf(__uint_as_float(o1[i]), c1, v);
-              o[i] = __float_as_uint(v);
-            }
-            if (!my) continue;
-            if (x.slot >= 0) {
-              float* dst = a.part + ((size_t)x.slot * a.rows + r) * D + c;
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) *reinterpret_cast<uint4*>(dst + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                b[i] = sum == 0.0f ? 0u : pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-              st_v8(a.out + at * D + c, b);
-            }
-          }
-          if (my && x.slot < 0 && a.lse && w == 0) a.lse[at] = sum == 0.0f ? -INFINITY : LN2 * (ref - (top > -INFINITY ? P_SHIFT : 0.0f) + log2f(sum));
-        }
-        if (flags & F_SOME) {
-          // neither group goes on before both have read (and seen that the unit is done)
-          tc_fence_before();
-          __syncwarp();
-          if (flags & F_TWO) {
-            if (lane == 0) mbar_arrive(&swap_in);
-            if (!warp_wait(&swap_in, segs)) break;
-          }
-          if (lane == 0) mbar_arrive(&swap_out);
-          if (!warp_wait(&swap_out, segs)) break;
-          ++segs;
-          if (!(flags & F_TWO)) qb ^= 1;
-        }
-        m = -INFINITY, l = 0.0f, mine = 0;
+      if (flags & F_EXIT) break;
+      // ---- the end of a unit's part
+      const bool some = flags & F_SOME, halves = some && !(flags & F_TWO), both = halves && x.blk > 1;
+      if (mine > 0) wait(&bar.o_done[w][(done - 1) & 1], (done - 1) >> 1);
+      float c0 = 1.0f, c1 = 0.0f;
+      if (halves) {
+        swap[w][r] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.swap_in);
+        wait(&bar.swap_in, swaps);
+        const float2 y0 = swap[0][r], y1 = swap[1][r];
+        m = fmaxf(y0.x, y1.x);
+        const float ref = m > -INFINITY ? m : 0.0f;
+        c0 = ex2(y0.x - ref), c1 = both ? ex2(y1.x - ref) : 0.0f;
+        l = scale_sum(y0.y, y0.x - ref) + (both ? scale_sum(y1.y, y1.x - ref) : 0.0f);
       }
+      tc_fence_after();
+      if (wait.left) store_rows<D>(a, x, lane_base + 256, r, w, m, l, c0, c1);
+      if (halves) {   // neither group goes on before both have read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.swap_out);
+        wait(&bar.swap_out, swaps);
+        ++swaps;
+      }
+      units += some;
+      m = -INFINITY, l = 0.0f, mine = 0;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&it_empty[slot]);
+      if (lane == 0) mbar_arrive(&bar.gr_empty[w][it & 3]);
     }
   }
-  // every MMA has completed before tensor memory is given back: the softmax has waited for the units' ends
+  if (!wait.left) set_err(a.err, BRE_DEVERR_TIMEOUT);
+  // every MMA has completed before tensor memory is given back
   tc_fence_before();
   __syncthreads();
-  if (warp == W_TREE_MMA) {
+  if (warp == W_S) {
+    if (works) mbar_wait_bounded(&bar.drain, 0, AT_WAIT);
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(COLS) : "memory");
   }
