@@ -44,10 +44,10 @@ constexpr float TT_SLACK = 7.0f;         // growth of a row's maximum (log2) tha
 // Costs of the shares: a block for one tile, for two tiles, and what a unit takes beside its blocks.
 constexpr int COST_ONE = 2, COST_TWO = 3, COST_UNIT = 6;
 
-enum : int { F_BLOCK = 1, F_FIRST = 2, F_FULL = 4, F_END = 8, F_EXIT = 16, F_TWO = 32, F_SOME = 64, F_ODD = 128, F_NEW = 256 };
+enum : int { F_BLOCK = 1, F_FULL = 4, F_END = 8, F_EXIT = 16, F_TWO = 32, F_SOME = 64, F_ODD = 128, F_NEW = 256, F_BEGIN = 512 };
 
 // What the walking warp tells the others: a block (F_ODD: of the second group, where there is one tile; F_NEW: the first
-// of its group in the unit), or the end of a unit's part.
+// of its group in the unit), or the beginning or the end of a unit's part.
 struct Item {
   int t0, n, h, blk;              // tokens, kv head; block (at the end: how many there were)
   int flags, slot, begin, kb;     // slot < 0: the whole unit, its outputs are final; running number of the block
@@ -106,6 +106,18 @@ __device__ __forceinline__ void mma_codes(uint32_t d, uint64_t a, uint64_t b, ui
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// Two FP16 values to E4M3 codes, nearest even, saturating; the difference of two pairs.
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
@@ -177,63 +189,45 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 }
 
 struct PlanMem {
-  int run[TT_WARPS], top[TT_WARPS];
-  uint32_t cut[TT_WARPS];
+  int run[TT_WARPS], top[TT_THREADS];
+  int last_run, last_top;  // of a chunk's last token: first token of its run, largest position of its tile
   long long sum[TT_WARPS];
   long long lo, hi, per;   // this CTA's share, costs lo .. hi (none if hi <= lo); length of a share
   long long found_at;      // cost before the tile in which the share begins
   int found;               // that tile's first token
 };
 
-// The cost of all tiles, summed up by the whole CTA, a thread a token; and where the CTA's share begins.  Rolled up as far as it
-// goes: the code runs once, and fetching it takes longer than running it.
+// The cost of all tiles, summed up by the whole CTA, a thread a token; and where the CTA's share begins.  Short rather than
+// quick: the code runs once, and a line of it takes longer to fetch than to run.
 __device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, per_one = 128 / a.G;
-  long long lo = -1;
-  for (int pass = 0;; ++pass) {   // a second pass, where the list is longer than the CTA, finds the place of the share
-    int run = -1, top = INT32_MIN;   // of the last token so far: first token of its run; largest position of its tile
-    long long sum = 0, mine = 0, at = 0;
+  long long lo = 0, per = 0, total = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {   // a second pass, where the list is longer than the CTA, finds the place of the share
+    int run = -1, top = INT32_MIN;
+    long long sum = 0, c = 0, at = 0;
     int from = 0;
 #pragma unroll 1
     for (int base = 0; base < a.T; base += TT_THREADS) {
       const int t = base + tid;
-      const bool in = t < a.T;
+      const bool in = t < a.T, before = in && t > 0, behind = t + 1 < a.T;
       const int s = in ? __ldg(a.seq + t) : 0, p = in ? __ldg(a.pos + t) : -1;
-      const int sb = in && t ? __ldg(a.seq + t - 1) : 0, pb = in && t ? __ldg(a.pos + t - 1) : -1;
-      const int sn = t + 1 < a.T ? __ldg(a.seq + t + 1) : 0, pn = t + 1 < a.T ? __ldg(a.pos + t + 1) : -1;
-      int r = in && (t == 0 || other_run(s, p, sb, pb)) ? t : -1;
-#pragma unroll 1
-      for (int o = 1; o < 32; o *= 2) {
-        const int x = __shfl_up_sync(0xffffffffu, r, o);
-        if (lane >= o) r = max(r, x);
-      }
-      if (lane == 31) m.run[warp] = r;
+      const int sb = before ? __ldg(a.seq + t - 1) : 0, pb = before ? __ldg(a.pos + t - 1) : -1;
+      const int sn = behind ? __ldg(a.seq + t + 1) : 0, pn = behind ? __ldg(a.pos + t + 1) : -1;
+      // first token of the run
+      const uint32_t begins = __ballot_sync(0xffffffffu, in && (t == 0 || other_run(s, p, sb, pb)));
+      if (lane == 0) m.run[warp] = begins ? base + 32 * warp + 31 - __clz(begins) : -1;
+      m.top[tid] = tid == 0 ? top : INT32_MIN;
       __syncthreads();
-#pragma unroll 1
-      for (int w = 0; w < warp; ++w) r = max(r, m.run[w]);
-      r = max(r, run);
-      const int idx = (t - r) % a.per;
-      // the largest position since the tile's first token
-      int v = p;
-      uint32_t cut = in && idx == 0;
-#pragma unroll 1
-      for (int o = 1; o < 32; o *= 2) {
-        const int x = __shfl_up_sync(0xffffffffu, v, o);
-        const uint32_t c = __shfl_up_sync(0xffffffffu, cut, o);
-        if (lane >= o) {
-          if (!cut) v = max(v, x);
-          cut |= c;
-        }
-      }
-      if (lane == 31) m.top[warp] = v, m.cut[warp] = cut;
+      const uint32_t upto = begins & (0xFFFFFFFFu >> (31 - lane));
+      const int former = max(run, __reduce_max_sync(0xffffffffu, lane < warp ? m.run[lane] : -1));
+      const int r = upto ? base + 32 * warp + 31 - __clz(upto) : former;
+      const int idx = (t - r) % a.per, slot = max(t - idx - base, 0);
+      if (in) atomicMax(&m.top[slot], p);
       __syncthreads();
-      int before = top;
-#pragma unroll 1
-      for (int w = 0; w < warp; ++w) before = m.cut[w] ? m.top[w] : max(before, m.top[w]);
-      if (!cut) v = max(v, before);
-      long long c = 0;
-      if (in && (t == a.T - 1 || other_run(s, p, sn, pn) || idx == a.per - 1))   // a tile's last token
-        c = Unit(idx + 1, v, a.tab.N, per_one).cost() * a.H;
+      c = 0;
+      if (in && (!behind || other_run(s, p, sn, pn) || idx == a.per - 1))   // a tile's last token
+        c = Unit(idx + 1, m.top[slot], a.tab.N, per_one).cost() * a.H;
       const long long own = c;
 #pragma unroll 1
       for (int o = 1; o < 32; o *= 2) {
@@ -241,31 +235,31 @@ __device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
         if (lane >= o) c += x;
       }
       if (lane == 31) m.sum[warp] = c;
+      if (tid == TT_THREADS - 1) m.last_run = r, m.last_top = m.top[slot];
       __syncthreads();
-      long long all = sum;
+      run = m.last_run, top = m.last_top;
+      at = sum + c - own;
 #pragma unroll 1
       for (int w = 0; w < TT_WARPS; ++w) {
-        if (w < warp) c += m.sum[w];
-        all += m.sum[w];
-        run = max(run, m.run[w]);   // the chunk's last token carries on
-        top = m.cut[w] ? m.top[w] : max(top, m.top[w]);
+        if (w < warp) at += m.sum[w];
+        sum += m.sum[w];
       }
-      mine = own, at = sum + c - own, from = t - idx;
-      sum = all;
-      if (pass && lo >= at && lo < at + mine) m.found = from, m.found_at = at;
+      c = own, from = t - idx;
+      if (pass && lo >= at && lo < at + c) m.found = from, m.found_at = at;
       __syncthreads();
     }
     if (pass) break;
     // No share is shorter than the step from a unit's first block to its second: every CTA between those of a unit's first
     // and last block then holds a block of it.
     const long long most = quotient(sum, COST_UNIT + COST_TWO);
-    const long long per = quotient(sum, most < 1 ? 1 : most < (long long)gridDim.x ? most : (long long)gridDim.x) + 1;
-    lo = per * blockIdx.x;
-    if (tid == 0) m.lo = lo, m.hi = min(lo + per, sum), m.per = per;
-    const bool one = a.T <= TT_THREADS;
-    if (one && lo >= at && lo < at + mine) m.found = from, m.found_at = at;
-    if (one || lo >= sum) break;
+    per = quotient(sum, most < 1 ? 1 : most < (long long)gridDim.x ? most : (long long)gridDim.x) + 1;
+    lo = per * blockIdx.x, total = sum;
+    if (a.T <= TT_THREADS) {
+      if (lo >= at && lo < at + c) m.found = from, m.found_at = at;
+      break;
+    }
   }
+  if (tid == 0) m.lo = lo, m.hi = min(lo + per, total), m.per = per;
   __syncthreads();
 }
 
@@ -316,57 +310,55 @@ __device__ __noinline__ float careful_weights(uint32_t S, const float* kf, const
 
 // What runs once a unit, or seldom, is out of line: the loops over the blocks shall stay close together.
 //
-// Queries of a unit's rows (of up to two tiles) into two E4M3 terms, by four warps; factors: of the rows' logits.
+// Queries of a unit's rows (of up to two tiles) into two E4M3 terms, by four warps, four lanes a row; factors: of the rows'
+// logits.
 template <int D>
 __device__ __noinline__ void load_queries(const TreeParams& a, const Item& x, unsigned char* sq, int buf0, float* factors) {
   using M = TreeMem<D>;
-  constexpr int CL = D / 32, UN = 8;   // channels a lane, rows of a warp in flight
-  const int lane = threadIdx.x & 31, rows = x.n * a.G, per_one = 128 / a.G;
+  constexpr int CL = D / 4, NV = CL / 8;   // channels a lane, 16-byte loads
+  const int lane = threadIdx.x & 31, sub = lane & 3, rows = x.n * a.G, per_one = 128 / a.G;
   const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // a row's factor is not negative: see the maximum
 #pragma unroll 1
-  for (int r0 = (threadIdx.x >> 5) - W_CONV; r0 < rows; r0 += 4 * UN) {
-    uint32_t w[UN][CL / 2];
+  for (int r = 8 * ((threadIdx.x >> 5) - W_CONV) + lane / 4; r - lane / 4 < rows; r += 32) {
+    const int tl = r / a.G;
+    uint4 w[NV];
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)(x.t0 + tl) * a.q_stride + (size_t)(x.h * a.G + r - tl * a.G) * D) + sub * NV;
 #pragma unroll
-    for (int j = 0; j < UN; ++j) {
-      const int r = r0 + 4 * j, tl = r / a.G;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + (long long)(x.t0 + tl) * a.q_stride +
-                                                              (size_t)(x.h * a.G + r - tl * a.G) * D) + lane * (CL / 2);
+    for (int i = 0; i < NV; ++i) w[i] = r < rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+    uint32_t mx = 0;
 #pragma unroll
-      for (int i = 0; i < CL / 2; ++i) w[j][i] = r < rows ? __ldg(src + i) ^ flip : 0u;
-    }
+    for (int i = 0; i < NV; ++i)
+      mx = __vmaxu2(__vmaxu2(mx, __vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu)), __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu));
+    mx = max(mx & 0xFFFFu, mx >> 16);
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // least e with max|q| <= 448 * 2^e
+    const int bits = (int)(min(mx, 0x7F7Fu) << 16);
+    const int e = max((bits >> 23) - 127 - 8 + ((bits & 0x7FFFFF) > 0x600000 ? 1 : 0), -118);
+    const float down = pow2f(-e);
+    // tile and row in it: a tile holds whole tokens
+    const int tile = r >= per_one * a.G, rr = r - tile * per_one * a.G;
+    unsigned char* const tile_at = sq + (buf0 + tile) * 2 * M::TERM;
 #pragma unroll
-    for (int j = 0; j < UN; ++j) {
-      const int r = r0 + 4 * j;
-      if (r >= rows) break;
-      uint32_t mx = 0;
+    for (int i = 0; i < NV / 2; ++i) {
+      uint32_t hi[4], rest[4];
 #pragma unroll
-      for (int i = 0; i < CL / 2; ++i) mx = __vmaxu2(mx, w[j][i] & 0x7FFF7FFFu);
-      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
-      // least e with max|q| <= 448 * 2^e
-      const int bits = (int)(min(mx, 0x7F7Fu) << 16);
-      const int e = max((bits >> 23) - 127 - 8 + ((bits & 0x7FFFFF) > 0x600000 ? 1 : 0), -118);
-      const float down = pow2f(-e);
-      uint32_t hi = 0, rest = 0;
-#pragma unroll
-      for (int i = 0; i < CL / 2; ++i) {
-        const float u = __uint_as_float(w[j][i] << 16) * down, v = __uint_as_float(w[j][i] & 0xFFFF0000u) * down;
-        const uint32_t c = e4m3x2(u, v);
-        const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(c));
-        hi |= c << (16 * i);
-        rest |= e4m3x2(u - f.x, v - f.y) << (16 * i);
+      for (int k = 0; k < 8; ++k) {
+        const uint4& v = w[2 * i + k / 4];
+        const uint32_t y = (k % 4 == 0 ? v.x : k % 4 == 1 ? v.y : k % 4 == 2 ? v.z : v.w) ^ flip;
+        // (FP16 holds what lies above 2^-23 of the largest exactly; the difference to the nearest code is exact)
+        const uint32_t h = pack_f16x2(__uint_as_float(y << 16) * down, __uint_as_float(y & 0xFFFF0000u) * down);
+        const uint32_t c = e4m3x2_of_f16x2(h), d = e4m3x2_of_f16x2(sub_f16x2(h, e4m3x2_to_f16x2(c)));
+        hi[k / 2] = k & 1 ? hi[k / 2] | c << 16 : c;
+        rest[k / 2] = k & 1 ? rest[k / 2] | d << 16 : d;
       }
-      // tile and row in it: a tile holds whole tokens
-      const int tile = r >= per_one * a.G, rr = r - tile * per_one * a.G;
-      unsigned char* dst = sq + (buf0 + tile) * 2 * M::TERM + swizzled<D>(rr, lane * CL / 16) + lane * CL % 16;
-      if constexpr (CL == 4) {
-        *reinterpret_cast<uint32_t*>(dst) = hi;
-        *reinterpret_cast<uint32_t*>(dst + M::TERM) = rest;
-      } else {
-        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)hi;
-        *reinterpret_cast<uint16_t*>(dst + M::TERM) = (uint16_t)rest;
+      unsigned char* dst = tile_at + swizzled<D>(rr, sub * (NV / 2) + i);
+      if (r < rows) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + M::TERM) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
       }
-      if (lane == 0) factors[tile * 128 + rr] = mx > 0x7F7Fu ? __int_as_float(0x7FC00000) : fabsf(a.scale) * LOG2E * pow2f(e);
     }
+    if (sub == 0 && r < rows) factors[tile * 128 + rr] = mx > 0x7F7Fu ? __int_as_float(0x7FC00000) : fabsf(a.scale) * LOG2E * pow2f(e);
   }
 }
 // Slots of a block that some row of the unit sees.  By a whole warp.
@@ -596,19 +588,20 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         }
         if (top >= 0 && top / KV_BLOCK >= a.tab.N && b0 == 0 && lane == 0) set_err(a.err, BRE_DEVERR_PAGE);
         int jb = 0;
+        if (top >= 0) publish(Item{t0, n, h, 0, F_BEGIN | two, slot, begin, kb}, -1);
 #pragma unroll 1
         for (int g = b0; g < b1 && top >= 0 && wait.left; g += 32) {
           const int my = g + lane < b1 ? kv_page(a.tab, s, g + lane, a.err) : -1;
 #pragma unroll 1
           for (uint32_t todo = __ballot_sync(0xffffffffu, my >= 0); todo && wait.left; todo &= todo - 1) {
             const int src = __ffs(todo) - 1, blk = g + src;
-            const int flags = F_BLOCK | (jb ? 0 : F_FIRST) | (blk < whole ? F_FULL : 0) | two | (jb & 1 ? F_ODD : 0) |
+            const int flags = F_BLOCK | (blk < whole ? F_FULL : 0) | two | (jb & 1 ? F_ODD : 0) |
                               (jb < (two ? 1 : 2) ? F_NEW : 0);
             publish(Item{t0, n, h, blk, flags, slot, begin, kb}, __shfl_sync(0xffffffffu, my, src));
             ++kb, ++jb;
           }
         }
-        publish(Item{t0, n, h, jb, F_END | two | (jb ? F_SOME : 0), slot, begin, kb}, -1);
+        publish(Item{t0, n, h, jb, F_END | two | (jb ? F_SOME : 0), slot, top >= 0 ? begin : -1, kb}, -1);
       }
       t0 += n;
     }
@@ -636,21 +629,21 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       if (!(flags & F_BLOCK)) {
         if (flags & F_EXIT) break;
         if (elect_one()) {
-          if (flags & F_SOME && live & 1) mma_commit(&bar.q_empty[0]);
-          if (flags & F_SOME && live & 2) mma_commit(&bar.q_empty[1]);
+          if (flags & F_END && live & 1) mma_commit(&bar.q_empty[0]);
+          if (flags & F_END && live & 2) mma_commit(&bar.q_empty[1]);
           mbar_arrive(&bar.k_empty[ks]);
         }
         __syncwarp();
-        if (flags & F_SOME) {
-          uses.a += live & 1, uses.b += live >> 1;
-          if (!two) qb ^= 1;
+        if (flags & F_BEGIN) {
+          live = two ? 3 : 1 << qb;
+          if (live & 1) wait(&bar.q_full[0], uses.a);
+          if (live & 2) wait(&bar.q_full[1], uses.b);
+        }
+        if (flags & F_END) {
+          if (live && !two) qb ^= 1;
+          uses.a += live & 1, uses.b += live >> 1, live = 0;
         }
         continue;
-      }
-      if (flags & F_FIRST) {
-        live = two ? 3 : 1 << qb;
-        if (live & 1) wait(&bar.q_full[0], uses.a);
-        if (live & 2) wait(&bar.q_full[1], uses.b);
       }
 #pragma unroll 1
       for (int g = 0; g <= two; ++g) {
@@ -725,7 +718,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       if (!wait.left) break;
       const int flags = to_v[vs].flags, two = flags & F_TWO;
       // the groups that hear of it
-      const int who = !(flags & F_BLOCK) || two ? 3 : flags & F_ODD ? 2 : 1;
+      const int who = flags & F_BEGIN ? 0 : !(flags & F_BLOCK) || two ? 3 : flags & F_ODD ? 2 : 1;
       auto tell = [&]() {   // by one warp
 #pragma unroll 1
         for (int g = 0; g < 2; ++g) {
@@ -741,19 +734,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         __syncwarp();
       };
       if (flags & F_BLOCK) {
-        if (flags & F_FIRST) {
-          // rows of up to two tiles; the buffers are free when the S of their former unit have been formed
-          last = two ? 3 : 1 << qb;
-          if (last & 1) wait(&bar.q_empty[0], uses.a + 1);
-          if (last & 2) wait(&bar.q_empty[1], uses.b + 1);
-          load_queries<D>(a, to_v[vs], sm + M::q, two ? 0 : qb, &q_factor[units % TT_QF][0][0]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (last & 1) mbar_arrive(&bar.q_full[0]);
-            if (last & 2) mbar_arrive(&bar.q_full[1]);
-          }
-        }
         const int st = kb & 3, sp = kb % TT_SC;
         // slots that some row sees (others may never have been written: their values become zeros)
         uint64_t seen = ~0ull;
@@ -813,6 +793,18 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.v16_full[st]);
         ++kb;
+      } else if (flags & F_BEGIN) {
+        // rows of up to two tiles; the buffers are free when the S of their former unit have been formed
+        last = two ? 3 : 1 << qb;
+        if (last & 1) wait(&bar.q_empty[0], uses.a + 1);
+        if (last & 2) wait(&bar.q_empty[1], uses.b + 1);
+        load_queries<D>(a, to_v[vs], sm + M::q, two ? 0 : qb, &q_factor[units % TT_QF][0][0]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (last & 1) mbar_arrive(&bar.q_full[0]);
+          if (last & 2) mbar_arrive(&bar.q_full[1]);
+        }
       } else {
         if (cw == 0) tell();
         if (flags & F_EXIT) {
@@ -823,8 +815,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
           if (lane == 0) mbar_arrive(&bar.v16_full[st]);
           break;
         }
-        if (flags & F_SOME) {
-          ++units, uses.a += last & 1, uses.b += last >> 1;
+        if (last) {
+          ++units, uses.a += last & 1, uses.b += last >> 1, last = 0;
           if (!two) qb ^= 1;
         }
       }
@@ -965,7 +957,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         wait(&bar.swap_out, swaps);
         ++swaps;
       }
-      units += some;
+      units += x.begin >= 0;   // (a unit of padding has no queries)
       m = -INFINITY, l = 0.0f, mine = 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.gr_empty[w][it & 3]);
