@@ -52,51 +52,59 @@ __global__ void __launch_bounds__(KR_THREADS) kv_rotate_kernel(const RotateArgs 
   pdl_wait();
   pdl_launch_dependents();
   const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.T - t0);
-  for (int i = threadIdx.x; i < nt; i += KR_THREADS) s_pos[i] = __ldg(a.pos + t0 + i);
-  for (int i = threadIdx.x; i < nt * a.pairs; i += KR_THREADS) {
-    const int t = i / a.pairs, j = i - t * a.pairs;
-    const uint64_t turn = (uint64_t)(uint32_t)max(__ldg(a.pos + t0 + t), 0) * __ldg(a.turns + j);
-    float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);   // half turns in [-1, 1]
-    cs[i] = make_float2(c * a.gain, s * a.gain * a.sign);
-  }
-  __syncthreads();
   const int per = a.items * a.groups, tl = threadIdx.x / per, rest = threadIdx.x - tl * per;
-  if (tl >= nt) return;
   const int group = rest / a.items, item = rest - group * a.items;
   const int turning = a.pairs / PAIRS;   // items that turn come first
-  const bool pad = s_pos[tl] < 0, turns = item < turning;
+  const bool mine = tl < nt, turns = item < turning;
   int at = 0, at2 = 0;
-  float c[PAIRS], s[PAIRS];
   if (turns) {
     at = HALF ? a.offset + item * V : a.offset + item * (V > 1 ? V : 2);
     at2 = HALF ? at + a.pairs : at + 1;
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-      const float2 f = cs[tl * a.pairs + item * PAIRS + i];
-      c[i] = f.x, s[i] = f.y;
-    }
   } else {
     at = (item - turning) * V;
     if (at >= a.offset) at += 2 * a.pairs;
   }
   const long long t = t0 + tl;
-  const int all = a.heads[0] + a.heads[1], step = a.groups * gridDim.y;
-  for (int h0 = group + blockIdx.y * a.groups; h0 < all; h0 += KR_UNROLL * step) {
-    Vec<V> x[KR_UNROLL], y[KR_UNROLL];
+  const int all = a.heads[0] + a.heads[1], step = a.groups * gridDim.y, first = group + blockIdx.y * a.groups;
+  Vec<V> x[KR_UNROLL], y[KR_UNROLL];
+  auto load = [&](int h0) {
 #pragma unroll
     for (int u = 0; u < KR_UNROLL; ++u) {
-      const int h = h0 + u * step, which = h >= a.heads[0];
-      if (h >= all) continue;
-      const uint16_t* p = a.in[which] + t * a.in_stride[which] + (long long)(h - (which ? a.heads[0] : 0)) * a.D;
+      const int h = h0 + u * step;
+      if (!mine || h >= all) continue;
+      const uint16_t* p = h < a.heads[0] ? a.in[0] + t * a.in_stride[0] + (long long)h * a.D
+                                         : a.in[1] + t * a.in_stride[1] + (long long)(h - a.heads[0]) * a.D;
       x[u].load(p + at);
       if (TWO && turns) y[u].load(p + at2);
     }
+  };
+  load(first);   // on their way while cosines and sines are formed
+  for (int i = threadIdx.x; i < nt; i += KR_THREADS) s_pos[i] = __ldg(a.pos + t0 + i);
+  for (int i = threadIdx.x; i < nt * a.pairs; i += KR_THREADS) {
+    const int tt = i / a.pairs, j = i - tt * a.pairs;
+    const uint64_t turn = (uint64_t)(uint32_t)max(__ldg(a.pos + t0 + tt), 0) * __ldg(a.turns + j);
+    float s, c;
+    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);   // half turns in [-1, 1]
+    cs[i] = make_float2(c * a.gain, s * a.gain * a.sign);
+  }
+  __syncthreads();
+  if (!mine) return;
+  const bool pad = s_pos[tl] < 0;
+  float c[PAIRS], s[PAIRS];
+  if (turns) {
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      const float2 f = cs[tl * a.pairs + item * PAIRS + i];
+      c[i] = f.x, s[i] = f.y;
+    }
+  }
+  for (int h0 = first; h0 < all; h0 += KR_UNROLL * step) {
 #pragma unroll
     for (int u = 0; u < KR_UNROLL; ++u) {
-      const int h = h0 + u * step, which = h >= a.heads[0];
+      const int h = h0 + u * step;
       if (h >= all) continue;
-      uint16_t* p = a.out[which] + t * a.out_stride[which] + (long long)(h - (which ? a.heads[0] : 0)) * a.D;
+      uint16_t* p = h < a.heads[0] ? a.out[0] + t * a.out_stride[0] + (long long)h * a.D
+                                   : a.out[1] + t * a.out_stride[1] + (long long)(h - a.heads[0]) * a.D;
       if (pad) {
 #pragma unroll
         for (int i = 0; i < V; ++i) x[u].x[i] = y[u].x[i] = 0;
@@ -112,6 +120,7 @@ __global__ void __launch_bounds__(KR_THREADS) kv_rotate_kernel(const RotateArgs 
       x[u].store(p + at);
       if (TWO && turns) y[u].store(p + at2);
     }
+    load(h0 + KR_UNROLL * step);
   }
 }
 
