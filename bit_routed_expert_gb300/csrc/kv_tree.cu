@@ -24,8 +24,8 @@
 // EV_LARGE, every token's own goes into its weight (see kv_attend.cu), by slower code.
 #include <atomic>
 
-#include "kv_attend.cuh"
 #include "kv_tc.cuh"
+#include "kv_tree.cuh"
 
 namespace bre {
 
@@ -40,7 +40,7 @@ constexpr int W_CONV = 8, W_LOAD = 12, W_S = 13, W_O = 14;
 // by the TT_V that the converting warps may be apart.
 constexpr int TT_K = 4, TT_V = 4, TT_V16 = 4, TT_GROUP = 4, TT_SC = 16, TT_QF = 8;
 constexpr int TT_MAX_CTAS = 160;
-constexpr float TT_SLACK = 7.0f;         // growth of a row's maximum (log2) that needs no rescaling
+constexpr float P_MOST = 32768.0f;       // a block's sum of weights up to which they are FP16 numbers for sure
 // Costs of the shares: a block for one tile, for two tiles, and what a unit takes beside its blocks.
 constexpr int COST_ONE = 2, COST_TWO = 3, COST_UNIT = 6;
 
@@ -130,25 +130,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-
-// Bit x - 64 blk set: the token sees slot x (of the 64 of a block).
-__device__ __forceinline__ uint64_t seen_bits(const uint64_t* __restrict__ mask, int words, int start, int pos, int blk) {
-  const long long x0 = (long long)blk * KV_BLOCK;
-  uint64_t own = pos >= x0 + 63 ? ~0ull : pos >= x0 ? (2ull << (pos - x0)) - 1ull : 0ull;
-  if (!mask || own == 0) return own;
-  const long long j = x0 - start;   // bit of the block's first slot
-  uint64_t tree = 0;
-  if (j < 0) {
-    if (j <= -64) return own;
-    tree = ((1ull << -j) - 1ull) | __ldg(mask) << -j;
-  } else {
-    const long long w = j / 64;
-    const int r = (int)(j % 64);
-    if (w < words) tree = __ldg(mask + w) >> r;
-    if (r && w + 1 < words) tree |= __ldg(mask + w + 1) << (64 - r);
-  }
-  return own & tree;
 }
 
 // ---------------------------------------------------------------------------
@@ -855,65 +836,62 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         if (warp_live) {
           const float top = ev_top[sp];
           if (flags & F_FULL && top == top) {
-            // the ordinary way: every row sees the whole block, and the block's values have one scale
-            uint32_t s[64];   // S, then S times the keys' scales
-            tmem_ld32(S, s);
-            tmem_ld32(S + 32, s + 32);
-            tmem_wait_ld();
-            float mx = -INFINITY, my = -INFINITY;
+            // The ordinary way: every row sees the whole block, and the block's values have one scale.  The weights are formed
+            // against the maximum so far without looking for the block's own.  Their sum bounds them: while it is below FP16's
+            // largest the maximum will do (it lags by 2^7 at most).  Else, and at first, S is looked through for the maximum.
+            uint32_t s[64], pk[32];
+            float sum;
+            auto weigh = [&]() {
+              const float add = top - (m > -INFINITY ? m - P_SHIFT : 0.0f);
+              const uint64_t f2 = pack2(f, f), a2 = pack2(add, add);
+              float sum0 = 0.0f, sum1 = 0.0f;
+              tmem_ld32(S, s);
+              tmem_ld32(S + 32, s + 32);
+              tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-              const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&kf[sp][c]);
-              const float2 v0 = unpack2(mul2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), k.x));
-              const float2 v1 = unpack2(mul2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), k.y));
-              mx = max3(mx, v0.x, v0.y), my = max3(my, v1.x, v1.y);
-              s[c] = __float_as_uint(v0.x), s[c + 1] = __float_as_uint(v0.y);
-              s[c + 2] = __float_as_uint(v1.x), s[c + 3] = __float_as_uint(v1.y);
-            }
-            mx = fmaf(fmaxf(mx, my), f, top);   // (f is not negative; a query that gives NaN has a NaN maximum)
-            if (m == -INFINITY) m = mx;         // nothing has been added for this row yet
-            if (__builtin_expect(__any_sync(0xffffffffu, mx > m + TT_SLACK), 0)) {
-              // some row's weights would outgrow FP16: all rows of the warp take their new maximum
+              for (int c = 0; c < 64; c += 4) {
+                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&kf[sp][c]);
+                const float2 v0 = unpack2(fma2(mul2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), k.x), f2, a2));
+                const float2 v1 = unpack2(fma2(mul2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), k.y), f2, a2));
+                const float p0 = ex2(v0.x), p1 = ex2(v0.y), p2 = ex2(v1.x), p3 = ex2(v1.y);
+                sum0 += p0, sum1 += p1;
+                sum0 += p2, sum1 += p3;
+                pk[c / 2] = pack_f16x2(p0, p1), pk[c / 2 + 1] = pack_f16x2(p2, p3);
+              }
+              sum = sum0 + sum1;
+            };
+            for (bool again = false;; again = true) {
+              weigh();
+              if (again || !__any_sync(0xffffffffu, tl >= 0 && (sum > P_MOST || m == -INFINITY))) break;
+              tmem_ld32(S, s);
+              tmem_ld32(S + 32, s + 32);
+              tmem_wait_ld();
+              float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < 64; c += 4) {
+                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&kf[sp][c]);
+                const float2 v0 = unpack2(mul2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), k.x));
+                const float2 v1 = unpack2(mul2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), k.y));
+                mx = max3(mx, v0.x, v0.y), my = max3(my, v1.x, v1.y);
+              }
+              mx = fmaf(fmaxf(mx, my), f, top);   // (f is not negative; a query that gives NaN has a NaN maximum)
+              // all rows of the warp take their new maximum
               if (mine > 0) wait(&bar.o_done[w][buf ^ 1], (done - 1) >> 1);
               tc_fence_after();
-              const float then = fmaxf(m, mx), d = m > -INFINITY ? m - then : 0.0f, sc = ex2(d);
+              const float then = m == -INFINITY ? mx : fmaxf(m, mx), d = m > -INFINITY ? m - then : 0.0f;
               l = scale_sum(l, d);
               m = then;
-              if (mine > 0) {
-                const uint32_t O = lane_base + 256 + w * 128;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(O + c, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sc);
-                  tmem_st16(O + c, o);
-                }
-              }
+              if (mine > 0) rescale<D>(lane_base + 256 + w * 128, ex2(d));
             }
-            const float add = top - (m > -INFINITY ? m - P_SHIFT : 0.0f);
-            const uint64_t f2 = pack2(f, f), add2 = pack2(add, add);
-            float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-            for (int half = 0; half < 64; half += 32) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int c = 0; c < 32; c += 2) {
-                const float2 y = unpack2(fma2(pack2(__uint_as_float(s[half + c]), __uint_as_float(s[half + c + 1])), f2, add2));
-                const float p0 = ex2(y.x), p1 = ex2(y.y);
-                sum0 += p0, sum1 += p1;
-                pk[c / 2] = pack_f16x2(p0, p1);
-              }
-              tmem_st16(S + half / 2, pk);
-            }
-            l = fmaf(sum0 + sum1, ex2(-top), l);
+            tmem_st16(S, pk);
+            tmem_st16(S + 16, pk + 16);
+            l = fmaf(sum, ex2(-top), l);
           } else {
             const uint64_t seen = tl < 0 ? 0ull : flags & F_FULL ? ~0ull
                 : seen_bits(a.mask ? a.mask + (size_t)(x.t0 + tl) * a.words : nullptr, a.words, x.begin, __ldg(a.pos + x.t0 + tl), x.blk);
             const float mx = careful_max(S, kf[sp], ev_f[sp], f, seen);
-            if (m == -INFINITY) m = mx;
-            if (__any_sync(0xffffffffu, mx > m + TT_SLACK)) {
+            if (m == -INFINITY) m = mx;   // nothing has been added for this row yet
+            if (__any_sync(0xffffffffu, mx > m)) {
               if (mine > 0) wait(&bar.o_done[w][buf ^ 1], (done - 1) >> 1);
               tc_fence_after();
               const float then = fmaxf(m, mx), d = m > -INFINITY ? m - then : 0.0f;
@@ -977,57 +955,15 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
 // ---------------------------------------------------------------------------
 // Joining the parts
 // ---------------------------------------------------------------------------
-// A warp a row: the parts' maxima and sums by the lanes, then the outputs, part after part.
-constexpr int TJ_WARPS = 4;
-
 template <int D>
-__global__ void __launch_bounds__(TJ_WARPS * 32) kv_tree_join_kernel(const TreeParams a) {
-  constexpr int CL = D / 32;
+__global__ void __launch_bounds__(JOIN_WARPS * 32) kv_tree_join_kernel(const TreeParams a) {
   pdl_wait();
   pdl_launch_dependents();
   const Join j = a.join[blockIdx.x];
-  const int lane = threadIdx.x & 31, rows = j.n * a.G;
   if (j.parts == 0) return;
-  for (int r = blockIdx.y * TJ_WARPS + (threadIdx.x >> 5); r < rows; r += gridDim.y * TJ_WARPS) {
-    auto slot_of = [&](int p) { return (size_t)(2 * (blockIdx.x + p) + (p == 0)); };
-    float top = -INFINITY;
-    for (int p = lane; p < j.parts; p += 32) top = fmaxf(top, a.ml[slot_of(p) * a.rows + r].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top > -INFINITY ? top : 0.0f;
-    float sum = 0.0f, v[CL];
-#pragma unroll
-    for (int i = 0; i < CL; ++i) v[i] = 0.0f;
-    for (int p0 = 0; p0 < j.parts; p0 += 32) {
-      const float2 y = p0 + lane < j.parts ? a.ml[slot_of(p0 + lane) * a.rows + r] : make_float2(-INFINITY, 0.0f);
-      const float w = ex2(y.x - ref);
-      sum += scale_sum(y.y, y.x - ref);
-      const int n = min(32, j.parts - p0);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-        const float* src = a.part + (slot_of(p0 + i) * a.rows + r) * D + lane * CL;
-        if constexpr (CL == 4) {
-          const float4 o = *reinterpret_cast<const float4*>(src);
-          v[0] = fmaf(wi, o.x, v[0]), v[1] = fmaf(wi, o.y, v[1]), v[2] = fmaf(wi, o.z, v[2]), v[3] = fmaf(wi, o.w, v[3]);
-        } else {
-          const float2 o = *reinterpret_cast<const float2*>(src);
-          v[0] = fmaf(wi, o.x, v[0]), v[1] = fmaf(wi, o.y, v[1]);
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const int tok = r / a.G;
-    const size_t at = ((size_t)(j.t0 + tok) * a.H + j.h) * a.G + (r - tok * a.G);
-    const float inv = 1.0f / sum;
-    uint32_t b[CL / 2];
-#pragma unroll
-    for (int i = 0; i < CL / 2; ++i) b[i] = sum == 0.0f ? 0u : pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
-    if constexpr (CL == 4) *reinterpret_cast<uint2*>(a.out + at * D + lane * CL) = make_uint2(b[0], b[1]);
-    else *reinterpret_cast<uint32_t*>(a.out + at * D + lane * CL) = b[0];
-    if (lane == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : LN2 * (ref - (top > -INFINITY ? P_SHIFT : 0.0f) + log2f(sum));
-  }
+  join_rows<D>(a.ml, a.part, j.parts, blockIdx.y, gridDim.y, j.n * a.G,
+               [&](int p, int r) { return (size_t)(2 * (blockIdx.x + p) + (p == 0)) * a.rows + r; },
+               [&](int r) { return ((size_t)(j.t0 + r / a.G) * a.H + j.h) * a.G + r % a.G; }, a.out, a.lse);
 }
 
 template <int D, bool PATIENT>
@@ -1043,8 +979,9 @@ cudaError_t launch(const TreeParams& a, const CUtensorMap& keys, int ctas, cudaS
   }
   cudaError_t e = launch_k(kv_tree_kernel<D, PATIENT>, dim3((unsigned)ctas), dim3(TT_THREADS), TreeMem<D>::bytes, s, a, keys);
   if (e != cudaSuccess) return e;
-  const int chunks = (a.rows + TJ_WARPS - 1) / TJ_WARPS;
-  return launch_k(kv_tree_join_kernel<D>, dim3((unsigned)ctas, (unsigned)(chunks < 32 ? chunks : 32)), dim3(TJ_WARPS * 32), 0, s, a);
+  // (a part's rows over several CTAs, of which those for a CTA that begins no shared unit have nothing to do)
+  const int chunks = a.rows < 32 ? a.rows : 32;
+  return launch_k(kv_tree_join_kernel<D>, dim3((unsigned)ctas, (unsigned)chunks), dim3(JOIN_WARPS * 32), 0, s, a);
 }
 
 int slot_rows(int T, int G) {   // rows of a part: those of two tiles, or all that the call has
@@ -1058,12 +995,19 @@ size_t kv_tree_ws_bytes(int T, int Hq, int H, int D) {
   const int G = Hq / H;
   if (G < 1 || G > 16) return 0;
   const size_t slots = 2 * TT_MAX_CTAS, rows = slot_rows(T, G);
-  return TT_MAX_CTAS * sizeof(Join) + slots * rows * (sizeof(float2) + D * sizeof(float));
+  const size_t tiles = TT_MAX_CTAS * sizeof(Join) + slots * rows * (sizeof(float2) + D * sizeof(float));
+  const size_t single = tree_rows_ws_bytes(T, H, G, D);
+  return tiles > single ? tiles : single;
 }
 
 cudaError_t launch_kv_attend_tree(const TreeArgs& t, cudaStream_t s) {
   const bre_kv_cache* c = t.cache;
   const int H = c->n_kv_heads, D = c->head_dim, G = t.Hq / H;
+  // A token at a time where a sequence has three at most on average, or the contexts are short.  Such a call reads a context
+  // once for each of its tokens (mostly from L2), but needs none of the tiles' preparations.  us, a token at a time / tiles,
+  // four kv heads, G = 8, D = 128, 64 sequences: 1 token over 16,384 183 / 395, 2 278 / 404, 4 501 / 407; 3 over 4,096 124 / 131,
+  // 4 134 / 132; 8 sequences, 8 tokens over 300: 14 / 32; G = 4, D = 64, eight kv heads, 64 sequences, 4 tokens over 200: 18 / 48.
+  if (t.tk.T <= 3LL * t.tk.B || (long long)t.tk.T * H * t.tk.N <= 4096) return launch_tree_rows(t, s);
   TreeParams a{};
   a.pages = static_cast<const uint8_t*>(c->pages), a.H = H, a.G = G, a.per = 2 * (128 / G);
   a.tab = KvTable{t.tk.table, t.tk.B, t.tk.N, c->n_pages};

@@ -1,0 +1,112 @@
+// What the kernels of the attention over the whole context share: which slots a token sees, and the joining of parts.
+#pragma once
+#include "kv_attend.cuh"
+
+namespace bre {
+
+// Bit x - 64 blk set: the token sees slot x (of the 64 of a block).
+__device__ __forceinline__ uint64_t seen_bits(const uint64_t* __restrict__ mask, int words, int start, int pos, int blk) {
+  const long long x0 = (long long)blk * KV_BLOCK;
+  uint64_t own = pos >= x0 + 63 ? ~0ull : pos >= x0 ? (2ull << (pos - x0)) - 1ull : 0ull;
+  if (!mask || own == 0) return own;
+  const long long j = x0 - start;   // bit of the block's first slot
+  uint64_t tree = 0;
+  if (j < 0) {
+    if (j <= -64) return own;
+    tree = ((1ull << -j) - 1ull) | __ldg(mask) << -j;
+  } else {
+    const long long w = j / 64;
+    const int r = (int)(j % 64);
+    if (w < words) tree = __ldg(mask + w) >> r;
+    if (r && w + 1 < words) tree |= __ldg(mask + w + 1) << (64 - r);
+  }
+  return own & tree;
+}
+
+// A row's parts (index(p): where part p's maximum and sum, and its output, lie), those from `from` on in steps of `step`,
+// joined in their order by a warp: the maxima and sums by the lanes, then the outputs.
+template <int D>
+struct Joined {
+  float top, sum, v[D / 32];   // maximum, sum, output of this lane's channels, relative to the maximum
+
+  template <typename Index>
+  __device__ __forceinline__ Joined(const float2* ml, const float* part, int parts, int from, int step, Index index) {
+    constexpr int CL = D / 32;
+    const int lane = threadIdx.x & 31;
+    top = -INFINITY, sum = 0.0f;
+    for (int p = from + lane * step; p < parts; p += 32 * step) top = fmaxf(top, ml[index(p)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top > -INFINITY ? top : 0.0f;
+#pragma unroll
+    for (int i = 0; i < CL; ++i) v[i] = 0.0f;
+    for (int p0 = from; p0 < parts; p0 += 32 * step) {
+      const int p = p0 + lane * step;
+      const float2 y = p < parts ? ml[index(p)] : make_float2(-INFINITY, 0.0f);
+      const float w = ex2(y.x - ref);
+      sum += scale_sum(y.y, y.x - ref);
+      const int n = min(32, (parts - p0 + step - 1) / step);
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float* src = part + index(p0 + i * step) * D + lane * CL;
+        if constexpr (CL == 4) {
+          const float4 o = *reinterpret_cast<const float4*>(src);
+          v[0] = fmaf(wi, o.x, v[0]), v[1] = fmaf(wi, o.y, v[1]), v[2] = fmaf(wi, o.z, v[2]), v[3] = fmaf(wi, o.w, v[3]);
+        } else {
+          const float2 o = *reinterpret_cast<const float2*>(src);
+          v[0] = fmaf(wi, o.x, v[0]), v[1] = fmaf(wi, o.y, v[1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  __device__ __forceinline__ void store(uint16_t* out, float* lse) const {
+    constexpr int CL = D / 32;
+    const int lane = threadIdx.x & 31;
+    const float inv = 1.0f / sum;
+    uint32_t b[CL / 2];
+#pragma unroll
+    for (int i = 0; i < CL / 2; ++i) b[i] = sum == 0.0f ? 0u : pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+    if constexpr (CL == 4) *reinterpret_cast<uint2*>(out + lane * CL) = make_uint2(b[0], b[1]);
+    else *reinterpret_cast<uint32_t*>(out + lane * CL) = b[0];
+    if (lane == 0 && lse) *lse = sum == 0.0f ? -INFINITY : LN2 * (top > -INFINITY ? top - P_SHIFT + log2f(sum) : log2f(sum));
+  }
+};
+
+constexpr int JOIN_WARPS = 8;
+// Rows first, first + stride, .. of `rows` by a CTA of JOIN_WARPS warps.  Few parts: a warp a row.  Many: a row at a time, its
+// parts dealt to the warps, whose results are joined once more (304 parts of 32 rows, a warp a row: 38 us).
+template <int D, typename Index, typename Place>
+__device__ __forceinline__ void join_rows(const float2* ml, const float* part, int parts, int first, int stride, int rows, Index index,
+                                          Place place, uint16_t* out, float* lse) {
+  __shared__ float2 sh_ml[2][JOIN_WARPS];
+  __shared__ float sh_part[2][JOIN_WARPS * D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (parts <= JOIN_WARPS) {
+    for (int r = first * JOIN_WARPS + warp; r < rows; r += stride * JOIN_WARPS) {
+      const size_t at = place(r);
+      Joined<D>(ml, part, parts, 0, 1, [&](int p) { return index(p, r); }).store(out + at * D, lse ? lse + at : nullptr);
+    }
+    return;
+  }
+  int turn = 0;
+  for (int r = first; r < rows; r += stride, turn ^= 1) {
+    const Joined<D> mine(ml, part, parts, warp, JOIN_WARPS, [&](int p) { return index(p, r); });
+    if (lane == 0) sh_ml[turn][warp] = make_float2(mine.top, mine.sum);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) sh_part[turn][warp * D + lane * (D / 32) + i] = mine.v[i];
+    __syncthreads();
+    if (warp == 0) {
+      const size_t at = place(r);
+      Joined<D>(sh_ml[turn], sh_part[turn], JOIN_WARPS, 0, 1, [](int p) { return (size_t)p; }).store(out + at * D, lse ? lse + at : nullptr);
+    }
+  }
+}
+
+// A token at a time (kv_tree_rows.cu)
+size_t tree_rows_ws_bytes(int T, int H, int G, int D);
+cudaError_t launch_tree_rows(const TreeArgs& a, cudaStream_t s);
+
+}  // namespace bre
