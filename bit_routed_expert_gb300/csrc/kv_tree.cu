@@ -9,12 +9,13 @@
 // order of the context (the same numbers whatever the order in which CTAs finish).  The host knows neither
 // lengths nor runs: every CTA adds up the work of all tiles itself and finds its place.
 //
-// Fifteen warps:
+// Sixteen warps:
 //   warps 0-3, 4-7  softmax, a thread a row: two tiles' rows of the same block, or, where there is one tile, its
 //                   rows of the even and of the odd blocks, each with a running maximum, sum and output of its own
-//   warps 8-11      queries into two E4M3 terms; the values' codes into FP16 in 128-byte-swizzled shared memory
+//   warps 8-11      queries into two E4M3 terms; the values' codes into FP16 in 128-byte-swizzled shared memory, two warps
+//                   for the even and two for the odd blocks
 //   warp 12         walks through the share, looks up pages and starts the copies (TMA: keys swizzled, values as they lie)
-//   warps 13, 14    issue the MMAs: S = Q K^T into tensor memory; O += P V with P read from tensor memory
+//   warps 13-15     issue the MMAs: S = Q K^T into tensor memory, by turns; O += P V with P read from tensor memory
 //
 // The keys' codes are an MMA operand as they lie in the cache.  A BF16 query is q = 2^e (a + b), a and b E4M3: a is
 // q's nearest code, b the rest's, so that the two products add up to that of q itself (see bre.h for what is lost).  Two
@@ -31,14 +32,14 @@ namespace bre {
 
 namespace {
 
-constexpr int TT_THREADS = 480;
+constexpr int TT_THREADS = 512;
 constexpr int TT_WARPS = TT_THREADS / 32;
-constexpr int W_CONV = 8, W_LOAD = 12, W_S = 13, W_O = 14;
+constexpr int W_CONV = 8, W_LOAD = 12, W_S = 13, W_O = 15;
 // Depths of the rings (powers of 2): keys with what the S warp is told, values with what the converting warps are told;
-// converted values; what either softmax group is told; scales; units' logit factors.  The last two need no barriers: a
-// softmax group has one of every two blocks, and the end of every unit, and lags behind by TT_GROUP of these and
-// by the TT_V that the converting warps may be apart.
-constexpr int TT_K = 4, TT_V = 4, TT_V16 = 4, TT_GROUP = 4, TT_SC = 16, TT_QF = 8;
+// converted values; what either softmax group is told; scales.  The last need no barriers: a
+// softmax group has one of every two blocks, and lags behind by TT_GROUP of these and by the TT_V that the converting
+// warps may be apart.
+constexpr int TT_K = 4, TT_V = 4, TT_V16 = 4, TT_GROUP = 4, TT_SC = 16;
 constexpr int TT_MAX_CTAS = 160;
 constexpr float P_MOST = 32768.0f;       // a block's sum of weights up to which they are FP16 numbers for sure
 // Costs of the shares: a block for one tile, for two tiles, and what a unit takes beside its blocks.
@@ -46,8 +47,8 @@ constexpr int COST_ONE = 2, COST_TWO = 3, COST_UNIT = 6;
 
 enum : int { F_BLOCK = 1, F_FULL = 4, F_END = 8, F_EXIT = 16, F_TWO = 32, F_SOME = 64, F_ODD = 128, F_NEW = 256, F_BEGIN = 512 };
 
-// What the walking warp tells the others: a block (F_ODD: of the second group, where there is one tile; F_NEW: the first
-// of its group in the unit), or the beginning or the end of a unit's part.
+// What the walking warp tells the others: a block (F_ODD: of the second group, where there is one tile; F_BEGIN: the first
+// of the unit's part; F_NEW: the first of its group), or the end of a unit's part.
 struct Item {
   int t0, n, h, blk;              // tokens, kv head; block (at the end: how many there were)
   int flags, slot, begin, kb;     // slot < 0: the whole unit, its outputs are final; running number of the block
@@ -79,6 +80,9 @@ struct TreeParams {
   float2* ml;               // [CTAs][2][rows]: maximum and sum
   float* part;              // [CTAs][2][rows][D]
   int rows;                 // rows of a slot
+  unsigned char* codes;     // [2 terms][kv heads][q_rows][D]: the queries as E4M3
+  float* factors;           // [kv heads][q_rows]: of their logits
+  int q_rows;               // tokens times heads of a group, or 128 if that is less
 };
 
 template <int D>
@@ -94,12 +98,6 @@ __device__ __forceinline__ uint64_t desc_codes(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)((8 * D) >> 4) << 32) | ((uint64_t)1 << 46) |
          ((uint64_t)(D == 128 ? 2 : 4) << 61);
 }
-// Byte of (row, 16-byte piece) in such a tile.
-template <int D>
-__device__ __forceinline__ int swizzled(int row, int piece) {
-  return row * D + ((piece ^ (D == 128 ? row & 7 : row >> 1 & 3)) << 4);
-}
-
 __device__ __forceinline__ void mma_codes(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -245,6 +243,52 @@ __device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
 }
 
 // ---------------------------------------------------------------------------
+// The queries as two E4M3 terms
+// ---------------------------------------------------------------------------
+// A lane 16 channels, for all tiles beforehand: tiles of several CTAs (parts of a long context) read the same queries, and code
+// that a CTA of the attention kernel runs once a unit comes from far away (four of its warps took 8,500 cycles for 128 rows).
+template <int D>
+__global__ void __launch_bounds__(256) kv_tree_queries_kernel(const TreeParams a) {
+  constexpr int LR = D / 16;   // lanes a row
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int sub = (int)(i % LR), Hq = a.H * a.G;
+  const long long row = i / LR;   // (whole warps stay: 32 is a multiple of LR)
+  const bool in = row < (long long)a.T * Hq;
+  const int t = in ? (int)(row / Hq) : 0, hq = in ? (int)(row % Hq) : 0, h = hq / a.G;
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint4* src = reinterpret_cast<const uint4*>(a.q + t * a.q_stride + (size_t)hq * D) + 2 * sub;
+  const uint4 u = __ldg(src), v = __ldg(src + 1);
+  const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  uint32_t mx = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, w[k] & 0x7FFF7FFFu);
+  mx = max(mx & 0xFFFFu, mx >> 16);
+#pragma unroll
+  for (int o = 1; o < LR; o *= 2) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  // least e with max|q| <= 448 * 2^e
+  const int bits = (int)(min(mx, 0x7F7Fu) << 16);
+  const int e = max((bits >> 23) - 127 - 8 + ((bits & 0x7FFFFF) > 0x600000 ? 1 : 0), -118);
+  const float down = pow2f(-e);
+  const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // a row's factor is not negative: see the maximum
+  uint32_t hi[4], rest[4];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t y = w[k] ^ flip;
+    // (FP16 holds what lies above 2^-23 of the largest exactly; the difference to the nearest code is exact)
+    const uint32_t f = pack_f16x2(__uint_as_float(y << 16) * down, __uint_as_float(y & 0xFFFF0000u) * down);
+    const uint32_t c = e4m3x2_of_f16x2(f), d = e4m3x2_of_f16x2(sub_f16x2(f, e4m3x2_to_f16x2(c)));
+    hi[k / 2] = k & 1 ? hi[k / 2] | c << 16 : c;
+    rest[k / 2] = k & 1 ? rest[k / 2] | d << 16 : d;
+  }
+  if (!in) return;
+  const size_t at = (size_t)h * a.q_rows + (size_t)t * a.G + (hq - h * a.G), term = (size_t)a.H * a.q_rows;
+  reinterpret_cast<uint4*>(a.codes + at * D)[sub] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  reinterpret_cast<uint4*>(a.codes + (term + at) * D)[sub] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+  if (sub == 0) a.factors[at] = mx > 0x7F7Fu ? __int_as_float(0x7FC00000) : fabsf(a.scale) * LOG2E * pow2f(e);
+}
+
+// ---------------------------------------------------------------------------
 // The attention kernel
 // ---------------------------------------------------------------------------
 
@@ -289,59 +333,34 @@ __device__ __noinline__ float careful_weights(uint32_t S, const float* kf, const
   return sum;
 }
 
+// The largest of half a block's S times the keys' scales.
+__device__ __noinline__ float half_max(uint32_t S, const float* kf) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 32; c += 16) {
+    uint32_t s[16];
+    tmem_ld16(S + c, s);
+    tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < 16; x += 2) mx = max3(mx, __uint_as_float(s[x]) * kf[c + x], __uint_as_float(s[x + 1]) * kf[c + x + 1]);
+  }
+  return mx;
+}
+// 32 weights times sc.
+__device__ __noinline__ void rescale_weights(uint32_t P, float sc) {
+  uint32_t w[16];
+  tmem_ld16(P, w);
+  tmem_wait_ld();
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    const float2 y = f16x2_to_f32x2(w[x]);
+    w[x] = pack_f16x2(y.x * sc, y.y * sc);
+  }
+  tmem_st16(P, w);
+}
+
 // What runs once a unit, or seldom, is out of line: the loops over the blocks shall stay close together.
 //
-// Queries of a unit's rows (of up to two tiles) into two E4M3 terms, by four warps, four lanes a row; factors: of the rows'
-// logits.
-template <int D>
-__device__ __noinline__ void load_queries(const TreeParams& a, const Item& x, unsigned char* sq, int buf0, float* factors) {
-  using M = TreeMem<D>;
-  constexpr int CL = D / 4, NV = CL / 8;   // channels a lane, 16-byte loads
-  const int lane = threadIdx.x & 31, sub = lane & 3, rows = x.n * a.G, per_one = 128 / a.G;
-  const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // a row's factor is not negative: see the maximum
-#pragma unroll 1
-  for (int r = 8 * ((threadIdx.x >> 5) - W_CONV) + lane / 4; r - lane / 4 < rows; r += 32) {
-    const int tl = r / a.G;
-    uint4 w[NV];
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)(x.t0 + tl) * a.q_stride + (size_t)(x.h * a.G + r - tl * a.G) * D) + sub * NV;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) w[i] = r < rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-    uint32_t mx = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      mx = __vmaxu2(__vmaxu2(mx, __vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu)), __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu));
-    mx = max(mx & 0xFFFFu, mx >> 16);
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // least e with max|q| <= 448 * 2^e
-    const int bits = (int)(min(mx, 0x7F7Fu) << 16);
-    const int e = max((bits >> 23) - 127 - 8 + ((bits & 0x7FFFFF) > 0x600000 ? 1 : 0), -118);
-    const float down = pow2f(-e);
-    // tile and row in it: a tile holds whole tokens
-    const int tile = r >= per_one * a.G, rr = r - tile * per_one * a.G;
-    unsigned char* const tile_at = sq + (buf0 + tile) * 2 * M::TERM;
-#pragma unroll
-    for (int i = 0; i < NV / 2; ++i) {
-      uint32_t hi[4], rest[4];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint4& v = w[2 * i + k / 4];
-        const uint32_t y = (k % 4 == 0 ? v.x : k % 4 == 1 ? v.y : k % 4 == 2 ? v.z : v.w) ^ flip;
-        // (FP16 holds what lies above 2^-23 of the largest exactly; the difference to the nearest code is exact)
-        const uint32_t h = pack_f16x2(__uint_as_float(y << 16) * down, __uint_as_float(y & 0xFFFF0000u) * down);
-        const uint32_t c = e4m3x2_of_f16x2(h), d = e4m3x2_of_f16x2(sub_f16x2(h, e4m3x2_to_f16x2(c)));
-        hi[k / 2] = k & 1 ? hi[k / 2] | c << 16 : c;
-        rest[k / 2] = k & 1 ? rest[k / 2] | d << 16 : d;
-      }
-      unsigned char* dst = tile_at + swizzled<D>(rr, sub * (NV / 2) + i);
-      if (r < rows) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(dst + M::TERM) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
-      }
-    }
-    if (sub == 0 && r < rows) factors[tile * 128 + rr] = mx > 0x7F7Fu ? __int_as_float(0x7FC00000) : fabsf(a.scale) * LOG2E * pow2f(e);
-  }
-}
 // Slots of a block that some row of the unit sees.  By a whole warp.
 __device__ __noinline__ uint64_t seen_by_some(const TreeParams& a, const Item& x) {
   uint64_t seen = 0;
@@ -371,33 +390,37 @@ __device__ __noinline__ bool far_below(const unsigned char* raw, int c0, int c1,
 }
 // The outputs of row r of group w: of two tiles each group has its rows; of one tile (O, O + 128: either group's part of
 // every row, times c0 and c1) each joins half of the channels.
+// (tr, head: the row's token in its tile and its head.)
 template <int D>
-__device__ __noinline__ void store_rows(const TreeParams& a, const Item& x, uint32_t O, int r, int w, float m, float l, float c0,
-                                        float c1) {
+__device__ __noinline__ void store_rows(const TreeParams& a, const Item& x, uint32_t O, int r, int per_one, int tr, int head, int w,
+                                        float m, float l, float c0, float c1) {
   const bool two = x.flags & F_TWO, some = x.flags & F_SOME, halves = some && !two, both = halves && x.blk > 1;
-  const int per_one = 128 / a.G, tr = r / a.G, row = (two ? w * per_one * a.G : 0) + r, tok = row / a.G;
+  const int row = (two ? w * per_one * a.G : 0) + r, tok = (two ? w * per_one : 0) + tr;
   const bool my = tr < per_one && tok < x.n && (two || some || w == 0);
   if (!__any_sync(0xffffffffu, my)) return;
-  const size_t at = ((size_t)(x.t0 + tok) * a.H + x.h) * a.G + (row - tok * a.G);
-  const size_t part = (size_t)x.slot * a.rows + row;
+  const size_t at = ((size_t)(x.t0 + tok) * a.H + x.h) * a.G + head, part = (size_t)x.slot * a.rows + row;
   if (my && (two || w == 0)) {
     if (x.slot >= 0) a.ml[part] = make_float2(m, l);
     else if (a.lse) a.lse[at] = l == 0.0f ? -INFINITY : LN2 * ((m > -INFINITY ? m - P_SHIFT : 0.0f) + log2f(l));
   }
   if (two) O += w * 128;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (x.slot < 0) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    c0 *= inv, c1 *= inv;
+  }
   const int cb = halves ? w * (D / 2) : 0, ce = halves ? cb + D / 2 : D;
+  const bool none = !some || (x.slot < 0 && l == 0.0f);
 #pragma unroll 1
   for (int c = cb; c < ce; c += 16) {
-    uint32_t o[16], o1[16], b[8];
-    if (some) tmem_ld16(O + c, o);
+    uint32_t o[16], o1[16];
+    tmem_ld16(O + c, o);
     if (both) tmem_ld16(O + 128 + c, o1);
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = some ? __uint_as_float(o[i]) * c0 : 0.0f;
-      if (both) v = fmaf(__uint_as_float(o1[i]), c1, v);
-      o[i] = __float_as_uint(v);
+    for (int i = 0; i < 16; ++i) o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * c0);
+    if (both && !none) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), c1, __uint_as_float(o[i])));
     }
     if (!my) continue;
     if (x.slot >= 0) {
@@ -405,8 +428,9 @@ __device__ __noinline__ void store_rows(const TreeParams& a, const Item& x, uint
       for (int i = 0; i < 16; i += 4)
         *reinterpret_cast<uint4*>(a.part + part * D + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
     } else {
+      uint32_t b[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = l == 0.0f ? 0u : pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+      for (int i = 0; i < 8; ++i) b[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
       st_v8(a.out + at * D + c, b);
     }
   }
@@ -456,7 +480,8 @@ struct TreeBars {
 
 template <int D, bool PATIENT>
 __global__ void __launch_bounds__(TT_THREADS, 1)
-    kv_tree_kernel(const __grid_constant__ TreeParams a, const __grid_constant__ CUtensorMap key_map) {
+    kv_tree_kernel(const __grid_constant__ TreeParams a, const __grid_constant__ CUtensorMap key_map,
+                   const __grid_constant__ CUtensorMap query_map) {
   using M = TreeMem<D>;
   constexpr uint32_t COLS = 512;   // tensor memory: S / P of either softmax group twice at 0 .. 255, their O at 256 and 384
   constexpr int PANEL = KV_BLOCK * 128;
@@ -466,7 +491,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   __shared__ int to_s[TT_K], to_o[TT_V16];
   __shared__ __align__(16) float kf[TT_SC][KV_BLOCK], ev_f[TT_SC][KV_BLOCK];   // keys' scales; the values' exponents
   __shared__ float ev_top[TT_SC];                  // the exponent that all weights of a block have; NaN: each has its own
-  __shared__ float q_factor[TT_QF][2][128];
   __shared__ float2 swap[2][128];                  // a row's maximum and sum in either softmax group
   __shared__ PlanMem plan;
   __shared__ uint32_t tmem_s;
@@ -476,12 +500,12 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   static_assert(TT_K == 4 && TT_V == 4 && TT_V16 == 4 && TT_GROUP == 4, "barriers are set up in one loop");
   if (tid < 4) {
     const int i = tid, g = i & 1, j = i >> 1;
-    mbar_init(&bar.k_full[i], 1), mbar_init(&bar.k_empty[i], 1), mbar_init(&bar.v_full[i], 1), mbar_init(&bar.v_empty[i], 4);
-    mbar_init(&bar.v16_full[i], 4), mbar_init(&bar.v16_empty[i], 1);
+    mbar_init(&bar.k_full[i], 1), mbar_init(&bar.k_empty[i], 2), mbar_init(&bar.v_full[i], 1), mbar_init(&bar.v_empty[i], 4);
+    mbar_init(&bar.v16_full[i], 2), mbar_init(&bar.v16_empty[i], 1);
     mbar_init(&bar.gr_full[0][i], 1), mbar_init(&bar.gr_full[1][i], 1), mbar_init(&bar.gr_empty[0][i], 4), mbar_init(&bar.gr_empty[1][i], 4);
     mbar_init(&bar.s_full[g][j], 1), mbar_init(&bar.p_full[g][j], 4), mbar_init(&bar.o_done[g][j], 1);
-    if (j == 0) mbar_init(&bar.q_full[g], 4), mbar_init(&bar.q_empty[g], 1);
-    if (i == 0) mbar_init(&bar.swap_in, 8), mbar_init(&bar.swap_out, 8), mbar_init(&bar.drain, 2);
+    if (j == 0) mbar_init(&bar.q_full[g], 1), mbar_init(&bar.q_empty[g], 2);
+    if (i == 0) mbar_init(&bar.swap_in, 8), mbar_init(&bar.swap_out, 8), mbar_init(&bar.drain, 3);
     fence_mbar_init();
   }
   if (warp == W_S) {
@@ -494,9 +518,9 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   pdl_launch_dependents();   // (only now that the CTA holds its tensor memory: see kv_attend_tiles.cu)
   tc_fence_after();
   const uint32_t tmem = tmem_s;
-  pdl_wait();
-
+  // What the plan is made from was there before the queries' kernel let this one start; what that kernel writes was not.
   make_plan(a, plan);
+  pdl_wait();
   const bool works = plan.lo < plan.hi;
   Waits<PATIENT> wait{PATIENT ? TRIES : (int)min(max(a.wait / 32, 1LL), (long long)INT32_MAX)};
 
@@ -505,7 +529,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   } else if (warp == W_LOAD) {
     // ---- walk: tiles from plan.found on, kv heads, blocks
     const int per_one = 128 / a.G;
-    int it = 0, kb = 0;
+    int it = 0, kb = 0, qb = 0;   // items, blocks; the next one-tile unit's query buffer
+    Pair uses{0, 0};              // units of either query buffer so far
     Join join{0, 0, 0, 0};
     // to the S warp and to the converting warps; page < 0: nothing to copy
     auto publish = [&](const Item& x, int page) {
@@ -569,36 +594,58 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         }
         if (top >= 0 && top / KV_BLOCK >= a.tab.N && b0 == 0 && lane == 0) set_err(a.err, BRE_DEVERR_PAGE);
         int jb = 0;
-        if (top >= 0) publish(Item{t0, n, h, 0, F_BEGIN | two, slot, begin, kb}, -1);
 #pragma unroll 1
         for (int g = b0; g < b1 && top >= 0 && wait.left; g += 32) {
           const int my = g + lane < b1 ? kv_page(a.tab, s, g + lane, a.err) : -1;
 #pragma unroll 1
           for (uint32_t todo = __ballot_sync(0xffffffffu, my >= 0); todo && wait.left; todo &= todo - 1) {
             const int src = __ffs(todo) - 1, blk = g + src;
-            const int flags = F_BLOCK | (blk < whole ? F_FULL : 0) | two | (jb & 1 ? F_ODD : 0) |
+            if (jb == 0) {   // the queries of one or two tiles; the buffers are free when the S of their former unit have been formed
+              const int first = two ? 0 : qb, last = two ? 1 : qb;
+#pragma unroll 1
+              for (int b = first; b <= last; ++b) {
+                wait(&bar.q_empty[b], uses[b] + 1);
+                if (wait.left) {
+                  if (lane == 0) {
+                    mbar_arrive_expect_tx(&bar.q_full[b], 2 * M::TERM);
+#pragma unroll 1
+                    for (int term = 0; term < 2; ++term)
+                      tma_load_3d(sm + M::q + (2 * b + term) * M::TERM, &query_map, 0, (t0 + (b - first) * per_one) * a.G,
+                                  term * a.H + h, &bar.q_full[b]);
+                  }
+                  uses.add(b);
+                }
+              }
+              __syncwarp();
+              if (!two) qb ^= 1;
+            }
+            const int flags = F_BLOCK | (blk < whole ? F_FULL : 0) | two | (jb & 1 ? F_ODD : 0) | (jb == 0 ? F_BEGIN : 0) |
                               (jb < (two ? 1 : 2) ? F_NEW : 0);
             publish(Item{t0, n, h, blk, flags, slot, begin, kb}, __shfl_sync(0xffffffffu, my, src));
             ++kb, ++jb;
           }
         }
-        publish(Item{t0, n, h, jb, F_END | two | (jb ? F_SOME : 0), slot, top >= 0 ? begin : -1, kb}, -1);
+        publish(Item{t0, n, h, jb, F_END | two | (jb ? F_SOME : 0), slot, begin, kb}, -1);
       }
       t0 += n;
     }
     publish(Item{0, 0, 0, 0, F_EXIT, -1, 0, 0}, -1);
     if (lane == 0) a.join[blockIdx.x] = join;
-    if (!wait.left)   // copies that are on their way still write to this CTA's shared memory
+    if (!wait.left) {   // copies that are on their way still write to this CTA's shared memory
       for (int i = max(0, it - 4); i < it; ++i) {
         mbar_wait_bounded(&bar.k_full[i & 3], i >> 2 & 1, AT_WAIT);
         mbar_wait_bounded(&bar.v_full[i & 3], i >> 2 & 1, AT_WAIT);
       }
-  } else if (warp == W_S) {
-    // ---- S = Q K^T: E4M3 operands, FP32 sums, M = 128
+      for (int b = 0; b < 2; ++b)
+        if (uses[b]) mbar_wait_bounded(&bar.q_full[b], (uses[b] - 1) & 1, AT_WAIT);
+    }
+  } else if (warp == W_S || warp == W_S + 1) {
+    // ---- S = Q K^T: E4M3 operands, FP32 sums, M = 128; a block each in turn
     const uint32_t id_s = (1u << 4) | ((uint32_t)(KV_BLOCK >> 3) << 17) | ((128u >> 4) << 24);
     const uint64_t q0 = desc_codes<D>(smem_u32(sm + M::q)), k0 = desc_codes<D>(smem_u32(sm + M::k));
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    int live = 0, qb = 0;           // the unit's query buffers; the next one-tile unit's buffer
+    const int me = warp - W_S;
+    int live = 0, qb = 0, kb = 0;   // the unit's query buffers; the next one-tile unit's buffer; blocks
     Pair cs{0, 0}, uses{0, 0};      // S of either group, units of either query buffer so far
 #pragma unroll 1
     for (int it = 0;; ++it) {
@@ -607,28 +654,32 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       if (!wait.left) break;
       // (a warp reduction: what the MMAs' operands are formed from is then in uniform registers, where they want it)
       const int flags = (int)__reduce_or_sync(0xffffffffu, (uint32_t)to_s[ks]), two = flags & F_TWO ? 1 : 0;
+      const bool mine = flags & F_BLOCK && (kb & 1) == me;
+      if (!mine && lane == 0) mbar_arrive(&bar.k_empty[ks]);
       if (!(flags & F_BLOCK)) {
         if (flags & F_EXIT) break;
-        if (elect_one()) {
-          if (flags & F_END && live & 1) mma_commit(&bar.q_empty[0]);
-          if (flags & F_END && live & 2) mma_commit(&bar.q_empty[1]);
-          mbar_arrive(&bar.k_empty[ks]);
-        }
-        __syncwarp();
-        if (flags & F_BEGIN) {
-          live = two ? 3 : 1 << qb;
-          if (live & 1) wait(&bar.q_full[0], uses.a);
-          if (live & 2) wait(&bar.q_full[1], uses.b);
-        }
-        if (flags & F_END) {
-          if (live && !two) qb ^= 1;
+        if (live) {
+          if (elect_one()) {   // (each warp's commit goes by its own products)
+            if (live & 1) mma_commit(&bar.q_empty[0]);
+            if (live & 2) mma_commit(&bar.q_empty[1]);
+          }
+          __syncwarp();
+          if (!two) qb ^= 1;
           uses.a += live & 1, uses.b += live >> 1, live = 0;
         }
         continue;
       }
+      ++kb;
+      if (flags & F_BEGIN) {
+        live = two ? 3 : 1 << qb;
+        if (live & 1) wait(&bar.q_full[0], uses.a);
+        if (live & 2) wait(&bar.q_full[1], uses.b);
+      }
 #pragma unroll 1
       for (int g = 0; g <= two; ++g) {
         const int w = two ? g : flags & F_ODD ? 1 : 0, qt = two ? g : qb, c = cs[w], buf = c & 1;
+        cs.add(w);
+        if (!mine) continue;
         wait(&bar.o_done[w][buf], (c >> 1) + 1);   // the weights that lay in S's columns have been used
         tc_fence_after();
         if (elect_one()) {
@@ -643,7 +694,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
           if (g == two) mma_commit(&bar.k_empty[ks]);
         }
         __syncwarp();
-        cs.add(w);
       }
     }
     // products that are under way still use tensor and shared memory
@@ -682,16 +732,16 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     if (elect_one()) mma_commit(&bar.drain);
     __syncwarp();
   } else if (warp >= W_CONV) {
-    // ---- queries to two terms; codes of values to FP16
-    constexpr int CH = D / 16, NP = KV_BLOCK * CH / 128;   // 16-code pieces of a row, pieces a thread
-    const int cw = warp - W_CONV, dt = cw * 32 + lane;
+    // ---- codes of values to FP16
+    constexpr int CH = D / 16, NP = KV_BLOCK * CH / 64;   // 16-code pieces of a row, pieces a thread
+    const int cw = warp - W_CONV, pair = cw >> 1, dt = (cw & 1) * 32 + lane;
     // where a thread's pieces go: two swizzled ones of 16 bytes each; the lanes of odd panels start with the second, so that
     // eight lanes meet all banks.  (The rows of a thread are whole multiples of 8 apart.)
     const int c = dt % CH, x0 = dt / CH;
     const bool second = (c / 4) & 1;
     const int o0 = (c / 4) * PANEL + x0 * 128 + (((2 * (c % 4)) ^ (x0 & 7)) << 4), first = second ? o0 ^ 16 : o0;
-    int qb = 0, units = 0, last = 0, kb = 0;
-    Pair uses{0, 0}, gr{0, 0};
+    int kb = 0;
+    Pair gr{0, 0};
 #pragma unroll 1
     for (int it = 0;; ++it) {
       const int vs = it & 3;
@@ -699,7 +749,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       if (!wait.left) break;
       const int flags = to_v[vs].flags, two = flags & F_TWO;
       // the groups that hear of it
-      const int who = flags & F_BEGIN ? 0 : !(flags & F_BLOCK) || two ? 3 : flags & F_ODD ? 2 : 1;
+      const int who = !(flags & F_BLOCK) || two ? 3 : flags & F_ODD ? 2 : 1;
       auto tell = [&]() {   // by one warp
 #pragma unroll 1
         for (int g = 0; g < 2; ++g) {
@@ -714,7 +764,9 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         }
         __syncwarp();
       };
-      if (flags & F_BLOCK) {
+      if (flags & F_BLOCK && (kb & 1) != pair) {
+        ++kb;   // the other pair's
+      } else if (flags & F_BLOCK) {
         const int st = kb & 3, sp = kb % TT_SC;
         // slots that some row sees (others may never have been written: their values become zeros)
         uint64_t seen = ~0ull;
@@ -729,7 +781,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         const int least = __reduce_min_sync(0xffffffffu, min(c0 ? c0 : 255, c1 ? c1 : 255));
         bool careful = top > EV_LARGE;
         if (top - least > 15) careful |= far_below<D>(raw, c0, c1, top);
-        if ((kb & 3) == cw) {   // this block's scales for the softmax
+        if ((kb >> 1 & 1) == (cw & 1)) {   // this block's scales for the softmax
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int x = lane + 32 * i, ek = scales[x], ev = i ? e1 : e0;
@@ -740,65 +792,42 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
           __syncwarp();
           tell();
         }
-        uint4 cur[NP];
-        uint32_t up[NP];   // 2^(the row's scale - the largest), at least 2^-15
-#pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          cur[j] = reinterpret_cast<const uint4*>(raw)[dt + j * 128];
-          const int d = min(max(top - (int)scales[KV_BLOCK + x0 + j * (128 / CH)], 0), 15);
-          up[j] = careful ? 0x3C003C00u : (d < 15 ? (uint32_t)(15 - d) << 10 : 1u << 9) * 0x10001u;
-        }
-        if (!(flags & F_FULL)) {
-#pragma unroll
-          for (int j = 0; j < NP; ++j)
-            if (!(seen >> (x0 + j * (128 / CH)) & 1ull)) cur[j] = make_uint4(0, 0, 0, 0);
-        }
         wait(&bar.v16_empty[st], (kb >> 2) + 1);
         unsigned char* const to = sm + M::v16 + st * M::V16 + first;
         const int other = first & 16 ? -16 : 16;
-#pragma unroll
+#pragma unroll 2
         for (int j = 0; j < NP; ++j) {
-          const uint32_t u[4] = {second ? cur[j].z : cur[j].x, second ? cur[j].w : cur[j].y, second ? cur[j].x : cur[j].z,
-                                 second ? cur[j].y : cur[j].w};
+          const int x = x0 + j * (64 / CH);
+          uint4 cur = reinterpret_cast<const uint4*>(raw)[dt + j * 64];
+          if (!(seen >> x & 1ull)) cur = make_uint4(0, 0, 0, 0);
+          // 2^(the row's scale - the largest), at least 2^-15
+          const int d = min(max(top - (int)scales[KV_BLOCK + x], 0), 15);
+          const uint32_t up = careful ? 0x3C003C00u : (d < 15 ? (uint32_t)(15 - d) << 10 : 1u << 9) * 0x10001u;
+          const uint32_t u[4] = {second ? cur.z : cur.x, second ? cur.w : cur.y, second ? cur.x : cur.z, second ? cur.y : cur.w};
           uint32_t o[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            o[2 * k] = mul_f16x2(e4m3x2_to_f16x2(u[k] & 0xFFFFu), up[j]);
-            o[2 * k + 1] = mul_f16x2(e4m3x2_to_f16x2(u[k] >> 16), up[j]);
+            o[2 * k] = mul_f16x2(e4m3x2_to_f16x2(u[k] & 0xFFFFu), up);
+            o[2 * k + 1] = mul_f16x2(e4m3x2_to_f16x2(u[k] >> 16), up);
           }
-          *reinterpret_cast<uint4*>(to + j * (128 / CH) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(to + j * (128 / CH) * 128 + other) = make_uint4(o[4], o[5], o[6], o[7]);
+          *reinterpret_cast<uint4*>(to + j * (64 / CH) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(to + j * (64 / CH) * 128 + other) = make_uint4(o[4], o[5], o[6], o[7]);
         }
         fence_proxy_async_smem();
         if (dt == 0) to_o[st] = flags;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.v16_full[st]);
         ++kb;
-      } else if (flags & F_BEGIN) {
-        // rows of up to two tiles; the buffers are free when the S of their former unit have been formed
-        last = two ? 3 : 1 << qb;
-        if (last & 1) wait(&bar.q_empty[0], uses.a + 1);
-        if (last & 2) wait(&bar.q_empty[1], uses.b + 1);
-        load_queries<D>(a, to_v[vs], sm + M::q, two ? 0 : qb, &q_factor[units % TT_QF][0][0]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (last & 1) mbar_arrive(&bar.q_full[0]);
-          if (last & 2) mbar_arrive(&bar.q_full[1]);
-        }
       } else {
         if (cw == 0) tell();
         if (flags & F_EXIT) {
+          if ((kb & 1) != pair) break;
           const int st = kb & 3;
           wait(&bar.v16_empty[st], (kb >> 2) + 1);
           if (dt == 0) to_o[st] = F_EXIT;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.v16_full[st]);
           break;
-        }
-        if (last) {
-          ++units, uses.a += last & 1, uses.b += last >> 1, last = 0;
-          if (!two) qb ^= 1;
         }
       }
       gr.a += who & 1, gr.b += who >> 1;
@@ -807,9 +836,9 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     }
   } else {
     // ---- softmax: row r of group w
-    const int w = warp >> 2, r = tid & 127;
+    const int w = warp >> 2, r = tid & 127, per_one = 128 / a.G, tr = r / a.G, head = r - tr * a.G;
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);   // lanes 32 (warp % 4) ..
-    int units = 0, swaps = 0, done = 0, mine = 0;   // units that had blocks, of one tile; products of the group, of this unit
+    int swaps = 0, done = 0, mine = 0;              // units of one tile; products of the group, of this unit
     float m = -INFINITY, l = 0.0f, f = 0.0f;        // m: the maximum that the weights are held against
     int tl = 0;
     bool warp_live = false;
@@ -823,69 +852,60 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         const int buf = done & 1, sp = x.kb % TT_SC;
         const uint32_t S = lane_base + w * 128 + buf * 64;
         if (flags & F_NEW) {
-          const int per_one = 128 / a.G, tr = r / a.G;
           tl = (flags & F_TWO ? w * per_one : 0) + tr;
           const bool live = tr < per_one && tl < x.n;
-          if (!live) tl = -1;
           warp_live = __any_sync(0xffffffffu, live);
+          f = live ? a.factors[(size_t)x.h * a.q_rows + (size_t)(x.t0 + tl) * a.G + head] : 0.0f;
+          if (!live) tl = -1;
         }
         wait(&bar.s_full[w][buf], done >> 1);
         tc_fence_after();
-        // (S has been formed from the queries, so all of their factors are there; what comes of other rows does not matter)
-        if (flags & F_NEW) f = tl >= 0 ? q_factor[units % TT_QF][flags & F_TWO ? w : 0][r] : 0.0f;
         if (warp_live) {
           const float top = ev_top[sp];
           if (flags & F_FULL && top == top) {
             // The ordinary way: every row sees the whole block, and the block's values have one scale.  The weights are formed
             // against the maximum so far without looking for the block's own.  Their sum bounds them: while it is below FP16's
-            // largest the maximum will do (it lags by 2^7 at most).  Else, and at first, S is looked through for the maximum.
-            uint32_t s[64], pk[32];
-            float sum;
-            auto weigh = [&]() {
-              const float add = top - (m > -INFINITY ? m - P_SHIFT : 0.0f);
-              const uint64_t f2 = pack2(f, f), a2 = pack2(add, add);
-              float sum0 = 0.0f, sum1 = 0.0f;
-              tmem_ld32(S, s);
-              tmem_ld32(S + 32, s + 32);
-              tmem_wait_ld();
+            // largest the maximum will do (it lags by 2^7 at most).  Else, and at first, the maximum of the half block is found.
+            // (Half a block at a time: a loop of half the code; the SM's instruction cache is short for five roles.)
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              uint32_t pk[16];
+              float sum;
+#pragma unroll 1
+              for (bool again = false;; again = true) {
+                uint32_t s[32];
+                const float* const kh = &kf[sp][half * 32];
+                const float add = top - (m > -INFINITY ? m - P_SHIFT : 0.0f);
+                const uint64_t f2 = pack2(f, f), a2 = pack2(add, add);
+                float sum0 = 0.0f, sum1 = 0.0f;
+                tmem_ld32(S + half * 32, s);
+                tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < 64; c += 4) {
-                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&kf[sp][c]);
-                const float2 v0 = unpack2(fma2(mul2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), k.x), f2, a2));
-                const float2 v1 = unpack2(fma2(mul2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), k.y), f2, a2));
-                const float p0 = ex2(v0.x), p1 = ex2(v0.y), p2 = ex2(v1.x), p3 = ex2(v1.y);
-                sum0 += p0, sum1 += p1;
-                sum0 += p2, sum1 += p3;
-                pk[c / 2] = pack_f16x2(p0, p1), pk[c / 2 + 1] = pack_f16x2(p2, p3);
+                for (int c = 0; c < 32; c += 4) {
+                  const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(kh + c);
+                  const float2 v0 = unpack2(fma2(mul2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), k.x), f2, a2));
+                  const float2 v1 = unpack2(fma2(mul2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), k.y), f2, a2));
+                  const float p0 = ex2(v0.x), p1 = ex2(v0.y), p2 = ex2(v1.x), p3 = ex2(v1.y);
+                  sum0 += p0, sum1 += p1;
+                  sum0 += p2, sum1 += p3;
+                  pk[c / 2] = pack_f16x2(p0, p1), pk[c / 2 + 1] = pack_f16x2(p2, p3);
+                }
+                sum = sum0 + sum1;
+                if (again || !__any_sync(0xffffffffu, tl >= 0 && (sum > P_MOST || m == -INFINITY))) break;
+                // all rows of the warp take their new maximum
+                const float mx = fmaf(half_max(S + half * 32, kh), f, top);   // (f is not negative; a query that gives NaN has a NaN maximum)
+                if (mine > 0) wait(&bar.o_done[w][buf ^ 1], (done - 1) >> 1);
+                tc_fence_after();
+                // (by whole steps, so that the weights of the block's first half stay FP16 numbers)
+                const float then = m == -INFINITY ? mx : m + fmaxf(ceilf(mx - m), 0.0f), d = m > -INFINITY ? m - then : 0.0f;
+                l = scale_sum(l, d);
+                m = then;
+                if (mine > 0) rescale<D>(lane_base + 256 + w * 128, ex2(d));
+                if (half) rescale_weights(S, ex2(d));
               }
-              sum = sum0 + sum1;
-            };
-            for (bool again = false;; again = true) {
-              weigh();
-              if (again || !__any_sync(0xffffffffu, tl >= 0 && (sum > P_MOST || m == -INFINITY))) break;
-              tmem_ld32(S, s);
-              tmem_ld32(S + 32, s + 32);
-              tmem_wait_ld();
-              float mx = -INFINITY, my = -INFINITY;
-#pragma unroll
-              for (int c = 0; c < 64; c += 4) {
-                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&kf[sp][c]);
-                const float2 v0 = unpack2(mul2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), k.x));
-                const float2 v1 = unpack2(mul2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), k.y));
-                mx = max3(mx, v0.x, v0.y), my = max3(my, v1.x, v1.y);
-              }
-              mx = fmaf(fmaxf(mx, my), f, top);   // (f is not negative; a query that gives NaN has a NaN maximum)
-              // all rows of the warp take their new maximum
-              if (mine > 0) wait(&bar.o_done[w][buf ^ 1], (done - 1) >> 1);
-              tc_fence_after();
-              const float then = m == -INFINITY ? mx : fmaxf(m, mx), d = m > -INFINITY ? m - then : 0.0f;
-              l = scale_sum(l, d);
-              m = then;
-              if (mine > 0) rescale<D>(lane_base + 256 + w * 128, ex2(d));
+              tmem_st16(S + half * 16, pk);
+              l = fmaf(sum, ex2(-top), l);
             }
-            tmem_st16(S, pk);
-            tmem_st16(S + 16, pk + 16);
-            l = fmaf(sum, ex2(-top), l);
           } else {
             const uint64_t seen = tl < 0 ? 0ull : flags & F_FULL ? ~0ull
                 : seen_bits(a.mask ? a.mask + (size_t)(x.t0 + tl) * a.words : nullptr, a.words, x.begin, __ldg(a.pos + x.t0 + tl), x.blk);
@@ -927,7 +947,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         l = scale_sum(y0.y, y0.x - ref) + (both ? scale_sum(y1.y, y1.x - ref) : 0.0f);
       }
       tc_fence_after();
-      if (wait.left) store_rows<D>(a, x, lane_base + 256, r, w, m, l, c0, c1);
+      if (wait.left) store_rows<D>(a, x, lane_base + 256, r, per_one, tr, head, w, m, l, c0, c1);
       if (halves) {   // neither group goes on before both have read
         tc_fence_before();
         __syncwarp();
@@ -935,7 +955,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         wait(&bar.swap_out, swaps);
         ++swaps;
       }
-      units += x.begin >= 0;   // (a unit of padding has no queries)
       m = -INFINITY, l = 0.0f, mine = 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.gr_empty[w][it & 3]);
@@ -967,7 +986,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_tree_join_kernel(const Tre
 }
 
 template <int D, bool PATIENT>
-cudaError_t launch(const TreeParams& a, const CUtensorMap& keys, int ctas, cudaStream_t s) {
+cudaError_t launch(const TreeParams& a, const CUtensorMap& keys, const CUtensorMap& queries, int ctas, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};   // devices on which the kernel may have its shared memory
   int dev = 0;
   cudaGetDevice(&dev);
@@ -977,7 +996,10 @@ cudaError_t launch(const TreeParams& a, const CUtensorMap& keys, int ctas, cudaS
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  cudaError_t e = launch_k(kv_tree_kernel<D, PATIENT>, dim3((unsigned)ctas), dim3(TT_THREADS), TreeMem<D>::bytes, s, a, keys);
+  const long long pieces = (long long)a.T * a.H * a.G * (D / 16);
+  cudaError_t e = launch_k(kv_tree_queries_kernel<D>, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, s, a);
+  if (e != cudaSuccess) return e;
+  e = launch_k(kv_tree_kernel<D, PATIENT>, dim3((unsigned)ctas), dim3(TT_THREADS), TreeMem<D>::bytes, s, a, keys, queries);
   if (e != cudaSuccess) return e;
   // (a part's rows over several CTAs, of which those for a CTA that begins no shared unit have nothing to do)
   const int chunks = a.rows < 32 ? a.rows : 32;
@@ -989,13 +1011,18 @@ int slot_rows(int T, int G) {   // rows of a part: those of two tiles, or all th
   return (int)(all < most ? all : most);
 }
 
+int query_rows(int T, int G) { return T * G < 128 ? 128 : T * G; }   // (a copied box is not larger than what it is copied from)
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+size_t codes_bytes(int T, int H, int G, int D) { return up256((size_t)2 * H * query_rows(T, G) * D); }
+
 }  // namespace
 
 size_t kv_tree_ws_bytes(int T, int Hq, int H, int D) {
   const int G = Hq / H;
   if (G < 1 || G > 16) return 0;
   const size_t slots = 2 * TT_MAX_CTAS, rows = slot_rows(T, G);
-  const size_t tiles = TT_MAX_CTAS * sizeof(Join) + slots * rows * (sizeof(float2) + D * sizeof(float));
+  const size_t tiles = codes_bytes(T, H, G, D) + up256((size_t)H * query_rows(T, G) * sizeof(float)) + TT_MAX_CTAS * sizeof(Join) +
+                       slots * rows * (sizeof(float2) + D * sizeof(float));
   const size_t single = tree_rows_ws_bytes(T, H, G, D);
   return tiles > single ? tiles : single;
 }
@@ -1016,7 +1043,10 @@ cudaError_t launch_kv_attend_tree(const TreeArgs& t, cudaStream_t s) {
   a.wait = ffn_wait_budget(0);   // 0: none set
   a.rows = slot_rows(a.T, G);
   const size_t slots = 2 * TT_MAX_CTAS;
-  a.join = static_cast<Join*>(t.ws);
+  a.q_rows = query_rows(a.T, G);
+  a.codes = static_cast<unsigned char*>(t.ws);
+  a.factors = reinterpret_cast<float*>(a.codes + codes_bytes(a.T, H, G, D));
+  a.join = reinterpret_cast<Join*>(reinterpret_cast<unsigned char*>(a.factors) + up256((size_t)H * a.q_rows * sizeof(float)));
   a.part = reinterpret_cast<float*>(a.join + TT_MAX_CTAS);
   a.ml = reinterpret_cast<float2*>(a.part + slots * a.rows * D);
   // a head's share of a page as rows of D bytes: 64 keys, 64 values, the scales
@@ -1024,12 +1054,16 @@ cudaError_t launch_kv_attend_tree(const TreeArgs& t, cudaStream_t s) {
   const uint64_t dims[3] = {(uint64_t)D, (uint64_t)(kv_page_bytes(D) / D), (uint64_t)c->n_pages * H};
   const uint64_t strides[2] = {(uint64_t)D, (uint64_t)kv_page_bytes(D)};
   const uint32_t box[3] = {(uint32_t)D, (uint32_t)KV_BLOCK, 1};
-  if (!encode_tiled(&keys, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c->pages, dims, strides, box,
-                    D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
-    return cudaErrorInvalidValue;
+  const auto swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (!encode_tiled(&keys, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c->pages, dims, strides, box, swizzle)) return cudaErrorInvalidValue;
+  CUtensorMap queries;
+  const uint64_t q_dims[3] = {(uint64_t)D, (uint64_t)a.q_rows, 2ull * H};
+  const uint64_t q_strides[2] = {(uint64_t)D, (uint64_t)a.q_rows * D};
+  const uint32_t q_box[3] = {(uint32_t)D, 128, 1};
+  if (!encode_tiled(&queries, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.codes, q_dims, q_strides, q_box, swizzle)) return cudaErrorInvalidValue;
   const int sms = device_sm_count(), ctas = sms < TT_MAX_CTAS ? sms : TT_MAX_CTAS;
-  if (a.wait) return D == 128 ? launch<128, false>(a, keys, ctas, s) : launch<64, false>(a, keys, ctas, s);
-  return D == 128 ? launch<128, true>(a, keys, ctas, s) : launch<64, true>(a, keys, ctas, s);
+  if (a.wait) return D == 128 ? launch<128, false>(a, keys, queries, ctas, s) : launch<64, false>(a, keys, queries, ctas, s);
+  return D == 128 ? launch<128, true>(a, keys, queries, ctas, s) : launch<64, true>(a, keys, queries, ctas, s);
 }
 
 }  // namespace bre
