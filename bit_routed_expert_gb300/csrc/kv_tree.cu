@@ -41,9 +41,11 @@ constexpr int W_CONV = 8, W_LOAD = 12, W_S = 13, W_O = 15;
 // warps may be apart.
 constexpr int TT_K = 4, TT_V = 4, TT_V16 = 4, TT_GROUP = 4, TT_SC = 16;
 constexpr int TT_MAX_CTAS = 160;
+constexpr int JOIN_CTAS = 4;             // of the joining kernel, for every one of the other
+constexpr int JOIN_FEW = 32;             // parts that a warp joins
 constexpr float P_MOST = 32768.0f;       // a block's sum of weights up to which they are FP16 numbers for sure
 // Costs of the shares: a block for one tile, for two tiles, and what a unit takes beside its blocks.
-constexpr int COST_ONE = 2, COST_TWO = 3, COST_UNIT = 6;
+constexpr int COST_ONE = 2, COST_TWO = 3, COST_UNIT = 10;
 
 enum : int { F_BLOCK = 1, F_FULL = 4, F_END = 8, F_EXIT = 16, F_TWO = 32, F_SOME = 64, F_ODD = 128, F_NEW = 256, F_BEGIN = 512 };
 
@@ -53,6 +55,9 @@ struct Item {
   int t0, n, h, blk;              // tokens, kv head; block (at the end: how many there were)
   int flags, slot, begin, kb;     // slot < 0: the whole unit, its outputs are final; running number of the block
 };
+
+constexpr int ITEM_WORDS = sizeof(Item) / sizeof(int);
+static_assert(ITEM_WORDS <= 32, "copied by a warp");
 
 // Where the parts of a unit that several CTAs share are to be found (written by the CTA that holds its first block).
 struct Join {
@@ -167,9 +172,13 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return a <= 0x7FFFFFFFLL && b <= 0x7FFFFFFFLL ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
+constexpr int KEPT = 32;
+
 struct PlanMem {
   int run[TT_WARPS], top[TT_THREADS];
   int last_run, last_top;  // of a chunk's last token: first token of its run, largest position of its tile
+  int kept_run[KEPT], kept_top[KEPT];   // before chunk i * every
+  long long kept_sum[KEPT];
   long long sum[TT_WARPS];
   long long lo, hi, per;   // this CTA's share, costs lo .. hi (none if hi <= lo); length of a share
   long long found_at;      // cost before the tile in which the share begins
@@ -180,14 +189,17 @@ struct PlanMem {
 // quick: the code runs once, and a line of it takes longer to fetch than to run.
 __device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, per_one = 128 / a.G;
+  const int every = (a.T / TT_THREADS / KEPT + 1) * TT_THREADS;
   long long lo = 0, per = 0, total = 0;
+  int start = 0, run = -1, top = INT32_MIN;
+  long long sum = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {   // a second pass, where the list is longer than the CTA, finds the place of the share
-    int run = -1, top = INT32_MIN;
-    long long sum = 0, c = 0, at = 0;
+    long long c = 0, at = 0;
     int from = 0;
 #pragma unroll 1
-    for (int base = 0; base < a.T; base += TT_THREADS) {
+    for (int base = start; base < a.T && (pass == 0 || sum <= lo); base += TT_THREADS) {
+      if (tid == 0 && base % every == 0) m.kept_run[base / every] = run, m.kept_top[base / every] = top, m.kept_sum[base / every] = sum;
       const int t = base + tid;
       const bool in = t < a.T, before = in && t > 0, behind = t + 1 < a.T;
       const int s = in ? __ldg(a.seq + t) : 0, p = in ? __ldg(a.pos + t) : -1;
@@ -237,6 +249,10 @@ __device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
       if (lo >= at && lo < at + c) m.found = from, m.found_at = at;
       break;
     }
+    // from the last state kept that lies not behind it
+    int k = (a.T - 1) / every;
+    while (k > 0 && m.kept_sum[k] > lo) --k;
+    start = k * every, run = m.kept_run[k], top = m.kept_top[k], sum = m.kept_sum[k];
   }
   if (tid == 0) m.lo = lo, m.hi = min(lo + per, total), m.per = per;
   __syncthreads();
@@ -361,12 +377,16 @@ __device__ __noinline__ void rescale_weights(uint32_t P, float sc) {
 
 // What runs once a unit, or seldom, is out of line: the loops over the blocks shall stay close together.
 //
-// Slots of a block that some row of the unit sees.  By a whole warp.
+// Slots of a block that token i of the unit sees.
+__device__ __noinline__ uint64_t seen_by(const TreeParams& a, const Item& x, int i) {
+  return seen_bits(a.mask ? a.mask + (size_t)(x.t0 + i) * a.words : nullptr, a.words, x.begin, __ldg(a.pos + x.t0 + i), x.blk);
+}
+// Slots that some row of it sees.  By a whole warp.
 __device__ __noinline__ uint64_t seen_by_some(const TreeParams& a, const Item& x) {
   uint64_t seen = 0;
 #pragma unroll 1
   for (int i = threadIdx.x & 31; i < x.n; i += 32)
-    seen |= seen_bits(a.mask ? a.mask + (size_t)(x.t0 + i) * a.words : nullptr, a.words, x.begin, __ldg(a.pos + x.t0 + i), x.blk);
+    seen |= seen_by(a, x, i);
   __syncwarp();
   return (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(seen >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)seen);
 }
@@ -494,7 +514,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   __shared__ float2 swap[2][128];                  // a row's maximum and sum in either softmax group
   __shared__ PlanMem plan;
   __shared__ uint32_t tmem_s;
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* const sm = sm_raw + ((0u - smem_u32(sm_raw)) & 1023u);   // (still known to be shared memory)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   static_assert(TT_K == 4 && TT_V == 4 && TT_V16 == 4 && TT_GROUP == 4, "barriers are set up in one loop");
@@ -738,8 +758,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     // where a thread's pieces go: two swizzled ones of 16 bytes each; the lanes of odd panels start with the second, so that
     // eight lanes meet all banks.  (The rows of a thread are whole multiples of 8 apart.)
     const int c = dt % CH, x0 = dt / CH;
-    const bool second = (c / 4) & 1;
-    const int o0 = (c / 4) * PANEL + x0 * 128 + (((2 * (c % 4)) ^ (x0 & 7)) << 4), first = second ? o0 ^ 16 : o0;
+    const int second = c & 4 ? 8 : 0;   // byte of the half that comes first
+    const int o0 = (c / 4) * PANEL + x0 * 128 + (((2 * (c % 4) + second / 8) ^ (x0 & 7)) << 4), away = (o0 ^ 16) - o0;
     int kb = 0;
     Pair gr{0, 0};
 #pragma unroll 1
@@ -750,85 +770,82 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       const int flags = to_v[vs].flags, two = flags & F_TWO;
       // the groups that hear of it
       const int who = !(flags & F_BLOCK) || two ? 3 : flags & F_ODD ? 2 : 1;
-      auto tell = [&]() {   // by one warp
-#pragma unroll 1
-        for (int g = 0; g < 2; ++g) {
-          if (!(who >> g & 1)) continue;
-          const int n = gr[g];
-          wait(&bar.gr_empty[g][n & 3], (n >> 2) + 1);
-          if (!wait.left) break;
-          if (lane == 0) {
-            group[g][n & 3] = to_v[vs];
-            mbar_arrive(&bar.gr_full[g][n & 3]);
-          }
-        }
-        __syncwarp();
-      };
-      if (flags & F_BLOCK && (kb & 1) != pair) {
+      const bool turn = (kb & 1) == pair;
+      if (flags & F_BLOCK && !turn) {
         ++kb;   // the other pair's
-      } else if (flags & F_BLOCK) {
-        const int st = kb & 3, sp = kb % TT_SC;
-        // slots that some row sees (others may never have been written: their values become zeros)
-        uint64_t seen = ~0ull;
-        if (!(flags & F_FULL)) seen = seen_by_some(a, to_v[vs]);
-        const unsigned char* raw = sm + M::v + vs * M::V;
-        const uint8_t* scales = raw + KV_BLOCK * D;
-        // the largest scale of the block's values (of a NaN row and of one that no row sees: does not count)
-        const int e0 = scales[KV_BLOCK + lane], e1 = scales[KV_BLOCK + 32 + lane];
-        const int c0 = e0 == KV_NAN || !((uint32_t)seen >> lane & 1u) ? 0 : e0;
-        const int c1 = e1 == KV_NAN || !((uint32_t)(seen >> 32) >> lane & 1u) ? 0 : e1;
-        const int top = max(__reduce_max_sync(0xffffffffu, max(c0, c1)), 1);
-        const int least = __reduce_min_sync(0xffffffffu, min(c0 ? c0 : 255, c1 ? c1 : 255));
-        bool careful = top > EV_LARGE;
-        if (top - least > 15) careful |= far_below<D>(raw, c0, c1, top);
-        if ((kb >> 1 & 1) == (cw & 1)) {   // this block's scales for the softmax
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int x = lane + 32 * i, ek = scales[x], ev = i ? e1 : e0;
-            kf[sp][x] = ek == KV_NAN || ev == KV_NAN ? __int_as_float(0x7FC00000) : pow2f(ek - 127);
-            ev_f[sp][x] = (float)((careful ? ev : top) - 127);
-          }
-          if (lane == 0) ev_top[sp] = careful ? __int_as_float(0x7FC00000) : (float)(top - 127);
-          __syncwarp();
-          tell();
-        }
-        wait(&bar.v16_empty[st], (kb >> 2) + 1);
-        unsigned char* const to = sm + M::v16 + st * M::V16 + first;
-        const int other = first & 16 ? -16 : 16;
-#pragma unroll 2
-        for (int j = 0; j < NP; ++j) {
-          const int x = x0 + j * (64 / CH);
-          uint4 cur = reinterpret_cast<const uint4*>(raw)[dt + j * 64];
-          if (!(seen >> x & 1ull)) cur = make_uint4(0, 0, 0, 0);
-          // 2^(the row's scale - the largest), at least 2^-15
-          const int d = min(max(top - (int)scales[KV_BLOCK + x], 0), 15);
-          const uint32_t up = careful ? 0x3C003C00u : (d < 15 ? (uint32_t)(15 - d) << 10 : 1u << 9) * 0x10001u;
-          const uint32_t u[4] = {second ? cur.z : cur.x, second ? cur.w : cur.y, second ? cur.x : cur.z, second ? cur.y : cur.w};
-          uint32_t o[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            o[2 * k] = mul_f16x2(e4m3x2_to_f16x2(u[k] & 0xFFFFu), up);
-            o[2 * k + 1] = mul_f16x2(e4m3x2_to_f16x2(u[k] >> 16), up);
-          }
-          *reinterpret_cast<uint4*>(to + j * (64 / CH) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(to + j * (64 / CH) * 128 + other) = make_uint4(o[4], o[5], o[6], o[7]);
-        }
-        fence_proxy_async_smem();
-        if (dt == 0) to_o[st] = flags;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.v16_full[st]);
-        ++kb;
       } else {
-        if (cw == 0) tell();
-        if (flags & F_EXIT) {
-          if ((kb & 1) != pair) break;
-          const int st = kb & 3;
+        const int st = kb & 3, sp = kb % TT_SC;
+        const unsigned char* const raw = sm + M::v + vs * M::V;
+        bool speaks = cw == 0;
+        uint32_t up0 = 0, up1 = 0;   // of rows lane and lane + 32: what their codes are multiplied with; 0: not seen
+        if (flags & F_BLOCK) {
+          // slots that some row sees (others may never have been written: their values become zeros)
+          uint64_t seen = ~0ull;
+          if (!(flags & F_FULL)) seen = seen_by_some(a, to_v[vs]);
+          const uint8_t* scales = raw + KV_BLOCK * D;
+          // the largest scale of the block's values (of a NaN row and of one that no row sees: does not count)
+          const int e0 = scales[KV_BLOCK + lane], e1 = scales[KV_BLOCK + 32 + lane];
+          const bool s0 = (uint32_t)seen >> lane & 1u, s1 = (uint32_t)(seen >> 32) >> lane & 1u;
+          const int c0 = e0 == KV_NAN || !s0 ? 0 : e0, c1 = e1 == KV_NAN || !s1 ? 0 : e1;
+          const int top = max(__reduce_max_sync(0xffffffffu, max(c0, c1)), 1);
+          const int least = __reduce_min_sync(0xffffffffu, min(c0 ? c0 : 255, c1 ? c1 : 255));
+          bool careful = top > EV_LARGE;
+          if (top - least > 15) careful |= far_below<D>(raw, c0, c1, top);
+          // FP16 pairs of 2^(the row's scale - the largest), at least 2^-15
+          auto relative = [&](int e) { return careful ? 0x3C003C00u : (uint32_t)max((15 - min(max(top - e, 0), 15)) << 10, 1 << 9) * 0x10001u; };
+          up0 = s0 ? relative(e0) : 0u, up1 = s1 ? relative(e1) : 0u;
+          speaks = (kb >> 1 & 1) == (cw & 1);
+          if (speaks) {   // this block's scales for the softmax
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int x = lane + 32 * i, ek = scales[x], ev = i ? e1 : e0;
+              kf[sp][x] = ek == KV_NAN || ev == KV_NAN ? __int_as_float(0x7FC00000) : pow2f(ek - 127);
+              ev_f[sp][x] = (float)((careful ? ev : top) - 127);
+            }
+            if (lane == 0) ev_top[sp] = careful ? __int_as_float(0x7FC00000) : (float)(top - 127);
+            __syncwarp();
+          }
+        }
+        if (speaks) {
+#pragma unroll 1
+          for (int g = 0; g < 2; ++g) {
+            if (!(who >> g & 1)) continue;
+            const int n = gr[g];
+            wait(&bar.gr_empty[g][n & 3], (n >> 2) + 1);
+            if (!wait.left) break;
+            if (lane < ITEM_WORDS) reinterpret_cast<int*>(&group[g][n & 3])[lane] = reinterpret_cast<const int*>(&to_v[vs])[lane];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.gr_full[g][n & 3]);
+          }
+          __syncwarp();
+        }
+        if (turn && flags & (F_BLOCK | F_EXIT)) {
           wait(&bar.v16_empty[st], (kb >> 2) + 1);
-          if (dt == 0) to_o[st] = F_EXIT;
+          if (flags & F_BLOCK) {
+            const unsigned char* from = raw + dt * 16;
+            unsigned char* to = sm + M::v16 + st * M::V16 + o0;
+#pragma unroll 2
+            for (int j = 0; j < NP; ++j) {
+              const uint32_t up = __shfl_sync(0xffffffffu, j < NP / 2 ? up0 : up1, x0 + j * (64 / CH));   // (lane modulo 32)
+              uint4 cur = *reinterpret_cast<const uint4*>(from);
+              if (up == 0) cur = make_uint4(0, 0, 0, 0);
+              const uint32_t u[4] = {second ? cur.z : cur.x, second ? cur.w : cur.y, second ? cur.x : cur.z, second ? cur.y : cur.w};
+              uint32_t y[8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                y[2 * i] = mul_f16x2(e4m3x2_to_f16x2(u[i] & 0xFFFFu), up), y[2 * i + 1] = mul_f16x2(e4m3x2_to_f16x2(u[i] >> 16), up);
+              *reinterpret_cast<uint4*>(to) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(to + away) = make_uint4(y[4], y[5], y[6], y[7]);
+              from += 64 * 16, to += 64 / CH * 128;
+            }
+          }
+          fence_proxy_async_smem();
+          if (dt == 0) to_o[st] = flags;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.v16_full[st]);
-          break;
+          ++kb;
         }
+        if (flags & F_EXIT) break;
       }
       gr.a += who & 1, gr.b += who >> 1;
       __syncwarp();
@@ -907,8 +924,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
               l = fmaf(sum, ex2(-top), l);
             }
           } else {
-            const uint64_t seen = tl < 0 ? 0ull : flags & F_FULL ? ~0ull
-                : seen_bits(a.mask ? a.mask + (size_t)(x.t0 + tl) * a.words : nullptr, a.words, x.begin, __ldg(a.pos + x.t0 + tl), x.blk);
+            const uint64_t seen = tl < 0 ? 0ull : flags & F_FULL ? ~0ull : seen_by(a, x, tl);
             const float mx = careful_max(S, kf[sp], ev_f[sp], f, seen);
             if (m == -INFINITY) m = mx;   // nothing has been added for this row yet
             if (__any_sync(0xffffffffu, mx > m)) {
@@ -974,15 +990,40 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
 // ---------------------------------------------------------------------------
 // Joining the parts
 // ---------------------------------------------------------------------------
+// Every CTA finds out which units there are to join, `ctas` at most, and takes its pieces of them: a row where it has
+// many parts, else a row a warp (see join_rows).
 template <int D>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) kv_tree_join_kernel(const TreeParams a) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32, 4) kv_tree_join_kernel(const TreeParams a, int ctas) {
+  static_assert(TT_MAX_CTAS <= JOIN_WARPS * 32, "a thread an entry");
+  __shared__ Join unit[TT_MAX_CTAS];
+  __shared__ int sum[JOIN_WARPS], upto[TT_MAX_CTAS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const Join j = a.join[blockIdx.x];
-  if (j.parts == 0) return;
-  join_rows<D>(a.ml, a.part, j.parts, blockIdx.y, gridDim.y, j.n * a.G,
-               [&](int p, int r) { return (size_t)(2 * (blockIdx.x + p) + (p == 0)) * a.rows + r; },
-               [&](int r) { return ((size_t)(j.t0 + r / a.G) * a.H + j.h) * a.G + r % a.G; }, a.out, a.lse);
+  const Join own = tid < ctas ? a.join[tid] : Join{0, 0, 0, 0};
+  const int rows = own.n * a.G;
+  int n = own.parts == 0 ? 0 : own.parts > JOIN_FEW ? rows : (rows + JOIN_WARPS - 1) / JOIN_WARPS;   // pieces
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int x = __shfl_up_sync(0xffffffffu, n, o);
+    if (lane >= o) n += x;
+  }
+  if (lane == 31) sum[warp] = n;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) n += sum[w];
+  if (tid < ctas) unit[tid] = own, upto[tid] = n;
+  __syncthreads();
+  for (int i = blockIdx.x; i < upto[ctas - 1]; i += gridDim.x) {
+    int u = 0;   // the first whose pieces end behind i
+#pragma unroll
+    for (int o = 128; o; o >>= 1)
+      if (u + o <= ctas && upto[u + o - 1] <= i) u += o;
+    const Join j = unit[u];
+    join_rows<D>(a.ml, a.part, j.parts, JOIN_FEW, i - (u ? upto[u - 1] : 0), 1 << 20, j.n * a.G,
+                 [&](int p, int r) { return (size_t)(2 * (u + p) + (p == 0)) * a.rows + r; },
+                 [&](int r) { return ((size_t)(j.t0 + r / a.G) * a.H + j.h) * a.G + r % a.G; }, a.out, a.lse);
+    __syncthreads();   // (join_rows' shared memory)
+  }
 }
 
 template <int D, bool PATIENT>
@@ -1001,9 +1042,7 @@ cudaError_t launch(const TreeParams& a, const CUtensorMap& keys, const CUtensorM
   if (e != cudaSuccess) return e;
   e = launch_k(kv_tree_kernel<D, PATIENT>, dim3((unsigned)ctas), dim3(TT_THREADS), TreeMem<D>::bytes, s, a, keys, queries);
   if (e != cudaSuccess) return e;
-  // (a part's rows over several CTAs, of which those for a CTA that begins no shared unit have nothing to do)
-  const int chunks = a.rows < 32 ? a.rows : 32;
-  return launch_k(kv_tree_join_kernel<D>, dim3((unsigned)ctas, (unsigned)chunks), dim3(JOIN_WARPS * 32), 0, s, a);
+  return launch_k(kv_tree_join_kernel<D>, dim3((unsigned)(JOIN_CTAS * ctas)), dim3(JOIN_WARPS * 32), 0, s, a, ctas);
 }
 
 int slot_rows(int T, int G) {   // rows of a part: those of two tiles, or all that the call has

@@ -1,5 +1,7 @@
 // What the kernels of the attention over the whole context share: which slots a token sees, and the joining of parts.
 #pragma once
+#include <type_traits>
+
 #include "kv_attend.cuh"
 
 namespace bre {
@@ -31,36 +33,48 @@ struct Joined {
 
   template <typename Index>
   __device__ __forceinline__ Joined(const float2* ml, const float* part, int parts, int from, int step, Index index) {
-    constexpr int CL = D / 32;
-    const int lane = threadIdx.x & 31;
-    top = -INFINITY, sum = 0.0f;
-    for (int p = from + lane * step; p < parts; p += 32 * step) top = fmaxf(top, ml[index(p)].x);
+    constexpr int CL = D / 32, AHEAD = 8;
+    using Piece = typename std::conditional<CL == 4, float4, float2>::type;
+    const int lane = threadIdx.x & 31, n = (parts - from + step - 1) / step;   // its parts
+    union Loaded {
+      Piece x;
+      float v[CL];
+    } o[AHEAD];
+    auto fetch = [&](int i0) {   // on their way while the weights are formed
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int i = 0; i < AHEAD; ++i) {
+        o[i].x = Piece{};
+        if (i0 + i < n) o[i].x = *reinterpret_cast<const Piece*>(part + index(from + (i0 + i) * step) * D + lane * CL);
+      }
+    };
+    fetch(0);
+    top = -INFINITY, sum = 0.0f;
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[index(from + i * step)].x);
+#pragma unroll
+    for (int j = 16; j; j >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, j));
     const float ref = top > -INFINITY ? top : 0.0f;
 #pragma unroll
-    for (int i = 0; i < CL; ++i) v[i] = 0.0f;
-    for (int p0 = from; p0 < parts; p0 += 32 * step) {
-      const int p = p0 + lane * step;
-      const float2 y = p < parts ? ml[index(p)] : make_float2(-INFINITY, 0.0f);
-      const float w = ex2(y.x - ref);
-      sum += scale_sum(y.y, y.x - ref);
-      const int n = min(32, (parts - p0 + step - 1) / step);
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-        const float* src = part + index(p0 + i * step) * D + lane * CL;
-        if constexpr (CL == 4) {
-          const float4 o = *reinterpret_cast<const float4*>(src);
-          v[0] = fmaf(wi, o.x, v[0]), v[1] = fmaf(wi, o.y, v[1]), v[2] = fmaf(wi, o.z, v[2]), v[3] = fmaf(wi, o.w, v[3]);
-        } else {
-          const float2 o = *reinterpret_cast<const float2*>(src);
-          v[0] = fmaf(wi, o.x, v[0]), v[1] = fmaf(wi, o.y, v[1]);
+    for (int c = 0; c < CL; ++c) v[c] = 0.0f;
+    float w = 0.0f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += AHEAD) {
+      if (i0 % 32 == 0) {
+        const float2 y = i0 + lane < n ? ml[index(from + (i0 + lane) * step)] : make_float2(-INFINITY, 0.0f);
+        w = ex2(y.x - ref);
+        sum += scale_sum(y.y, y.x - ref);
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
+        if (i0 + i < n) {
+#pragma unroll
+          for (int c = 0; c < CL; ++c) v[c] = fmaf(wi, o[i].v[c], v[c]);
         }
       }
+      if (i0 + AHEAD < n) fetch(i0 + AHEAD);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int j = 16; j; j >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, j);
   }
   __device__ __forceinline__ void store(uint16_t* out, float* lse) const {
     constexpr int CL = D / 32;
@@ -76,15 +90,15 @@ struct Joined {
 };
 
 constexpr int JOIN_WARPS = 8;
-// Rows first, first + stride, .. of `rows` by a CTA of JOIN_WARPS warps.  Few parts: a warp a row.  Many: a row at a time, its
-// parts dealt to the warps, whose results are joined once more (304 parts of 32 rows, a warp a row: 38 us).
+// Rows first, first + stride, .. of `rows` by a CTA of JOIN_WARPS warps.  Few parts (up to `few`): a warp a row.  Many: a row at
+// a time, its parts dealt to the warps, whose results are joined once more (304 parts of 32 rows, a warp a row: 38 us).
 template <int D, typename Index, typename Place>
-__device__ __forceinline__ void join_rows(const float2* ml, const float* part, int parts, int first, int stride, int rows, Index index,
+__device__ __forceinline__ void join_rows(const float2* ml, const float* part, int parts, int few, int first, int stride, int rows, Index index,
                                           Place place, uint16_t* out, float* lse) {
   __shared__ float2 sh_ml[2][JOIN_WARPS];
   __shared__ float sh_part[2][JOIN_WARPS * D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (parts <= JOIN_WARPS) {
+  if (parts <= few) {
     for (int r = first * JOIN_WARPS + warp; r < rows; r += stride * JOIN_WARPS) {
       const size_t at = place(r);
       Joined<D>(ml, part, parts, 0, 1, [&](int p) { return index(p, r); }).store(out + at * D, lse ? lse + at : nullptr);

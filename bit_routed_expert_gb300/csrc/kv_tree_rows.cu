@@ -107,7 +107,7 @@ template <int D>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_tree_rows_join_kernel(const TreeRows a, int rows) {
   pdl_wait();
   pdl_launch_dependents();
-  join_rows<D>(a.ml, a.part, a.shares, blockIdx.x, gridDim.x, rows,
+  join_rows<D>(a.ml, a.part, a.shares, JOIN_WARPS, blockIdx.x, gridDim.x, rows,
                [&](int p, int r) { return ((size_t)(r / a.G) * a.shares + p) * a.G + r % a.G; }, [](int r) { return (size_t)r; }, a.out, a.lse);
 }
 
