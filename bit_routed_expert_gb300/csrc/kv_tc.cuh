@@ -70,6 +70,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 #undef BRE_IN
 }
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
+#define BRE_IN(i) "r"(r[i])
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), BRE_R8(BRE_IN, 0) : "memory");
+#undef BRE_IN
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 

@@ -317,12 +317,13 @@ __device__ __noinline__ float careful_max(uint32_t S, const float* kf, const flo
   float mx = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < KV_BLOCK; c += 16) {
+    const uint32_t bits = (uint32_t)(seen >> c);
     uint32_t s[16];
     tmem_ld16(S + c, s);
     tmem_wait_ld();
 #pragma unroll
     for (int x = 0; x < 16; ++x)
-      if (seen >> (c + x) & 1ull) mx = fmaxf(mx, fmaf(__uint_as_float(s[x]) * kf[c + x], f, ev[c + x]));
+      if (bits >> x & 1u) mx = fmaxf(mx, fmaf(__uint_as_float(s[x]) * kf[c + x], f, ev[c + x]));
   }
   return mx;
 }
@@ -330,21 +331,22 @@ __device__ __noinline__ float careful_max(uint32_t S, const float* kf, const flo
 __device__ __noinline__ float careful_weights(uint32_t S, const float* kf, const float* ev, float f, float base, uint64_t seen) {
   float sum = 0.0f;
 #pragma unroll 1
-  for (int c = 0; c < KV_BLOCK; c += 32) {
-    uint32_t s[32], pk[16];
-    tmem_ld32(S + c, s);
+  for (int c = 0; c < KV_BLOCK; c += 16) {
+    const uint32_t bits = (uint32_t)(seen >> c);
+    uint32_t s[16], pk[8];
+    tmem_ld16(S + c, s);
     tmem_wait_ld();
 #pragma unroll
-    for (int x = 0; x < 32; x += 2) {
+    for (int x = 0; x < 16; x += 2) {
       float v0 = fmaf(__uint_as_float(s[x]) * kf[c + x], f, ev[c + x]) - base;
       float v1 = fmaf(__uint_as_float(s[x + 1]) * kf[c + x + 1], f, ev[c + x + 1]) - base;
-      if (!(seen >> (c + x) & 1ull)) v0 = -INFINITY;
-      if (!(seen >> (c + x + 1) & 1ull)) v1 = -INFINITY;
-      if (seen >> (c + x) & 1ull) sum += exp2f(v0 - ev[c + x]);
-      if (seen >> (c + x + 1) & 1ull) sum += exp2f(v1 - ev[c + x + 1]);
+      if (!(bits >> x & 1u)) v0 = -INFINITY;
+      if (!(bits >> (x + 1) & 1u)) v1 = -INFINITY;
+      if (bits >> x & 1u) sum += exp2f(v0 - ev[c + x]);
+      if (bits >> (x + 1) & 1u) sum += exp2f(v1 - ev[c + x + 1]);
       pk[x / 2] = pack_f16x2(ex2(v0), ex2(v1));
     }
-    tmem_st16(S + c / 2, pk);
+    tmem_st8(S + c / 2, pk);
   }
   return sum;
 }
@@ -470,24 +472,25 @@ __device__ __noinline__ void rescale(uint32_t O, float sc) {
 }
 
 // A warp's waits.  In line and short: five roles' code competes for the SM's instruction cache.  A try suspends the warp for
-// a few hundred cycles, so that TRIES take a second or so; where a budget is set (PATIENT false) a wait polls.  A wait that runs out
-// makes every later one of the warp give up at once; who has waited for a ring's slot must look at `left` before using it.
-constexpr int TRIES = 1 << 23;
+// up to 2 us (without that time given they poll so often that they cost the others 1 to 2%), so that TRIES take a few
+// seconds at most; where a budget is set (PATIENT false) a wait polls.  A wait that runs out makes every later one of the
+// warp give up at once; who has waited for a ring's slot must look at `left` before using it.
+constexpr int TRIES = 1 << 21;
 template <bool PATIENT>
 struct Waits {
   int left;   // tries of a wait; 0: some wait has given up
   __device__ __forceinline__ void operator()(uint64_t* bar, int phase) {
-#define BRE_WAIT(how)                                                                                                     \
+#define BRE_WAIT(how, hint)                                                                                                \
   asm volatile(                                                                                                           \
       "{\n\t.reg .pred p;\n\t.reg .s32 n;\n\tmov.s32 n, %0;\n"                                                             \
-      "AGAIN:\n\tmbarrier." how ".parity.shared::cta.b64 p, [%1], %2;\n\tvote.sync.all.pred p, p, 0xffffffff;\n\t"        \
+      "AGAIN:\n\tmbarrier." how ".parity.shared::cta.b64 p, [%1], %2" hint ";\n\tvote.sync.all.pred p, p, 0xffffffff;\n\t"        \
       "@p bra THERE;\n\tsub.s32 n, n, 1;\n\tsetp.gt.s32 p, n, 0;\n\t@p bra AGAIN;\n\tmov.s32 %0, 0;\n"                   \
       "THERE:\n\t}"                                                                                                       \
       : "+r"(left)                                                                                                        \
       : "r"(smem_u32(bar)), "r"((uint32_t)phase & 1u)                                                                     \
       : "memory")
-    if (PATIENT) BRE_WAIT("try_wait");
-    else BRE_WAIT("test_wait");
+    if (PATIENT) BRE_WAIT("try_wait", ", 2000");
+    else BRE_WAIT("test_wait", "");
 #undef BRE_WAIT
   }
 };
@@ -824,7 +827,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
           if (flags & F_BLOCK) {
             const unsigned char* from = raw + dt * 16;
             unsigned char* to = sm + M::v16 + st * M::V16 + o0;
-#pragma unroll 2
+#pragma unroll 4
             for (int j = 0; j < NP; ++j) {
               const uint32_t up = __shfl_sync(0xffffffffu, j < NP / 2 ? up0 : up1, x0 + j * (64 / CH));   // (lane modulo 32)
               uint4 cur = *reinterpret_cast<const uint4*>(from);
