@@ -294,6 +294,8 @@ bre_status kv_attend_tree(const bre_kv_cache* cache, const void* q_bf16, int64_t
   if ((st = kv_check_q(cache, q_bf16, q_stride, n_heads, 1)) != BRE_OK) return st;
   if (mask && (!start || words <= 0 || !aligned(mask, 8) || !aligned(start, 4))) return BRE_ERR_ARG;
   if (mask && words > 1024) return BRE_ERR_UNSUPPORTED;
+  // (the tiles' copies address heads of pages, and rows of queries, by 32-bit numbers)
+  if ((int64_t)cache->n_pages * cache->n_kv_heads > INT32_MAX || (int64_t)T * n_heads > INT32_MAX / 2) return BRE_ERR_UNSUPPORTED;
   if (!out_bf16 || !aligned(out_bf16, 32) || !aligned(lse, 4) || !(scale - scale == 0.0f)) return BRE_ERR_ARG;
   const size_t need = kv_tree_ws_bytes(T, n_heads, cache->n_kv_heads, cache->head_dim);
   if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return BRE_ERR_WORKSPACE;

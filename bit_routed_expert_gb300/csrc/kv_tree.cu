@@ -1053,9 +1053,11 @@ int slot_rows(int T, int G) {   // rows of a part: those of two tiles, or all th
   return (int)(all < most ? all : most);
 }
 
-int query_rows(int T, int G) { return T * G < 128 ? 128 : T * G; }   // (a copied box is not larger than what it is copied from)
+// (a copied box is not larger than what it is copied from)
+long long query_rows(int T, int G) { return (long long)T * G < 128 ? 128 : (long long)T * G; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 size_t codes_bytes(int T, int H, int G, int D) { return up256((size_t)2 * H * query_rows(T, G) * D); }
+size_t factor_bytes(int T, int H, int G) { return up256((size_t)H * query_rows(T, G) * sizeof(float)); }
 
 }  // namespace
 
@@ -1063,7 +1065,7 @@ size_t kv_tree_ws_bytes(int T, int Hq, int H, int D) {
   const int G = Hq / H;
   if (G < 1 || G > 16) return 0;
   const size_t slots = 2 * TT_MAX_CTAS, rows = slot_rows(T, G);
-  const size_t tiles = codes_bytes(T, H, G, D) + up256((size_t)H * query_rows(T, G) * sizeof(float)) + TT_MAX_CTAS * sizeof(Join) +
+  const size_t tiles = codes_bytes(T, H, G, D) + factor_bytes(T, H, G) + TT_MAX_CTAS * sizeof(Join) +
                        slots * rows * (sizeof(float2) + D * sizeof(float));
   const size_t single = tree_rows_ws_bytes(T, H, G, D);
   return tiles > single ? tiles : single;
@@ -1072,11 +1074,14 @@ size_t kv_tree_ws_bytes(int T, int Hq, int H, int D) {
 cudaError_t launch_kv_attend_tree(const TreeArgs& t, cudaStream_t s) {
   const bre_kv_cache* c = t.cache;
   const int H = c->n_kv_heads, D = c->head_dim, G = t.Hq / H;
-  // A token at a time where a sequence has three at most on average, or the contexts are short.  Such a call reads a context
-  // once for each of its tokens (mostly from L2), but needs none of the tiles' preparations.  us, a token at a time / tiles,
-  // four kv heads, G = 8, D = 128, 64 sequences: 1 token over 16,384 183 / 395, 2 278 / 404, 4 501 / 407; 3 over 4,096 124 / 131,
-  // 4 134 / 132; 8 sequences, 8 tokens over 300: 14 / 32; G = 4, D = 64, eight kv heads, 64 sequences, 4 tokens over 200: 18 / 48.
-  if (t.tk.T <= 3LL * t.tk.B || (long long)t.tk.T * H * t.tk.N <= 4096) return launch_tree_rows(t, s);
+  // A token at a time where that costs less: such a call reads a context once for each of its tokens (mostly from L2), but needs
+  // none of the tiles' preparations, worth some 6,000 blocks of a token's (16 bits a key, D = 128), and a tile's block takes as long
+  // as two and a half of those.  us, a token at a time / tiles, four kv heads, G = 8, D = 128: 64 sequences of 4,096,
+  // 2 tokens each 82 / 113, 3 125 / 114; 8 of 16,384, 3 60 / 66, 4 75 / 66; 32 of 2,048, 3 35 / 46, 4 41 / 47; 16 of 1,024, 8
+  // 27 / 29; one of 4,096, 16 22 / 33; one of 65,536, 4 41 / 40.  D = 64: 16 of 4,096, eight kv heads, G = 1, 4 42 / 56, 8
+  // 72 / 57; 64 of 200, eight kv heads, G = 4, 4 18 / 43.  G = 16: 16 of 8,192, two kv heads, D = 64, 2 29 / 35, 4 46 / 36.
+  const long long blocks = (long long)H * t.tk.N, halves = (G > 8 ? 2 : 1) * (D / 64);
+  if (t.tk.T * halves * blocks <= 5 * t.tk.B * blocks + 12000) return launch_tree_rows(t, s);
   TreeParams a{};
   a.pages = static_cast<const uint8_t*>(c->pages), a.H = H, a.G = G, a.per = 2 * (128 / G);
   a.tab = KvTable{t.tk.table, t.tk.B, t.tk.N, c->n_pages};
@@ -1085,10 +1090,10 @@ cudaError_t launch_kv_attend_tree(const TreeArgs& t, cudaStream_t s) {
   a.wait = ffn_wait_budget(0);   // 0: none set
   a.rows = slot_rows(a.T, G);
   const size_t slots = 2 * TT_MAX_CTAS;
-  a.q_rows = query_rows(a.T, G);
+  a.q_rows = (int)query_rows(a.T, G);
   a.codes = static_cast<unsigned char*>(t.ws);
   a.factors = reinterpret_cast<float*>(a.codes + codes_bytes(a.T, H, G, D));
-  a.join = reinterpret_cast<Join*>(reinterpret_cast<unsigned char*>(a.factors) + up256((size_t)H * a.q_rows * sizeof(float)));
+  a.join = reinterpret_cast<Join*>(reinterpret_cast<unsigned char*>(a.factors) + factor_bytes(a.T, H, G));
   a.part = reinterpret_cast<float*>(a.join + TT_MAX_CTAS);
   a.ml = reinterpret_cast<float2*>(a.part + slots * a.rows * D);
   // a head's share of a page as rows of D bytes: 64 keys, 64 values, the scales

@@ -382,13 +382,13 @@ bre_status kv_attend(const bre_kv_cache *cache, const void *q_bf16, int64_t q_st
  * drafted tokens were stored by kv_append at positions start[b] + j in the order of the tree's nodes; a node's bits are its
  * ancestors' and its own.  (Their rotary positions go by the depth in the tree, not by their place.)  The call's tokens of one
  * sequence should follow one another in the list: then each key is read once for all of them.
- * Logits, maxima and sums are FP32, the logits with their value's scale as in kv_attend.  A query enters as the sum of two E4M3
- * numbers times a power of two that takes its head's largest magnitude to 224 .. 448: exactly down to 2^-10 of that, off
- * by 2^-19 of it at most below.  The probabilities enter the second product as FP16, as in kv_attend.
+ * Logits, maxima and sums are FP32.  A query enters as FP16, as in kv_attend, or, where a sequence has many tokens in the call, as
+ * the sum of two E4M3 numbers times a power of two that takes its head's largest magnitude to 224 .. 448: exactly down to
+ * 2^-10 of that, off by 2^-19 of it at most below.  The probabilities enter the second product as FP16, as in kv_attend.
  *   start [B] int32 (negative counts as 0) and mask [T][words] uint64, or both NULL; out, lse as in kv_attend.
  *   ws: kv_attend_tree_workspace(T, ...) bytes of scratch, 256-byte aligned, which need no initialisation; calls that
  *   share it must be ordered (two graphs that may run at the same time need one each).
- * Requires G <= 16, words <= 1024. */
+ * Requires G <= 16, words <= 1024, n_pages * n_kv_heads < 2^31, T * n_heads < 2^30. */
 size_t kv_attend_tree_workspace(int T, int n_heads, int n_kv_heads, int head_dim);
 bre_status kv_attend_tree(const bre_kv_cache* cache, const void* q_bf16, int64_t q_stride, int n_heads, const int32_t* seq,
                           const int32_t* pos, int T, const int32_t* table, int B, int N, const int32_t* start,
@@ -468,8 +468,8 @@ bre_status kv_resize(const bre_kv_cache* cache, int32_t* refs, int32_t* table, i
                      const int32_t* end, void* ws, size_t ws_bytes, int32_t* dev_err, bre_stream_t stream);
 
 /* Budget, in SM clock cycles, of the bounded waits inside the expert FFN kernels
- * (moe_expert_ffn, both paths) and kv_attend's tile kernel for calls made after this one, from any
- * thread of the process; 0 restores the defaults (about 1 s on the decode path, 2 s on the others).  A wait
+ * (moe_expert_ffn, both paths) and the tile kernels of kv_attend and kv_attend_tree for calls made after this one, from any
+ * thread of the process; 0 restores the defaults (about 1 s on the decode path, 2 s on the others, a few seconds in kv_attend_tree).  A wait
  * that runs out sets BRE_DEVERR_TIMEOUT in the call's dev_err; the kernel then waits, with the
  * default budget, for the copies and tensor-core operations it has in flight, frees its tensor
  * memory and returns, and that call's outputs are invalid.  The next call on the same workspace

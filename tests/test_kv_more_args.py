@@ -68,6 +68,7 @@ def test_tree_refuses():
     assert tree(Hq=3, qs=192) == tree(Hq=0) == tree(scale=math.nan) == tree(scale=math.inf) == BRE_ERR_ARG
     assert tree(start=None) == tree(words=0) == tree(words=-1) == tree(mask=C.c_void_p((1 << 20) + 4)) == tree(start=ODD) == BRE_ERR_ARG
     assert tree(Hq=34, qs=34 * 64) == tree(words=1025) == BRE_ERR_UNSUPPORTED
+    assert tree(cache(n_pages=2 ** 30)) == tree(T=2 ** 27, Hq=32, qs=2048) == BRE_ERR_UNSUPPORTED   # 32-bit rows of pages, of queries
     need = _lib.load().kv_attend_tree_workspace(3, 4, 2, 64)
     if need:
         assert tree(ws=None, wsb=0) == tree(wsb=need - 1) == tree(ws=C.c_void_p((1 << 20) + 16)) == BRE_ERR_WORKSPACE
@@ -96,6 +97,8 @@ def test_page_calls_refuse():
 def test_workspaces_grow_with_the_sizes():
     L = _lib.load()
     assert L.kv_resize_workspace(0, 1, 1) == L.kv_attend_tree_workspace(0, 8, 2, 64) == 0
+    sizes = [L.kv_attend_tree_workspace(T, 32, 2, 64) for T in (1, 7, 500, 2 ** 20, 2 ** 30, 2 ** 31 - 1)]
+    assert sizes == sorted(sizes) and sizes[0] > 0 and sizes[-1] > 2 ** 40
     sizes = [L.kv_resize_workspace(n, b, N) for n, b, N in ((4, 1, 1), (400, 1, 1), (400, 7, 1), (400, 7, 900), (10 ** 6, 7, 900))]
     assert sizes == sorted(sizes) and sizes[0] > 0
 
