@@ -45,7 +45,7 @@ constexpr int JOIN_CTAS = 4;             // of the joining kernel, for every one
 constexpr int JOIN_FEW = 32;             // parts that a warp joins
 constexpr float P_MOST = 32768.0f;       // a block's sum of weights up to which they are FP16 numbers for sure
 // Costs of the shares: a block for one tile, for two tiles, and what a unit takes beside its blocks.
-constexpr int COST_ONE = 2, COST_TWO = 3, COST_UNIT = 10;
+constexpr int COST_ONE = 2, COST_TWO = 3, COST_UNIT = 16;
 
 enum : int { F_BLOCK = 1, F_FULL = 4, F_END = 8, F_EXIT = 16, F_TWO = 32, F_SOME = 64, F_ODD = 128, F_NEW = 256, F_BEGIN = 512 };
 
@@ -214,7 +214,17 @@ __device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
       const int former = max(run, __reduce_max_sync(0xffffffffu, lane < warp ? m.run[lane] : -1));
       const int r = upto ? base + 32 * warp + 31 - __clz(upto) : former;
       const int idx = (t - r) % a.per, slot = max(t - idx - base, 0);
-      if (in) atomicMax(&m.top[slot], p);
+      // the largest position of a tile: of its tokens in this warp, then by the last of these (a lane behind the list has -1 and
+      // belongs to the last tile, or to none that counts)
+      const uint32_t heads = __ballot_sync(0xffffffffu, idx == 0) | 1u;
+      const int behind_head = lane - (31 - __clz(heads & (0xFFFFFFFFu >> (31 - lane))));
+      int high = p;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, high, o);
+        if (behind_head >= o) high = max(high, x);
+      }
+      if (lane == 31 || heads >> (lane + 1) & 1u) atomicMax(&m.top[slot], high);
       __syncthreads();
       c = 0;
       if (in && (!behind || other_run(s, p, sn, pn) || idx == a.per - 1))   // a tile's last token
@@ -230,7 +240,7 @@ __device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
       __syncthreads();
       run = m.last_run, top = m.last_top;
       at = sum + c - own;
-#pragma unroll 1
+#pragma unroll 4
       for (int w = 0; w < TT_WARPS; ++w) {
         if (w < warp) at += m.sum[w];
         sum += m.sum[w];
@@ -1025,7 +1035,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 4) kv_tree_join_kernel(const 
     join_rows<D>(a.ml, a.part, j.parts, JOIN_FEW, i - (u ? upto[u - 1] : 0), 1 << 20, j.n * a.G,
                  [&](int p, int r) { return (size_t)(2 * (u + p) + (p == 0)) * a.rows + r; },
                  [&](int r) { return ((size_t)(j.t0 + r / a.G) * a.H + j.h) * a.G + r % a.G; }, a.out, a.lse);
-    __syncthreads();   // (join_rows' shared memory)
+    if (j.parts > JOIN_FEW) __syncthreads();   // (join_rows' shared memory)
   }
 }
 
