@@ -362,6 +362,9 @@ bre_status kv_compact(const bre_kv_cache* cache, const int32_t* table, int B, in
   if (!start || !count || A < 0 || (A > 0 && !nodes) || !aligned(start, 4) || !aligned(nodes, 4) || !aligned(count, 4) ||
       !aligned(length, 4))
     return BRE_ERR_ARG;
+  // (the lists are read by many CTAs, of which one writes the length)
+  auto apart = [&](const int32_t* p, int64_t n) { return !length || !p || length + B <= p || p + n <= length; };
+  if (!apart(start, B) || !apart(count, B) || !apart(nodes, (int64_t)B * A)) return BRE_ERR_ARG;
   return cuda_status(launch_kv_compact(cache, table, B, N, start, nodes, A, count, length, dev_err,
                                        reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -441,7 +441,8 @@ bre_status bre_rope_turns(int rot_dim, double theta, int scaling, double factor,
  * it is, length[b] = start[b].  The bounds of the blocks from start[b] / 64 up to length[b] are made anew from the keys
  * of the tokens before length[b].  nodes [B][A] int32 ascend; a list that does not, a count above A, a start below 0 or a
  * token without a page sets BRE_DEVERR_PAGE and leaves that sequence as it is, with length[b] = start[b].
- *   start, count [B]; length [B] int32 out, or NULL.  None of the blocks may be shared. */
+ *   start, count [B]; length [B] int32 out, or NULL; it may not overlap the other lists (BRE_ERR_ARG).  None of the blocks
+ *   may be shared. */
 bre_status kv_compact(const bre_kv_cache* cache, const int32_t* table, int B, int N, const int32_t* start, const int32_t* nodes,
                       int A, const int32_t* count, int32_t* length, int32_t* dev_err, bre_stream_t stream);
 

@@ -87,6 +87,10 @@ def test_page_calls_refuse():
     for f in (compact, fork, resize):
         assert f(table=None) == f(B=0) == f(N=0) == f(table=ODD) == BRE_ERR_ARG
     assert compact(start=None) == compact(nodes=None) == compact(count=None) == compact(A=-1) == compact(length=ODD) == BRE_ERR_ARG
+    apart = [C.c_void_p((1 << 20) + (i << 16)) for i in range(3)]
+    for i in range(3):   # a length that is one of the lists, or begins inside of it
+        lists = dict(zip(("start", "count", "nodes"), apart))
+        assert compact(length=apart[i], B=3, **lists) == compact(length=C.c_void_p(apart[i].value + 8), B=3, **lists) == BRE_ERR_ARG
     assert fork(refs=None) == fork(parent=None) == fork(length=None) == fork(refs=ODD) == BRE_ERR_ARG
     assert resize(refs=None) == resize(start=None) == resize(end=None) == resize(start=ODD) == BRE_ERR_ARG
     assert fork(B=49153) == fork(B=40000, N=60000) == resize(B=40000, N=60000) == BRE_ERR_UNSUPPORTED
