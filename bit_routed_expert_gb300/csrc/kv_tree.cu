@@ -5,16 +5,25 @@
 // each row, so DRAM sets the pace up to about 128 rows and the tensor cores beyond.
 //
 // One CTA an SM, which takes an equal share of the call's work: (rows, kv head) units one after the other, each a run of
-// blocks; a share may begin and end inside a unit.  Such parts go to the workspace, and a second kernel joins them in the
+// blocks; a share may begin and end inside a unit.  Such parts go to the workspace, and another kernel joins them in the
 // order of the context (the same numbers whatever the order in which CTAs finish).  The host knows neither
-// lengths nor runs: every CTA adds up the work of all tiles itself and finds its place.
+// lengths nor runs: every CTA adds up the work of all tiles itself and finds its place.  A kernel before forms the queries'
+// two terms.
+//
+// What bounds it: not the tensor cores nor DRAM yet, but the roles' chains of short steps (a wait is some 150 cycles
+// even where nothing is to be waited for) and instruction fetch: five roles' loops share a small instruction cache, so that code
+// that runs seldom costs some 250 cycles for every 128 bytes of it.  Hence little code: loops that are not unrolled far, what is
+// seldom out of line.  A step of 64 tokens takes 1,600 cycles for one tile and 2,200 for two, whose products take 1,260.
+// D = 128, G = 8, four kv heads: 32 sequences of up to 16,384 tokens, 16 drafts each, 122 us (2.3 TB/s); one of
+// 131,072, 64 drafts, 153 us (0.90 PFLOP/s, 0.47 of cuBLAS's); a prompt of 4,096 behind 4,096, 471 us (0.87 PFLOP/s).
 //
 // Sixteen warps:
 //   warps 0-3, 4-7  softmax, a thread a row: two tiles' rows of the same block, or, where there is one tile, its
 //                   rows of the even and of the odd blocks, each with a running maximum, sum and output of its own
-//   warps 8-11      queries into two E4M3 terms; the values' codes into FP16 in 128-byte-swizzled shared memory, two warps
-//                   for the even and two for the odd blocks
-//   warp 12         walks through the share, looks up pages and starts the copies (TMA: keys swizzled, values as they lie)
+//   warps 8-11      the values' codes into FP16 in 128-byte-swizzled shared memory, two warps for the even and two for the odd
+//                   blocks (four for every block: 3% slower for one tile, 2% faster for two; eight warps: 20% slower)
+//   warp 12         walks through the share, looks up pages and starts the copies (TMA: queries and keys swizzled, values as
+//                   they lie)
 //   warps 13-15     issue the MMAs: S = Q K^T into tensor memory, by turns; O += P V with P read from tensor memory
 //
 // The keys' codes are an MMA operand as they lie in the cache.  A BF16 query is q = 2^e (a + b), a and b E4M3: a is
@@ -271,8 +280,9 @@ __device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
 // ---------------------------------------------------------------------------
 // The queries as two E4M3 terms
 // ---------------------------------------------------------------------------
-// A lane 16 channels, for all tiles beforehand: tiles of several CTAs (parts of a long context) read the same queries, and code
-// that a CTA of the attention kernel runs once a unit comes from far away (four of its warps took 8,500 cycles for 128 rows).
+// A lane 16 channels, for all tiles beforehand: CTAs that hold parts of one context read the same queries, and the attention
+// kernel is short of instruction cache (four of its warps took 8,500 cycles for 128 rows).  It takes 1 us for few rows; for
+// 4,096 tokens of 32 heads 13 us, about as much as the attention kernel gained there.
 template <int D>
 __global__ void __launch_bounds__(256) kv_tree_queries_kernel(const TreeParams a) {
   constexpr int LR = D / 16;   // lanes a row
@@ -674,6 +684,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     }
   } else if (warp == W_S || warp == W_S + 1) {
     // ---- S = Q K^T: E4M3 operands, FP32 sums, M = 128; a block each in turn
+    // (Neither warp is four items ahead of the other, and uses c - 2 and c of a group's S are by the same warp or four items
+    // apart: when a use waits for its buffer's last one, the one before that has long been waited for.)
     const uint32_t id_s = (1u << 4) | ((uint32_t)(KV_BLOCK >> 3) << 17) | ((128u >> 4) << 24);
     const uint64_t q0 = desc_codes<D>(smem_u32(sm + M::q)), k0 = desc_codes<D>(smem_u32(sm + M::k));
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
