@@ -21,7 +21,7 @@
 //   warps 0-3, 4-7  softmax, a thread a row: two tiles' rows of the same block, or, where there is one tile, its
 //                   rows of the even and of the odd blocks, each with a running maximum, sum and output of its own
 //   warps 8-11      the values' codes into FP16 in 128-byte-swizzled shared memory, two warps for the even and two for the odd
-//                   blocks (four for every block: 3% slower for one tile, 2% faster for two; eight warps: 20% slower)
+//                   blocks (eight warps: 20% slower)
 //   warp 12         walks through the share, looks up pages and starts the copies (TMA: queries and keys swizzled, values as
 //                   they lie)
 //   warps 13-15     issue the MMAs: S = Q K^T into tensor memory, by turns; O += P V with P read from tensor memory
@@ -517,7 +517,7 @@ struct Waits {
 
 struct TreeBars {
   uint64_t k_full[TT_K], k_empty[TT_K], v_full[TT_V], v_empty[TT_V], v16_full[TT_V16], v16_empty[TT_V16];
-  uint64_t gr_full[2][TT_GROUP], gr_empty[2][TT_GROUP], s_full[2][2], p_full[2][2], o_done[2][2], q_full[2], q_empty[2];
+  uint64_t gr_full[2][TT_GROUP], gr_empty[2][TT_GROUP], p_full[2][2], o_done[2][2], q_full[2], q_empty[2];
   uint64_t swap_in, swap_out, drain;
 };
 
@@ -545,8 +545,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     const int i = tid, g = i & 1, j = i >> 1;
     mbar_init(&bar.k_full[i], 1), mbar_init(&bar.k_empty[i], 2), mbar_init(&bar.v_full[i], 1), mbar_init(&bar.v_empty[i], 4);
     mbar_init(&bar.v16_full[i], 2), mbar_init(&bar.v16_empty[i], 1);
-    mbar_init(&bar.gr_full[0][i], 1), mbar_init(&bar.gr_full[1][i], 1), mbar_init(&bar.gr_empty[0][i], 4), mbar_init(&bar.gr_empty[1][i], 4);
-    mbar_init(&bar.s_full[g][j], 1), mbar_init(&bar.p_full[g][j], 4), mbar_init(&bar.o_done[g][j], 1);
+    mbar_init(&bar.gr_full[0][i], 2), mbar_init(&bar.gr_full[1][i], 2), mbar_init(&bar.gr_empty[0][i], 4), mbar_init(&bar.gr_empty[1][i], 4);
+    mbar_init(&bar.p_full[g][j], 4), mbar_init(&bar.o_done[g][j], 1);
     if (j == 0) mbar_init(&bar.q_full[g], 1), mbar_init(&bar.q_empty[g], 2);
     if (i == 0) mbar_init(&bar.swap_in, 8), mbar_init(&bar.swap_out, 8), mbar_init(&bar.drain, 3);
     fence_mbar_init();
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const int me = warp - W_S;
     int live = 0, qb = 0, kb = 0;   // the unit's query buffers; the next one-tile unit's buffer; blocks
-    Pair cs{0, 0}, uses{0, 0};      // S of either group, units of either query buffer so far
+    Pair cs{0, 0}, gr{0, 0}, uses{0, 0};   // S and messages of either group, units of either query buffer so far
 #pragma unroll 1
     for (int it = 0;; ++it) {
       const int ks = it & 3;
@@ -712,6 +712,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
           if (!two) qb ^= 1;
           uses.a += live & 1, uses.b += live >> 1, live = 0;
         }
+        ++gr.a, ++gr.b;
         continue;
       }
       ++kb;
@@ -722,8 +723,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       }
 #pragma unroll 1
       for (int g = 0; g <= two; ++g) {
-        const int w = two ? g : flags & F_ODD ? 1 : 0, qt = two ? g : qb, c = cs[w], buf = c & 1;
-        cs.add(w);
+        const int w = two ? g : flags & F_ODD ? 1 : 0, qt = two ? g : qb, c = cs[w], n = gr[w], buf = c & 1;
+        cs.add(w), gr.add(w);
         if (!mine) continue;
         wait(&bar.o_done[w][buf], (c >> 1) + 1);   // the weights that lay in S's columns have been used
         tc_fence_after();
@@ -735,7 +736,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
               mma_codes(st, qd + ((term * M::TERM + kk * 32) >> 4), kd + ((kk * 32) >> 4), id_s, term + kk > 0);
-          mma_commit(&bar.s_full[w][buf]);
+          mma_commit(&bar.gr_full[w][n & 3]);
           if (g == two) mma_commit(&bar.k_empty[ks]);
         }
         __syncwarp();
@@ -840,7 +841,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
             if (!wait.left) break;
             if (lane < ITEM_WORDS) reinterpret_cast<int*>(&group[g][n & 3])[lane] = reinterpret_cast<const int*>(&to_v[vs])[lane];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.gr_full[g][n & 3]);
+            if (lane == 0 || (lane == 1 && !(flags & F_BLOCK))) mbar_arrive(&bar.gr_full[g][n & 3]);   // (of a block S is the other half)
           }
           __syncwarp();
         }
@@ -900,10 +901,9 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
           f = live ? a.factors[(size_t)x.h * a.q_rows + (size_t)(x.t0 + tl) * a.G + head] : 0.0f;
           if (!live) tl = -1;
         }
-        wait(&bar.s_full[w][buf], done >> 1);
-        tc_fence_after();
+        const float top = ev_top[sp];
+        tc_fence_after();   // (S is there as well)
         if (warp_live) {
-          const float top = ev_top[sp];
           if (flags & F_FULL && top == top) {
             // The ordinary way: every row sees the whole block, and the block's values have one scale.  The weights are formed
             // against the maximum so far without looking for the block's own.  Their sum bounds them: while it is below FP16's
