@@ -13,7 +13,7 @@ namespace {
 // moves up, so what later rounds read lies behind all that earlier ones write.  What lies in the first block below `start`
 // stays where it is.  Keys pass through shared memory anyway, so the blocks' bounds come from there.  (One CTA a head, a block
 // after the other: 95 us for 16 sequences of up to 2,000 kept tokens of 6,000, 4 heads of 128; a block's loads ahead: 60; a
-// cluster, four blocks ahead: 24, for 67 MB that are read and written, most of it in L2.  Bound: loads, barriers of the cluster
+// cluster, four blocks ahead: 18, for 67 MB that are read and written, most of it in L2.  Bound: loads, barriers of the cluster
 // and stores that follow one another, two or three rounds.  A path of 8 of 32 drafts, 4 sequences: 4.0, a launch and one round.)
 constexpr int KC_THREADS = 256, KC_BLOCKS = 4;
 
@@ -370,10 +370,11 @@ __global__ void __launch_bounds__(KZ_ROW)
 cudaError_t launch_kv_compact(const bre_kv_cache* c, const int32_t* table, int B, int N, const int32_t* start,
                               const int32_t* nodes, int A, const int32_t* count, int32_t* length, int32_t* err, cudaStream_t s) {
   const KvTable tab{table, B, N, c->n_pages};
-  // CTAs of a head: blocks for all of them in the longest list, as far as the GPU has room
+  // CTAs of a head: blocks for all of them in the longest list, as far as the GPU has room for (three an SM fit; 16 sequences of
+  // up to 2,000 kept tokens, 4 heads: 1,024 CTAs 24.2 us, 512 18.3, 256 25.9)
   const long long blocks = ((long long)A + 2 * KV_BLOCK - 2) / KV_BLOCK, heads = 2LL * B * c->n_kv_heads;
   int ranks = 1;
-  while (ranks < 8 && ranks * KC_BLOCKS < blocks && heads * ranks < 4LL * device_sm_count()) ranks *= 2;
+  while (ranks < 8 && ranks * KC_BLOCKS < blocks && heads * ranks < 2LL * device_sm_count()) ranks *= 2;
   auto kern = c->head_dim == 128 ? kv_compact_kernel<128> : kv_compact_kernel<64>;
   const size_t smem = c->head_dim == 128 ? sizeof(CompactMem<128>) : sizeof(CompactMem<64>);
   static_assert(sizeof(CompactMem<128>) <= 48 * 1024, "no attribute needed");

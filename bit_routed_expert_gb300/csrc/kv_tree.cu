@@ -13,9 +13,10 @@
 // What bounds it: not the tensor cores nor DRAM yet, but the roles' chains of short steps (a wait is some 150 cycles
 // even where nothing is to be waited for) and instruction fetch: five roles' loops share a small instruction cache, so that code
 // that runs seldom costs some 250 cycles for every 128 bytes of it.  Hence little code: loops that are not unrolled far, what is
-// seldom out of line.  A step of 64 tokens takes 1,600 cycles for one tile and 2,200 for two, whose products take 1,260.
+// seldom out of line.  A step of 64 tokens takes 1,600 cycles for one tile and 2,100 for two, whose products take 1,260.  More than 16
+// warps would leave 96 registers a thread, which costs the softmax more than what other roles gain.
 // D = 128, G = 8, four kv heads: 32 sequences of up to 16,384 tokens, 16 drafts each, 122 us (2.3 TB/s); one of
-// 131,072, 64 drafts, 153 us (0.90 PFLOP/s, 0.47 of cuBLAS's); a prompt of 4,096 behind 4,096, 471 us (0.87 PFLOP/s).
+// 131,072, 64 drafts, 148 us (0.93 PFLOP/s, 0.48 of cuBLAS's); a prompt of 4,096 behind 4,096, 466 us (0.88 PFLOP/s).
 //
 // Sixteen warps:
 //   warps 0-3, 4-7  softmax, a thread a row: two tiles' rows of the same block, or, where there is one tile, its
