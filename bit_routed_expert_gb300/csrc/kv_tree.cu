@@ -13,10 +13,11 @@
 // What bounds it: not the tensor cores nor DRAM yet, but the roles' chains of short steps (a wait is some 150 cycles
 // even where nothing is to be waited for) and instruction fetch: five roles' loops share a small instruction cache, so that code
 // that runs seldom costs some 250 cycles for every 128 bytes of it.  Hence little code: loops that are not unrolled far, what is
-// seldom out of line.  A step of 64 tokens takes 1,600 cycles for one tile and 2,100 for two, whose products take 1,260.  More than 16
+// seldom out of line.  A step of 64 tokens takes 1,500 cycles for one tile and 2,100 for two, whose products take 1,260: with two the
+// softmax, the conversion and the issue of O's products take 1,700 to 1,800 each, and wait for one another.  More than 16
 // warps would leave 96 registers a thread, which costs the softmax more than what other roles gain.
-// D = 128, G = 8, four kv heads: 32 sequences of up to 16,384 tokens, 16 drafts each, 122 us (2.3 TB/s); one of
-// 131,072, 64 drafts, 148 us (0.93 PFLOP/s, 0.48 of cuBLAS's); a prompt of 4,096 behind 4,096, 466 us (0.88 PFLOP/s).
+// D = 128, G = 8, four kv heads: 32 sequences of up to 16,384 tokens, 16 drafts each, 116 us (2.5 TB/s); one of
+// 131,072, 64 drafts, 150 us (0.92 PFLOP/s, 0.48 of cuBLAS's); a prompt of 4,096 behind 4,096, 470 us (0.88 PFLOP/s).
 //
 // Sixteen warps:
 //   warps 0-3, 4-7  softmax, a thread a row: two tiles' rows of the same block, or, where there is one tile, its
@@ -25,7 +26,8 @@
 //                   blocks (eight warps: 20% slower)
 //   warp 12         walks through the share, looks up pages and starts the copies (TMA: queries and keys swizzled, values as
 //                   they lie)
-//   warps 13-15     issue the MMAs: S = Q K^T into tensor memory, by turns; O += P V with P read from tensor memory
+//   warps 13, 14    issue either group's S = Q K^T into tensor memory and tell it of its blocks and of units' ends
+//   warp 15         issues O += P V, with P read from tensor memory
 //
 // The keys' codes are an MMA operand as they lie in the cache.  A BF16 query is q = 2^e (a + b), a and b E4M3: a is
 // q's nearest code, b the rest's, so that the two products add up to that of q itself (see bre.h for what is lost).  Two
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     const int i = tid, g = i & 1, j = i >> 1;
     mbar_init(&bar.k_full[i], 1), mbar_init(&bar.k_empty[i], 2), mbar_init(&bar.v_full[i], 1), mbar_init(&bar.v_empty[i], 4);
     mbar_init(&bar.v16_full[i], 2), mbar_init(&bar.v16_empty[i], 1);
-    mbar_init(&bar.gr_full[0][i], 2), mbar_init(&bar.gr_full[1][i], 2), mbar_init(&bar.gr_empty[0][i], 4), mbar_init(&bar.gr_empty[1][i], 4);
+    mbar_init(&bar.gr_full[0][i], 3), mbar_init(&bar.gr_full[1][i], 3), mbar_init(&bar.gr_empty[0][i], 4), mbar_init(&bar.gr_empty[1][i], 4);
     mbar_init(&bar.p_full[g][j], 4), mbar_init(&bar.o_done[g][j], 1);
     if (j == 0) mbar_init(&bar.q_full[g], 1), mbar_init(&bar.q_empty[g], 2);
     if (i == 0) mbar_init(&bar.swap_in, 8), mbar_init(&bar.swap_out, 8), mbar_init(&bar.drain, 3);
@@ -684,15 +686,13 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         if (uses[b]) mbar_wait_bounded(&bar.q_full[b], (uses[b] - 1) & 1, AT_WAIT);
     }
   } else if (warp == W_S || warp == W_S + 1) {
-    // ---- S = Q K^T: E4M3 operands, FP32 sums, M = 128; a block each in turn
-    // (Neither warp is four items ahead of the other, and uses c - 2 and c of a group's S are by the same warp or four items
-    // apart: when a use waits for its buffer's last one, the one before that has long been waited for.)
+    // ---- S = Q K^T: E4M3 operands, FP32 sums, M = 128; a warp either group's
     const uint32_t id_s = (1u << 4) | ((uint32_t)(KV_BLOCK >> 3) << 17) | ((128u >> 4) << 24);
     const uint64_t q0 = desc_codes<D>(smem_u32(sm + M::q)), k0 = desc_codes<D>(smem_u32(sm + M::k));
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const int me = warp - W_S;
-    int live = 0, qb = 0, kb = 0;   // the unit's query buffers; the next one-tile unit's buffer; blocks
-    Pair cs{0, 0}, gr{0, 0}, uses{0, 0};   // S and messages of either group, units of either query buffer so far
+    const int w = __shfl_sync(0xffffffffu, warp - W_S, 0);
+    int live = 0, qb = 0, c = 0, n = 0;   // the unit's query buffers; the next one-tile unit's; the group's S, messages so far
+    Pair uses{0, 0};                      // units of either query buffer so far
 #pragma unroll 1
     for (int it = 0;; ++it) {
       const int ks = it & 3;
@@ -700,47 +700,53 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       if (!wait.left) break;
       // (a warp reduction: what the MMAs' operands are formed from is then in uniform registers, where they want it)
       const int flags = (int)__reduce_or_sync(0xffffffffu, (uint32_t)to_s[ks]), two = flags & F_TWO ? 1 : 0;
-      const bool mine = flags & F_BLOCK && (kb & 1) == me;
-      if (!mine && lane == 0) mbar_arrive(&bar.k_empty[ks]);
-      if (!(flags & F_BLOCK)) {
-        if (flags & F_EXIT) break;
-        if (live) {
-          if (elect_one()) {   // (each warp's commit goes by its own products)
-            if (live & 1) mma_commit(&bar.q_empty[0]);
-            if (live & 2) mma_commit(&bar.q_empty[1]);
-          }
-          __syncwarp();
-          if (!two) qb ^= 1;
-          uses.a += live & 1, uses.b += live >> 1, live = 0;
-        }
-        ++gr.a, ++gr.b;
-        continue;
-      }
-      ++kb;
       if (flags & F_BEGIN) {
         live = two ? 3 : 1 << qb;
         if (live & 1) wait(&bar.q_full[0], uses.a);
         if (live & 2) wait(&bar.q_full[1], uses.b);
       }
-#pragma unroll 1
-      for (int g = 0; g <= two; ++g) {
-        const int w = two ? g : flags & F_ODD ? 1 : 0, qt = two ? g : qb, c = cs[w], n = gr[w], buf = c & 1;
-        cs.add(w), gr.add(w);
-        if (!mine) continue;
-        wait(&bar.o_done[w][buf], (c >> 1) + 1);   // the weights that lay in S's columns have been used
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t st = tm + w * 128 + buf * 64;
-          const uint64_t qd = q0 + ((qt * 2 * M::TERM) >> 4), kd = k0 + ((ks * M::K) >> 4);
+      const bool block = flags & F_BLOCK, mine = !block || two || (flags & F_ODD ? 1 : 0) == w;
+      if (mine) {
+        const int buf = c & 1;
+        if (block) {
+          wait(&bar.o_done[w][buf], (c >> 1) + 1);   // the weights that lay in S's columns have been used
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t st = tm + w * 128 + buf * 64;
+            const uint64_t qd = q0 + (((two ? w : qb) * 2 * M::TERM) >> 4), kd = k0 + ((ks * M::K) >> 4);
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
+            for (int term = 0; term < 2; ++term)
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-              mma_codes(st, qd + ((term * M::TERM + kk * 32) >> 4), kd + ((kk * 32) >> 4), id_s, term + kk > 0);
-          mma_commit(&bar.gr_full[w][n & 3]);
-          if (g == two) mma_commit(&bar.k_empty[ks]);
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_codes(st, qd + ((term * M::TERM + kk * 32) >> 4), kd + ((kk * 32) >> 4), id_s, term + kk > 0);
+            mma_commit(&bar.gr_full[w][n & 3]);
+          }
+          __syncwarp();
+          ++c;
+        }
+        // the group's message (of a block two more parts are to come: its S and its scales)
+        wait(&bar.gr_empty[w][n & 3], (n >> 2) + 1);
+        if (!wait.left) break;
+        if (lane < ITEM_WORDS) reinterpret_cast<int*>(&group[w][n & 3])[lane] = reinterpret_cast<const int*>(&to_v[ks])[lane];
+        __syncwarp();
+        if (lane < (block ? 1 : 3)) mbar_arrive(&bar.gr_full[w][n & 3]);
+        ++n;
+      }
+      if (block && mine) {   // (the message has been copied as well)
+        if (elect_one()) mma_commit(&bar.k_empty[ks]);
+      } else if (lane == 0) {
+        mbar_arrive(&bar.k_empty[ks]);
+      }
+      __syncwarp();
+      if (flags & F_EXIT) break;
+      if (!block && live) {
+        if (elect_one()) {   // (each warp's commit goes by its own products)
+          if (live & 1) mma_commit(&bar.q_empty[0]);
+          if (live & 2) mma_commit(&bar.q_empty[1]);
         }
         __syncwarp();
+        if (!two) qb ^= 1;
+        uses.a += live & 1, uses.b += live >> 1, live = 0;
       }
     }
     // products that are under way still use tensor and shared memory
@@ -803,7 +809,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       } else {
         const int st = kb & 3, sp = kb % TT_SC;
         const unsigned char* const raw = sm + M::v + vs * M::V;
-        bool speaks = cw == 0;
         uint32_t up0 = 0, up1 = 0;   // of rows lane and lane + 32: what their codes are multiplied with; 0: not seen
         if (flags & F_BLOCK) {
           // slots that some row sees (others may never have been written: their values become zeros)
@@ -821,8 +826,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
           // FP16 pairs of 2^(the row's scale - the largest), at least 2^-15
           auto relative = [&](int e) { return careful ? 0x3C003C00u : (uint32_t)max((15 - min(max(top - e, 0), 15)) << 10, 1 << 9) * 0x10001u; };
           up0 = s0 ? relative(e0) : 0u, up1 = s1 ? relative(e1) : 0u;
-          speaks = (kb >> 1 & 1) == (cw & 1);
-          if (speaks) {   // this block's scales for the softmax
+          if ((kb >> 1 & 1) == (cw & 1)) {   // this block's scales for the softmax, by one of the two warps
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int x = lane + 32 * i, ek = scales[x], ev = i ? e1 : e0;
@@ -831,20 +835,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
             }
             if (lane == 0) ev_top[sp] = careful ? __int_as_float(0x7FC00000) : (float)(top - 127);
             __syncwarp();
+            if (lane < 2 && who >> lane & 1) mbar_arrive(&bar.gr_full[lane][gr[lane] & 3]);
           }
-        }
-        if (speaks) {
-#pragma unroll 1
-          for (int g = 0; g < 2; ++g) {
-            if (!(who >> g & 1)) continue;
-            const int n = gr[g];
-            wait(&bar.gr_empty[g][n & 3], (n >> 2) + 1);
-            if (!wait.left) break;
-            if (lane < ITEM_WORDS) reinterpret_cast<int*>(&group[g][n & 3])[lane] = reinterpret_cast<const int*>(&to_v[vs])[lane];
-            __syncwarp();
-            if (lane == 0 || (lane == 1 && !(flags & F_BLOCK))) mbar_arrive(&bar.gr_full[g][n & 3]);   // (of a block S is the other half)
-          }
-          __syncwarp();
         }
         if (turn && flags & (F_BLOCK | F_EXIT)) {
           wait(&bar.v16_empty[st], (kb >> 2) + 1);

@@ -384,7 +384,8 @@ bre_status kv_attend(const bre_kv_cache *cache, const void *q_bf16, int64_t q_st
  * sequence should follow one another in the list: then each key is read once for all of them.
  * Logits, maxima and sums are FP32.  A query enters as FP16, as in kv_attend, or, where a sequence has many tokens in the call, as
  * the sum of two E4M3 numbers times a power of two that takes its head's largest magnitude to 224 .. 448: exactly down to
- * 2^-10 of that, off by 2^-19 of it at most below.  The probabilities enter the second product as FP16, as in kv_attend.
+ * 2^-10 of that, off by 2^-19 of it at most below (of heads whose largest magnitude is 2^-109 or more).  The probabilities
+ * enter the second product as FP16, as in kv_attend.
  *   start [B] int32 (negative counts as 0) and mask [T][words] uint64, or both NULL; out, lse as in kv_attend.
  *   ws: kv_attend_tree_workspace(T, ...) bytes of scratch, 256-byte aligned, which need no initialisation; calls that
  *   share it must be ordered (two graphs that may run at the same time need one each).
