@@ -16,8 +16,8 @@
 // seldom out of line.  A step of 64 tokens takes 1,500 cycles for one tile and 2,100 for two, whose products take 1,260: with two the
 // softmax, the conversion and the issue of O's products take 1,700 to 1,800 each, and wait for one another.  More than 16
 // warps would leave 96 registers a thread, which costs the softmax more than what other roles gain.
-// D = 128, G = 8, four kv heads: 32 sequences of up to 16,384 tokens, 16 drafts each, 116 us (2.5 TB/s); one of
-// 131,072, 64 drafts, 150 us (0.92 PFLOP/s, 0.48 of cuBLAS's); a prompt of 4,096 behind 4,096, 470 us (0.88 PFLOP/s).
+// D = 128, G = 8, four kv heads: 32 sequences of up to 16,384 tokens, 16 drafts each, 113 us (2.5 TB/s); one of
+// 131,072, 64 drafts, 152 us (0.90 PFLOP/s, 0.47 of cuBLAS's); a prompt of 4,096 behind 4,096, 463 us (0.89 PFLOP/s).
 //
 // Sixteen warps:
 //   warps 0-3, 4-7  softmax, a thread a row: two tiles' rows of the same block, or, where there is one tile, its
@@ -54,7 +54,7 @@ constexpr int W_CONV = 8, W_LOAD = 12, W_S = 13, W_O = 15;
 constexpr int TT_K = 4, TT_V = 4, TT_V16 = 4, TT_GROUP = 4, TT_SC = 16;
 constexpr int TT_MAX_CTAS = 160;
 constexpr int JOIN_CTAS = 4;             // of the joining kernel, for every one of the other
-constexpr int JOIN_FEW = 32;             // parts that a warp joins
+constexpr int JOIN_FEW = 32;             // parts that half a warp joins
 constexpr float P_MOST = 32768.0f;       // a block's sum of weights up to which they are FP16 numbers for sure
 // Costs of the shares: a block for one tile, for two tiles, and what a unit takes beside its blocks.
 constexpr int COST_ONE = 2, COST_TWO = 3, COST_UNIT = 16;
@@ -1008,8 +1008,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
 // ---------------------------------------------------------------------------
 // Joining the parts
 // ---------------------------------------------------------------------------
-// Every CTA finds out which units there are to join, `ctas` at most, and takes its pieces of them: a row where it has
-// many parts, else a row a warp (see join_rows).
+// Every CTA finds out which units there are to join, `ctas` at most, and takes its pieces of them (see join_at_once).
 template <int D>
 __global__ void __launch_bounds__(JOIN_WARPS * 32, 4) kv_tree_join_kernel(const TreeParams a, int ctas) {
   static_assert(TT_MAX_CTAS <= JOIN_WARPS * 32, "a thread an entry");
@@ -1020,7 +1019,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 4) kv_tree_join_kernel(const 
   pdl_launch_dependents();
   const Join own = tid < ctas ? a.join[tid] : Join{0, 0, 0, 0};
   const int rows = own.n * a.G;
-  int n = own.parts == 0 ? 0 : own.parts > JOIN_FEW ? rows : (rows + JOIN_WARPS - 1) / JOIN_WARPS;   // pieces
+  const int at_once = join_at_once(own.parts, JOIN_FEW);
+  int n = own.parts == 0 ? 0 : (rows + at_once - 1) / at_once;   // pieces
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
     const int x = __shfl_up_sync(0xffffffffu, n, o);

@@ -26,46 +26,50 @@ __device__ __forceinline__ uint64_t seen_bits(const uint64_t* __restrict__ mask,
 }
 
 // A row's parts (index(p): where part p's maximum and sum, and its output, lie), those from `from` on in steps of `step`,
-// joined in their order by a warp: the maxima and sums by the lanes, then the outputs.
-template <int D>
+// joined in their order by LANES neighbouring lanes of a warp: the maxima and sums by the lanes, then the outputs.
+template <int D, int LANES>
 struct Joined {
-  float top, sum, v[D / 32];   // maximum, sum, output of this lane's channels, relative to the maximum
+  static constexpr int CL = D / LANES, AHEAD = LANES / 4;   // channels of a lane; parts on their way
+  float top, sum, v[CL];   // maximum, sum, output of this lane's channels, relative to the maximum
 
   template <typename Index>
   __device__ __forceinline__ Joined(const float2* ml, const float* part, int parts, int from, int step, Index index) {
-    constexpr int CL = D / 32, AHEAD = 8;
-    using Piece = typename std::conditional<CL == 4, float4, float2>::type;
-    const int lane = threadIdx.x & 31, n = (parts - from + step - 1) / step;   // its parts
+    using Piece = typename std::conditional<CL % 4 == 0, float4, float2>::type;
+    constexpr int PIECES = CL * (int)sizeof(float) / (int)sizeof(Piece);
+    const int lane = threadIdx.x % LANES, n = (parts - from + step - 1) / step;   // its parts (as many for all of the warp)
     union Loaded {
-      Piece x;
+      Piece x[PIECES];
       float v[CL];
     } o[AHEAD];
     auto fetch = [&](int i0) {   // on their way while the weights are formed
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        o[i].x = Piece{};
-        if (i0 + i < n) o[i].x = *reinterpret_cast<const Piece*>(part + index(from + (i0 + i) * step) * D + lane * CL);
-      }
+      for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+        for (int k = 0; k < PIECES; ++k) {
+          o[i].x[k] = Piece{};
+          if (i0 + i < n) o[i].x[k] = reinterpret_cast<const Piece*>(part + index(from + (i0 + i) * step) * D + lane * CL)[k];
+        }
     };
     fetch(0);
     top = -INFINITY, sum = 0.0f;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[index(from + i * step)].x);
+    for (int i = lane; i < n; i += LANES) top = fmaxf(top, ml[index(from + i * step)].x);
+    __syncwarp();
 #pragma unroll
-    for (int j = 16; j; j >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, j));
+    for (int j = LANES / 2; j; j >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, j));
     const float ref = top > -INFINITY ? top : 0.0f;
 #pragma unroll
     for (int c = 0; c < CL; ++c) v[c] = 0.0f;
     float w = 0.0f;
 #pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += AHEAD) {
-      if (i0 % 32 == 0) {
+      if (i0 % LANES == 0) {
         const float2 y = i0 + lane < n ? ml[index(from + (i0 + lane) * step)] : make_float2(-INFINITY, 0.0f);
         w = ex2(y.x - ref);
         sum += scale_sum(y.y, y.x - ref);
       }
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
+        const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) % LANES, LANES);
         if (i0 + i < n) {
 #pragma unroll
           for (int c = 0; c < CL; ++c) v[c] = fmaf(wi, o[i].v[c], v[c]);
@@ -74,47 +78,54 @@ struct Joined {
       if (i0 + AHEAD < n) fetch(i0 + AHEAD);
     }
 #pragma unroll
-    for (int j = 16; j; j >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, j);
+    for (int j = LANES / 2; j; j >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, j);
   }
   __device__ __forceinline__ void store(uint16_t* out, float* lse) const {
-    constexpr int CL = D / 32;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x % LANES;
     const float inv = 1.0f / sum;
     uint32_t b[CL / 2];
 #pragma unroll
     for (int i = 0; i < CL / 2; ++i) b[i] = sum == 0.0f ? 0u : pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
-    if constexpr (CL == 4) *reinterpret_cast<uint2*>(out + lane * CL) = make_uint2(b[0], b[1]);
+    if constexpr (CL == 8) *reinterpret_cast<uint4*>(out + lane * CL) = make_uint4(b[0], b[1], b[2], b[3]);
+    else if constexpr (CL == 4) *reinterpret_cast<uint2*>(out + lane * CL) = make_uint2(b[0], b[1]);
     else *reinterpret_cast<uint32_t*>(out + lane * CL) = b[0];
     if (lane == 0 && lse) *lse = sum == 0.0f ? -INFINITY : LN2 * (top > -INFINITY ? top - P_SHIFT + log2f(sum) : log2f(sum));
   }
 };
 
+// Rows that a CTA of JOIN_WARPS warps joins at a time.  Few parts: half a warp a row (a prompt of 4,096 tokens, 38,912 rows of
+// 2 parts: 463 us in all, 474 by whole warps; 2,048 rows of 19 parts: 152 and 149).  Many: the CTA a row, its parts dealt to
+// the warps, whose results are joined once more (304 parts of 32 rows by warps: 38 us).
 constexpr int JOIN_WARPS = 8;
-// Rows first, first + stride, .. of `rows` by a CTA of JOIN_WARPS warps.  Few parts (up to `few`): a warp a row.  Many: a row at
-// a time, its parts dealt to the warps, whose results are joined once more (304 parts of 32 rows, a warp a row: 38 us).
+__host__ __device__ constexpr int join_at_once(int parts, int few) { return parts <= few ? 2 * JOIN_WARPS : 1; }
+// Pieces first, first + stride, .. of `rows` by a CTA.
 template <int D, typename Index, typename Place>
 __device__ __forceinline__ void join_rows(const float2* ml, const float* part, int parts, int few, int first, int stride, int rows, Index index,
                                           Place place, uint16_t* out, float* lse) {
   __shared__ float2 sh_ml[2][JOIN_WARPS];
   __shared__ float sh_part[2][JOIN_WARPS * D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (parts <= few) {
-    for (int r = first * JOIN_WARPS + warp; r < rows; r += stride * JOIN_WARPS) {
+  const int at_once = join_at_once(parts, few);
+  if (at_once > 1) {
+    for (int r0 = first * at_once + 2 * warp; r0 < rows; r0 += stride * at_once) {
+      const int r = min(r0 + lane / 16, rows - 1);   // (both halves of a warp stay together)
+      const Joined<D, 16> row(ml, part, parts, 0, 1, [&](int p) { return index(p, r); });
       const size_t at = place(r);
-      Joined<D>(ml, part, parts, 0, 1, [&](int p) { return index(p, r); }).store(out + at * D, lse ? lse + at : nullptr);
+      if (r0 + lane / 16 < rows) row.store(out + at * D, lse ? lse + at : nullptr);
+      __syncwarp();
     }
     return;
   }
   int turn = 0;
   for (int r = first; r < rows; r += stride, turn ^= 1) {
-    const Joined<D> mine(ml, part, parts, warp, JOIN_WARPS, [&](int p) { return index(p, r); });
+    const Joined<D, 32> mine(ml, part, parts, warp, JOIN_WARPS, [&](int p) { return index(p, r); });
     if (lane == 0) sh_ml[turn][warp] = make_float2(mine.top, mine.sum);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) sh_part[turn][warp * D + lane * (D / 32) + i] = mine.v[i];
     __syncthreads();
     if (warp == 0) {
       const size_t at = place(r);
-      Joined<D>(sh_ml[turn], sh_part[turn], JOIN_WARPS, 0, 1, [](int p) { return (size_t)p; }).store(out + at * D, lse ? lse + at : nullptr);
+      Joined<D, 32>(sh_ml[turn], sh_part[turn], JOIN_WARPS, 0, 1, [](int p) { return (size_t)p; }).store(out + at * D, lse ? lse + at : nullptr);
     }
   }
 }

@@ -125,8 +125,8 @@ cudaError_t launch(const TreeRows& a, int T, cudaStream_t s) {
   const cudaError_t e = launch_k(kern, dim3((unsigned)(units * a.shares)), dim3(AR_WARPS * 32), 0, s, a);
   if (e != cudaSuccess || a.shares == 1) return e;
   const int rows = (int)(units * a.G);   // (of few units, as there are several shares)
-  return launch_k(kv_tree_rows_join_kernel<D>, dim3((unsigned)(a.shares > JOIN_WARPS ? rows : (rows + JOIN_WARPS - 1) / JOIN_WARPS)),
-                  dim3(JOIN_WARPS * 32), 0, s, a, rows);
+  const int at_once = join_at_once(a.shares, JOIN_WARPS);
+  return launch_k(kv_tree_rows_join_kernel<D>, dim3((unsigned)((rows + at_once - 1) / at_once)), dim3(JOIN_WARPS * 32), 0, s, a, rows);
 }
 
 }  // namespace
