@@ -17,7 +17,7 @@
 // softmax, the conversion and the issue of O's products take 1,700 to 1,800 each, and wait for one another.  More than 16
 // warps would leave 96 registers a thread, which costs the softmax more than what other roles gain.
 // D = 128, G = 8, four kv heads: 32 sequences of up to 16,384 tokens, 16 drafts each, 113 us (2.5 TB/s); one of
-// 131,072, 64 drafts, 152 us (0.90 PFLOP/s, 0.47 of cuBLAS's); a prompt of 4,096 behind 4,096, 463 us (0.89 PFLOP/s).
+// 131,072, 64 drafts, 151 us (0.91 PFLOP/s, 0.47 of cuBLAS's); a prompt of 4,096 behind 4,096, 452 us (0.91 PFLOP/s).
 //
 // Sixteen warps:
 //   warps 0-3, 4-7  softmax, a thread a row: two tiles' rows of the same block, or, where there is one tile, its
@@ -209,14 +209,24 @@ __device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
   for (int pass = 0; pass < 2; ++pass) {   // a second pass, where the list is longer than the CTA, finds the place of the share
     long long c = 0, at = 0;
     int from = 0;
+    int next[6];   // sequence and position of a thread's token, the one before it and the one behind it, of the next chunk
+    auto fetch = [&](int base) {
+      const int t = base + tid;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int u = i == 0 ? t : i == 1 ? t - 1 : t + 1;
+        const bool is = u >= 0 && u < a.T;
+        next[2 * i] = is ? __ldg(a.seq + u) : 0, next[2 * i + 1] = is ? __ldg(a.pos + u) : -1;
+      }
+    };
+    fetch(start);
 #pragma unroll 1
     for (int base = start; base < a.T && (pass == 0 || sum <= lo); base += TT_THREADS) {
       if (tid == 0 && base % every == 0) m.kept_run[base / every] = run, m.kept_top[base / every] = top, m.kept_sum[base / every] = sum;
       const int t = base + tid;
-      const bool in = t < a.T, before = in && t > 0, behind = t + 1 < a.T;
-      const int s = in ? __ldg(a.seq + t) : 0, p = in ? __ldg(a.pos + t) : -1;
-      const int sb = before ? __ldg(a.seq + t - 1) : 0, pb = before ? __ldg(a.pos + t - 1) : -1;
-      const int sn = behind ? __ldg(a.seq + t + 1) : 0, pn = behind ? __ldg(a.pos + t + 1) : -1;
+      const bool in = t < a.T, behind = t + 1 < a.T;
+      const int s = next[0], p = next[1], sb = next[2], pb = next[3], sn = next[4], pn = next[5];
+      fetch(base + TT_THREADS);
       // first token of the run
       const uint32_t begins = __ballot_sync(0xffffffffu, in && (t == 0 || other_run(s, p, sb, pb)));
       if (lane == 0) m.run[warp] = begins ? base + 32 * warp + 31 - __clz(begins) : -1;
@@ -251,12 +261,14 @@ __device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
       if (tid == TT_THREADS - 1) m.last_run = r, m.last_top = m.top[slot];
       __syncthreads();
       run = m.last_run, top = m.last_top;
-      at = sum + c - own;
-#pragma unroll 4
-      for (int w = 0; w < TT_WARPS; ++w) {
-        if (w < warp) at += m.sum[w];
-        sum += m.sum[w];
-      }
+      // the warps' sums, in two parts of 32 bits (a chunk's are below 2^51)
+      const long long of = lane < TT_WARPS ? m.sum[lane] : 0, mine = lane < warp ? of : 0;
+      auto all = [](long long x) {
+        const uint32_t low = __reduce_add_sync(0xffffffffu, (uint32_t)x & 0xFFFFFFu), high = __reduce_add_sync(0xffffffffu, (uint32_t)(x >> 24));
+        return ((long long)high << 24) + low;
+      };
+      at = sum + c - own + all(mine);
+      sum += all(of);
       c = own, from = t - idx;
       if (pass && lo >= at && lo < at + c) m.found = from, m.found_at = at;
       __syncthreads();
