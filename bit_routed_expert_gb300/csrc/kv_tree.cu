@@ -188,7 +188,9 @@ constexpr int KEPT = 32;
 
 struct PlanMem {
   int run[TT_WARPS], top[TT_THREADS];
-  int last_run, last_top;  // of a chunk's last token: first token of its run, largest position of its tile
+  // of a chunk's last token: first token of its run, largest position of its tile so far (of none, if the tile ends with the chunk:
+  // the next chunk's first tile is then another one, whose cost would count the former's position)
+  int last_run, last_top;
   int kept_run[KEPT], kept_top[KEPT];   // before chunk i * every
   long long kept_sum[KEPT];
   long long sum[TT_WARPS];
@@ -249,8 +251,8 @@ __device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
       if (lane == 31 || heads >> (lane + 1) & 1u) atomicMax(&m.top[slot], high);
       __syncthreads();
       c = 0;
-      if (in && (!behind || other_run(s, p, sn, pn) || idx == a.per - 1))   // a tile's last token
-        c = Unit(idx + 1, m.top[slot], a.tab.N, per_one).cost() * a.H;
+      const bool last = in && (!behind || other_run(s, p, sn, pn) || idx == a.per - 1);   // a tile's last token
+      if (last) c = Unit(idx + 1, m.top[slot], a.tab.N, per_one).cost() * a.H;
       const long long own = c;
 #pragma unroll 1
       for (int o = 1; o < 32; o *= 2) {
@@ -258,7 +260,7 @@ __device__ __noinline__ void make_plan(const TreeParams& a, PlanMem& m) {
         if (lane >= o) c += x;
       }
       if (lane == 31) m.sum[warp] = c;
-      if (tid == TT_THREADS - 1) m.last_run = r, m.last_top = m.top[slot];
+      if (tid == TT_THREADS - 1) m.last_run = r, m.last_top = last ? INT32_MIN : m.top[slot];
       __syncthreads();
       run = m.last_run, top = m.last_top;
       // the warps' sums, in two parts of 32 bits (a chunk's are below 2^51)
