@@ -1096,7 +1096,7 @@ size_t kv_tree_ws_bytes(int T, int Hq, int H, int D) {
   const size_t slots = 2 * TT_MAX_CTAS, rows = slot_rows(T, G);
   const size_t tiles = codes_bytes(T, H, G, D) + factor_bytes(T, H, G) + TT_MAX_CTAS * sizeof(Join) +
                        slots * rows * (sizeof(float2) + D * sizeof(float));
-  const size_t single = tree_rows_ws_bytes(T, H, G, D);
+  const size_t single = tree_rows_ws_bytes(H, G, D);
   return tiles > single ? tiles : single;
 }
 

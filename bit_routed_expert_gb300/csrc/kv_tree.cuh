@@ -131,7 +131,7 @@ __device__ __forceinline__ void join_rows(const float2* ml, const float* part, i
 }
 
 // A token at a time (kv_tree_rows.cu)
-size_t tree_rows_ws_bytes(int T, int H, int G, int D);
+size_t tree_rows_ws_bytes(int H, int G, int D);
 cudaError_t launch_tree_rows(const TreeArgs& a, cudaStream_t s);
 
 }  // namespace bre

@@ -131,9 +131,10 @@ cudaError_t launch(const TreeRows& a, int T, cudaStream_t s) {
 
 }  // namespace
 
-size_t tree_rows_ws_bytes(int T, int H, int G, int D) {
-  const long long units = (long long)T * H, shares = most_shares(units);
-  return shares == 1 ? 0 : (size_t)(units * shares) * G * (sizeof(float2) + D * sizeof(float));
+// Enough for every call of as many tokens or fewer: these may have more shares in all (whole numbers for each: three tokens of
+// four kv heads have 12 x 101, one has 4 x 304), but never more than TREE_ROWS_CTAS.
+size_t tree_rows_ws_bytes(int H, int G, int D) {
+  return most_shares(H) == 1 ? 0 : (size_t)TREE_ROWS_CTAS * G * (sizeof(float2) + D * sizeof(float));
 }
 
 cudaError_t launch_tree_rows(const TreeArgs& t, cudaStream_t s) {

@@ -387,8 +387,8 @@ bre_status kv_attend(const bre_kv_cache *cache, const void *q_bf16, int64_t q_st
  * 2^-10 of that, off by 2^-19 of it at most below (of heads whose largest magnitude is 2^-109 or more).  The probabilities
  * enter the second product as FP16, as in kv_attend.
  *   start [B] int32 (negative counts as 0) and mask [T][words] uint64, or both NULL; out, lse as in kv_attend.
- *   ws: kv_attend_tree_workspace(T, ...) bytes of scratch, 256-byte aligned, which need no initialisation; calls that
- *   share it must be ordered (two graphs that may run at the same time need one each).
+ *   ws: kv_attend_tree_workspace(T, ...) bytes of scratch, 256-byte aligned, which need no initialisation; enough for calls
+ *   of fewer tokens too; calls that share it must be ordered (two graphs that may run at the same time need one each).
  * Requires G <= 16, words <= 1024, n_pages * n_kv_heads < 2^31, T * n_heads < 2^30. */
 size_t kv_attend_tree_workspace(int T, int n_heads, int n_kv_heads, int head_dim);
 bre_status kv_attend_tree(const bre_kv_cache* cache, const void* q_bf16, int64_t q_stride, int n_heads, const int32_t* seq,
