@@ -58,7 +58,7 @@ const char* bre_status_string(bre_status s) {
   return "unknown status";
 }
 
-size_t moe_route_workspace(int T, int E) { return (T > 0 && E > 0) ? route_ws_bytes(T, E) : 0; }
+size_t moe_route_workspace(int T, int E) { return (T > 0 && E > 0) ? route_ws_upto(T, E) : 0; }
 
 bre_status moe_route(const void* x_bf16, const float* w_r, const float* bias, int T, int d, int E, int k,
                      int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes, bre_stream_t stream) {

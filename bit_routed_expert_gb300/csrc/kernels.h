@@ -22,7 +22,8 @@ cudaError_t launch_engram_inject(const uint8_t* table, long long n_rows, const i
                                  float* gate_out, int32_t* err, void* ws, cudaStream_t s);
 
 // router
-size_t route_ws_bytes(int T, int E);
+size_t route_ws_bytes(int T, int E);   // of a call with T tokens
+size_t route_ws_upto(int T, int E);    // of any call with 1 .. T tokens
 cudaError_t launch_route(const uint16_t* x, const float* w_r, const float* bias, int T, int d, int E, int k,
                          int32_t* ids, float* w, void* ws, cudaStream_t s);
 cudaError_t launch_route_ex(const uint16_t* x, const float* w_r, const float* bias, int T, int d, int E, int k,

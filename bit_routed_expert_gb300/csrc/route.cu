@@ -1108,6 +1108,8 @@ size_t route_ws_bytes(int T, int E) {
   return s + 256;
 }
 
+size_t route_ws_upto(int T, int E) { return std::max(route_ws_bytes(T, E), route_ws_bytes(std::min(T, SMALL_T_MAX), E)); }
+
 namespace {
 cudaError_t route_impl(const uint16_t* x, const float* w_r, const float* bias, int T, int d, int E, int k,
                        int32_t* ids, float* w, void* ws, const PermOut& po, const RouteVar& rv, bool* permuted,

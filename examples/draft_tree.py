@@ -35,7 +35,7 @@ class TreeLayer(SparseLayer):
     grow: refs counts the entries of the table that name each page."""
 
     def __init__(self, dev, T_max: int, B: int, max_len: int):
-        super().__init__(dev, max(T_max, 128), B, max_len)   # (the router's scratch for 32 tokens is as large as for 128)
+        super().__init__(dev, T_max, B, max_len)
         self.table.fill_(-1)
         self.refs = torch.zeros(self.table.numel(), dtype=torch.int32, device=dev)
         self.turns, self.gain = rope_turns(self.DIM, device=dev)

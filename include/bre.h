@@ -104,8 +104,8 @@ const char *bre_status_string(bre_status s);
  * scores.
  *   x_bf16 [T][d] BF16; w_r [d][E] FP32 row-major; bias [E] FP32 or NULL;
  *   topk_ids [T][k] int32 out; topk_w [T][k] FP32 out.
- *   ws: moe_route_workspace(T, E) bytes of scratch, zero-filled once after
- *   allocation (the call leaves it ready for the next call).
+ *   ws: moe_route_workspace(T, E) bytes of scratch (enough for fewer tokens too),
+ *   zero-filled once after allocation (the call leaves it ready for the next call).
  * Requires 1 <= k <= min(E, 32), E <= 1024, d % 32 == 0. */
 size_t moe_route_workspace(int T, int E);
 bre_status moe_route(const void *x_bf16, const float *w_r, const float *bias, int T, int d, int E, int k,

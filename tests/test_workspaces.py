@@ -3,7 +3,9 @@ import pytest
 import torch
 
 import kv_reference as R
-from bit_routed_expert_gb300 import KvCache, kv_attend_tree, kv_attend_tree_workspace
+from bit_routed_expert_gb300 import (KvCache, kv_attend_tree, kv_attend_tree_workspace, moe_expert_ffn_workspace, moe_route_workspace,
+                                     synth)
+from helpers import device_layer
 
 
 @pytest.mark.parametrize("H", [1, 2, 3, 4, 8, 40, 610])
@@ -12,6 +14,27 @@ from bit_routed_expert_gb300 import KvCache, kv_attend_tree, kv_attend_tree_work
 def test_tree_attention(H, G, D):
     sizes = [kv_attend_tree_workspace(T, H * G, H, D) for T in range(1, 1400)]
     assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (8, 2), (64, 8), (384, 6), (1024, 32)])
+def test_moe(E, k):
+    """The small-batch router, for up to 32 tokens, needs more than the other for some more."""
+    sizes = [moe_route_workspace(T, E) for T in range(1, 700)]
+    assert sizes == sorted(sizes)
+    sizes = [moe_expert_ffn_workspace(T, k, E, 512, 256, 256) for T in range(1, 700)]
+    assert sizes == sorted(sizes)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T_max", [33, 64, 127])
+def test_moe_layer_of_fewer_tokens(cuda_dev, T_max):
+    layer, full = device_layer(3, 0, synth.TINY, T_max, cuda_dev), device_layer(3, 0, synth.TINY, 256, cuda_dev)
+    x = R.rows(4, T_max, synth.TINY.d).to(cuda_dev)
+    for T in (T_max, 24, 32, 1, T_max, 9):
+        out, info = layer.forward(x[:T])
+        want, also = full.forward(x[:T])
+        assert torch.equal(out, want) and torch.equal(info["ids"], also["ids"])
+    assert int(layer.dev_err) == 0
 
 
 @pytest.mark.gpu
