@@ -367,16 +367,47 @@ def rope_turns(rot_dim: int, theta: float = 10000.0, scaling: str | None = None,
     return turns.to(device), gain.value
 
 
+def _rotate(q, k, pos, turns, gain, offset, interleaved, backward, q_out, k_out, stream):
+    rc, q_out, k_out = _lib.load_kv().rotate(q, k, pos, turns, gain, offset, interleaved, backward, q_out, k_out, _raw(stream))
+    if rc:
+        check(rc, "kv_rotate")
+    return q_out, k_out
+
+
+class _Rotate(torch.autograd.Function):
+    """kv_rotate of queries or keys that require gradients: the map is linear, its gradient the transposed one."""
+
+    @staticmethod
+    def forward(ctx, q, k, pos, turns, gain, offset, interleaved, backward, stream):
+        ctx.save_for_backward(pos, turns)
+        ctx.set_materialize_grads(False)
+        ctx.how = gain, offset, interleaved, not backward
+        out = _rotate(q, k, pos, turns, gain, offset, interleaved, backward, None, None, stream)
+        ctx.mark_non_differentiable(*(o for o, needs in zip(out, ctx.needs_input_grad) if o is not None and not needs))
+        return out
+
+    @staticmethod
+    def backward(ctx, q_grad, k_grad):
+        pos, turns = ctx.saved_tensors
+        none = (None,) * 7
+        q_grad, k_grad = (g if g is None else g.contiguous() for g in (q_grad, k_grad))
+        if q_grad is None:
+            return (None, None if k_grad is None else kv_rotate(k_grad, None, pos, turns, *ctx.how)[0], *none)
+        return (*kv_rotate(q_grad, k_grad, pos, turns, *ctx.how), *none)
+
+
 def kv_rotate(q, k, pos, turns, gain: float = 1.0, offset: int = 0, interleaved: bool = False, backward: bool = False, q_out=None,
               k_out=None, stream=None):
     """Rotary positions: channels offset .. offset + 2 len(turns) - 1 of every head of q [T, n_heads, D] and k [T, n_kv_heads, D]
     (BF16, possibly slices of a projection's rows; k may be None) turn by pos[t] * turns (int64, rope_turns), as two halves
     or, interleaved, as neighbours.  backward: the transposed rotation, for gradients.  Returns (q_out, k_out): new tensors
-    unless given; q_out=q, k_out=k works in place."""
-    rc, q_out, k_out = _lib.load_kv().rotate(q, k, pos, turns, gain, offset, interleaved, backward, q_out, k_out, _raw(stream))
-    if rc:
-        check(rc, "kv_rotate")
-    return q_out, k_out
+    unless given; q_out=q, k_out=k works in place.  Gradients flow to q and k where autograd records; such a call takes no
+    q_out or k_out (ValueError)."""
+    if torch.is_grad_enabled() and (getattr(q, "requires_grad", False) or getattr(k, "requires_grad", False)):
+        if q_out is not None or k_out is not None:
+            raise ValueError("q_out and k_out do not go with gradients: use torch.no_grad(), or leave them out")
+        return _Rotate.apply(q, k, pos, turns, gain, offset, interleaved, backward, stream)
+    return _rotate(q, k, pos, turns, gain, offset, interleaved, backward, q_out, k_out, stream)
 
 
 def kv_compact(cache: KvCache, table, start, nodes, count, length=None, dev_err=None, stream=None):
