@@ -31,6 +31,11 @@ __device__ __forceinline__ float scale_sum(float l, float d) {
   return l * h * h;
 }
 
+// What weights are held against, m the maximum: 2^8 times as large as it, unless it is so large that the 8 would be lost, or
+// doubled, in rounding.
+constexpr float M_LARGE = 0x1p26f;
+__device__ __forceinline__ float weights_base(float m) { return fabsf(m) < M_LARGE ? m - P_SHIFT : m; }
+
 struct AttendArgs {
   const uint8_t* pages;
   int H, G;

@@ -188,9 +188,10 @@ struct Rows {
 #pragma unroll
         for (int d = 4; d < 32; d *= 2) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], d));
         mx[c] = fmaxf(mx[c], m[nt][c]);
-        const float base_m = mx[c] > -INFINITY ? mx[c] - P_SHIFT : 0.0f;   // NaN logits have no maximum
-        const float r0 = ex2(m[nt][c] - P_SHIFT - base_m);
-        l[nt][c] = scale_sum(l[nt][c], m[nt][c] - P_SHIFT - base_m);
+        const float base_m = mx[c] > -INFINITY ? weights_base(mx[c]) : 0.0f;   // NaN logits have no maximum
+        const float lower = weights_base(m[nt][c]) - base_m;
+        const float r0 = ex2(lower);
+        l[nt][c] = scale_sum(l[nt][c], lower);
         m[nt][c] = mx[c];
         float without = l[nt][c];
         if (large) {

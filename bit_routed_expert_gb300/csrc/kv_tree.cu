@@ -56,6 +56,10 @@ constexpr int TT_MAX_CTAS = 160;
 constexpr int JOIN_CTAS = 4;             // of the joining kernel, for every one of the other
 constexpr int JOIN_FEW = 32;             // parts that half a warp joins
 constexpr float P_MOST = 32768.0f;       // a block's sum of weights up to which they are FP16 numbers for sure
+// Logits are below 2^24.7 (128 products of codes up to 448) times the row's factor and the key's scale.  Where these are below F_LARGE
+// and 2^K_LARGE, that is 2^26.7, an unrounded one is off by 4 at most from a rounded maximum that is as large.
+constexpr float F_LARGE = 0.25f;         // |q| of 880 for D = 128 and the usual scale
+constexpr int K_LARGE = 4;               // |k| of 7,168
 // Costs of the shares: a block for one tile, for two tiles, and what a unit takes beside its blocks.
 constexpr int COST_ONE = 2, COST_TWO = 3, COST_UNIT = 16;
 
@@ -349,7 +353,7 @@ __global__ void __launch_bounds__(256) kv_tree_queries_kernel(const TreeParams a
 // for the ordinary way: every token has an exponent ev of its own in its weight, and the terms of the sum of exponentials
 // are formed without it (they may be of any size where the weight has vanished).  By a whole warp.
 //
-// The largest logit plus ev.
+// The largest logit plus ev.  (A key's scale times the row's factor is exact; times S either may pass 2^128.)
 __device__ __noinline__ float careful_max(uint32_t S, const float* kf, const float* ev, float f, uint64_t seen) {
   float mx = -INFINITY;
 #pragma unroll 1
@@ -360,7 +364,7 @@ __device__ __noinline__ float careful_max(uint32_t S, const float* kf, const flo
     tmem_wait_ld();
 #pragma unroll
     for (int x = 0; x < 16; ++x)
-      if (bits >> x & 1u) mx = fmaxf(mx, fmaf(__uint_as_float(s[x]) * kf[c + x], f, ev[c + x]));
+      if (bits >> x & 1u) mx = fmaxf(mx, fmaf(__uint_as_float(s[x]), kf[c + x] * f, ev[c + x]));
   }
   return mx;
 }
@@ -375,8 +379,8 @@ __device__ __noinline__ float careful_weights(uint32_t S, const float* kf, const
     tmem_wait_ld();
 #pragma unroll
     for (int x = 0; x < 16; x += 2) {
-      float v0 = fmaf(__uint_as_float(s[x]) * kf[c + x], f, ev[c + x]) - base;
-      float v1 = fmaf(__uint_as_float(s[x + 1]) * kf[c + x + 1], f, ev[c + x + 1]) - base;
+      float v0 = fmaf(__uint_as_float(s[x]), kf[c + x] * f, ev[c + x]) - base;
+      float v1 = fmaf(__uint_as_float(s[x + 1]), kf[c + x + 1] * f, ev[c + x + 1]) - base;
       if (!(bits >> x & 1u)) v0 = -INFINITY;
       if (!(bits >> (x + 1) & 1u)) v1 = -INFINITY;
       if (bits >> x & 1u) sum += exp2f(v0 - ev[c + x]);
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   __shared__ Item to_v[TT_V], group[2][TT_GROUP];
   __shared__ int to_s[TT_K], to_o[TT_V16];
   __shared__ __align__(16) float kf[TT_SC][KV_BLOCK], ev_f[TT_SC][KV_BLOCK];   // keys' scales; the values' exponents
-  __shared__ float ev_top[TT_SC];                  // the exponent that all weights of a block have; NaN: each has its own
+  __shared__ float ev_top[TT_SC];                  // the exponent that all weights of a block have; NaN: each has its own, or keys are large
   __shared__ float2 swap[2][128];                  // a row's maximum and sum in either softmax group
   __shared__ PlanMem plan;
   __shared__ uint32_t tmem_s;
@@ -841,13 +845,16 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
           auto relative = [&](int e) { return careful ? 0x3C003C00u : (uint32_t)max((15 - min(max(top - e, 0), 15)) << 10, 1 << 9) * 0x10001u; };
           up0 = s0 ? relative(e0) : 0u, up1 = s1 ? relative(e1) : 0u;
           if ((kb >> 1 & 1) == (cw & 1)) {   // this block's scales for the softmax, by one of the two warps
+            bool k_large = false;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int x = lane + 32 * i, ek = scales[x], ev = i ? e1 : e0;
+              k_large |= ek > 127 + K_LARGE;
               kf[sp][x] = ek == KV_NAN || ev == KV_NAN ? __int_as_float(0x7FC00000) : pow2f(ek - 127);
               ev_f[sp][x] = (float)((careful ? ev : top) - 127);
             }
-            if (lane == 0) ev_top[sp] = careful ? __int_as_float(0x7FC00000) : (float)(top - 127);
+            k_large = __any_sync(0xffffffffu, k_large);
+            if (lane == 0) ev_top[sp] = careful || k_large ? __int_as_float(0x7FC00000) : (float)(top - 127);
             __syncwarp();
             if (lane < 2 && who >> lane & 1) mbar_arrive(&bar.gr_full[lane][gr[lane] & 3]);
           }
@@ -891,7 +898,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     int swaps = 0, done = 0, mine = 0;              // units of one tile; products of the group, of this unit
     float m = -INFINITY, l = 0.0f, f = 0.0f;        // m: the maximum that the weights are held against
     int tl = 0;
-    bool warp_live = false;
+    bool warp_live = false, large = false;
 #pragma unroll 1
     for (int it = 0;; ++it) {
       wait(&bar.gr_full[w][it & 3], it >> 2);
@@ -906,13 +913,15 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
           const bool live = tr < per_one && tl < x.n;
           warp_live = __any_sync(0xffffffffu, live);
           f = live ? a.factors[(size_t)x.h * a.q_rows + (size_t)(x.t0 + tl) * a.G + head] : 0.0f;
+          large = __any_sync(0xffffffffu, f > F_LARGE);
           if (!live) tl = -1;
         }
         const float top = ev_top[sp];
         tc_fence_after();   // (S is there as well)
         if (warp_live) {
-          if (flags & F_FULL && top == top) {
-            // The ordinary way: every row sees the whole block, and the block's values have one scale.  The weights are formed
+          if (flags & F_FULL && top == top && !large) {
+            // The ordinary way: every row sees the whole block, the block's values have one scale, and neither the rows' factors nor
+            // the keys' scales are large.  The weights are formed
             // against the maximum so far without looking for the block's own.  Their sum bounds them: while it is below FP16's
             // largest the maximum will do (it lags by 2^7 at most).  Else, and at first, the maximum of the half block is found.
             // (Half a block at a time: a loop of half the code; the SM's instruction cache is short for five roles.)
@@ -945,8 +954,10 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
                 const float mx = fmaf(half_max(S + half * 32, kh), f, top);   // (f is not negative; a query that gives NaN has a NaN maximum)
                 if (mine > 0) wait(&bar.o_done[w][buf ^ 1], (done - 1) >> 1);
                 tc_fence_after();
-                // (by whole steps, so that the weights of the block's first half stay FP16 numbers)
-                const float then = m == -INFINITY ? mx : m + fmaxf(ceilf(mx - m), 0.0f), d = m > -INFINITY ? m - then : 0.0f;
+                // (by whole steps, so that the weights of the block's first half stay FP16 numbers; of a step that leaves none of
+                // them the difference may be rounded)
+                const float step = ceilf(mx - m);
+                const float then = step < 1024.0f ? m + fmaxf(step, 0.0f) : mx, d = m > -INFINITY ? m - then : 0.0f;
                 l = scale_sum(l, d);
                 m = then;
                 if (mine > 0) rescale<D>(lane_base + 256 + w * 128, ex2(d));
@@ -967,7 +978,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
               m = then;
               if (mine > 0) rescale<D>(lane_base + 256 + w * 128, ex2(d));
             }
-            l += careful_weights(S, kf[sp], ev_f[sp], f, m > -INFINITY ? m - P_SHIFT : 0.0f, seen);
+            l += careful_weights(S, kf[sp], ev_f[sp], f, m > -INFINITY ? weights_base(m) : 0.0f, seen);
           }
           tmem_wait_st();
         }
