@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(KC_THREADS)
                       const int32_t* __restrict__ count, int32_t* __restrict__ length, int32_t* err) {
   constexpr int LR = D / 16, ROWS = KC_BLOCKS * KV_BLOCK;   // lanes a row
   static_assert(KC_THREADS == 64 * KC_BLOCKS, "two warps a block");
-  extern __shared__ unsigned char raw[];
+  extern __shared__ __align__(16) unsigned char raw[];
   CompactMem<D>& sh = *reinterpret_cast<CompactMem<D>*>(raw);
   pdl_wait();
   pdl_launch_dependents();

@@ -103,7 +103,7 @@ template <int D, typename Index, typename Place>
 __device__ __forceinline__ void join_rows(const float2* ml, const float* part, int parts, int few, int first, int stride, int rows, Index index,
                                           Place place, uint16_t* out, float* lse) {
   __shared__ float2 sh_ml[2][JOIN_WARPS];
-  __shared__ float sh_part[2][JOIN_WARPS * D];
+  __shared__ __align__(16) float sh_part[2][JOIN_WARPS * D];   // (read in 16-byte pieces)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int at_once = join_at_once(parts, few);
   if (at_once > 1) {

@@ -32,7 +32,7 @@ struct TreeRows {
 template <int D, int NT>
 __global__ void __launch_bounds__(AR_WARPS * 32, ar_ctas(D, NT)) kv_tree_rows_kernel(const TreeRows a) {
   constexpr int MT = D / 16, PB = kv_page_bytes(D);
-  __shared__ float part_o[AR_WARPS][8 * NT][D];
+  __shared__ __align__(8) float part_o[AR_WARPS][8 * NT][D];
   __shared__ float part_m[AR_WARPS][8 * NT], part_l[AR_WARPS][8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int share = blockIdx.x % a.shares, row = blockIdx.x / a.shares, t = row / a.H, h = row - t * a.H;
