@@ -308,6 +308,16 @@ bre_status kv_attend_tree(const bre_kv_cache* cache, const void* q_bf16, int64_t
   return cuda_status(launch_kv_attend_tree(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Whether some of T rows of wa 2-byte elements, sa apart, from a on lie over some of those of wb, sb apart, from b on.  (Of different
+// strides rows that lie between one another count too.)
+static bool rows_meet(const void* a, int64_t sa, int64_t wa, const void* b, int64_t sb, int64_t wb, int64_t T) {
+  const int64_t d = (reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) / 2;
+  if (T == 1 || sa != sb) return d < (T - 1) * sa + wa && -d < (T - 1) * sb + wb;
+  int64_t m = d / sa, off = d % sa;   // row i + m of a begins `off` before row i of b
+  if (off < 0) --m, off += sa;
+  return (off < wa && m > -T && m < T) || (sa - off < wb && m + 1 > -T && m + 1 < T);
+}
+
 bre_status kv_rotate(const void* q_bf16, int64_t q_stride, int n_heads, const void* k_bf16, int64_t k_stride, int n_kv_heads,
                      int head_dim, const int32_t* pos, int T, const uint64_t* turns, int n_pairs, float gain, int offset,
                      int interleaved, int backward, void* q_out_bf16, int64_t q_out_stride, void* k_out_bf16,
@@ -327,6 +337,17 @@ bre_status kv_rotate(const void* q_bf16, int64_t q_stride, int n_heads, const vo
   if (!pos || !aligned(pos, 4) || !rows_ok(q_bf16, q_stride, q_out_bf16, q_out_stride, n_heads) ||
       (k_bf16 && !rows_ok(k_bf16, k_stride, k_out_bf16, k_out_stride, n_kv_heads)))
     return BRE_ERR_ARG;
+  // an output may be its input, and lies over nothing else: in which order threads read and write is open
+  const int64_t wq = (int64_t)n_heads * head_dim, wk = (int64_t)n_kv_heads * head_dim;
+  if (!(q_out_bf16 == q_bf16 && (T == 1 || q_out_stride == q_stride)) && rows_meet(q_bf16, q_stride, wq, q_out_bf16, q_out_stride, wq, T))
+    return BRE_ERR_ARG;
+  if (k_bf16) {
+    if (!(k_out_bf16 == k_bf16 && (T == 1 || k_out_stride == k_stride)) && rows_meet(k_bf16, k_stride, wk, k_out_bf16, k_out_stride, wk, T))
+      return BRE_ERR_ARG;
+    if (rows_meet(k_bf16, k_stride, wk, q_out_bf16, q_out_stride, wq, T) || rows_meet(q_bf16, q_stride, wq, k_out_bf16, k_out_stride, wk, T) ||
+        rows_meet(k_out_bf16, k_out_stride, wk, q_out_bf16, q_out_stride, wq, T))
+      return BRE_ERR_ARG;
+  }
   const RotateRows q{static_cast<const uint16_t*>(q_bf16), static_cast<uint16_t*>(q_out_bf16), q_stride, q_out_stride, n_heads};
   RotateRows k{};
   if (k_bf16)

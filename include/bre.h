@@ -404,8 +404,8 @@ bre_status kv_attend_tree(const bre_kv_cache* cache, const void* q_bf16, int64_t
  * that wrap at a full turn) up to the rounding of turns and 2^-25 of half a turn.  Pairs: interleaved 0: a_i = channel
  * offset + i, b_i = offset + n_pairs + i; else offset + 2 i and offset + 2 i + 1.  A row with a negative position gives zeros.
  *   q, q_out [T][n_heads][D], k, k_out [T][n_kv_heads][D]: BF16, rows `stride` elements apart; k NULL: queries only;
- *   an output may be its input (with the same stride) but may not overlap it otherwise.  pos [T] int32,
- *   turns [n_pairs] uint64 on the device (bre_rope_turns).
+ *   an output may be its input (with the same stride) but may not overlap it otherwise, nor the other input or output
+ *   (BRE_ERR_ARG).  pos [T] int32, turns [n_pairs] uint64 on the device (bre_rope_turns).
  * Requires D % 8 == 0, D <= 256, n_pairs >= 1, offset + 2 n_pairs <= D. */
 bre_status kv_rotate(const void* q_bf16, int64_t q_stride, int n_heads, const void* k_bf16, int64_t k_stride, int n_kv_heads,
                      int head_dim, const int32_t* pos, int T, const uint64_t* turns, int n_pairs, float gain, int offset,
