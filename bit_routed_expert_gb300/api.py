@@ -349,13 +349,14 @@ def kv_attend_tree(q, cache: KvCache, seq, pos, table, start=None, mask=None, sc
     return out, lse
 
 
-ROPE_SCALINGS = ("linear", "base", "ramp", "bands")   # BRE_ROPE_* from 1 on (include/bre.h has the formulas)
+ROPE_SCALINGS = ("linear", "base", "ramp", "bands", "ramp_past")   # BRE_ROPE_* from 1 on (include/bre.h has the formulas)
 
 
 def rope_turns(rot_dim: int, theta: float = 10000.0, scaling: str | None = None, factor: float = 1.0, low: float = 1.0,
                high: float | None = None, length: float = 0.0, device="cpu"):
     """The frequencies of kv_rotate for rot_dim channels: (turns int64 [rot_dim / 2] on `device`, gain).  scaling, for contexts
-    `factor` times as long as the `length` trained on: "linear", "base", "ramp" or "bands"."""
+    `factor` times as long as the `length` trained on: "linear", "base", "ramp" (which ends at the last pair at most; "ramp_past",
+    as the method was published, may end behind it) or "bands"."""
     if scaling is not None and scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be None or one of {ROPE_SCALINGS}")
     how = 0 if scaling is None else 1 + ROPE_SCALINGS.index(scaling)

@@ -359,7 +359,7 @@ bre_status kv_rotate(const void* q_bf16, int64_t q_stride, int n_heads, const vo
 bre_status bre_rope_turns(int rot_dim, double theta, int scaling, double factor, double low, double high, double length,
                           uint64_t* turns, float* gain) {
   if (rot_dim <= 0 || rot_dim % 2 || !turns || !gain || !(theta > 1.0) || std::isinf(theta)) return BRE_ERR_ARG;
-  if (scaling < BRE_ROPE_PLAIN || scaling > BRE_ROPE_BANDS) return BRE_ERR_UNSUPPORTED;
+  if (scaling < BRE_ROPE_PLAIN || scaling > BRE_ROPE_RAMP_PAST) return BRE_ERR_UNSUPPORTED;
   if (scaling != BRE_ROPE_PLAIN && (!(factor > 0.0) || std::isinf(factor))) return BRE_ERR_ARG;
   if (scaling >= BRE_ROPE_RAMP && (!(length > 0.0) || std::isinf(length) || !(low > 0.0) || !(high > low) || std::isinf(high)))
     return BRE_ERR_ARG;

@@ -187,14 +187,15 @@ bool rope_turns(int rot_dim, double theta, int scaling, double factor, double lo
   const double pi2 = 6.283185307179586476925286766559;
   double base = theta;
   if (scaling == BRE_ROPE_BASE && rot_dim > 2) base = theta * std::pow(factor, rot_dim / (rot_dim - 2.0));
-  *gain = scaling == BRE_ROPE_RAMP && factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  const bool ramp = scaling == BRE_ROPE_RAMP || scaling == BRE_ROPE_RAMP_PAST;
+  *gain = ramp && factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
   auto pair_of = [&](double n) { return rot_dim * std::log(length / (n * pi2)) / (2.0 * std::log(base)); };
-  const double first = std::fmax(std::floor(scaling == BRE_ROPE_RAMP ? pair_of(high) : 0.0), 0.0);
-  const double last = std::fmin(std::ceil(scaling == BRE_ROPE_RAMP ? pair_of(low) : 0.0), rot_dim / 2 - 1.0);
+  const double first = std::fmax(std::floor(ramp ? pair_of(high) : 0.0), 0.0);
+  const double last = std::fmin(std::ceil(ramp ? pair_of(low) : 0.0), scaling == BRE_ROPE_RAMP_PAST ? rot_dim - 1.0 : rot_dim / 2 - 1.0);
   for (int i = 0; i < rot_dim / 2; ++i) {
     double f = std::pow(base, -2.0 * i / rot_dim);
     if (scaling == BRE_ROPE_LINEAR) f /= factor;
-    if (scaling == BRE_ROPE_RAMP) {
+    if (ramp) {
       const double r = std::fmin(std::fmax((i - first) / std::fmax(last - first, 0.001), 0.0), 1.0);
       f = f / factor * r + f * (1.0 - r);
     }

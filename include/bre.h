@@ -421,13 +421,18 @@ bre_status kv_rotate(const void* q_bf16, int64_t q_stride, int n_heads, const vo
  *                    p(n) = rot_dim ln(length / (2 pi n)) / (2 ln theta) is the pair that makes n turns in `length`,
  *                    a = max(floor(p(high)), 0), b = min(ceil(p(low)), rot_dim / 2 - 1); gain = 0.1 ln(factor) + 1
  *   BRE_ROPE_BANDS   (1 - w) f_i / factor + w f_i, w = clamp((length f_i / (2 pi) - low) / (high - low), 0, 1)
- * The gain of the others (and for factor <= 1) is 1.  low and high are turns in `length` (usual: 1 and 32 for the ramp,
- * 1 and 4 for bands) and, like length, only looked at for those two.  Host arithmetic in 64 bits; no GPU is needed. */
+ *   BRE_ROPE_RAMP_PAST  as BRE_ROPE_RAMP with b = min(ceil(p(low)), rot_dim - 1)
+ * The gain of the others (and for factor <= 1) is 1.  low and high are turns in `length` (usual: 1 and 32 for the ramps,
+ * 1 and 4 for bands) and, like length, only looked at for those three.  Host arithmetic in 64 bits; no GPU is needed.
+ * The two ramps are the same unless the slowest pair makes more than `low` turns in `length` (theta 10,000 and lengths from some
+ * 50,000 on): BRE_ROPE_RAMP then ends at the last pair, which gets f / factor in full; the method as published goes on
+ * behind it, so models trained with that need BRE_ROPE_RAMP_PAST. */
 #define BRE_ROPE_PLAIN 0
 #define BRE_ROPE_LINEAR 1
 #define BRE_ROPE_BASE 2
 #define BRE_ROPE_RAMP 3
 #define BRE_ROPE_BANDS 4
+#define BRE_ROPE_RAMP_PAST 5
 bre_status bre_rope_turns(int rot_dim, double theta, int scaling, double factor, double low, double high, double length,
                           uint64_t* turns, float* gain);
 
