@@ -333,7 +333,15 @@ def kv_attend(q, cache: KvCache, seq, pos, table, ids, scale: float | None = Non
     return out, lse
 
 
+def _int32(**numbers):
+    """ctypes would cut them."""
+    for name, v in numbers.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} is outside 32 bits: {v}")
+
+
 def kv_attend_tree_workspace(T: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    _int32(T=T, n_heads=n_heads, n_kv_heads=n_kv_heads, head_dim=head_dim)
     return _lib.load().kv_attend_tree_workspace(T, n_heads, n_kv_heads, head_dim)
 
 
@@ -359,6 +367,7 @@ def rope_turns(rot_dim: int, theta: float = 10000.0, scaling: str | None = None,
     as the method was published, may end behind it) or "bands"."""
     if scaling is not None and scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be None or one of {ROPE_SCALINGS}")
+    _int32(rot_dim=rot_dim)
     how = 0 if scaling is None else 1 + ROPE_SCALINGS.index(scaling)
     if high is None:
         high = 4.0 if scaling == "bands" else 32.0
@@ -430,6 +439,7 @@ def kv_fork(cache: KvCache, refs, table, parent, length, dev_err=None, stream=No
 
 
 def kv_resize_workspace(n_pages: int, B: int, N: int) -> int:
+    _int32(n_pages=n_pages, B=B, N=N)
     return _lib.load().kv_resize_workspace(n_pages, B, N)
 
 
