@@ -350,6 +350,8 @@ def kv_attend_tree(q, cache: KvCache, seq, pos, table, start=None, mask=None, sc
     """Attention of q [T, n_heads, D] (BF16) over the whole cached context.  mask None: causal, every token
     x <= pos[t].  Else the sequence's first start[b] tokens (int32 [B]) and, of those drafted behind them, the ones whose bit
     x - start[b] of mask[t] is set (int64 [T, words], 64 bits a word).  Returns (out, lse) as kv_attend.
+    Many tokens of few of the table's sequences (a chunk of a prompt) are several times as fast with a table of these rows
+    alone, such as table[b:b + 1] with seq all 0 (include/bre.h).
     ws: uint8 [kv_attend_tree_workspace(...)], one for calls that may run at the same time each; a new one if None."""
     rc, out, lse = _lib.load_kv().attend_tree(cache, q, seq, pos, table, start, mask, scale, ws, out, lse, dev_err, _raw(stream))
     if rc:

@@ -16,8 +16,8 @@
 // seldom out of line.  A step of 64 tokens takes 1,500 cycles for one tile and 2,100 for two, whose products take 1,260: with two the
 // softmax, the conversion and the issue of O's products take 1,700 to 1,800 each, and wait for one another.  More than 16
 // warps would leave 96 registers a thread, which costs the softmax more than what other roles gain.
-// D = 128, G = 8, four kv heads: 32 sequences of up to 16,384 tokens, 16 drafts each, 113 us (2.5 TB/s); one of
-// 131,072, 64 drafts, 151 us (0.91 PFLOP/s, 0.47 of cuBLAS's); a prompt of 4,096 behind 4,096, 452 us (0.91 PFLOP/s).
+// D = 128, G = 8, four kv heads: 32 sequences of up to 16,384 tokens, 16 drafts each, 115 us (2.5 TB/s); one of
+// 131,072, 64 drafts, 157 us (0.87 PFLOP/s, 0.45 of cuBLAS's); a prompt of 4,096 behind 4,096, 466 us (0.88 PFLOP/s).
 //
 // Sixteen warps:
 //   warps 0-3, 4-7  softmax, a thread a row: two tiles' rows of the same block, or, where there is one tile, its
@@ -34,7 +34,8 @@
 // products of 8-bit operands take the tensor cores as long as one of 16-bit ones, and the keys need no conversion.  A key's
 // scale multiplies its logit.  A value's scale goes into its FP16 value relative to the block's largest, which is exact down to
 // 2^-15 of that, and the largest one into the block's weights; where a row is further below, or the scale is above
-// EV_LARGE, every token's own goes into its weight (see kv_attend.cu), by slower code.
+// EV_LARGE, every token's own goes into its weight (see kv_attend.cu), by slower code.  So do blocks and rows whose logits
+// may be too large for FP32's steps (F_LARGE, K_LARGE): to look at every block's product of both instead cost prompts 3%.
 #include <atomic>
 
 #include "kv_tc.cuh"
@@ -1120,6 +1121,10 @@ cudaError_t launch_kv_attend_tree(const TreeArgs& t, cudaStream_t s) {
   // 2 tokens each 82 / 113, 3 125 / 114; 8 of 16,384, 3 60 / 66, 4 75 / 66; 32 of 2,048, 3 35 / 46, 4 41 / 47; 16 of 1,024, 8
   // 27 / 29; one of 4,096, 16 22 / 33; one of 65,536, 4 41 / 40.  D = 64: 16 of 4,096, eight kv heads, G = 1, 4 42 / 56, 8
   // 72 / 57; 64 of 200, eight kv heads, G = 4, 4 18 / 43.  G = 16: 16 of 8,192, two kv heads, D = 64, 2 29 / 35, 4 46 / 36.
+  // The rule counts the table's rows, as the host does not know how many sequences have tokens in the call.  Those figures are
+  // for tables of as many rows; tokens of one sequence behind 16,384 with a table of 256 rows / of one: 64 tokens 120 / 58, 512
+  // 860 / 155, 640 1,050 / 190; D = 64, 1,280 1,262 / 308.  (bre.h says what a caller can do; tiles for all of these would
+  // cost batches of single tokens, whose tables look the same, twice their time.)
   const long long blocks = (long long)H * t.tk.N, halves = (G > 8 ? 2 : 1) * (D / 64);
   if (t.tk.T * halves * blocks <= 5 * t.tk.B * blocks + 12000) return launch_tree_rows(t, s);
   TreeParams a{};
