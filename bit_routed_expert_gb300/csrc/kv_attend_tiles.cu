@@ -99,7 +99,7 @@ __device__ __forceinline__ float careful_logits(uint32_t S, float2 kt, const flo
 }
 // The weights against the maximum m over those logits; what they add to the row's sum.
 __device__ __forceinline__ float careful_weights(uint32_t S, const float* ev, float m, int n) {
-  const float base = m > -INFINITY ? m - P_SHIFT : 0.0f;
+  const float base = m > -INFINITY ? weights_base(m) : 0.0f;
   float sum = 0.0f;
 #pragma unroll 1
   for (int c = 0; c < KV_BLOCK; c += 32) {
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) kv_attend_tiles_kernel(const At
         l = scale_sum(l, d);
         rescale<D>(lane_base + 128, sc);
       }
-      const float base = m > -INFINITY ? m - P_SHIFT : 0.0f;
+      const float base = m > -INFINITY ? weights_base(m) : 0.0f;
       const uint64_t nb2 = pack2(-base, -base);
       uint64_t add = 0;
 #pragma unroll 1
